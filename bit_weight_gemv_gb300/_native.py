@@ -62,6 +62,30 @@ class lowbit_gemm_desc(ctypes.Structure):
 
 _SIGS["lowbit_gemm_int4_grouped"] = (_i, [ctypes.POINTER(lowbit_gemm_desc), _i, _i, _vp])
 _SIGS["lmhead_argmax_verify_noalloc"] = (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp])
+
+
+class _PagedBatch(ctypes.Structure):
+    """lowbit_paged_batch (mirrors the C struct)."""
+    _fields_ = [("cu_q", _vp), ("kv_lens", _vp), ("block_table", _vp),
+                ("table_stride", ctypes.c_int64), ("B", _i), ("T", _i), ("width", _i)]
+
+
+class _PagedCache(ctypes.Structure):
+    """lowbit_paged_cache (mirrors the C struct)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("num_pages", _i), ("page_size", _i), ("heads", _i), ("head_dim", _i),
+                ("dtype", _i), ("k_scale", _vp), ("v_scale", _vp)]
+
+
+_i64 = ctypes.c_int64
+_SIGS["lowbit_kv_append"] = (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _i, _i, _i,
+                                  ctypes.POINTER(_PagedBatch), ctypes.POINTER(_PagedCache), _vp, _vp])
+_SIGS["lowbit_paged_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
+_SIGS["lowbit_paged_attention"] = (_i, [_vp, _i64, _i, ctypes.POINTER(_PagedBatch),
+                                        ctypes.POINTER(_PagedCache), ctypes.c_float, _i, _i, _vp,
+                                        _vp, _vp, _sz, _vp])
+_SIGS["lowbit_sample"] = (_i, [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
     _f.restype = _res
@@ -416,3 +440,147 @@ def lowbit_draft_argmax_q8(H, packed_head, M, N, K, id_map, ids, workspace, stre
     _check(lib.lowbit_draft_argmax_q8(_ptr(H), _ptr(packed_head), M, N, K, _ptr(id_map), _ptr(ids),
                                       _ptr(workspace), workspace.numel(), _stream(stream)),
            "lowbit_draft_argmax_q8")
+
+
+class lowbit_paged_cache:
+    """A paged key/value cache as the library takes it: k and v of shape
+    [num_pages][page_size][heads][head_dim], bf16 or float8_e4m3fn, head_dim dense, the other
+    strides free (a cache stored [num_pages][heads][page_size][head_dim] is passed as its
+    transpose(1, 2)) and the same for both.  k_scale, v_scale: fp32 [heads] of an e4m3 cache
+    (None = 1).  The object keeps the tensors alive; build it once per layer."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        for t, nm in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4 \
+                    or t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or t.stride(3) != 1:
+                raise TypeError(f"{nm} must be a CUDA tensor [pages][page_size][heads][dim], bf16 or "
+                                "float8_e4m3fn, with a dense last dimension")
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must agree in shape, strides, dtype and device")
+        fp8 = k.dtype == torch.float8_e4m3fn
+        for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                continue
+            if not fp8:
+                raise ValueError(f"{nm} belongs to an e4m3 cache")
+            _need(t, torch.float32, nm)
+            if t.numel() != k.shape[2]:
+                raise ValueError(f"{nm} must hold one value per head")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.head_dim, self.page_size = k.shape[2], k.shape[3], k.shape[1]
+        self.struct = _PagedCache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
+                                  k.shape[0], k.shape[1], k.shape[2], k.shape[3], 1 if fp8 else 0,
+                                  None if k_scale is None else k_scale.data_ptr(),
+                                  None if v_scale is None else v_scale.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+def _rows(t, heads, dim, name):
+    """A bf16 CUDA tensor [T][heads][dim] whose rows may be apart (a slice of a wider product)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [T][{heads}][{dim}]")
+    if t.shape[0] > 1 and t.stride(0) < heads * dim or t.stride(2) != 1 \
+            or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: heads must be dense within a row")
+    return max(t.stride(0), heads * dim) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _batch(cu_q, kv_lens, block_table, T):
+    _need(cu_q, torch.int32, "cu_q")
+    _need(kv_lens, torch.int32, "kv_lens")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 \
+            or not block_table.is_cuda or block_table.dim() != 2 \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise TypeError("block_table must be an int32 CUDA tensor [requests][pages] with dense rows")
+    B = kv_lens.numel()
+    if cu_q.numel() != B + 1 or block_table.shape[0] != B:
+        raise ValueError("cu_q, kv_lens and block_table must describe the same requests")
+    stride = block_table.stride(0) if B > 1 else max(block_table.stride(0), block_table.shape[1])
+    return _PagedBatch(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), stride, B, T,
+                       block_table.shape[1])
+
+
+def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved=False,
+                     stream=None):
+    """Rotary positions on q [T][Hq][D] (into q_out; both may be None) and k [T][heads][D], and
+    k and v into `cache` (a lowbit_paged_cache) at the positions that cu_q, kv_lens and
+    block_table give.  rope: fp32 [positions][rot], cos then sin, or None."""
+    T = k.shape[0] if isinstance(k, torch.Tensor) else 0
+    ks = _rows(k, cache.heads, cache.head_dim, "k")
+    vs = _rows(v, cache.heads, cache.head_dim, "v")
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same rows")
+    qs = Hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        qs = _rows(q, Hq, cache.head_dim, "q")
+        _need(q_out, torch.bfloat16, "q_out")
+        if q.shape[0] != T or q_out.numel() != T * Hq * cache.head_dim:
+            raise ValueError("q and q_out must have k's rows")
+    rows = rot = 0
+    if rope is not None:
+        _need(rope, torch.float32, "rope")
+        if rope.dim() != 2:
+            raise ValueError("rope must have shape [positions][rot]")
+        rows, rot = rope.shape
+    batch = _batch(cu_q, kv_lens, block_table, T)
+    _check(lib.lowbit_kv_append(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Hq, _ptr(rope), rows, rot,
+                                1 if interleaved else 0, ctypes.byref(batch), cache.ref, _ptr(q_out),
+                                _stream(stream)), "lowbit_kv_append")
+
+
+def lowbit_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int) -> int:
+    return lib.lowbit_paged_attention_workspace_bytes(T, B, Hq, Hk, D)
+
+
+def lowbit_paged_attention(q, cache, cu_q, kv_lens, block_table, out, workspace, scale=None,
+                           causal=True, window=0, lse=None, stream=None):
+    """out [T][Hq][D] = attention of q [T][Hq][D] over each request's keys in `cache` (a
+    lowbit_paged_cache); scale None = 1/sqrt(D); lse fp32 [T][Hq] or None."""
+    Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    D = cache.head_dim
+    qs = _rows(q, Hq, D, "q")
+    T = q.shape[0]
+    _need(out, torch.bfloat16, "out")
+    _need(workspace, torch.uint8, "workspace")
+    if out.numel() != T * Hq * D:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.numel() != T * Hq:
+            raise ValueError("lse must have shape [T][Hq]")
+    batch = _batch(cu_q, kv_lens, block_table, T)
+    _check(lib.lowbit_paged_attention(_ptr(q), qs, Hq, ctypes.byref(batch), cache.ref,
+                                      D ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                      window, _ptr(out), _ptr(lse), _ptr(workspace),
+                                      workspace.numel(), _stream(stream)), "lowbit_paged_attention")
+
+
+def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,
+                  logprob=None, kept=None, stream=None):
+    """One token per row of logits [M][V] (fp32 or bf16, rows may be apart) from the uniform
+    numbers u [M]; every other argument may be None (see include/lowbit.h)."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2 \
+            or logits.dtype not in (torch.float32, torch.bfloat16) \
+            or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise TypeError("logits must be an fp32 or bf16 CUDA tensor [M][V] with dense rows")
+    M, V = logits.shape
+    for t, dt, n, nm in ((u, torch.float32, M, "u"), (ids, torch.int32, M, "ids"),
+                         (temperature, torch.float32, M, "temperature"),
+                         (top_k, torch.int32, M, "top_k"), (top_p, torch.float32, M, "top_p"),
+                         (min_p, torch.float32, M, "min_p"), (id_map, torch.int32, V, "id_map"),
+                         (logprob, torch.float32, M, "logprob"), (kept, torch.int32, M, "kept")):
+        if t is None and nm not in ("u", "ids"):
+            continue
+        _need(t, dt, nm)
+        if t.numel() != n:
+            raise ValueError(f"{nm} must hold {n} values")
+    _check(lib.lowbit_sample(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0,
+                             logits.stride(0) if M > 1 else max(logits.stride(0), V), M, V,
+                             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
+                             _ptr(id_map), _ptr(ids), _ptr(logprob), _ptr(kept), _stream(stream)),
+           "lowbit_sample")

@@ -1,0 +1,86 @@
+// Definitions shared by the kernels that work on a paged key/value cache: the batch and cache as
+// the kernels see them, host-side validation, and the schedule that splits attention work.
+#pragma once
+
+#include "common.cuh"
+
+namespace lowbit {
+
+constexpr int kMaxHeadDim = 256;
+constexpr int kMaxPageSize = 1024;
+constexpr int kMaxBatch = 1 << 16;
+constexpr int kMaxTokens = 1 << 24;
+
+// lowbit_paged_batch and lowbit_paged_cache with what the host has derived.
+struct PagedArgs {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  long long table_stride;
+  int B, T, width;             // requests, rows of the token arrays, columns of the block table
+  uint8_t* k;
+  uint8_t* v;
+  long long page_stride, token_stride, head_stride;  // bytes
+  int pages, page_shift, page_mask;
+  int Hk;
+  const float* k_scale;
+  const float* v_scale;
+  int* err;
+};
+
+// Checks of the two descriptors; fills `a` (all but err).
+lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_paged_cache* cache,
+                              PagedArgs* a);
+
+// First row, new tokens and whole length of request b.  A request that the arrays describe
+// inconsistently (decreasing offsets, rows past T, more keys than its pages hold) counts as one
+// without tokens, and the device error word says so.
+struct Request {
+  int row0, n, kv;
+};
+__device__ __forceinline__ Request load_request(const PagedArgs& a, int b) {
+  Request r;
+  r.row0 = a.cu_q[b];
+  r.n = a.cu_q[b + 1] - r.row0;
+  r.kv = a.kv_lens[b];
+  if (r.row0 < 0 || r.n < 0 || r.row0 > a.T - r.n || r.kv < 0 ||
+      (long long)r.kv > ((long long)a.width << a.page_shift)) {
+    record_error(a.err, LOWBIT_ERR_INVALID_ARG);
+    r.row0 = r.n = r.kv = 0;
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------- attention schedule
+// A work item is (request, key/value head, tile of R query rows); query row r of a request is
+// token r / G, head r % G of the group, so the rows that share keys share a tile.  An item costs
+// its number of key tiles of BN, counted from the tile that holds the first key any of its rows
+// sees.  Items are laid end to end (request, then head, then query tile) and the whole length is
+// cut into equal chunks, one per CTA: ragged batches balance by construction, and an item that
+// crosses a cut is finished by the combine kernel from its pieces' (maximum, sum, output).
+struct Span {
+  int lo, hi;  // keys [lo, hi) that some row of the tile sees; lo == hi: none
+};
+struct ItemShape {
+  int G, R, BN;
+  int causal, window;
+};
+__device__ __forceinline__ Span tile_span(const ItemShape& s, const Request& q, int qt) {
+  const int r0 = qt * s.R, r1 = min(r0 + s.R, q.n * s.G) - 1;
+  const int p0 = q.kv - q.n + r0 / s.G, p1 = q.kv - q.n + r1 / s.G;
+  Span k;
+  k.hi = s.causal ? max(0, min(q.kv, p1 + 1)) : q.kv;
+  k.lo = s.window ? max(0, p0 - s.window + 1) : 0;
+  if (k.lo >= k.hi) k.lo = k.hi = 0;
+  return k;
+}
+// Key tiles of the span; a tile without visible keys still costs one, which writes its zeros.
+__device__ __forceinline__ int tile_cost(const ItemShape& s, const Span& k) {
+  const int first = k.lo / s.BN * s.BN;
+  return max(1, (k.hi - first + s.BN - 1) / s.BN);
+}
+__device__ __forceinline__ int query_tiles(const ItemShape& s, const Request& q) {
+  return (int)(((long long)q.n * s.G + s.R - 1) / s.R);
+}
+
+}  // namespace lowbit

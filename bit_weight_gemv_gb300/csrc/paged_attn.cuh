@@ -1,0 +1,200 @@
+// What the attention kernels share: their arguments, the walk over a CTA's share of the work,
+// the pieces of items that were cut, and the launch of a kernel with its combine step.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace lowbit {
+
+constexpr int kMaxDevices = 64;
+// Query rows of all pieces together: every CTA may leave two (the item it starts inside of and
+// the one it ends inside of).  The workspace holds D + 2 floats for each; a kernel's grid is
+// limited so that 2 * CTAs * rows stays within it.
+constexpr int kMaxPieceRows = 2 * 152 * 128;
+
+struct AttnArgs {
+  PagedArgs p;
+  ItemShape shape;
+  const uint16_t* q;
+  long long q_stride;
+  int Hq;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* piece_o;   // [slot][R][D], relative to the piece's maximum, not divided by its sum
+  float2* piece_ml; // [slot][R]: maximum (of scale * score * log2 e) and sum
+  int ctas;
+};
+
+cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);
+
+// A CTA's share [begin, end) of the work, in key tiles, and where begin falls.
+struct Plan {
+  long long begin, end, chunk;
+  long long off;  // of begin inside request b's work
+  int b;
+};
+// Key tiles of all heads of request b.  `lane` < 0: by one thread alone, else by a whole warp.
+__device__ __forceinline__ long long head_cost(const ItemShape& s, const Request& q, int lane) {
+  long long c = 0;
+  const int nq = query_tiles(s, q);
+  for (int i = lane < 0 ? 0 : lane; i < nq; i += lane < 0 ? 1 : 32) c += tile_cost(s, tile_span(s, q, i));
+  if (lane >= 0)
+    for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+  return c;
+}
+
+// The CTA's share, by all NT threads of the block (a multiple of 32); `pl` is valid after the
+// next __syncthreads.  Requests are summed one per thread, or one per warp where each has many
+// query tiles.
+template <int NT>
+__device__ __forceinline__ void make_plan(const AttnArgs& a, Plan& pl, int cta) {
+  __shared__ long long s_warp[NT / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool by_warp = (long long)a.p.T * a.shape.G > 4LL * a.shape.R * a.p.B;
+  long long total = 0, chunk = 0, begin = 0, end = 0;
+  if (tid == 0) pl.b = a.p.B, pl.off = 0, pl.begin = pl.end = 0;
+  // pass 0 sums, pass 1 finds the request that holds `begin`; one pass serves when every request
+  // has a thread of its own
+  const int step = by_warp ? NT / 32 : NT;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long carry = 0;
+    for (int b0 = 0; b0 < a.p.B; b0 += step) {
+      const int b = b0 + (by_warp ? warp : tid);
+      long long c = 0;
+      if (b < a.p.B) {
+        const Request q = load_request(a.p, b);
+        c = head_cost(a.shape, q, by_warp ? lane : -1) * a.p.Hk;
+      }
+      long long incl = c;  // inclusive sum over the requests of this warp
+      if (!by_warp)
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(~0u, incl, o);
+          if (lane >= o) incl += v;
+        }
+      __syncthreads();
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      long long before = carry;
+      for (int i = 0; i < NT / 32; ++i) {
+        if (i < warp) before += s_warp[i];
+        carry += s_warp[i];
+      }
+      if (pass == 0 && a.p.B <= step) {
+        total = carry;
+        chunk = (total + a.ctas - 1) / a.ctas;
+        begin = (long long)cta * chunk;
+        end = begin + chunk < total ? begin + chunk : total;
+      }
+      if (pass == 1 || a.p.B <= step) {
+        const long long at = before + incl - c;
+        if (begin < total && begin >= at && begin < at + c && (!by_warp || lane == 0)) {
+          pl.b = b;
+          pl.off = begin - at;
+          pl.begin = begin;
+          pl.end = end;
+        }
+      }
+    }
+    if (a.p.B <= step) break;
+    total = carry;
+    chunk = (total + a.ctas - 1) / a.ctas;
+    begin = (long long)cta * chunk;
+    end = begin + chunk < total ? begin + chunk : total;
+  }
+  if (tid == 0) pl.chunk = chunk;
+}
+
+// The walk over items from the plan's start: every warp keeps its own copy.
+struct Walk {
+  Request q;
+  Span span;
+  int b, h, qt, nq;
+  int tile, tiles;  // next key tile of the item, and how many it has
+};
+__device__ __forceinline__ void walk_item(const AttnArgs& a, Walk& w) {
+  w.span = tile_span(a.shape, w.q, w.qt);
+  w.tiles = tile_cost(a.shape, w.span);
+}
+// By whole warps.
+__device__ __forceinline__ Walk walk_start(const AttnArgs& a, const Plan& pl) {
+  const int lane = threadIdx.x & 31;
+  Walk w;
+  w.b = pl.b;
+  w.q = load_request(a.p, w.b);
+  w.nq = query_tiles(a.shape, w.q);
+  if (w.nq == 1) {
+    w.qt = 0;
+    walk_item(a, w);
+    w.h = (int)(pl.off / w.tiles);
+    w.tile = (int)(pl.off - (long long)w.h * w.tiles);
+    return w;
+  }
+  const long long each = head_cost(a.shape, w.q, lane);
+  w.h = (int)(pl.off / each);
+  long long rest = pl.off - w.h * each;
+  w.qt = 0;
+  w.tile = 0;
+  for (int i0 = 0; i0 < w.nq; i0 += 32) {
+    const int i = i0 + lane;
+    const long long c = i < w.nq ? tile_cost(a.shape, tile_span(a.shape, w.q, i)) : 0;
+    long long incl = c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(~0u, incl > rest);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      w.qt = i0 + src;
+      w.tile = (int)(rest - __shfl_sync(~0u, incl - c, src));
+      break;
+    }
+    rest -= __shfl_sync(~0u, incl, 31);
+  }
+  walk_item(a, w);
+  return w;
+}
+// To the next item; false past the last request.
+__device__ __forceinline__ bool walk_next(const AttnArgs& a, Walk& w) {
+  w.tile = 0;
+  if (++w.qt == w.nq) {
+    w.qt = 0;
+    if (++w.h == a.p.Hk) {
+      w.h = 0;
+      do {
+        if (++w.b >= a.p.B) return false;
+        w.q = load_request(a.p, w.b);
+        w.nq = query_tiles(a.shape, w.q);
+      } while (w.nq == 0);
+    }
+  }
+  walk_item(a, w);
+  return true;
+}
+
+// Columns c..c+3 of one finished row: acc / l, rounded once, and the row's lse.
+__device__ __forceinline__ void store_row(const AttnArgs& a, long long row, int D, int c, float4 acc,
+                                          float m, float l, float vscale) {
+  const float f = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);  // l NaN: NaN
+  uint2 v;
+  v.x = (uint32_t)float_to_bf16_bits(acc.x * f) | ((uint32_t)float_to_bf16_bits(acc.y * f) << 16);
+  v.y = (uint32_t)float_to_bf16_bits(acc.z * f) | ((uint32_t)float_to_bf16_bits(acc.w * f) << 16);
+  *reinterpret_cast<uint2*>(a.out + row * D + c) = v;
+  if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
+__device__ __forceinline__ void store_piece(const AttnArgs& a, long long slot, int R, int D, int row, int c,
+                                            float4 acc, float m, float l) {
+  *reinterpret_cast<float4*>(a.piece_o + (slot * R + row) * D + c) = acc;
+  if (c == 0) a.piece_ml[slot * R + row] = make_float2(m, l);
+}
+
+// Launches `kernel` over a.ctas resident CTAs and the combine step behind it.
+cudaError_t launch_attention(void (*kernel)(const AttnArgs), const AttnArgs& a, int threads, int smem, int D,
+                             cudaStream_t s);
+
+}  // namespace lowbit

@@ -323,6 +323,122 @@ lowbit_status lmhead_accept_keys(const uint64_t* keys, int W, int M, const int32
                                  int32_t* argmax, int32_t* n_accept, int32_t* bonus, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Between the products: a paged key/value cache, attention over it, and sampling.
+ *
+ * A decoder layer's q, k and v products are followed by lowbit_kv_append (rotary positions, keys
+ * and values into the cache) and lowbit_paged_attention (the new tokens over the cache), whose
+ * output feeds the o product.  Both take the same description of the batch, on the device, so a
+ * captured graph serves steps whose lengths differ.
+ */
+
+/* Which rows of the token arrays belong to which request.  Row cu_q[b] + i (0 <= i < n,
+ * n = cu_q[b+1] - cu_q[b]) is new token i of request b; its position is kv_lens[b] - n + i,
+ * where kv_lens[b] counts all keys of the request, the new ones included.  Position p is in
+ * slot p % page_size of page block_table[b][p / page_size].  n = 0 is an idle request; rows past
+ * cu_q[B] belong to nobody and are neither read nor written.
+ * The kernels check what they read: a request whose cu_q decreases or passes T, or whose
+ * kv_lens is negative or passes width * page_size, is skipped; a token whose page is outside
+ * 0..num_pages-1 is not appended, and a key in such a page is read as zeros.  Each records
+ * LOWBIT_ERR_INVALID_ARG in the device error word. */
+typedef struct lowbit_paged_batch {
+  const int32_t* cu_q;         /* device, [B + 1] */
+  const int32_t* kv_lens;      /* device, [B] */
+  const int32_t* block_table;  /* device, [B][table_stride], `width` entries used per row */
+  int64_t table_stride;        /* elements, >= width */
+  int B;                       /* requests, 1..65536 */
+  int T;                       /* rows of the token arrays, 0..2^24 */
+  int width;                   /* pages a request may have, >= 1 */
+} lowbit_paged_batch;
+
+#define LOWBIT_CACHE_BF16 0 /* keys and values as bf16 */
+#define LOWBIT_CACHE_E4M3 1 /* as e4m3, times k_scale / v_scale of the head */
+
+/* A cache of num_pages pages of page_size slots (a power of two, 1..1024) for `heads` key/value
+ * heads of head_dim 64, 128 or 256.  Element (page, slot, head, d) of k (and v) is at
+ * page * page_stride + slot * token_stride + head * head_stride + d: strides in elements,
+ * positive multiples of 16 bytes, so both orders of heads and slots fit.  The two arrays are
+ * 16-byte aligned and share the strides. */
+typedef struct lowbit_paged_cache {
+  void* k;
+  void* v;
+  int64_t page_stride, token_stride, head_stride;
+  int num_pages, page_size, heads, head_dim;
+  int dtype;                   /* LOWBIT_CACHE_BF16 or LOWBIT_CACHE_E4M3 */
+  const float* k_scale;        /* device, [heads], or NULL for 1 (e4m3 only; else NULL) */
+  const float* v_scale;
+} lowbit_paged_cache;
+
+/* Rotary positions on the new tokens' queries and keys, and keys and values into the cache.
+ *   q : bf16 [T][Hq][D] or NULL, k, v : bf16 [T][heads][D]; D = head_dim; the token strides
+ *       q_stride, k_stride, v_stride are in elements (multiples of 8; heads are dense), so the
+ *       three may be column ranges of one product's output.  16-byte aligned.
+ *   rope : fp32 [rope_rows][rot], 16-byte aligned: row p holds cos then sin (rot/2 each) of
+ *       position p.  rot is a multiple of 16, at most D; rot = 0 (rope NULL) rotates nothing.
+ *       Element pair j is (x[j], x[j + rot/2]), or (x[2j], x[2j + 1]) when `interleaved`:
+ *         a' = a cos - b sin,  b' = b cos + a sin   (fp32, every product and sum rounded).
+ *       Elements from rot on, and values, are not rotated.
+ *   q_out : bf16 [T][Hq][D], dense, 16-byte aligned (NULL with q); may be q itself.
+ *   In the cache a bf16 element is rounded once; an e4m3 element is x / scale rounded to
+ *   nearest-even and clipped to +-448 (NaN stays NaN).  Slots of other positions keep their
+ *   contents.  A position at or past rope_rows is not appended and recorded in the device
+ *   error word. */
+lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                               int64_t k_stride, const uint16_t* v, int64_t v_stride, int Hq,
+                               const float* rope, int rope_rows, int rot, int interleaved,
+                               const lowbit_paged_batch* batch, const lowbit_paged_cache* cache,
+                               uint16_t* q_out, void* stream);
+
+/* Bytes of lowbit_paged_attention's workspace for up to T rows and B requests of Hq query and
+ * Hk key/value heads of D (0 for invalid shapes). */
+size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D);
+
+/* Attention of every request's new tokens over its cached keys, grouped heads (query head h
+ * reads key/value head h / (Hq / heads)):
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j over the keys j the token sees:
+ *   j < kv_lens[b]; j <= its position when `causal`; j > its position - window when window > 0.
+ *   A token that sees no key gets zeros, and -inf as lse.
+ *   q   : bf16 [T][Hq][D], token stride q_stride (elements, a multiple of 8), 16-byte aligned.
+ *   out : bf16 [T][Hq][D] dense, 16-byte aligned.    lse : fp32 [T][Hq] or NULL: the natural
+ *   logarithm of the softmax's denominator (log sum_j exp(scale * q . k_j)).
+ *   workspace : lowbit_paged_attention_workspace_bytes() bytes, 16-byte aligned, any contents.
+ *   Scores, softmax statistics and outputs are held in fp32; the softmax weights enter their
+ *   product with v rounded to bf16 (bf16 cache) or fp16 (e4m3 cache).  Slots outside a request's
+ *   span are never used, whatever they hold.  A non-finite value inside the span may reach every
+ *   row of the token's tile (up to 128 rows) that is computed with it.  The result does not
+ *   depend on timing: the same call gives the same bits. */
+lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq,
+                                     const lowbit_paged_batch* batch,
+                                     const lowbit_paged_cache* cache, float scale, int causal,
+                                     int window, uint16_t* out, float* lse, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+#define LOWBIT_LOGITS_FP32 0
+#define LOWBIT_LOGITS_BF16 1
+
+/* One token per row of logits, from given uniform numbers.
+ *   logits : [M][V] fp32 or bf16 (dtype), row stride row_stride elements; M >= 1, 1 <= V <= 2^19.
+ *   temperature, top_p, min_p : fp32 [M], top_k : int32 [M]; NULL = 1, 1, 0, 0 (no truncation).
+ *   u : fp32 [M] in [0, 1) (others are clamped, NaN counts as 0).
+ *   Per row, with z the logits (NaN counts as -inf, +inf as the largest finite value):
+ *     w_i = exp((z_i - max z) * (1 / temperature)) in fp32, 0 where z_i = -inf, and its mass
+ *     m_i = w_i * 2^40 rounded to a whole number: all sums below are exact in 64 bits and do
+ *     not depend on their order.  Temperatures below 1e-6 (or NaN) are greedy (top_k = 1);
+ *     above 1e6 they count as 1e6.
+ *     Tokens are ordered by larger z, then lower index.  top_k keeps the first k (k <= 0 or
+ *     > V: all); top_p then keeps, of the mass S of those, the tokens whose preceding mass is
+ *     below max(1, ceil(top_p * S)) (top_p >= 1: all); min_p drops those with w < min(min_p, 1).
+ *     With S the kept mass, the token is the first in index order whose inclusive kept mass
+ *     exceeds floor(u * S).
+ *   ids     : int32 [M] out: the token (id_map[token] when id_map, int32 [V], is not NULL), or
+ *             -1 for a row without a finite logit.
+ *   logprob : fp32 [M] out or NULL: log(m / S) of the token (-inf with id -1).
+ *   kept    : int32 [M] out or NULL: tokens of nonzero mass that remain. */
+lowbit_status lowbit_sample(const void* logits, int dtype, int64_t row_stride, int M, int V,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const float* u, const int32_t* id_map,
+                            int32_t* ids, float* logprob, int32_t* kept, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * For callers that cannot allocate device memory.
  */
 
