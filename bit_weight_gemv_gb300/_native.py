@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -64,10 +65,8 @@ _SIGS["lowbit_gemm_int4_grouped"] = (_i, [ctypes.POINTER(lowbit_gemm_desc), _i, 
 _SIGS["lmhead_argmax_verify_noalloc"] = (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp])
 
 
-class _PagedBatch(ctypes.Structure):
-    """lowbit_paged_batch (mirrors the C struct)."""
-    _fields_ = [("cu_q", _vp), ("kv_lens", _vp), ("block_table", _vp),
-                ("table_stride", ctypes.c_int64), ("B", _i), ("T", _i), ("width", _i)]
+# lowbit_paged_batch, packed field by field (a ctypes.Structure costs three times the host time)
+_PAGED_BATCH = struct.Struct("@PPPqiii0q")
 
 
 class _PagedCache(ctypes.Structure):
@@ -80,9 +79,9 @@ class _PagedCache(ctypes.Structure):
 
 _i64 = ctypes.c_int64
 _SIGS["lowbit_kv_append"] = (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _i, _i, _i,
-                                  ctypes.POINTER(_PagedBatch), ctypes.POINTER(_PagedCache), _vp, _vp])
+                                  _vp, ctypes.POINTER(_PagedCache), _vp, _vp])
 _SIGS["lowbit_paged_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
-_SIGS["lowbit_paged_attention"] = (_i, [_vp, _i64, _i, ctypes.POINTER(_PagedBatch),
+_SIGS["lowbit_paged_attention"] = (_i, [_vp, _i64, _i, _vp,
                                         ctypes.POINTER(_PagedCache), ctypes.c_float, _i, _i, _vp,
                                         _vp, _vp, _sz, _vp])
 _SIGS["lowbit_sample"] = (_i, [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
@@ -104,13 +103,20 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The handle of torch's current stream without building a Stream object around it (a third of a
+# small call's host time); the public way where a torch build lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t, dtype, name):
@@ -475,31 +481,41 @@ class lowbit_paged_cache:
         self.ref = ctypes.byref(self.struct)
 
 
-def _rows(t, heads, dim, name):
-    """A bf16 CUDA tensor [T][heads][dim] whose rows may be apart (a slice of a wider product)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+def _rows(t, dim, name):
+    """(rows, heads, row stride) of a bf16 CUDA tensor [T][heads][dim] whose rows may be apart (a
+    slice of a wider product)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [T][{heads}][{dim}]")
-    if t.shape[0] > 1 and t.stride(0) < heads * dim or t.stride(2) != 1 \
-            or (heads > 1 and t.stride(1) != dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} must have shape [T][heads][{dim}]")
+    T, heads, _ = shape
+    row, head, one = t.stride()
+    if T <= 1:
+        row = heads * dim if row < heads * dim or row % 8 else row
+    if row < heads * dim or one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}: heads must be dense within a row")
-    return max(t.stride(0), heads * dim) if t.shape[0] <= 1 else t.stride(0)
+    return T, heads, row
 
 
 def _batch(cu_q, kv_lens, block_table, T):
+    """A lowbit_paged_batch as bytes."""
     _need(cu_q, torch.int32, "cu_q")
     _need(kv_lens, torch.int32, "kv_lens")
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 \
-            or not block_table.is_cuda or block_table.dim() != 2 \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise TypeError("block_table must be an int32 CUDA tensor [requests][pages] with dense rows")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 \
+            or not block_table.is_cuda:
+        raise TypeError("block_table must be an int32 CUDA tensor")
+    shape = block_table.shape
     B = kv_lens.numel()
-    if cu_q.numel() != B + 1 or block_table.shape[0] != B:
-        raise ValueError("cu_q, kv_lens and block_table must describe the same requests")
-    stride = block_table.stride(0) if B > 1 else max(block_table.stride(0), block_table.shape[1])
-    return _PagedBatch(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), stride, B, T,
-                       block_table.shape[1])
+    if len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:
+        raise ValueError("cu_q [requests + 1], kv_lens [requests] and block_table [requests][pages] "
+                         "must describe the same requests")
+    row, one = block_table.stride()
+    width = shape[1]
+    if width > 1 and one != 1:
+        raise ValueError("block_table: rows must be dense")
+    return _PAGED_BATCH.pack(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+                             row if B > 1 else max(row, width), B, T, width)
 
 
 def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved=False,
@@ -507,30 +523,29 @@ def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, in
     """Rotary positions on q [T][Hq][D] (into q_out; both may be None) and k [T][heads][D], and
     k and v into `cache` (a lowbit_paged_cache) at the positions that cu_q, kv_lens and
     block_table give.  rope: fp32 [positions][rot], cos then sin, or None."""
-    T = k.shape[0] if isinstance(k, torch.Tensor) else 0
-    ks = _rows(k, cache.heads, cache.head_dim, "k")
-    vs = _rows(v, cache.heads, cache.head_dim, "v")
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same rows")
-    qs = Hq = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
-        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
-        qs = _rows(q, Hq, cache.head_dim, "q")
+    D = cache.head_dim
+    T, H, ks = _rows(k, D, "k")
+    Tv, Hv, vs = _rows(v, D, "v")
+    if Tv != T or H != cache.heads or Hv != H:
+        raise ValueError("k and v must have the same rows and the cache's heads")
+    qs = Hq = qp = op = rp = rows = rot = 0
+    if q is not None and q_out is not None:
+        Tq, Hq, qs = _rows(q, D, "q")
         _need(q_out, torch.bfloat16, "q_out")
-        if q.shape[0] != T or q_out.numel() != T * Hq * cache.head_dim:
+        if Tq != T or q_out.numel() != T * Hq * D:
             raise ValueError("q and q_out must have k's rows")
-    rows = rot = 0
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q is not q_out:
+        raise ValueError("q and q_out go together")
     if rope is not None:
         _need(rope, torch.float32, "rope")
-        if rope.dim() != 2:
-            raise ValueError("rope must have shape [positions][rot]")
         rows, rot = rope.shape
-    batch = _batch(cu_q, kv_lens, block_table, T)
-    _check(lib.lowbit_kv_append(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Hq, _ptr(rope), rows, rot,
-                                1 if interleaved else 0, ctypes.byref(batch), cache.ref, _ptr(q_out),
-                                _stream(stream)), "lowbit_kv_append")
+        rp = rope.data_ptr()
+    st = lib.lowbit_kv_append(qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, Hq, rp, rows, rot,
+                              1 if interleaved else 0, _batch(cu_q, kv_lens, block_table, T),
+                              cache.ref, op, _stream(stream))
+    if st:
+        raise LowbitError(st, "lowbit_kv_append")
 
 
 def lowbit_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int) -> int:
@@ -541,23 +556,24 @@ def lowbit_paged_attention(q, cache, cu_q, kv_lens, block_table, out, workspace,
                            causal=True, window=0, lse=None, stream=None):
     """out [T][Hq][D] = attention of q [T][Hq][D] over each request's keys in `cache` (a
     lowbit_paged_cache); scale None = 1/sqrt(D); lse fp32 [T][Hq] or None."""
-    Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
     D = cache.head_dim
-    qs = _rows(q, Hq, D, "q")
-    T = q.shape[0]
+    T, Hq, qs = _rows(q, D, "q")
     _need(out, torch.bfloat16, "out")
     _need(workspace, torch.uint8, "workspace")
     if out.numel() != T * Hq * D:
         raise ValueError("out must have q's shape")
+    lp = 0
     if lse is not None:
         _need(lse, torch.float32, "lse")
         if lse.numel() != T * Hq:
             raise ValueError("lse must have shape [T][Hq]")
-    batch = _batch(cu_q, kv_lens, block_table, T)
-    _check(lib.lowbit_paged_attention(_ptr(q), qs, Hq, ctypes.byref(batch), cache.ref,
-                                      D ** -0.5 if scale is None else scale, 1 if causal else 0,
-                                      window, _ptr(out), _ptr(lse), _ptr(workspace),
-                                      workspace.numel(), _stream(stream)), "lowbit_paged_attention")
+        lp = lse.data_ptr()
+    st = lib.lowbit_paged_attention(q.data_ptr(), qs, Hq, _batch(cu_q, kv_lens, block_table, T),
+                                    cache.ref, D ** -0.5 if scale is None else scale,
+                                    1 if causal else 0, window, out.data_ptr(), lp,
+                                    workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if st:
+        raise LowbitError(st, "lowbit_paged_attention")
 
 
 def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,
@@ -565,22 +581,26 @@ def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_
     """One token per row of logits [M][V] (fp32 or bf16, rows may be apart) from the uniform
     numbers u [M]; every other argument may be None (see include/lowbit.h)."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2 \
-            or logits.dtype not in (torch.float32, torch.bfloat16) \
-            or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise TypeError("logits must be an fp32 or bf16 CUDA tensor [M][V] with dense rows")
+            or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be an fp32 or bf16 CUDA tensor [M][V]")
     M, V = logits.shape
-    for t, dt, n, nm in ((u, torch.float32, M, "u"), (ids, torch.int32, M, "ids"),
-                         (temperature, torch.float32, M, "temperature"),
-                         (top_k, torch.int32, M, "top_k"), (top_p, torch.float32, M, "top_p"),
-                         (min_p, torch.float32, M, "min_p"), (id_map, torch.int32, V, "id_map"),
-                         (logprob, torch.float32, M, "logprob"), (kept, torch.int32, M, "kept")):
-        if t is None and nm not in ("u", "ids"):
-            continue
-        _need(t, dt, nm)
+    row, one = logits.stride()
+    if V > 1 and one != 1:
+        raise ValueError("logits: rows must be dense")
+
+    def at(t, dtype, n, name):
+        if t is None:
+            return 0
+        _need(t, dtype, name)
         if t.numel() != n:
-            raise ValueError(f"{nm} must hold {n} values")
-    _check(lib.lowbit_sample(_ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0,
-                             logits.stride(0) if M > 1 else max(logits.stride(0), V), M, V,
-                             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
-                             _ptr(id_map), _ptr(ids), _ptr(logprob), _ptr(kept), _stream(stream)),
-           "lowbit_sample")
+            raise ValueError(f"{name} must hold {n} values")
+        return t.data_ptr()
+
+    f, i = torch.float32, torch.int32
+    st = lib.lowbit_sample(logits.data_ptr(), 1 if logits.dtype is torch.bfloat16 else 0,
+                           row if M > 1 else max(row, V), M, V, at(temperature, f, M, "temperature"),
+                           at(top_k, i, M, "top_k"), at(top_p, f, M, "top_p"), at(min_p, f, M, "min_p"),
+                           at(u, f, M, "u"), at(id_map, i, V, "id_map"), at(ids, i, M, "ids"),
+                           at(logprob, f, M, "logprob"), at(kept, i, M, "kept"), _stream(stream))
+    if st:
+        raise LowbitError(st, "lowbit_sample")

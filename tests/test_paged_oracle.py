@@ -111,7 +111,8 @@ P = 0x10000      # never dereferenced: every call below is refused on the host
 
 def batch(n, **kw):
     f = dict(cu_q=P, kv_lens=P, block_table=P, table_stride=8, B=2, T=4, width=8)
-    return n._PagedBatch(**(f | kw))
+    f |= kw
+    return n._PAGED_BATCH.pack(*(f[x] or 0 for x in ("cu_q", "kv_lens", "block_table", "table_stride", "B", "T", "width")))
 
 
 def cache(n, **kw):
@@ -135,13 +136,13 @@ def append(n, b, c, **kw):
     f = dict(q=P, qs=4 * 128, k=P, ks=2 * 128, v=P, vs=2 * 128, Hq=4, rope=P, rows=100, rot=128, q_out=P)
     f |= kw
     return n.lib.lowbit_kv_append(f["q"], f["qs"], f["k"], f["ks"], f["v"], f["vs"], f["Hq"], f["rope"],
-                                  f["rows"], f["rot"], 0, ctypes.byref(b), ctypes.byref(c), f["q_out"], None)
+                                  f["rows"], f["rot"], 0, b, ctypes.byref(c), f["q_out"], None)
 
 
 def attend(n, b, c, **kw):
     f = dict(q=P, qs=4 * 128, Hq=4, scale=0.1, window=0, out=P, lse=P, ws=P, bytes=1 << 40)
     f |= kw
-    return n.lib.lowbit_paged_attention(f["q"], f["qs"], f["Hq"], ctypes.byref(b), ctypes.byref(c), f["scale"],
+    return n.lib.lowbit_paged_attention(f["q"], f["qs"], f["Hq"], b, ctypes.byref(c), f["scale"],
                                         1, f["window"], f["out"], f["lse"], f["ws"], f["bytes"], None)
 
 
