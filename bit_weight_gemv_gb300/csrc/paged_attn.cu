@@ -510,7 +510,11 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t s) {
   a.ctas = ctas;
   a.shape.R = C::kRows;
   a.shape.BN = kBN;
-  return launch_attention(attn_mma_kernel<D, MT, FP8>, a, kThreads, C::kSmem, D, s);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
+  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<D, MT, FP8>, a);
+  return e != cudaSuccess ? e : launch_combine(a, D, s);
 }
 
 template <int D, bool FP8>
@@ -524,23 +528,25 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attention(void (*kernel)(const AttnArgs), const AttnArgs& a, int threads, int smem, int D,
-                             cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.ctas);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess || a.ctas < 2) return e;
-  cfg.gridDim = dim3((unsigned)(a.ctas - 1));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 0;
+void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int threads, int smem,
+                      cudaStream_t s) {
+  *cfg = {};
+  cfg->gridDim = dim3((unsigned)ctas);
+  cfg->blockDim = dim3((unsigned)threads);
+  cfg->dynamicSmemBytes = (size_t)smem;
+  cfg->stream = s;
+  *attr = {};
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
+  if (a.ctas < 2) return cudaSuccess;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  attention_config(&cfg, &attr, a.ctas - 1, kThreads, 0, s);
   if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
   if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a);
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256>, a);
@@ -594,7 +600,12 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.lse = lse;
   a.piece_o = static_cast<float*>(workspace);
   a.piece_ml = reinterpret_cast<float2*>(a.piece_o + (size_t)kMaxPieceRows * D);
-  const cudaError_t e = launch_attention_mma(a, D, cache->dtype == LOWBIT_CACHE_E4M3, static_cast<cudaStream_t>(stream));
+  const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Rows that share a request's keys, on average: the host knows the totals only.
+  const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
+  const cudaError_t e = rows > 32 && attention_tc_fits(a, D, fp8) ? launch_attention_tc(a, D, rows > 128, s)
+                                                                 : launch_attention_mma(a, D, fp8, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 

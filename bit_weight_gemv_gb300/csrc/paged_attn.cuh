@@ -14,7 +14,7 @@ constexpr int kMaxDevices = 64;
 // Query rows of all pieces together: every CTA may leave two (the item it starts inside of and
 // the one it ends inside of).  The workspace holds D + 2 floats for each; a kernel's grid is
 // limited so that 2 * CTAs * rows stays within it.
-constexpr int kMaxPieceRows = 2 * 152 * 128;
+constexpr int kMaxPieceRows = 2 * 152 * 256;
 
 struct AttnArgs {
   PagedArgs p;
@@ -193,8 +193,14 @@ __device__ __forceinline__ void store_piece(const AttnArgs& a, long long slot, i
   if (c == 0) a.piece_ml[slot * R + row] = make_float2(m, l);
 }
 
-// Launches `kernel` over a.ctas resident CTAs and the combine step behind it.
-cudaError_t launch_attention(void (*kernel)(const AttnArgs), const AttnArgs& a, int threads, int smem, int D,
-                             cudaStream_t s);
+// Launch configuration of an attention kernel of `ctas` resident CTAs, and the combine step behind it.
+void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int threads, int smem,
+                      cudaStream_t s);
+cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s);
+
+// The tensor-core kernel (paged_attn_tc.cu): whether it can take the call, and its launch with 256
+// (`pair`) or 128 query rows per item.
+bool attention_tc_fits(const AttnArgs& a, int D, bool fp8);
+cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool pair, cudaStream_t s);
 
 }  // namespace lowbit

@@ -1,0 +1,615 @@
+// Attention over a paged cache on the fifth-generation tensor cores, for many query rows per
+// key/value head (prompt chunks, verify blocks of grouped heads).  Same mathematics and schedule
+// as attn_mma_kernel (see paged_attn.cu and paged.cuh).
+//
+// One CTA per SM, two "slots" of 128 query rows that keep the tensor pipe busy in turn:
+//   warps 0-3, 4-7 -- softmax of slot 0 and 1, one thread per row: read the row's 128 scores from
+//       tensor memory, fold them into (m, l) and write the weights back as bf16 over the scores,
+//       where they are the A operand of the product with V;
+//   warp 8 -- copies: K and V tiles of 128 keys by TMA, one box per page and 64-element half;
+//   (warps 10 and 11 only fill their warpgroup, whose registers go to the softmax);
+//   warp 9 -- issues the MMAs: S = Q K^T (both in shared memory) and O += P V (P in tensor memory,
+//       V as it lies in the cache, keys along the reduction).
+// PAIR: the slots hold different rows and share every tile (256 rows per item).  Otherwise both
+// slots hold the same 128 rows and take alternate tiles; their (m, l, O) are joined at the end.
+// O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
+// since the value the weights refer to, so most tiles never touch it (weights up to 2^8 round to
+// bf16 with the same relative error, and sums are fp32).
+#include "common.cuh"
+#include "paged.cuh"
+#include "paged_attn.cuh"
+#include "ptx.cuh"
+
+namespace lowbit {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTcThreads = 384;
+constexpr int kTcBN = 128;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr float kGrow = 8.0f;
+
+template <int D>
+struct Tc {
+  static constexpr int kTile = 128 * D * 2;   // 128 rows of Q, K or V
+  static constexpr int kHalves = D / 64;      // 64-element (128-byte) halves of a row
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+  static constexpr uint32_t kS = 0, kO = 256;  // tensor memory columns: S (and P) of slot s at 128 s,
+};                                             // O at 256 + D s
+
+struct TcShared {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t joined, left;  // both slots' statistics are written; both slots have read both O
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 4-D tiled tensor copy (TMA) global -> shared.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// D[tmem] (+)= A[smem] x B[smem]^T, issued by one thread.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Matrix descriptor of an operand whose reduction runs over rows of 128 bytes (64 elements of the
+// other dimension, 128-byte swizzle): 8-row groups 1024 bytes apart, the next 64 elements
+// `half_bytes` on.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t half_bytes) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(half_bytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two fp32 operations at once, each rounded as the single one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// A wait that remembers failure: once one has given up, the role leaves its loops.
+#define WAIT_OR(bar, parity, what)                 \
+  if (!mbar_wait(smem_addr(&(bar)), (parity))) {   \
+    record_error(p.err, LOWBIT_ERR_TIMEOUT);       \
+    what;                                          \
+  }
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kTcThreads, 1)
+attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap) {
+  using C = Tc<D>;
+  constexpr int S = C::kStages;
+  constexpr int kRows = PAIR ? 256 : 128;
+  extern __shared__ uint8_t raw[];
+  __shared__ Plan plan;
+  __shared__ TcShared sh;
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, ring = base + 2 * C::kTile;
+  // the second Q tile's place holds the two slots' statistics when they share the first
+  float2* const ml = reinterpret_cast<float2*>(raw + (base - smem_addr(raw)) + C::kTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedArgs& p = a.p;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&sh.kv_full[i]), 1), mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.q_full[i]), PAIR ? 128 : 256);
+      mbar_init(smem_addr(&sh.s_full[i]), 1);
+      mbar_init(smem_addr(&sh.p_full[i]), 128);
+      mbar_init(smem_addr(&sh.o_full[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.joined), 256);
+    mbar_init(smem_addr(&sh.left), 256);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  make_plan<kTcThreads>(a, plan, blockIdx.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int G = a.shape.G;
+
+  if (plan.begin < plan.end) {
+    Walk it = walk_start(a, plan);
+    int left = (int)(plan.end - plan.begin);
+
+    // Registers: 384 threads launch with 168 each (64,512); 256 softmax threads take 208 and the
+    // other 128 keep 80 (63,488).
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------------ copies
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int filled = 0;  // loads issued, up to S
+      const int box = min(p.page_mask + 1, kTcBN), boxes = kTcBN / box;  // keys per box
+      auto load = [&](const CUtensorMap* map, int kt) {
+        WAIT_OR(sh.kv_empty[stage], phase ^ 1, { ok = false; return; });
+        const int key0 = it.span.lo / kTcBN * kTcBN + kt * kTcBN + lane * box;
+        const bool mine = lane < boxes && key0 < it.span.hi && key0 + box > it.span.lo;
+        int page = 0;
+        if (mine) {
+          page = __ldg(p.table + (long long)it.b * p.table_stride + (key0 >> p.page_shift));
+          // a page outside the cache is outside the tensor map: the copy fills zeros
+          if (page < 0 || page >= p.pages) record_error(p.err, LOWBIT_ERR_INVALID_ARG), page = -1;
+        }
+        const int n = __popc(__ballot_sync(~0u, mine));
+        const uint32_t bar = smem_addr(&sh.kv_full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * 128 * C::kHalves));
+        __syncwarp();
+        if (mine)
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_4d(ring + stage * C::kTile + h * (kTcBN * 128) + lane * box * 128, map, 64 * h,
+                        key0 & p.page_mask, it.h, page, bar);
+        if (++stage == S) stage = 0, phase ^= 1;
+        if (filled < S) ++filled;
+      };
+      for (;;) {
+        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        load(&kmap, kt0);
+        if (!PAIR && ok && n > 1) load(&kmap, kt0 + 1);
+        for (int j = 0; j < n && ok; ++j) {
+          load(&vmap, kt0 + j);
+          const int next = j + (PAIR ? 1 : 2);
+          if (next < n && ok) load(&kmap, kt0 + next);
+        }
+        left -= n;
+        if (!ok || left <= 0 || !walk_next(a, it)) break;
+      }
+      // Leave only when no copy is in flight and every release has arrived.
+      for (int i = 0; i < filled; ++i) {
+        if (--stage < 0) stage = S - 1, phase ^= 1;
+        mbar_wait(smem_addr(&sh.kv_full[stage]), phase);
+        if (ok) mbar_wait(smem_addr(&sh.kv_empty[stage]), phase);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ MMA issue
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      constexpr uint32_t kIdQK = umma_idesc_bf16(128, 128);
+      constexpr uint32_t kIdPV = umma_idesc_bf16(128, D) | (1u << 16);  // B with rows along the reduction
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      auto qk = [&](int slot, int st) {
+        if (lane == 0) {
+          const uint32_t qa = q_at + (PAIR ? slot * C::kTile : 0), kb = ring + st * C::kTile;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
+            umma_ss(tmem + C::kS + 128 * slot, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), kIdQK, k > 0);
+          }
+          umma_commit(smem_addr(&sh.s_full[slot]));
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int slot, int st, bool add) {
+        if (lane == 0) {
+          const uint32_t vb = ring + st * C::kTile;
+#pragma unroll
+          for (int k = 0; k < kTcBN / 16; ++k)
+            umma_ts(tmem + C::kO + D * slot, tmem + C::kS + 128 * slot + 8 * k,
+                    smem_desc_mn(vb + k * 2048, kTcBN * 128), kIdPV, add || k > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t& bar) {
+        if (lane == 0) umma_commit(smem_addr(&bar));
+        __syncwarp();
+      };
+      auto advance = [&]() {
+        const int st = stage;
+        if (++stage == S) stage = 0, phase ^= 1;
+        return st;
+      };
+      bool ok = true;
+      for (;;) {
+        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        const int key_first = it.span.lo / kTcBN * kTcBN + kt0 * kTcBN;
+        const int slots = PAIR && it.q.n * G - it.qt * kRows <= 128 ? 1 : 2;
+        // Waits for the next K tile; returns its stage.
+        auto next_tile = [&]() {
+          WAIT_OR(sh.kv_full[stage], phase, ok = false);
+          return advance();
+        };
+        // The V tile of keys key0..: rows outside the span (unwritten slots, stale buffers) become
+        // zeros, since 0 * NaN would reach the sums.
+        auto next_v = [&](int key0) {
+          WAIT_OR(sh.kv_full[stage], phase, ok = false);
+          if (ok && (key0 < it.span.lo || key0 + kTcBN > it.span.hi)) {
+            const uint32_t vb = ring + stage * C::kTile;
+            for (int i = lane; i < kTcBN * C::kHalves * 8; i += 32) {
+              const int row = (i >> 3) & (kTcBN - 1), key = key0 + row;
+              if (key < it.span.lo || key >= it.span.hi)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + i * 16), "r"(0) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          return advance();
+        };
+        for (int s = 0; s < (PAIR ? slots : 1) && ok; ++s) {
+          WAIT_OR(sh.q_full[s], q_phase[s], ok = false);
+          q_phase[s] ^= 1;
+        }
+        tc_fence_after();
+        if (!ok) break;
+        if (PAIR) {
+          int st = next_tile();
+          if (!ok) break;
+          for (int s = 0; s < slots; ++s) qk(s, st);
+          commit(sh.kv_empty[st]);
+          for (int j = 0; j < n && ok; ++j) {
+            const int sv = next_v(key_first + j * kTcBN);
+            int sk = 0;
+            for (int s = 0; s < slots && ok; ++s) {
+              WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
+              p_phase[s] ^= 1;
+              tc_fence_after();
+              pv(s, sv, j > 0);
+              if (s == slots - 1) commit(sh.kv_empty[sv]);
+              if (j + 1 == n) {
+                commit(sh.o_full[s]);
+              } else {
+                if (s == 0) sk = next_tile();
+                if (!ok) break;
+                qk(s, sk);
+                if (s == slots - 1) commit(sh.kv_empty[sk]);
+              }
+            }
+          }
+        } else {
+          for (int s = 0; s < min(n, 2) && ok; ++s) {
+            const int st = next_tile();
+            if (!ok) break;
+            qk(s, st);
+            commit(sh.kv_empty[st]);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const int s = j & 1;
+            const int sv = next_v(key_first + j * kTcBN);
+            if (!ok) break;
+            WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
+            p_phase[s] ^= 1;
+            tc_fence_after();
+            pv(s, sv, j > 1);
+            commit(sh.kv_empty[sv]);
+            if (j + 2 < n) {
+              const int st = next_tile();
+              if (!ok) break;
+              qk(s, st);
+              commit(sh.kv_empty[st]);
+            } else {
+              commit(sh.o_full[s]);
+            }
+          }
+          if (ok && n == 1) commit(sh.o_full[1]);
+        }
+        if (!ok) break;
+        left -= n;
+        if (left <= 0 || !walk_next(a, it)) break;
+      }
+      if (!ok) {  // nothing of this CTA may still be in flight when it leaves
+        commit(sh.s_full[0]);
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000LL) {}
+      }
+    } else if (warp > kMmaWarp) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    } else {
+      // ------------------------------------------------------------------ softmax
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      const int slot = warp >> 2, row = (warp & 3) * 32 + lane, t128 = tid & 127;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_at = tmem + C::kS + 128 * slot + lanes;
+      const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // of the scale, given to q
+      // a scale of zero keeps masked scores at -inf
+      const float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+      uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
+      bool first = true, ok = true;
+      for (;;) {
+        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        const int rows = it.q.n * G, r0 = it.qt * kRows;
+        const int r_tile = r0 + (PAIR ? slot * 128 : 0);
+        const bool active = r_tile < rows;
+        const int key_first = it.span.lo / kTcBN * kTcBN + kt0 * kTcBN;
+
+        // Q rows into shared memory (swizzled as TMA would leave them)
+        if (active) {
+          constexpr int kChunks = D / 8;
+          const uint32_t dst = q_at + (PAIR ? slot * C::kTile : 0);
+          for (int i = PAIR ? t128 : tid; i < 128 * kChunks; i += PAIR ? 128 : 256) {
+            const int rr = i / kChunks, c = i % kChunks, r = r_tile + rr;
+            if (r >= rows) break;
+            const int tok = r / G;
+            uint4 v = *reinterpret_cast<const uint4*>(a.q + (long long)(it.q.row0 + tok) * a.q_stride +
+                                                      (long long)(it.h * G + r - tok * G) * D + c * 8);
+            v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             dst + (c / 8) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(smem_addr(&sh.q_full[PAIR ? slot : 0]));
+        }
+
+        // the keys this row sees
+        const int r = r_tile + row, tok = r / G;
+        const bool in = r < rows;
+        const int pos = it.q.kv - it.q.n + tok;
+        const int jhi = in ? (a.shape.causal ? min(it.q.kv, pos + 1) : it.q.kv) : 0;
+        const int jlo = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
+        const bool work = __any_sync(~0u, in);  // a warp without rows only keeps the pace
+
+        float m = -INFINITY, l = 0.0f;  // m: what the weights so far refer to
+        int steps = 0;
+        if (active && ok) {
+          for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2, ++steps) {
+            WAIT_OR(sh.s_full[slot], s_phase, { ok = false; break; });
+            s_phase ^= 1;
+            tc_fence_after();
+            if (work) {
+              float s[128];
+              const int key0 = key_first + j * kTcBN;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
+              tmem_ld_wait();
+              if (__any_sync(~0u, in && (key0 < jlo || key0 + kTcBN > jhi))) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                  if (key0 + i < jlo || key0 + i >= jhi) s[i] = -INFINITY;
+              }
+              float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+              for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], i + 4 + e < 128 ? fmaxf(s[i + e], s[i + 4 + e]) : s[i + e]);
+              }
+              const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * coef;
+              const bool grow = top > m + kGrow;  // from -inf: any finite maximum
+              if (__any_sync(~0u, grow)) {
+                const float f = grow ? exp2_approx(m - top) : 1.0f;
+                if (grow) m = top;
+                l *= f;
+                // the product before this one is complete: its tensor work came before these scores'
+                if (steps > 0) {
+                  const uint32_t o_at = tmem + C::kO + D * slot + lanes;
+#pragma unroll
+                  for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(o_at + c, o);
+                  }
+                }
+              }
+              const float ref = m == -INFINITY ? 0.0f : -m;
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float2 x = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), make_float2(coef, coef),
+                                  make_float2(ref, ref));
+                  x.x = exp2_approx(x.x);
+                  x.y = exp2_approx(x.y);
+                  sum[i & 1] = add2(sum[i & 1], x);
+                  w[i] = pack_bf16x2(x.x, x.y);
+                }
+                tmem_st16(s_at + 16 * c, w);
+              }
+              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+              tmem_st_wait();
+            }
+            tc_fence_before();
+            mbar_arrive(smem_addr(&sh.p_full[slot]));
+          }
+        }
+
+        // ---- the item's rows leave
+        const bool whole = kt0 == 0 && n == it.tiles;
+        const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * kRows + (PAIR ? slot * 128 : 0) + row;
+        if (PAIR) {
+          if (active && ok) {
+            WAIT_OR(sh.o_full[slot], o_phase, ok = false);
+            o_phase ^= 1;
+          }
+        } else if (ok) {
+          ml[128 * slot + row] = make_float2(m, l);
+          mbar_arrive(smem_addr(&sh.joined));
+          WAIT_OR(sh.joined, j_phase, ok = false);
+          if (ok) WAIT_OR(sh.o_full[0], o_phase, ok = false);
+          if (ok) WAIT_OR(sh.o_full[1], o_phase, ok = false);
+          o_phase ^= 1;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (active && work) {
+          // PAIR: this slot's row.  Else both slots' parts of the row; each slot stores half of it.
+          float f0 = 1.0f, f1 = 0.0f;
+          if (!PAIR) {
+            const float2 x = ml[row], y = ml[128 + row];
+            m = fmaxf(x.x, y.x);
+            f0 = m == -INFINITY ? 0.0f : exp2_approx(x.x - m);
+            f1 = m == -INFINITY ? 0.0f : exp2_approx(y.x - m);
+            l = f0 * x.y + f1 * y.y;
+          }
+          const bool two = !PAIR && n > 1;
+          const float inv = whole ? (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) : 1.0f;
+          const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
+          constexpr int kCols = PAIR ? D : D / 2;
+          const int c0 = PAIR ? 0 : slot * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t x[16], y[16];
+            tmem_ld16(tmem + C::kO + (PAIR ? D * slot : 0) + lanes + c0 + c, x);
+            if (two) tmem_ld16(tmem + C::kO + D + lanes + c0 + c, y);
+            tmem_ld_wait();
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] = __uint_as_float(x[i]);
+              if (!PAIR) v[i] = two ? f0 * v[i] + f1 * __uint_as_float(y[i]) : f0 * v[i];
+              v[i] *= inv;
+            }
+            if (in && whole) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0 + c);
+              dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+              dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
+            } else if (in) {
+              float4* dst = reinterpret_cast<float4*>(a.piece_o + piece * D + c0 + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          }
+          if (in && (PAIR || slot == 0)) {
+            if (!whole) a.piece_ml[piece] = make_float2(m, l);
+            else if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+          }
+        }
+        tc_fence_before();
+        if (!PAIR) {  // the next item's products overwrite what both slots read here
+          mbar_arrive(smem_addr(&sh.left));
+          WAIT_OR(sh.left, j_phase, { ok = false; break; });
+          j_phase ^= 1;
+        }
+        first = false;
+        left -= n;
+        if (left <= 0 || !walk_next(a, it)) break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// The cache as [page][head][slot][D], boxes of 64 elements by one page's slots (at most 128).
+bool encode_cache(CUtensorMap* map, const PagedArgs& p, void* at, int D) {
+  const auto encode = map_encoder();
+  if (!encode) return false;
+  const int ps = p.page_mask + 1;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)ps, (cuuint64_t)p.Hk, (cuuint64_t)p.pages};
+  cuuint64_t strides[3] = {(cuuint64_t)p.token_stride, (cuuint64_t)p.head_stride, (cuuint64_t)p.page_stride};
+  cuuint32_t box[4] = {64, (cuuint32_t)(ps < kTcBN ? ps : kTcBN), 1, 1};
+  cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool PAIR>
+cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
+  using C = Tc<D>;
+  static std::atomic<int> ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int ctas = ready[dev].load(std::memory_order_relaxed);
+  if (!ctas) {
+    e = cudaFuncSetAttribute(attn_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    int sms = 0;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    ctas = std::max(1, std::min(sms, kMaxPieceRows / 2 / (PAIR ? 256 : 128)));
+    ready[dev].store(ctas, std::memory_order_relaxed);
+  }
+  CUtensorMap kmap, vmap;
+  if (!encode_cache(&kmap, a.p, a.p.k, D) || !encode_cache(&vmap, a.p, a.p.v, D)) return cudaErrorNotSupported;
+  a.ctas = ctas;
+  a.shape.R = PAIR ? 256 : 128;
+  a.shape.BN = kTcBN;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  attention_config(&cfg, &attr, ctas, kTcThreads, C::kSmem, s);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, PAIR>, a, kmap, vmap);
+  return e != cudaSuccess ? e : launch_combine(a, D, s);
+}
+
+}  // namespace
+
+// True where the kernel can run: bf16, heads of 64 or 128, pages that TMA can box, strides and
+// addresses within its limits.
+bool attention_tc_fits(const AttnArgs& a, int D, bool fp8) {
+  return !fp8 && D <= 128 && a.p.page_mask + 1 >= 16 && a.p.page_stride < (1LL << 40) &&
+         a.p.token_stride < (1LL << 40) && a.p.head_stride < (1LL << 40);
+}
+
+cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool pair, cudaStream_t s) {
+  if (D == 64) return pair ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
+  return pair ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
+}
+
+}  // namespace lowbit
