@@ -22,6 +22,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 128;
+constexpr int kJoinThreads = 512;
 constexpr int kBN = 64;  // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -133,7 +134,8 @@ attn_mma_kernel(const AttnArgs a) {
   for (;;) {
     const Request q = it.q;
     const int b = it.b;
-    const int kt0 = it.tile, kt1 = min(it.tiles, it.tile + left);
+    const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
+    if (kt1 == kt0) return;
     const Span span = it.span;
     const int base_key = span.lo / kBN * kBN;
     const int r0 = it.qt * C::kRows;
@@ -440,52 +442,82 @@ attn_mma_kernel(const AttnArgs a) {
     }
     __syncthreads();  // the ring and s_ml are free again
     first = false;
-    left -= kt1 - kt0;
     if (left <= 0 || !walk_next(a, it)) return;
   }
 }
 
-// Items that the cuts went through: block j looks at cut j.  The blocks of one item's cuts share
-// its rows, so the work of joining spreads over as many blocks as there are pieces.
+// Items that the cuts went through: blocks (j, *) look at cut j.  The blocks of one item's cuts
+// share its rows, so the work of joining spreads over as many blocks as there are pieces, times
+// gridDim.y.  A warp takes
+// a row: its lanes hold the pieces' (maximum, sum) 32 at a time, so the weights cost one round
+// trip, and then one part of the row each, whose loads do not wait for one another.
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_combine_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const AttnArgs a) {
   __shared__ Plan plan;
   // the schedule reads the batch alone, which no kernel since the attention's start has written
-  make_plan<kThreads>(a, plan, blockIdx.x + 1);
+  make_plan<kJoinThreads>(a, plan, blockIdx.x + 1);
   __syncthreads();
+  Walk it;
+  bool cut = plan.begin < plan.end;
+  if (cut) {
+    it = walk_start(a, plan);
+    cut = it.tile > 0;  // else the cut fell between two items, or inside a lead
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (plan.begin >= plan.end) return;
-  const Walk it = walk_start(a, plan);
-  if (it.tile == 0) return;  // the cut fell between two items
-  const long long from = plan.begin - it.tile;
-  const long long c0 = from / plan.chunk, c1 = (from + it.tiles - 1) / plan.chunk;  // CTAs with a piece
-  const int n = (int)(c1 - c0), mine = (int)(blockIdx.x + 1 - (c0 + 1));
+  if (!cut) return;
+  const long long tiles_at = plan.begin - it.tile;           // where the item's tiles begin
+  const long long from = tiles_at - a.shape.lead;            // and its lead
+  const long long c0 = quotient(tiles_at, plan.chunk);       // CTAs with a piece: c0..c0 + n
+  const int n = (int)(quotient(tiles_at + it.tiles - 1, plan.chunk) - c0);
+  const int shares = n * gridDim.y, mine = (int)(blockIdx.x + 1 - (c0 + 1)) * gridDim.y + blockIdx.y;
   const long long slot0 = 2 * c0 + (from > c0 * plan.chunk ? 1 : 0);
-  const int G = a.shape.G, R = a.shape.R, r0 = it.qt * R;
+  const int G = a.shape.G, R = 1 << a.shape.r_shift, r0 = it.qt << a.shape.r_shift;
   const int rows = min(R, it.q.n * G - r0);
-  const int ra = (int)((long long)rows * mine / n), rb = (int)((long long)rows * (mine + 1) / n);
+  const int ra = (int)((long long)rows * mine / shares), rb = (int)((long long)rows * (mine + 1) / shares);
   const float vscale = a.p.v_scale ? __ldg(a.p.v_scale + it.h) : 1.0f;
-  constexpr int kQuads = D / 4;
-  for (int idx = ra * kQuads + threadIdx.x; idx < rb * kQuads; idx += kThreads) {
-    const int row = idx / kQuads, c = (idx % kQuads) * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart);
+  for (int row = ra + warp; row < rb; row += kJoinThreads / 32) {
     float m = -INFINITY;
-    for (int i = 0; i <= n; ++i) {
-      const long long slot = i ? 2 * (c0 + i) : slot0;
-      m = fmaxf(m, a.piece_ml[slot * R + row].x);
+    for (int i = lane; i <= n; i += 32) m = fmaxf(m, a.piece_ml[(i ? 2 * (c0 + i) : slot0) * R + row].x);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    float l = 0.0f, acc[kParts][kPart] = {};
+    for (int i0 = 0; i0 <= n; i0 += 32) {
+      float f = 0.0f;
+      if (i0 + lane <= n) {
+        const int i = i0 + lane;
+        const float2 ml = a.piece_ml[(i ? 2 * (c0 + i) : slot0) * R + row];
+        f = m == -INFINITY ? 0.0f : ex2(ml.x - m);
+        l += f * ml.y;
+      }
+      const int k1 = min(32, n + 1 - i0);
+#pragma unroll 8
+      for (int k = 0; k < k1; ++k) {
+        const float fk = __shfl_sync(~0u, f, k);
+        const long long slot = i0 + k ? 2 * (c0 + i0 + k) : slot0;
+        const float* src = a.piece_o + (slot * R + row) * D + lane * kPart;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          float v[kPart];
+          if (kPart == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + q * 128);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+          for (int e = 0; e < kPart; ++e) acc[q][e] += fk * v[e];
+        }
+      }
     }
-    float l = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i <= n; ++i) {
-      const long long slot = i ? 2 * (c0 + i) : slot0;
-      const float2 ml = a.piece_ml[slot * R + row];
-      const float f = m == -INFINITY ? 0.0f : ex2(ml.x - m);
-      const float4 v = *reinterpret_cast<const float4*>(a.piece_o + (slot * R + row) * D + c);
-      l += f * ml.y;
-      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-    }
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
     const int r = r0 + row, tok = r / G;
-    store_row(a, (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G), D, c, acc, m, l, vscale);
+    const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
+    const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      uint16_t* dst = a.out + orow * D + q * 128 + lane * kPart;
+      const uint32_t lo = pack2<false>(acc[q][0] * s, acc[q][1] * s);
+      if (kPart == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2<false>(acc[q][kPart - 2] * s, acc[q][kPart - 1] * s));
+      else *reinterpret_cast<uint32_t*>(dst) = lo;
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
   }
 }
 
@@ -508,8 +540,10 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t s) {
     ready[dev].store(ctas, std::memory_order_relaxed);
   }
   a.ctas = ctas;
-  a.shape.R = C::kRows;
-  a.shape.BN = kBN;
+  a.shape.r_shift = MT == 1 ? 4 : (MT == 2 ? 5 : 6);
+  a.shape.bn_shift = 6;
+  a.shape.lead = tune("LEAD", 4);
+  a.min_chunk = tune("MINC", 1);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
@@ -546,7 +580,8 @@ cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
   if (a.ctas < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
-  attention_config(&cfg, &attr, a.ctas - 1, kThreads, 0, s);
+  attention_config(&cfg, &attr, a.ctas - 1, kJoinThreads, 0, s);
+  cfg.gridDim.y = a.shape.r_shift > 6 ? 1u << (a.shape.r_shift - 6) : 1;  // 64 rows of an item each
   if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
   if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a);
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256>, a);
@@ -591,7 +626,7 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
     return LOWBIT_ERR_ALIGN;
   a.p.err = device_error_word();
   if (!a.p.err) return LOWBIT_ERR_CUDA;
-  a.shape = ItemShape{Hq / cache->heads, 0, 0, causal != 0, window};
+  a.shape = ItemShape{Hq / cache->heads, 0, 0, 0, causal != 0, window};
   a.q = q;
   a.q_stride = q_stride;
   a.Hq = Hq;

@@ -200,7 +200,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         if (filled < S) ++filled;
       };
       for (;;) {
-        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        const int kt0 = it.tile, n = walk_take(it, left);
+        if (n == 0) break;
         load(&kmap, kt0);
         if (!PAIR && ok && n > 1) load(&kmap, kt0 + 1);
         for (int j = 0; j < n && ok; ++j) {
@@ -208,7 +209,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           const int next = j + (PAIR ? 1 : 2);
           if (next < n && ok) load(&kmap, kt0 + next);
         }
-        left -= n;
         if (!ok || left <= 0 || !walk_next(a, it)) break;
       }
       // Leave only when no copy is in flight and every release has arrived.
@@ -258,7 +258,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       };
       bool ok = true;
       for (;;) {
-        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        const int kt0 = it.tile, n = walk_take(it, left);
+        if (n == 0) break;
         const int key_first = it.span.lo / kTcBN * kTcBN + kt0 * kTcBN;
         const int slots = PAIR && it.q.n * G - it.qt * kRows <= 128 ? 1 : 2;
         // Waits for the next K tile; returns its stage.
@@ -340,7 +341,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           if (ok && n == 1) commit(sh.o_full[1]);
         }
         if (!ok) break;
-        left -= n;
         if (left <= 0 || !walk_next(a, it)) break;
       }
       if (!ok) {  // nothing of this CTA may still be in flight when it leaves
@@ -362,7 +362,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
       bool first = true, ok = true;
       for (;;) {
-        const int kt0 = it.tile, n = min(it.tiles - kt0, left);
+        const int kt0 = it.tile, n = walk_take(it, left);
+        if (n == 0) break;
         const int rows = it.q.n * G, r0 = it.qt * kRows;
         const int r_tile = r0 + (PAIR ? slot * 128 : 0);
         const bool active = r_tile < rows;
@@ -532,7 +533,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           j_phase ^= 1;
         }
         first = false;
-        left -= n;
         if (left <= 0 || !walk_next(a, it)) break;
       }
     }
@@ -589,8 +589,10 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   if (!encode_cache(&kmap, a.p, a.p.k, D) || !encode_cache(&vmap, a.p, a.p.v, D)) return cudaErrorNotSupported;
   a.ctas = ctas;
-  a.shape.R = PAIR ? 256 : 128;
-  a.shape.BN = kTcBN;
+  a.shape.r_shift = PAIR ? 8 : 7;
+  a.shape.bn_shift = 7;
+  a.shape.lead = tune("LEADTC", PAIR ? 2 : 4);
+  a.min_chunk = tune("MINCTC", 1);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   attention_config(&cfg, &attr, ctas, kTcThreads, C::kSmem, s);
