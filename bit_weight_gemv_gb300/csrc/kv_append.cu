@@ -177,9 +177,10 @@ lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_page
       ps > kMaxPageSize || (ps & (ps - 1)) || cache->heads < 1 || cache->heads > 4096 ||
       (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256))
     return LOWBIT_ERR_SHAPE;
+  if ((int64_t)ps * cache->head_dim * size < 128) return LOWBIT_ERR_SHAPE;  // a tensor copy's alignment
   const int64_t strides[3] = {cache->page_stride, cache->token_stride, cache->head_stride};
   for (const int64_t s : strides)
-    if (s <= 0 || s * size % 16) return LOWBIT_ERR_ALIGN;
+    if (s <= 0 || s >= (int64_t)1 << 39 || s * size % 16) return LOWBIT_ERR_ALIGN;
   if (!aligned16(cache->k) || !aligned16(cache->v) || ((uintptr_t)batch->cu_q & 3) ||
       ((uintptr_t)batch->kv_lens & 3) || ((uintptr_t)batch->block_table & 3) ||
       ((uintptr_t)cache->k_scale & 3) || ((uintptr_t)cache->v_scale & 3))

@@ -4,11 +4,13 @@
 // with (m, l, o) of any two sets of keys joined by m = max(m1, m2), l = l1 e^(m1-m) + l2 e^(m2-m)
 // and o likewise -- so a tile of keys is folded in at a time, and a long axis is split freely.
 //
-// attn_mma_kernel works on the warp-level MMA (m16n8k16, fp32 accumulation).  A CTA of four
-// warps holds 16 * MT query rows (the rows of one key/value head that share its keys) and takes
-// key tiles of 64 through a ring of cp.async stages; with MT < 4 row groups the other warps
-// take different keys of the tile and the CTA joins them at the end.  The grid is resident and
-// the work is cut evenly over it (see paged.cuh); attn_combine_kernel joins items that were cut.
+// attn_mma_kernel works on the warp-level MMA (m16n8k16, fp32 accumulation).  A CTA holds 16 * MT
+// query rows (the rows of one key/value head that share its keys) and takes key tiles of 64 from a
+// ring that a fifth warp fills by TMA, one box per page and 128-byte part of a row; with MT < 4 row
+// groups the four compute warps take different keys of the tile and join at the item's end.  The
+// copying warp walks the items on its own, so the next item's tiles arrive while one is finished.
+// The grid is resident and the work is cut evenly over it (see paged.cuh); attn_combine_kernel
+// joins items that were cut.
 #include "common.cuh"
 #include "paged.cuh"
 #include "paged_attn.cuh"
@@ -21,20 +23,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 160;
+constexpr int kComputeThreads = 128;
 constexpr int kJoinThreads = 512;
 constexpr int kBN = 64;  // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const int n = real ? 16 : 0;  // the rest of the 16 bytes is written as zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -86,58 +80,140 @@ struct Cfg {
   static constexpr int kWarpsK = 4 / MT;               // warps that split a tile's keys
   static constexpr int kRows = 16 * MT;
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);  // one key's or value's row
+  static constexpr int kPart = kRowBytes < 128 ? kRowBytes : 128;  // of it, what one box holds
+  static constexpr int kParts = kRowBytes / kPart;
   static constexpr int kHalf = kBN * kRowBytes;        // one tile's keys (or values)
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = kStage >= 65536 ? 3 : (kStage >= 32768 ? 3 : 4);
   static constexpr int kSteps = D / 16;
   static constexpr bool kQShared = D > 128;            // query fragments in shared memory
   static constexpr int kQBytes = kQShared ? MT * kSteps * 512 : 0;
-  static constexpr int kSmem = kStages * kStage + kQBytes;
-  static constexpr int kOut = kWarpsK * 16 * MT * (D + 4) * 4;  // joining buffer (reuses the ring)
-  static_assert(kOut <= kStages * kStage, "joining buffer");
+  // Two CTAs per SM where three stages of a CTA fit half of its shared memory (all but heads of 256
+  // in bf16), and as many stages as then fit, up to six.
+  static constexpr int kCtas = 3 * kStage + kQBytes + 2048 <= 113 * 1024 ? 2 : 1;
+  static constexpr int kFit = ((kCtas == 2 ? 113 : 226) * 1024 - 2048 - kQBytes) / kStage;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kSmem = 1024 + kStages * kStage + kQBytes;
+  static_assert(2 * 64 * D <= kStage, "two warps' outputs pass through one stage");
 };
 
-// Byte offset of 16-byte chunk c of row r of a tile: the chunk index is XORed with a function of
-// the row that takes 8 different values over 8 rows (128-byte rows and longer), so ldmatrix's
-// 8 rows and the 16-byte loads of two rows' halves both meet every bank once.
+// Byte offset of 16-byte chunk c of row r of a tile, as the tensor copy swizzles it: parts of 128
+// bytes (chunk index XOR row mod 8) one after another, or rows of 64 bytes (XOR row / 2 mod 4).
 template <int RB>
 __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
-  const int x = RB >= 128 ? (((r & 1) << 2) | ((r >> 1) & 3)) : ((r >> 1) & 3);
-  return (uint32_t)(r * RB + ((c ^ x) << 4));
+  if (RB == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)((c >> 3) * (kBN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// Key (inside a group of eight) that the score matrix's column i stands for.  Over an e4m3 cache a
+// lane reads 16 bytes of a key's row; taking rows 0, 4, 1, 5, ... puts the two rows that eight
+// lanes read at once into different halves of the banks.  Values use the same order.
+template <int RB, bool FP8>
+__device__ __forceinline__ int key_of(int i) {
+  return FP8 && RB >= 128 ? ((i >> 1) | ((i & 1) << 2)) : i;
 }
 
+struct RingBars {
+  uint64_t full[8], empty[8];
+};
+
 template <int D, int MT, bool FP8>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, MT, FP8>::kSmem <= 110 * 1024 ? 2 : 1))
-attn_mma_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
+attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, MT, FP8>;
   constexpr int RB = C::kRowBytes, S = C::kStages;
   constexpr int kNT = 2 * MT;       // 8-key tiles per warp
   constexpr int kDT = D / 8;        // 8-dim tiles
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t raw[];
   __shared__ Plan plan;
-  __shared__ float s_ml[4][16][2];
+  __shared__ RingBars bars;
+  __shared__ float2 s_ml[4][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int wr = warp / C::kWarpsK, wk = warp % C::kWarpsK;  // row group, key group
-  const uint32_t ring = smem_addr(smem);
+  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+  uint8_t* const smem = raw + (ring - smem_addr(raw));
   const PagedArgs& p = a.p;
 
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 4);
+    fence_mbar_init();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   make_plan<kThreads>(a, plan, blockIdx.x);
   __syncthreads();
-
   if (plan.begin >= plan.end) return;
   Walk it = walk_start(a, plan);
   int left = (int)(plan.end - plan.begin);
-  bool first = true;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == 4) {
+    // -------------------------------------------------------------------- copies
+    const int box = min(p.page_mask + 1, kBN), boxes = kBN / box;  // keys per box
+    int filled = 0;
+    bool ok = true;
+    for (;;) {
+      const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
+      if (kt1 == kt0) break;
+      const int first = (it.span.lo & ~(kBN - 1)) + lane * box;
+      const int32_t* row = p.table + (long long)it.b * p.table_stride;
+      // Page of this lane's box of tile kt (-2: no key of it is seen), looked up one tile ahead.
+      auto page_of = [&](int kt, int extra) {
+        const int key = first + kt * kBN + extra * box;
+        if (lane + extra >= boxes || key >= it.span.hi || key + box <= it.span.lo) return -2;
+        const int page = __ldg(row + (key >> p.page_shift));
+        if (page >= 0 && page < p.pages) return page;
+        record_error(p.err, LOWBIT_ERR_INVALID_ARG);
+        return -1;  // outside the tensor map: the copy fills zeros
+      };
+      int next = page_of(kt0, 0);
+      for (int kt = kt0; kt < kt1; ++kt) {
+        const int page = next;
+        if (kt + 1 < kt1) next = page_of(kt + 1, 0);
+        if (!mbar_wait(smem_addr(&bars.empty[stage]), phase ^ 1)) {
+          record_error(p.err, LOWBIT_ERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_addr(&bars.full[stage]);
+        const int page2 = boxes > 32 ? page_of(kt, 32) : -2;  // pages of one slot: 64 boxes
+        const int n = __popc(__ballot_sync(~0u, page != -2)) + __popc(__ballot_sync(~0u, page2 != -2));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * RB * 2));
+        __syncwarp();
+        const int slot = (first + kt * kBN) & p.page_mask;
+        auto copy = [&](int pg, int i) {
+          const uint32_t dst = ring + stage * C::kStage + i * box * C::kPart;
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part) {
+            constexpr int kElems = C::kPart / (FP8 ? 1 : 2);
+            tma_load_4d(dst + part * (kBN * C::kPart), &kmap, part * kElems, slot, it.h, pg, bar);
+            tma_load_4d(dst + C::kHalf + part * (kBN * C::kPart), &vmap, part * kElems, slot, it.h, pg, bar);
+          }
+        };
+        if (page != -2) copy(page, lane);
+        if (page2 != -2) copy(page2, lane + 32);
+        if (++stage == S) stage = 0, phase ^= 1;
+        if (filled < S) ++filled;
+      }
+      if (!ok || left <= 0 || !walk_next(a, it)) break;
+    }
+    // leave only when no copy is in flight
+    for (int i = 0; i < filled; ++i) {
+      if (--stage < 0) stage = S - 1, phase ^= 1;
+      mbar_wait(smem_addr(&bars.full[stage]), phase);
+    }
+    return;
+  }
+
+  const int g = lane >> 2, t = lane & 3;
+  const int wr = warp / C::kWarpsK, wk = warp % C::kWarpsK;  // row group, key group
+  const int wkey = wk * kNT * 8;                              // this warp's keys inside a tile
+  bool first = true, ok = true;
   for (;;) {
     const Request q = it.q;
-    const int b = it.b;
     const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
     if (kt1 == kt0) return;
     const Span span = it.span;
-    const int base_key = span.lo / kBN * kBN;
+    const int base_key = span.lo & ~(kBN - 1);
     const int r0 = it.qt * C::kRows;
     const int rows = q.n * a.shape.G;  // query rows of the request for this head
 
@@ -162,9 +238,10 @@ attn_mma_kernel(const AttnArgs a) {
     // ---- query fragments; with an e4m3 cache the row is scaled by a power of two into fp16
     uint32_t qf[C::kQShared ? 1 : C::kSteps][4];
     float coef[2];  // exponent per unit of the raw product, in powers of two
+    uint4* const qs = reinterpret_cast<uint4*>(smem + S * C::kStage) + (size_t)wr * C::kSteps * 32;
     {
       const float ks = FP8 && p.k_scale ? __ldg(p.k_scale + it.h) : 1.0f;
-      float scale2 = a.scale * ks * kLog2e;
+      const float scale2 = a.scale * ks * kLog2e;
       const uint16_t* src[2];
       float up[2] = {1.0f, 1.0f};
 #pragma unroll
@@ -176,8 +253,9 @@ attn_mma_kernel(const AttnArgs a) {
         if (FP8) {
           float m = 0.0f;
           if (qrow[i] >= 0)
-            for (int d = t * 8; d < D; d += 32) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src[i] + d);
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src[i] + d + t * 8);
               const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -193,7 +271,6 @@ attn_mma_kernel(const AttnArgs a) {
           coef[i] = scale2 * __uint_as_float((uint32_t)(127 + ee) << 23);
         }
       }
-      uint4* qs = reinterpret_cast<uint4*>(smem + S * C::kStage) + (size_t)wr * C::kSteps * 32;
 #pragma unroll
       for (int st = 0; st < C::kSteps; ++st) {
         uint32_t f[4];
@@ -214,32 +291,8 @@ attn_mma_kernel(const AttnArgs a) {
           for (int i = 0; i < 4; ++i) qf[st][i] = f[i];
         }
       }
-      if (C::kQShared) __syncthreads();
+      if (C::kQShared) named_barrier(1, kComputeThreads);
     }
-
-    // ---- copy of key tile kt into stage st: rows outside the span become zeros
-    auto load_tile = [&](int kt, int st) {
-      constexpr int kChunks = RB / 16;
-      constexpr int kIter = kBN * kChunks / kThreads;
-      const uint32_t dst = ring + st * C::kStage;
-      const long long head = (long long)it.h * p.head_stride;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int idx = tid + i * kThreads;
-        const int r = idx / kChunks, c = idx % kChunks;
-        const int key = base_key + kt * kBN + r;
-        bool real = key >= span.lo && key < span.hi;
-        long long at = 0;
-        if (real) {
-          const int page = __ldg(p.table + (long long)b * p.table_stride + (key >> p.page_shift));
-          real = page >= 0 && page < p.pages;
-          if (!real) record_error(p.err, LOWBIT_ERR_INVALID_ARG);
-          else at = (long long)page * p.page_stride + (long long)(key & p.page_mask) * p.token_stride + head + c * 16;
-        }
-        cp_async16(dst + chunk_off<RB>(r, c), p.k + at, real);
-        cp_async16(dst + C::kHalf + chunk_off<RB>(r, c), p.v + at, real);
-      }
-    };
 
     float o[kDT][4];
 #pragma unroll
@@ -247,24 +300,28 @@ attn_mma_kernel(const AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int last = 0;  // stage of the item's last tile, released after the join
 
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-      if (kt0 + s < kt1) load_tile(kt0 + s, s);
-      cp_async_commit();
-    }
-    int stage = 0;
     for (int kt = kt0; kt < kt1; ++kt) {
-      cp_async_wait<S - 2>();
-      __syncthreads();
-      {
-        const int ns = stage == 0 ? S - 1 : stage - 1;  // the stage that tile kt - 1 has left
-        if (kt + S - 1 < kt1) load_tile(kt + S - 1, ns);
-        cp_async_commit();
+      if (ok && !mbar_wait(smem_addr(&bars.full[stage]), phase)) {
+        record_error(p.err, LOWBIT_ERR_TIMEOUT);
+        ok = false;
       }
       const uint32_t ks = ring + stage * C::kStage, vs = ks + C::kHalf;
       const int key0 = base_key + kt * kBN;
-      const int wkey = wk * kNT * 8;  // this warp's keys inside the tile
+
+      // Values outside the span (unwritten slots, what an earlier tile left) become zeros, since
+      // 0 * NaN would reach the sums.  Every warp clears all rows that it reads.
+      if (key0 < span.lo || key0 + kBN > span.hi) {
+        constexpr int kChunks = RB / 16;
+        for (int i = lane; i < kNT * 8 * kChunks; i += 32) {
+          const int r = wkey + i / kChunks;
+          if (key0 + r < span.lo || key0 + r >= span.hi)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + chunk_off<RB>(r, i % kChunks)), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
 
       // scores of 16 rows and kNT * 8 keys
       float sc[kNT][4];
@@ -279,7 +336,7 @@ attn_mma_kernel(const AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (C::kQShared) {
-              const uint4 v = reinterpret_cast<const uint4*>(smem + S * C::kStage)[((size_t)wr * C::kSteps + 4 * j + e) * 32 + lane];
+              const uint4 v = qs[(4 * j + e) * 32 + lane];
               qa[e][0] = v.x, qa[e][1] = v.y, qa[e][2] = v.z, qa[e][3] = v.w;
             } else {
 #pragma unroll
@@ -288,7 +345,7 @@ attn_mma_kernel(const AttnArgs a) {
           }
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            const uint4 kw = lds128(ks + chunk_off<RB>(wkey + n * 8 + g, 4 * j + t));
+            const uint4 kw = lds128(ks + chunk_off<RB>(wkey + n * 8 + key_of<RB, FP8>(g), 4 * j + t));
             const uint32_t ww[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -300,7 +357,7 @@ attn_mma_kernel(const AttnArgs a) {
         for (int st = 0; st < C::kSteps; ++st) {
           uint32_t qa[4];
           if (C::kQShared) {
-            const uint4 v = reinterpret_cast<const uint4*>(smem + S * C::kStage)[((size_t)wr * C::kSteps + st) * 32 + lane];
+            const uint4 v = qs[st * 32 + lane];
             qa[0] = v.x, qa[1] = v.y, qa[2] = v.z, qa[3] = v.w;
           } else {
 #pragma unroll
@@ -325,7 +382,7 @@ attn_mma_kernel(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           sc[n][e] *= coef[e >> 1];
-          const int key = key0 + wkey + n * 8 + 2 * t + (e & 1);
+          const int key = key0 + wkey + n * 8 + key_of<RB, FP8>(2 * t + (e & 1));
           if (masked && (key < jlo[e >> 1] || key >= jhi[e >> 1])) sc[n][e] = -INFINITY;
           tm[e >> 1] = fmaxf(tm[e >> 1], sc[n][e]);
         }
@@ -363,7 +420,7 @@ attn_mma_kernel(const AttnArgs a) {
       // o += weights x values
 #pragma unroll
       for (int k2 = 0; k2 < kNT / 2; ++k2) {
-        const int r = wkey + k2 * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        const int r = wkey + k2 * 16 + ((lane >> 3) & 1) * 8 + key_of<RB, FP8>(lane & 7);
         if (FP8) {
 #pragma unroll
           for (int d = 0; d < D / 32; ++d) {
@@ -387,60 +444,103 @@ attn_mma_kernel(const AttnArgs a) {
           }
         }
       }
-      stage = stage + 1 == S ? 0 : stage + 1;
+      last = stage;
+      if (kt + 1 < kt1 || MT == 4) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.empty[stage]));
+      }
+      if (++stage == S) stage = 0, phase ^= 1;
     }
-    cp_async_wait<0>();
-    __syncthreads();  // every warp is done with the ring, which now takes the outputs
 
-    // ---- join the warps of a row group and store
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(~0u, l[i], 1);
       l[i] += __shfl_xor_sync(~0u, l[i], 2);
+    }
+    // ---- join the warps of a row group, through the last tile's stage: two warps' fragments fit
+    if (MT < 4) {
       if (t == 0) {
-        s_ml[warp][g + 8 * i][0] = m[i];
-        s_ml[warp][g + 8 * i][1] = l[i];
+        s_ml[warp][g] = make_float2(m[0], l[0]);
+        s_ml[warp][g + 8] = make_float2(m[1], l[1]);
       }
-    }
-    float* so = reinterpret_cast<float*>(smem) + (size_t)warp * 16 * (D + 4);
+      named_barrier(1, kComputeThreads);  // also: every warp is done with the last tile
 #pragma unroll
-    for (int d = 0; d < kDT; ++d)
+      for (int i = 0; i < 2; ++i) {
+        float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = g + 8 * (e >> 1);
-        const int col = FP8 ? 16 * (d / 2) + 4 * t + 2 * (e & 1) + (d & 1) : 8 * d + 2 * t + (e & 1);
-        so[row * (D + 4) + col] = o[d][e];
+        for (int k = 0; k < C::kWarpsK; ++k) mm = fmaxf(mm, s_ml[wr * C::kWarpsK + k][g + 8 * i].x);
+        const float f = mm == -INFINITY ? 0.0f : ex2(m[i] - mm);
+#pragma unroll
+        for (int k = 0; k < C::kWarpsK; ++k) {
+          const float2 x = s_ml[wr * C::kWarpsK + k][g + 8 * i];
+          ll += (mm == -INFINITY ? 0.0f : ex2(x.x - mm)) * x.y;
+        }
+        m[i] = mm;
+        l[i] = ll;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) o[d][2 * i] *= f, o[d][2 * i + 1] *= f;
       }
-    __syncthreads();
-    const bool whole = kt0 == 0 && kt1 == it.tiles;
-    const long long slot = 2LL * blockIdx.x + (first ? 0 : 1);
-    const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
-    constexpr int kQuads = D / 4;
-    for (int idx = tid; idx < C::kRows * kQuads; idx += kThreads) {
-      const int row = idx / kQuads, c = (idx % kQuads) * 4;
-      const int r = r0 + row;
-      if (r >= rows) break;
-      const int wbase = (row >> 4) * C::kWarpsK, lr = row & 15;
-      float mm = -INFINITY;
+      float4* const buf = reinterpret_cast<float4*>(smem + last * C::kStage) + lane;
+      auto give = [&](int place) {
 #pragma unroll
-      for (int k = 0; k < C::kWarpsK; ++k) mm = fmaxf(mm, s_ml[wbase + k][lr][0]);
-      float ll = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int d = 0; d < kDT; ++d) buf[(place * kDT + d) * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+      };
+      auto take = [&](int place) {
 #pragma unroll
-      for (int k = 0; k < C::kWarpsK; ++k) {
-        const float f = mm == -INFINITY ? 0.0f : ex2(s_ml[wbase + k][lr][0] - mm);
-        ll += f * s_ml[wbase + k][lr][1];
-        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (size_t)((wbase + k) * 16 + lr) * (D + 4) + c);
-        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-      }
-      if (whole) {
-        const int tok = r / a.shape.G;
-        store_row(a, (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G), D, c, acc, mm, ll, vscale);
+        for (int d = 0; d < kDT; ++d) {
+          const float4 v = buf[(place * kDT + d) * 32];
+          o[d][0] += v.x, o[d][1] += v.y, o[d][2] += v.z, o[d][3] += v.w;
+        }
+      };
+      if (MT == 1) {
+        if (wk >= 2) give(wk - 2);
+        named_barrier(1, kComputeThreads);
+        if (wk < 2) take(wk);
+        if (wk == 1) give(1);  // over what it has just read
+        named_barrier(1, kComputeThreads);
+        if (wk == 0) take(1);
       } else {
-        store_piece(a, slot, C::kRows, D, row, c, acc, mm, ll);
+        if (wk == 1) give(wr);
+        named_barrier(1, kComputeThreads);
+        if (wk == 0) take(wr);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&bars.empty[last]));
+    }
+
+    // ---- store: the row group's first warp holds its rows
+    if (wk == 0 && ok) {
+      const bool whole = kt0 == 0 && kt1 == it.tiles;
+      const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (qrow[i] < 0) continue;
+        const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * C::kRows + wr * 16 + g + 8 * i;
+        const float f = whole ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
+        uint16_t* const dst = a.out + qrow[i] * D;
+        float* const part = a.piece_o + piece * D;
+#pragma unroll
+        for (int d = 0; d < kDT; d += 2) {
+          const float x0 = o[d][2 * i] * f, x1 = o[d][2 * i + 1] * f, y0 = o[d + 1][2 * i] * f, y1 = o[d + 1][2 * i + 1] * f;
+          if (FP8) {  // dims 8 d + 4 t ..: even ones in tile d, odd ones in tile d + 1
+            if (whole) *reinterpret_cast<uint2*>(dst + 8 * d + 4 * t) = make_uint2(pack2<false>(x0, y0), pack2<false>(x1, y1));
+            else *reinterpret_cast<float4*>(part + 8 * d + 4 * t) = make_float4(x0, y0, x1, y1);
+          } else if (whole) {
+            *reinterpret_cast<uint32_t*>(dst + 8 * d + 2 * t) = pack2<false>(x0, x1);
+            *reinterpret_cast<uint32_t*>(dst + 8 * d + 8 + 2 * t) = pack2<false>(y0, y1);
+          } else {
+            *reinterpret_cast<float2*>(part + 8 * d + 2 * t) = make_float2(x0, x1);
+            *reinterpret_cast<float2*>(part + 8 * d + 8 + 2 * t) = make_float2(y0, y1);
+          }
+        }
+        if (t == 0) {
+          if (!whole) a.piece_ml[piece] = make_float2(m[i], l[i]);
+          else if (a.lse) a.lse[qrow[i]] = l[i] == 0.0f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
+        }
       }
     }
-    __syncthreads();  // the ring and s_ml are free again
+    if (C::kQShared || MT < 4) named_barrier(1, kComputeThreads);  // s_ml and qs are free again
     first = false;
     if (left <= 0 || !walk_next(a, it)) return;
   }
@@ -539,6 +639,9 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t s) {
     ctas = std::max(1, std::min(sms * per, kMaxPieceRows / 2 / C::kRows));
     ready[dev].store(ctas, std::memory_order_relaxed);
   }
+  CUtensorMap kmap, vmap;
+  if (!encode_cache(&kmap, a.p, a.p.k, D, FP8, kBN) || !encode_cache(&vmap, a.p, a.p.v, D, FP8, kBN))
+    return cudaErrorNotSupported;
   a.ctas = ctas;
   a.shape.r_shift = MT == 1 ? 4 : (MT == 2 ? 5 : 6);
   a.shape.bn_shift = 6;
@@ -547,7 +650,7 @@ cudaError_t launch_mma(AttnArgs a, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
-  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<D, MT, FP8>, a);
+  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<D, MT, FP8>, a, kmap, vmap);
   return e != cudaSuccess ? e : launch_combine(a, D, s);
 }
 
@@ -585,6 +688,28 @@ cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
   if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
   if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a);
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256>, a);
+}
+
+bool encode_cache(CUtensorMap* map, const PagedArgs& p, void* at, int D, bool fp8, int keys) {
+  // looked up once, on the first call
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  if (!encode) return false;
+  const int ps = p.page_mask + 1, part = fp8 ? (D < 128 ? D : 128) : 64;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)ps, (cuuint64_t)p.Hk, (cuuint64_t)p.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride, (cuuint64_t)p.head_stride, (cuuint64_t)p.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)part, (cuuint32_t)(ps < keys ? ps : keys), 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                fp8 && D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s) {

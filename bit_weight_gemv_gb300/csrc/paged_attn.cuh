@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace lowbit {
 
@@ -194,21 +195,19 @@ __device__ __forceinline__ bool walk_next(const AttnArgs& a, Walk& w) {
   return true;
 }
 
-// Columns c..c+3 of one finished row: acc / l, rounded once, and the row's lse.
-__device__ __forceinline__ void store_row(const AttnArgs& a, long long row, int D, int c, float4 acc,
-                                          float m, float l, float vscale) {
-  const float f = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);  // l NaN: NaN
-  uint2 v;
-  v.x = (uint32_t)float_to_bf16_bits(acc.x * f) | ((uint32_t)float_to_bf16_bits(acc.y * f) << 16);
-  v.y = (uint32_t)float_to_bf16_bits(acc.z * f) | ((uint32_t)float_to_bf16_bits(acc.w * f) << 16);
-  *reinterpret_cast<uint2*>(a.out + row * D + c) = v;
-  if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+// 4-D tiled tensor copy (TMA) global -> shared.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void store_piece(const AttnArgs& a, long long slot, int R, int D, int row, int c,
-                                            float4 acc, float m, float l) {
-  *reinterpret_cast<float4*>(a.piece_o + (slot * R + row) * D + c) = acc;
-  if (c == 0) a.piece_ml[slot * R + row] = make_float2(m, l);
-}
+
+// The cache as [page][head][slot][D], boxes of 128 bytes (64, where a row has no more) by one page's
+// slots, at most `keys`, swizzled over the box's row length.
+bool encode_cache(CUtensorMap* map, const PagedArgs& p, void* at, int D, bool fp8, int keys);
 
 // Launch configuration of an attention kernel of `ctas` resident CTAs, and the combine step behind it.
 void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int threads, int smem,

@@ -58,15 +58,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
       : "r"(taddr)
       : "memory");
 }
-// 4-D tiled tensor copy (TMA) global -> shared.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
 // D[tmem] (+)= A[smem] x B[smem]^T, issued by one thread.
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -371,19 +362,29 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 
         // Q rows into shared memory (swizzled as TMA would leave them)
         if (active) {
-          constexpr int kChunks = D / 8;
+          constexpr int kChunks = D / 8, kAll = PAIR ? 128 : 256, kMine = 128 * kChunks / kAll, kBatch = 8;
           const uint32_t dst = q_at + (PAIR ? slot * C::kTile : 0);
-          for (int i = PAIR ? t128 : tid; i < 128 * kChunks; i += PAIR ? 128 : 256) {
-            const int rr = i / kChunks, c = i % kChunks, r = r_tile + rr;
-            if (r >= rows) break;
-            const int tok = r / G;
-            uint4 v = *reinterpret_cast<const uint4*>(a.q + (long long)(it.q.row0 + tok) * a.q_stride +
-                                                      (long long)(it.h * G + r - tok * G) * D + c * 8);
-            v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             dst + (c / 8) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
+          const int t0 = PAIR ? t128 : tid;
+#pragma unroll
+          for (int i0 = 0; i0 < kMine; i0 += kBatch) {
+            uint4 v[kBatch];  // loaded together, then stored: one round trip per batch
+#pragma unroll
+            for (int i = 0; i < kBatch && i0 + i < kMine; ++i) {
+              const int rr = (t0 + (i0 + i) * kAll) / kChunks, c = (t0 + (i0 + i) * kAll) % kChunks, r = r_tile + rr;
+              const int tok = r / G;
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (r < rows)
+                v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.q.row0 + tok) * a.q_stride +
+                                                       (long long)(it.h * G + r - tok * G) * D + c * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch && i0 + i < kMine; ++i) {
+              const int rr = (t0 + (i0 + i) * kAll) / kChunks, c = (t0 + (i0 + i) * kAll) % kChunks;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               dst + (c / 8) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
+                           "r"(v[i].x ^ sign), "r"(v[i].y ^ sign), "r"(v[i].z ^ sign), "r"(v[i].w ^ sign)
+                           : "memory");
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&sh.q_full[PAIR ? slot : 0]));
@@ -543,32 +544,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess)
-      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// The cache as [page][head][slot][D], boxes of 64 elements by one page's slots (at most 128).
-bool encode_cache(CUtensorMap* map, const PagedArgs& p, void* at, int D) {
-  const auto encode = map_encoder();
-  if (!encode) return false;
-  const int ps = p.page_mask + 1;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)ps, (cuuint64_t)p.Hk, (cuuint64_t)p.pages};
-  cuuint64_t strides[3] = {(cuuint64_t)p.token_stride, (cuuint64_t)p.head_stride, (cuuint64_t)p.page_stride};
-  cuuint32_t box[4] = {64, (cuuint32_t)(ps < kTcBN ? ps : kTcBN), 1, 1};
-  cuuint32_t step[4] = {1, 1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool PAIR>
 cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   using C = Tc<D>;
@@ -587,7 +562,7 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
     ready[dev].store(ctas, std::memory_order_relaxed);
   }
   CUtensorMap kmap, vmap;
-  if (!encode_cache(&kmap, a.p, a.p.k, D) || !encode_cache(&vmap, a.p, a.p.v, D)) return cudaErrorNotSupported;
+  if (!encode_cache(&kmap, a.p, a.p.k, D, false, kTcBN) || !encode_cache(&vmap, a.p, a.p.v, D, false, kTcBN)) return cudaErrorNotSupported;
   a.ctas = ctas;
   a.shape.r_shift = PAIR ? 8 : 7;
   a.shape.bn_shift = 7;
@@ -605,8 +580,7 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
 // True where the kernel can run: bf16, heads of 64 or 128, pages that TMA can box, strides and
 // addresses within its limits.
 bool attention_tc_fits(const AttnArgs& a, int D, bool fp8) {
-  return !fp8 && D <= 128 && a.p.page_mask + 1 >= 16 && a.p.page_stride < (1LL << 40) &&
-         a.p.token_stride < (1LL << 40) && a.p.head_stride < (1LL << 40);
+  return !fp8 && D <= 128 && a.p.page_mask + 1 >= 16;
 }
 
 cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool pair, cudaStream_t s) {

@@ -353,10 +353,10 @@ typedef struct lowbit_paged_batch {
 #define LOWBIT_CACHE_BF16 0 /* keys and values as bf16 */
 #define LOWBIT_CACHE_E4M3 1 /* as e4m3, times k_scale / v_scale of the head */
 
-/* A cache of num_pages pages of page_size slots (a power of two, 1..1024) for `heads` key/value
- * heads of head_dim 64, 128 or 256.  Element (page, slot, head, d) of k (and v) is at
+/* A cache of num_pages pages of page_size slots (a power of two, 1..1024; at least 2 with e4m3
+ * heads of 64) for `heads` key/value heads of head_dim 64, 128 or 256.  Element (page, slot, head, d) of k (and v) is at
  * page * page_stride + slot * token_stride + head * head_stride + d: strides in elements,
- * positive multiples of 16 bytes, so both orders of heads and slots fit.  The two arrays are
+ * positive multiples of 16 bytes below 2^39, so both orders of heads and slots fit.  The two arrays are
  * 16-byte aligned and share the strides. */
 typedef struct lowbit_paged_cache {
   void* k;
