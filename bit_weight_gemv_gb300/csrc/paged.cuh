@@ -66,15 +66,21 @@ struct Span {
 };
 struct ItemShape {
   int G;
+  uint32_t g_inv;         // floor(2^32 / G), at most 2^32 - 1
   int r_shift, bn_shift;  // R = 1 << r_shift rows, BN = 1 << bn_shift keys
   int lead;
   int causal, window;
 };
+// r / G: the product with floor(2^32 / G) is short of it by less than one.
+__device__ __forceinline__ int token_of(const ItemShape& s, int r) {
+  const uint32_t q = __umulhi((uint32_t)r, s.g_inv);
+  return (int)(q + ((uint32_t)r - q * s.G >= (uint32_t)s.G ? 1u : 0u));
+}
 __device__ __forceinline__ Span tile_span(const ItemShape& s, const Request& q, int qt) {
   const int r0 = qt << s.r_shift, r1 = min(r0 + (1 << s.r_shift), q.n * s.G) - 1;
   Span k;
-  k.hi = s.causal ? max(0, min(q.kv, q.kv - q.n + r1 / s.G + 1)) : q.kv;
-  k.lo = s.window ? max(0, q.kv - q.n + r0 / s.G - s.window + 1) : 0;
+  k.hi = s.causal ? max(0, min(q.kv, q.kv - q.n + token_of(s, r1) + 1)) : q.kv;
+  k.lo = s.window ? max(0, q.kv - q.n + token_of(s, r0) - s.window + 1) : 0;
   if (k.lo >= k.hi) k.lo = k.hi = 0;
   return k;
 }

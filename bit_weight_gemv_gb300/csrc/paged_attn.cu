@@ -124,7 +124,6 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   constexpr int kNT = 2 * MT;       // 8-key tiles per warp
   constexpr int kDT = D / 8;        // 8-dim tiles
   extern __shared__ uint8_t raw[];
-  __shared__ Plan plan;
   __shared__ RingBars bars;
   __shared__ float2 s_ml[4][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -138,11 +137,11 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  make_plan<kThreads>(a, plan, blockIdx.x);
-  __syncthreads();
-  if (plan.begin >= plan.end) return;
-  Walk it = walk_start(a, plan);
-  int left = (int)(plan.end - plan.begin);
+  __syncthreads();  // the barriers are initialised
+  Walk it;
+  Share share;
+  if (!start_walk<kThreads>(a, blockIdx.x, it, share)) return;
+  int left = share.left;
   int stage = 0;
   uint32_t phase = 0;
 
@@ -223,7 +222,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + wr * 16 + g + 8 * i;
-      const int tok = r / a.shape.G;
+      const int tok = token_of(a.shape, r);
       const bool in = r < rows;
       const int pos = q.kv - q.n + tok;
       jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
@@ -232,8 +231,8 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
     }
     // keys that every row of the CTA's tile sees need no mask
     const int last_row = min(r0 + C::kRows, rows) - 1;
-    const int all_lo = a.shape.window ? max(0, q.kv - q.n + last_row / a.shape.G - a.shape.window + 1) : 0;
-    const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + r0 / a.shape.G + 1) : q.kv;
+    const int all_lo = a.shape.window ? max(0, q.kv - q.n + token_of(a.shape, last_row) - a.shape.window + 1) : 0;
+    const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
 
     // ---- query fragments; with an e4m3 cache the row is scaled by a power of two into fp16
     uint32_t qf[C::kQShared ? 1 : C::kSteps][4];
@@ -241,54 +240,59 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
     uint4* const qs = reinterpret_cast<uint4*>(smem + S * C::kStage) + (size_t)wr * C::kSteps * 32;
     {
       const float ks = FP8 && p.k_scale ? __ldg(p.k_scale + it.h) : 1.0f;
-      const float scale2 = a.scale * ks * kLog2e;
-      const uint16_t* src[2];
-      float up[2] = {1.0f, 1.0f};
+      uint32_t f[C::kSteps][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + wr * 16 + g + 8 * i;
-        const int tok = r / a.shape.G;
-        src[i] = a.q + (long long)(q.row0 + tok) * a.q_stride + (long long)(it.h * a.shape.G + r - tok * a.shape.G) * D;
-        coef[i] = scale2;
-        if (FP8) {
-          float m = 0.0f;
-          if (qrow[i] >= 0)
+        const int tok = token_of(a.shape, r);
+        const uint16_t* src = a.q + (long long)(q.row0 + tok) * a.q_stride + (long long)(it.h * a.shape.G + r - tok * a.shape.G) * D;
 #pragma unroll
-            for (int d = 0; d < D; d += 32) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src[i] + d + t * 8);
-              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int st = 0; st < C::kSteps; ++st)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
+          for (int half = 0; half < 2; ++half) {
+            // bf16: columns 16 st + 2t (+8); e4m3: the order in which a 16-byte load of a key's
+            // row hands them out, 64 (st/4) + 16 t + 4 (st%4) (+2)
+            const int col = FP8 ? 64 * (st / 4) + 16 * t + 4 * (st % 4) + half * 2 : 16 * st + 2 * t + half * 8;
+            f[st][2 * half + i] = qrow[i] >= 0 ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+          }
+      }
+      coef[0] = coef[1] = a.scale * ks * kLog2e;
+      if (FP8) {
+        // the four lanes of a row hold all of it
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = 0.0f;
+#pragma unroll
+          for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t v = f[st][2 * half + i];
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u))));
             }
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-          // 2^-e with 2^e <= m < 2^(e+1): the row's largest becomes 1..2.  A row of zeros, or one
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          // 2^-e with 2^e <= top < 2^(e+1): the row's largest becomes 1..2.  A row of zeros, or one
           // with an Inf or a NaN, stays as it is.
-          const int e = (int)(__float_as_uint(m) >> 23) - 127;
-          const int ee = (m > 0.0f && e < 128) ? max(-100, min(100, e)) : 0;
-          up[i] = __uint_as_float((uint32_t)(127 - ee) << 23);
-          coef[i] = scale2 * __uint_as_float((uint32_t)(127 + ee) << 23);
+          const int e = (int)(__float_as_uint(top) >> 23) - 127;
+          const int ee = (top > 0.0f && e < 128) ? max(-100, min(100, e)) : 0;
+          const float up = __uint_as_float((uint32_t)(127 - ee) << 23);
+          coef[i] *= __uint_as_float((uint32_t)(127 + ee) << 23);
+#pragma unroll
+          for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t v = f[st][2 * half + i];
+              f[st][2 * half + i] = pack2<true>(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+            }
         }
       }
 #pragma unroll
       for (int st = 0; st < C::kSteps; ++st) {
-        uint32_t f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = i & 1;
-          // bf16: columns 16 st + 2t (+8); e4m3: the order in which a 16-byte load of a key's
-          // row hands them out, 64 (st/4) + 16 t + 4 (st%4) (+2)
-          const int col = FP8 ? 64 * (st / 4) + 16 * t + 4 * (st % 4) + (i >> 1) * 2 : 16 * st + 2 * t + (i >> 1) * 8;
-          uint32_t v = qrow[row] >= 0 ? *reinterpret_cast<const uint32_t*>(src[row] + col) : 0u;
-          if (FP8) v = pack2<true>(__uint_as_float(v << 16) * up[row], __uint_as_float(v & 0xFFFF0000u) * up[row]);
-          f[i] = v;
-        }
         if (C::kQShared) {
-          if (wk == 0) qs[st * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+          if (wk == 0) qs[st * 32 + lane] = make_uint4(f[st][0], f[st][1], f[st][2], f[st][3]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qf[st][i] = f[i];
+          for (int i = 0; i < 4; ++i) qf[C::kQShared ? 0 : st][i] = f[st][i];
         }
       }
       if (C::kQShared) named_barrier(1, kComputeThreads);
@@ -553,24 +557,19 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
 // trip, and then one part of the row each, whose loads do not wait for one another.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const AttnArgs a) {
-  __shared__ Plan plan;
   // the schedule reads the batch alone, which no kernel since the attention's start has written
-  make_plan<kJoinThreads>(a, plan, blockIdx.x + 1);
-  __syncthreads();
   Walk it;
-  bool cut = plan.begin < plan.end;
-  if (cut) {
-    it = walk_start(a, plan);
-    cut = it.tile > 0;  // else the cut fell between two items, or inside a lead
-  }
+  Share share;
+  // otherwise the cut fell between two items, inside a lead, or past the end
+  const bool cut = start_walk<kJoinThreads>(a, blockIdx.x + 1, it, share) && it.tile > 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!cut) return;
-  const long long tiles_at = plan.begin - it.tile;           // where the item's tiles begin
+  const long long tiles_at = share.begin - it.tile;           // where the item's tiles begin
   const long long from = tiles_at - a.shape.lead;            // and its lead
-  const long long c0 = quotient(tiles_at, plan.chunk);       // CTAs with a piece: c0..c0 + n
-  const int n = (int)(quotient(tiles_at + it.tiles - 1, plan.chunk) - c0);
+  const long long c0 = quotient(tiles_at, share.chunk);       // CTAs with a piece: c0..c0 + n
+  const int n = (int)(quotient(tiles_at + it.tiles - 1, share.chunk) - c0);
   const int shares = n * gridDim.y, mine = (int)(blockIdx.x + 1 - (c0 + 1)) * gridDim.y + blockIdx.y;
-  const long long slot0 = 2 * c0 + (from > c0 * plan.chunk ? 1 : 0);
+  const long long slot0 = 2 * c0 + (from > c0 * share.chunk ? 1 : 0);
   const int G = a.shape.G, R = 1 << a.shape.r_shift, r0 = it.qt << a.shape.r_shift;
   const int rows = min(R, it.q.n * G - r0);
   const int ra = (int)((long long)rows * mine / shares), rb = (int)((long long)rows * (mine + 1) / shares);
@@ -607,7 +606,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const AttnAr
       }
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    const int r = r0 + row, tok = r / G;
+    const int r = r0 + row, tok = token_of(a.shape, r);
     const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
     const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
@@ -751,7 +750,8 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
     return LOWBIT_ERR_ALIGN;
   a.p.err = device_error_word();
   if (!a.p.err) return LOWBIT_ERR_CUDA;
-  a.shape = ItemShape{Hq / cache->heads, 0, 0, 0, causal != 0, window};
+  const int G = Hq / cache->heads;
+  a.shape = ItemShape{G, G > 1 ? (uint32_t)((1ull << 32) / G) : 0xFFFFFFFFu, 0, 0, 0, causal != 0, window};
   a.q = q;
   a.q_stride = q_stride;
   a.Hq = Hq;

@@ -36,95 +36,33 @@ struct AttnArgs {
 
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);
 
-// A CTA's share [begin, end) of the work, in key tiles and leads, and where begin falls.
-struct Plan {
-  long long begin, end, chunk;
-  long long off;  // of begin inside request b's work
-  int b;
-};
-
 // a / b of nonnegative numbers: 32-bit where both fit (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
+__device__ __forceinline__ long long warp_sum(long long c) {
+  for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+  return c;
+}
+__device__ __forceinline__ long long warp_inclusive(long long c, int lane) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(~0u, c, o);
+    if (lane >= o) c += v;
+  }
+  return c;
+}
 
-// Cost of one head of request b.  `lane` < 0: by one thread alone, else by a whole warp.
+// Cost of one head of request b: by one thread, or (`lane` >= 0) by a whole warp.
 __device__ __forceinline__ long long head_cost(const ItemShape& s, const Request& q, int lane) {
   const int nq = query_tiles(s, q);
   if (nq == 1) return tile_cost(s, tile_span(s, q, 0)) + s.lead;
   long long c = 0;
   for (int i = lane < 0 ? 0 : lane; i < nq; i += lane < 0 ? 1 : 32) c += tile_cost(s, tile_span(s, q, i)) + s.lead;
-  if (lane >= 0)
-    for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
-  return c;
+  return lane < 0 ? c : warp_sum(c);
 }
 
-// The CTA's share, by all NT threads of the block (a multiple of 32); `pl` is valid after the
-// next __syncthreads.  Requests are summed one per thread, or one per warp where each has many
-// query tiles.
-template <int NT>
-__device__ __forceinline__ void make_plan(const AttnArgs& a, Plan& pl, int cta) {
-  __shared__ long long s_warp[NT / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool by_warp = (long long)a.p.T * a.shape.G > (4LL << a.shape.r_shift) * a.p.B;
-  long long total = 0, chunk = 0, begin = 0, end = 0;
-  if (tid == 0) pl.b = a.p.B, pl.off = 0, pl.begin = pl.end = 0;
-  // pass 0 sums, pass 1 finds the request that holds `begin`; one pass serves when every request
-  // has a thread (or a warp) of its own
-  const int step = by_warp ? NT / 32 : NT;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long carry = 0;
-    for (int b0 = 0; b0 < a.p.B; b0 += step) {
-      const int b = b0 + (by_warp ? warp : tid);
-      long long c = 0;
-      if (b < a.p.B) {
-        const Request q = load_request(a.p, b);
-        c = head_cost(a.shape, q, by_warp ? lane : -1) * a.p.Hk;
-      }
-      long long incl = c;  // inclusive sum over the requests of this warp
-      if (!by_warp)
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(~0u, incl, o);
-          if (lane >= o) incl += v;
-        }
-      if (b0) __syncthreads();
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      long long before = carry;
-#pragma unroll
-      for (int i = 0; i < NT / 32; ++i) {
-        const long long v = s_warp[i];
-        if (i < warp) before += v;
-        carry += v;
-      }
-      if (pass == 0 && a.p.B <= step) {
-        total = carry;
-        chunk = max((long long)a.min_chunk, quotient(total + a.ctas - 1, a.ctas));
-        begin = (long long)cta * chunk;
-        end = min(begin + chunk, total);
-      }
-      if (pass == 1 || a.p.B <= step) {
-        const long long at = before + incl - c;
-        if (begin < total && begin >= at && begin < at + c && (!by_warp || lane == 0)) {
-          pl.b = b;
-          pl.off = begin - at;
-          pl.begin = begin;
-          pl.end = end;
-        }
-      }
-    }
-    if (a.p.B <= step) break;
-    total = carry;
-    chunk = max((long long)a.min_chunk, quotient(total + a.ctas - 1, a.ctas));
-    begin = (long long)cta * chunk;
-    end = min(begin + chunk, total);
-    __syncthreads();
-  }
-  if (tid == 0) pl.chunk = chunk;
-}
-
-// The walk over items from the plan's start: every warp keeps its own copy.
+// The walk over a CTA's share of the items: every warp keeps its own copy.
 struct Walk {
   Request q;
   Span span;
@@ -138,37 +76,158 @@ __device__ __forceinline__ void walk_item(const AttnArgs& a, Walk& w, int off) {
   w.lead = max(0, a.shape.lead - off);
   w.tile = max(0, off - a.shape.lead);
 }
-// By whole warps.
-__device__ __forceinline__ Walk walk_start(const AttnArgs& a, const Plan& pl) {
+
+// The share of CTA `cta`: its first unit, how many, and the walk to the first; false if it has
+// none.  By all NT threads of the block.
+struct Share {
+  long long begin, chunk;
+  int left;
+};
+// The short way, every warp on its own: up to 32 requests of one query tile each, one per lane, in
+// 32 bits.  A decode or verify step is over in some microseconds, of which the instructions a
+// CTA touches for the first time are a large part (about 6 cycles each when they come from
+// memory), so this way is kept apart from the general one: 0 = not applicable, 1 = found,
+// -1 = the CTA has no share.
+__device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk& w, Share& sh) {
   const int lane = threadIdx.x & 31;
-  Walk w;
-  w.b = pl.b;
+  if (a.p.B > 32) return 0;
+  Request q = {0, 0, 0};
+  if (lane < a.p.B) q = load_request(a.p, lane);
+  // one tile holds every row: its keys end with the request's, whatever the mask
+  const int lo = a.shape.window ? max(0, q.kv - q.n - a.shape.window + 1) : 0;
+  const bool none = lo >= q.kv;
+  const int tiles = none ? 1 : ((q.kv - 1) >> a.shape.bn_shift) - (lo >> a.shape.bn_shift) + 1;
+  const uint32_t cost = q.n ? (uint32_t)(tiles + a.shape.lead) : 0;
+  const bool big = (long long)q.n * a.shape.G > (1 << a.shape.r_shift) || (unsigned long long)cost * a.p.Hk > (1u << 25);
+  if (__any_sync(~0u, big)) return 0;
+  uint32_t incl = cost * a.p.Hk;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const uint32_t total = __shfl_sync(~0u, incl, 31);
+  const uint32_t chunk = max((uint32_t)a.min_chunk, (total + a.ctas - 1) / a.ctas);
+  const uint32_t begin = cta * chunk;
+  if (begin >= total) return -1;
+  sh.begin = begin;
+  sh.chunk = chunk;
+  sh.left = (int)min(chunk, total - begin);
+  const int src = __ffs(__ballot_sync(~0u, incl > begin)) - 1;
+  uint32_t off = begin - __shfl_sync(~0u, incl - cost * a.p.Hk, src);
+  const uint32_t each = __shfl_sync(~0u, cost, src);
+  w.b = src;
+  w.q.row0 = __shfl_sync(~0u, q.row0, src);
+  w.q.n = __shfl_sync(~0u, q.n, src);
+  w.q.kv = __shfl_sync(~0u, q.kv, src);
+  w.span.lo = __shfl_sync(~0u, none ? 0 : lo, src);
+  w.span.hi = __shfl_sync(~0u, none ? 0 : q.kv, src);
+  w.h = (int)(off / each);
+  off -= w.h * each;
+  w.nq = 1;
+  w.qt = 0;
+  w.tiles = (int)each - a.shape.lead;
+  w.lead = max(0, a.shape.lead - (int)off);
+  w.tile = max(0, (int)off - a.shape.lead);
+  return 1;
+}
+// Up to 32 requests every warp sums them on its own (one per lane, or one after another where each
+// has many query tiles), so that nothing waits for a barrier; above, the block does.
+template <int NT>
+__device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, Share& sh) {
+  __shared__ long long s_warp[NT / 32], s_off;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int brief = start_walk_short(a, cta, w, sh);
+  if (brief) return brief > 0;
+  const bool tall = (long long)a.p.T * a.shape.G > (4LL << a.shape.r_shift) * a.p.B;
+  long long total, off = 0;
+  auto share = [&]() {
+    sh.chunk = max((long long)a.min_chunk, quotient(total + a.ctas - 1, a.ctas));
+    sh.begin = (long long)cta * sh.chunk;
+    sh.left = (int)(min(sh.begin + sh.chunk, total) - sh.begin);
+    return sh.left > 0;
+  };
+  w.b = 0;
+  if (a.p.B <= 32) {
+    long long sum = 0;
+    if (tall) {
+#pragma unroll 1
+      for (int b = 0; b < a.p.B; ++b) {
+        const long long c = head_cost(a.shape, load_request(a.p, b), lane) * a.p.Hk;
+        if (lane == b) sum = c;
+      }
+    } else if (lane < a.p.B) {
+      sum = head_cost(a.shape, load_request(a.p, lane), -1) * a.p.Hk;
+    }
+    const long long incl = warp_inclusive(sum, lane);
+    total = __shfl_sync(~0u, incl, 31);
+    if (!share()) return false;
+    w.b = __ffs(__ballot_sync(~0u, incl > sh.begin)) - 1;
+    off = sh.begin - __shfl_sync(~0u, incl - sum, w.b);
+  } else {
+    // One pass where every request has a thread (or a warp) of its own; else pass 0 sums and pass 1
+    // finds the request that holds the share's begin.
+    const int step = tall ? NT / 32 : NT;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      long long carry = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.p.B; b0 += step) {
+        const int b = b0 + (tall ? warp : tid);
+        long long c = 0;
+        if (b < a.p.B) c = head_cost(a.shape, load_request(a.p, b), tall ? lane : -1) * a.p.Hk;
+        const long long incl = tall ? c : warp_inclusive(c, lane);
+        if (b0 || pass) __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        long long before = carry;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+          const long long v = s_warp[i];
+          if (i < warp) before += v;
+          carry += v;
+        }
+        if (a.p.B <= step) {
+          total = carry;
+          if (!share()) return false;  // the whole block alike
+        }
+        const long long at = before + incl - c;
+        if ((pass || a.p.B <= step) && sh.begin >= at && sh.begin < at + c && (!tall || lane == 0))
+          s_b = b, s_off = sh.begin - at;
+      }
+      total = carry;
+      if (a.p.B <= step) break;
+      if (!pass && !share()) return false;
+    }
+    __syncthreads();
+    w.b = s_b;
+    off = s_off;
+  }
   w.q = load_request(a.p, w.b);
+
+  // the head, the query tile and the place inside the item
   w.nq = query_tiles(a.shape, w.q);
   const long long each = head_cost(a.shape, w.q, lane);
-  w.h = (int)quotient(pl.off, each);
-  long long rest = pl.off - w.h * each;
+  w.h = (int)quotient(off, each);
+  off -= w.h * each;
   w.qt = 0;
   if (w.nq > 1)
     for (int i0 = 0; i0 < w.nq; i0 += 32) {
       const int i = i0 + lane;
       const long long c = i < w.nq ? tile_cost(a.shape, tile_span(a.shape, w.q, i)) + a.shape.lead : 0;
-      long long incl = c;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const unsigned past = __ballot_sync(~0u, incl > rest);
+      const long long incl = warp_inclusive(c, lane);
+      const unsigned past = __ballot_sync(~0u, incl > off);
       if (past) {
         const int src = __ffs(past) - 1;
         w.qt = i0 + src;
-        rest -= __shfl_sync(~0u, incl - c, src);
+        off -= __shfl_sync(~0u, incl - c, src);
         break;
       }
-      rest -= __shfl_sync(~0u, incl, 31);
+      off -= __shfl_sync(~0u, incl, 31);
     }
-  walk_item(a, w, (int)rest);
-  return w;
+  walk_item(a, w, (int)off);
+  return true;
 }
 // Key tiles of the current item that fall into what is left of the share, which they use up;
 // 0 when the share ends before its tiles.

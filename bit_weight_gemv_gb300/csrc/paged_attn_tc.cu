@@ -120,7 +120,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   constexpr int S = C::kStages;
   constexpr int kRows = PAIR ? 256 : 128;
   extern __shared__ uint8_t raw[];
-  __shared__ Plan plan;
   __shared__ TcShared sh;
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, ring = base + 2 * C::kTile;
@@ -147,16 +146,17 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  make_plan<kTcThreads>(a, plan, blockIdx.x);
+  Walk it;
+  Share share;
+  const bool busy = start_walk<kTcThreads>(a, blockIdx.x, it, share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int G = a.shape.G;
 
-  if (plan.begin < plan.end) {
-    Walk it = walk_start(a, plan);
-    int left = (int)(plan.end - plan.begin);
+  if (busy) {
+    int left = share.left;
 
     // Registers: 384 threads launch with 168 each (64,512); 256 softmax threads take 208 and the
     // other 128 keep 80 (63,488).
@@ -371,7 +371,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
             for (int i = 0; i < kBatch && i0 + i < kMine; ++i) {
               const int rr = (t0 + (i0 + i) * kAll) / kChunks, c = (t0 + (i0 + i) * kAll) % kChunks, r = r_tile + rr;
-              const int tok = r / G;
+              const int tok = token_of(a.shape, r);
               v[i] = make_uint4(0, 0, 0, 0);
               if (r < rows)
                 v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.q.row0 + tok) * a.q_stride +
@@ -391,7 +391,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         }
 
         // the keys this row sees
-        const int r = r_tile + row, tok = r / G;
+        const int r = r_tile + row, tok = token_of(a.shape, r);
         const bool in = r < rows;
         const int pos = it.q.kv - it.q.n + tok;
         const int jhi = in ? (a.shape.causal ? min(it.q.kv, pos + 1) : it.q.kv) : 0;
@@ -405,9 +405,48 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             WAIT_OR(sh.s_full[slot], s_phase, { ok = false; break; });
             s_phase ^= 1;
             tc_fence_after();
-            if (work) {
+            const int key0 = key_first + j * kTcBN;
+            // the maximum grew: l and (past the slot's first tile) O follow the new reference
+            auto refer = [&](float top) {
+              const bool grow = top > m + kGrow;  // from -inf: any finite maximum
+              if (__any_sync(~0u, grow)) {
+                const float f = grow ? exp2_approx(m - top) : 1.0f;
+                if (grow) m = top;
+                l *= f;
+                // the product before this one is complete: its tensor work came before these scores'
+                if (steps > 0) {
+                  const uint32_t o_at = tmem + C::kO + D * slot + lanes;
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(o_at + c, o);
+                  }
+                }
+              }
+            };
+            // weights of 32 scores, as bf16 pairs, and their sum into l
+            auto weigh = [&](const float* s, int c) {
+              const float ref = m == -INFINITY ? 0.0f : -m;
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(coef, coef), make_float2(ref, ref));
+                x.x = exp2_approx(x.x);
+                x.y = exp2_approx(x.y);
+                sum[i & 1] = add2(sum[i & 1], x);
+                w[i] = pack_bf16x2(x.x, x.y);
+              }
+              tmem_st16(s_at + 16 * c, w);
+              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            };
+            if (work && PAIR) {
+              // all 128 scores at once, straight through: the prompt kernels run long enough
               float s[128];
-              const int key0 = key_first + j * kTcBN;
 #pragma unroll
               for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
               tmem_ld_wait();
@@ -422,43 +461,35 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], i + 4 + e < 128 ? fmaxf(s[i + e], s[i + 4 + e]) : s[i + e]);
               }
-              const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * coef;
-              const bool grow = top > m + kGrow;  // from -inf: any finite maximum
-              if (__any_sync(~0u, grow)) {
-                const float f = grow ? exp2_approx(m - top) : 1.0f;
-                if (grow) m = top;
-                l *= f;
-                // the product before this one is complete: its tensor work came before these scores'
-                if (steps > 0) {
-                  const uint32_t o_at = tmem + C::kO + D * slot + lanes;
+              refer(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * coef);
 #pragma unroll
-                  for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_at + c, o);
-                    tmem_ld_wait();
+              for (int c = 0; c < 4; ++c) weigh(s + 32 * c, c);
+              tmem_st_wait();
+            } else if (work) {
+              // 32 scores at a time, read once for the maximum and once for the weights, in a loop
+              // that stays rolled: unrolled, a call's first tile waited 5 us for its instructions
+              const bool masked = __any_sync(~0u, in && (key0 < jlo || key0 + kTcBN > jhi));
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                const int c = i & 3;
+                float s[32];
+                tmem_ld32(s_at + 32 * c, s);
+                tmem_ld_wait();
+                if (masked) {
+                  const int from = jlo - key0 - 32 * c, to = jhi - key0 - 32 * c;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st16(o_at + c, o);
-                  }
+                  for (int k = 0; k < 32; ++k)
+                    if (k < from || k >= to) s[k] = -INFINITY;
+                }
+                if (i < 4) {
+#pragma unroll
+                  for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(s[k], s[k + 1]));
+                  if (i == 3) refer(top * coef);
+                } else {
+                  weigh(s, c);
                 }
               }
-              const float ref = m == -INFINITY ? 0.0f : -m;
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float2 x = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), make_float2(coef, coef),
-                                  make_float2(ref, ref));
-                  x.x = exp2_approx(x.x);
-                  x.y = exp2_approx(x.y);
-                  sum[i & 1] = add2(sum[i & 1], x);
-                  w[i] = pack_bf16x2(x.x, x.y);
-                }
-                tmem_st16(s_at + 16 * c, w);
-              }
-              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
               tmem_st_wait();
             }
             tc_fence_before();
