@@ -52,59 +52,60 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
+template <int D, bool FP8, bool INTER, int TOKENS>
+__global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kPer = D / 16;  // threads per head
-  const int t = blockIdx.x;
-  __shared__ int s_pos, s_page;
+  const int t0 = blockIdx.x * TOKENS, tid = threadIdx.x, lane = tid & 31;
+  __shared__ int s_pos[TOKENS], s_page[TOKENS];
+  const PagedArgs& p = a.p;
+  const int nq = a.q ? a.Hq : 0;
+  const int units = (nq + 2 * p.Hk) * kPer;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // The token's request: the last one whose first row is at or before t.
-  const PagedArgs& p = a.p;
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 256) {
-    const int b = b0 + threadIdx.x;
-    before += __syncthreads_count(b < p.B && p.cu_q[b + 1] <= t);
-  }
-  if (threadIdx.x == 0) {
+  // a warp looks up each token's place
+  if (tid < 32 * TOKENS) {
+    const int t = t0 + (tid >> 5);
+    // its request: as many requests end at or before row t as precede it
+    int b = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const bool before = b0 + lane < p.B && p.cu_q[b0 + lane + 1] <= t;
+      b += __popc(__ballot_sync(~0u, before));
+    }
     int pos = -1, page = -1;
-    if (before < p.B && t >= p.cu_q[before]) {
-      const Request r = load_request(p, before);
+    if (t < p.T && b < p.B && t >= p.cu_q[b]) {
+      const Request r = load_request(p, b);
       if (t - r.row0 < r.n) {
         pos = r.kv - r.n + (t - r.row0);
         const bool in = pos >= 0 && (a.rot == 0 || pos < a.rope_rows);
-        if (in) page = p.table[(long long)before * p.table_stride + (pos >> p.page_shift)];
+        if (in) page = p.table[(long long)b * p.table_stride + (pos >> p.page_shift)];
         if (!in || page < 0 || page >= p.pages) {
           record_error(p.err, LOWBIT_ERR_INVALID_ARG);
           pos = -1;
         }
       }
     }
-    s_pos = pos;
-    s_page = page;
+    if (lane == 0) s_pos[tid >> 5] = pos, s_page[tid >> 5] = page;
   }
   __syncthreads();
-  const int pos = s_pos;
-  if (pos < 0) return;
-  const long long slot = (long long)s_page * p.page_stride + (long long)(pos & p.page_mask) * p.token_stride;
-  const float* row = a.rope + (long long)pos * a.rot;
 
-  const int nq = a.q ? a.Hq : 0;
-  const int units = (nq + 2 * p.Hk) * kPer;
-  for (int u = threadIdx.x; u < units; u += 256) {
+#pragma unroll 2
+  for (int i = tid; i < units * TOKENS; i += 256) {
+    const int which = TOKENS == 1 ? 0 : i / units, u = TOKENS == 1 ? i : i - which * units;
+    const int t = t0 + which, pos = s_pos[which];
+    if (pos < 0) continue;
     const int head = u / kPer, j = u % kPer;
     const int kind = head < nq ? 0 : (head < nq + p.Hk ? 1 : 2);  // q, k, v
     const int h = kind == 0 ? head : (kind == 1 ? head - nq : head - nq - p.Hk);
-    const uint16_t* src = kind == 0 ? a.q + (long long)t * a.q_stride
-                        : kind == 1 ? a.k + (long long)t * a.k_stride
-                                    : a.v + (long long)t * a.v_stride;
-    src += (long long)h * D;
+    const uint16_t* src = (kind == 0 ? a.q + (long long)t * a.q_stride
+                         : kind == 1 ? a.k + (long long)t * a.k_stride
+                                     : a.v + (long long)t * a.v_stride) + (long long)h * D;
     const bool turn = kind != 2 && 16 * j < a.rot;
-    int ia = 16 * j, ib = 16 * j + 8;
-    if (!INTER && turn) ia = 8 * j, ib = a.rot / 2 + 8 * j;
+    const int ia = !INTER && turn ? 8 * j : 16 * j, ib = !INTER && turn ? a.rot / 2 + 8 * j : 16 * j + 8;
     float x[8], y[8];
     unpack8(*reinterpret_cast<const uint4*>(src + ia), x);
     unpack8(*reinterpret_cast<const uint4*>(src + ib), y);
+    const long long slot = (long long)s_page[which] * p.page_stride + (long long)(pos & p.page_mask) * p.token_stride;
+    const float* row = a.rope + (long long)pos * a.rot;
     if (turn) {
       float c[8], s[8];
       const float4* pc = reinterpret_cast<const float4*>(row + 8 * j);
@@ -141,10 +142,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   }
 }
 
-template <int D>
+template <int D, int TOKENS>
 cudaError_t launch(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.p.T);
+  cfg.gridDim = dim3((unsigned)((a.p.T + TOKENS - 1) / TOKENS));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
@@ -153,10 +154,14 @@ cudaError_t launch(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (fp8)
-    return inter ? cudaLaunchKernelEx(&cfg, kv_append_kernel<D, true, true>, a)
-                 : cudaLaunchKernelEx(&cfg, kv_append_kernel<D, true, false>, a);
-  return inter ? cudaLaunchKernelEx(&cfg, kv_append_kernel<D, false, true>, a)
-               : cudaLaunchKernelEx(&cfg, kv_append_kernel<D, false, false>, a);
+    return inter ? cudaLaunchKernelEx(&cfg, kv_append_kernel<D, true, true, TOKENS>, a)
+                 : cudaLaunchKernelEx(&cfg, kv_append_kernel<D, true, false, TOKENS>, a);
+  return inter ? cudaLaunchKernelEx(&cfg, kv_append_kernel<D, false, true, TOKENS>, a)
+               : cudaLaunchKernelEx(&cfg, kv_append_kernel<D, false, false, TOKENS>, a);
+}
+template <int D>
+cudaError_t launch_tokens(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
+  return a.p.T > 1520 ? launch<D, 8>(a, fp8, inter, s) : launch<D, 1>(a, fp8, inter, s);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -232,8 +237,8 @@ extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, c
   a.q_out = q_out;
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3, inter = interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 64 ? launch<64>(a, fp8, inter, s)
-                      : D == 128 ? launch<128>(a, fp8, inter, s)
-                                 : launch<256>(a, fp8, inter, s);
+  const cudaError_t e = D == 64 ? launch_tokens<64>(a, fp8, inter, s)
+                      : D == 128 ? launch_tokens<128>(a, fp8, inter, s)
+                                 : launch_tokens<256>(a, fp8, inter, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }

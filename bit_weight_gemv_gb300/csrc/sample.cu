@@ -4,20 +4,23 @@
 // A weight w = exp((z - max) / T) becomes a whole number, w * 2^40 rounded, so every sum below is
 // a 64-bit integer: exact, the same in any order, and free to be taken with atomics.
 //
-// A cluster of CTAs takes one row, each a contiguous slice that stays in its shared memory, so the
-// row is read once.  Truncation keeps a prefix of the order (larger logit, then lower index):
+// A cluster of CTAs takes one row, each a contiguous slice.  Few rows: up to 16 CTAs, whose slices
+// stay in their shared memory, so the row is read once.  Many rows: four CTAs read theirs again for
+// each pass, from L2, which holds the rows in flight; the exchanges between passes then cost a
+// larger part of the GPU nothing.  Truncation keeps a prefix of the order (larger logit, then lower index):
 //   1. the largest logit, over the cluster;
 //   2. with top-p alone, the whole mass S.  What stays ends among the weights above (1 - p) S / V,
 //      since the others sum to (1 - p) S at most, so only those are looked at further;
 //   3. a histogram over 1024 equal steps of (max - z) / T (28.5 covers every weight that does not
 //      round to zero) of counts, or of counts and masses, merged over the cluster: the step in
 //      which the prefix ends, and how many tokens (n) lie up to it;
-//   4. n <= 2048, nearly always: those tokens go to the first CTA, which sorts them (grouped by
-//      step already, so a token is only compared with its own step's) and finishes the row;
-//      else the cut is narrowed down by the key's digits to a threshold key and the number of
-//      tokens equal to it that stay, and the draw walks the segments that the warps own.
+//   4. n <= 2048, usually: those tokens go to the first CTA, which sorts them and finishes the row;
+//      else only the tokens of that step do, which gives the threshold key and the number of tokens
+//      equal to it that stay, and the draw walks the segments that the warps own.  (A step with
+//      more than 2048 tokens, such as a row of equal logits, is narrowed down by its keys' digits.)
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -54,8 +57,7 @@ struct SampleArgs {
 };
 
 __device__ __forceinline__ float clean(float z) {
-  if (!(z >= -INFINITY)) z = -INFINITY;     // NaN
-  return fminf(z, 3.402823466e38f) + 0.0f;  // -0 becomes +0
+  return fminf(fmaxf(z, -INFINITY), 3.402823466e38f) + 0.0f;  // NaN to -inf, -0 to +0
 }
 // Ascending with descending z, and back.
 __device__ __forceinline__ uint32_t down_key(float z) {
@@ -66,7 +68,7 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k : ~k & 0x7FFFFFFFu);
 }
 __device__ __forceinline__ float weight_of(float z, float top, float rate) {
-  return z == -INFINITY ? 0.0f : expf((z - top) * rate);
+  return expf((z - top) * rate);  // top is finite: -inf gives 0
 }
 // w * 2^40 rounded, as hi * 2^20 + lo: both parts are taken by adding 1.5 * 2^23, which leaves the
 // rounded integer in the low bits; the remainder between them is exact.
@@ -90,16 +92,16 @@ struct Shared {
   uint32_t count[kBins], lo[kBins], hi[kBins];  // this CTA's histogram; the mass in two words
   uint32_t all_count[kBins];                    // the cluster's
   u64 all_mass[kBins];
-  u64 cand[kCap];                               // first CTA: key << 32 | index, grouped by step
+  u64 cand[kCap];                               // key << 32 | index: this CTA's, then in the first one all
   u64 warp_mass[kWarps], warp_tie[kWarps];
   uint32_t warp_count[kWarps], warp_ties[kWarps];
   float warp_max[kWarps], rank_max[kMaxCluster];
   u64 rank_mass[kMaxCluster], rank_tie[kMaxCluster], rank_total[kMaxCluster];
-  uint32_t rank_count[kMaxCluster], rank_ties[kMaxCluster];
+  uint32_t rank_count[kMaxCluster], rank_ties[kMaxCluster], rank_cand[kMaxCluster];
   // the bin that a search found, and what precedes it
   int bin, found;
-  uint32_t count_before, kept;
-  u64 mass_before, total, kept_mass;
+  uint32_t count_before, cut, stay;
+  u64 mass_before, one;
 };
 
 __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, u64 v) {
@@ -153,9 +155,9 @@ __device__ __forceinline__ void add_mass(Shared& s, int bin, u64 mass) {
   if (up) atomicAdd(&s.hi[bin], up);
 }
 // The first bin with (count up to it) >= k, or with (mass up to it) >= limit, and what precedes
-// it; s.bin = kBins if there is none, with the whole count and mass.  Turns all_count into the
-// counts that precede each bin when `prefix`.  All threads; the results are ready after it.
-__device__ __noinline__ void find_bin(Shared& s, bool by_mass, uint32_t k, u64 limit, bool prefix) {
+// it; s.bin = kBins if there is none, with the whole count and mass.  All threads; the results are
+// ready after it.
+__device__ __noinline__ void find_bin(Shared& s, bool by_mass, uint32_t k, u64 limit) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t c0 = s.all_count[2 * tid], c1 = s.all_count[2 * tid + 1];
   const u64 m0 = by_mass ? s.all_mass[2 * tid] : 0, m1 = by_mass ? s.all_mass[2 * tid + 1] : 0;
@@ -180,7 +182,6 @@ __device__ __noinline__ void find_bin(Shared& s, bool by_mass, uint32_t k, u64 l
     s.mass_before = mb + m0 + m1;
     s.found = 0;
   }
-  if (prefix) s.all_count[2 * tid] = cb, s.all_count[2 * tid + 1] = cb + c0;
   __syncthreads();
 }
 
@@ -201,52 +202,77 @@ __device__ __forceinline__ void finish(const SampleArgs& a, int m, int i, u64 ma
   if (a.kept) a.kept[m] = (int32_t)kept;
 }
 
-template <bool BF16>
-struct Slice;
-template <>
-struct Slice<false> {
-  const float* at;
+// Four neighbouring logits of a slice, by their place in it: from shared memory (places past the
+// row hold -inf), or from the row itself.
+template <bool BF16, bool HELD>
+struct Slice {
+  const uint8_t* at;   // HELD: the slice in shared memory; else the slice in the row
+  int end;             // places of the slice inside the row
+  int aligned;
   __device__ __forceinline__ void get4(int i, float (&z)[4]) const {
-    const float4 v = *reinterpret_cast<const float4*>(at + i);
-    z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
-  }
-};
-template <>
-struct Slice<true> {
-  const uint16_t* at;
-  __device__ __forceinline__ void get4(int i, float (&z)[4]) const {
-    const uint2 v = *reinterpret_cast<const uint2*>(at + i);
-    z[0] = clean(__uint_as_float(v.x << 16)), z[1] = clean(__uint_as_float(v.x & 0xFFFF0000u));
-    z[2] = clean(__uint_as_float(v.y << 16)), z[3] = clean(__uint_as_float(v.y & 0xFFFF0000u));
+    if (HELD && !BF16) {
+      const float4 v = *reinterpret_cast<const float4*>(at + 4 * i);
+      z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+      return;
+    }
+    if (HELD || (aligned && i + 4 <= end)) {
+      if (BF16) {
+        const uint2 v = HELD ? *reinterpret_cast<const uint2*>(at + 2 * i) : __ldg(reinterpret_cast<const uint2*>(at + 2 * i));
+        z[0] = __uint_as_float(v.x << 16), z[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        z[2] = __uint_as_float(v.y << 16), z[3] = __uint_as_float(v.y & 0xFFFF0000u);
+      } else {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(at + 4 * i));
+        z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[e] = -INFINITY;
+        if (i + e < end)
+          z[e] = BF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(at) + i + e))
+                      : __ldg(reinterpret_cast<const float*>(at) + i + e);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = clean(z[e]);
   }
 };
 
-// The first CTA's end of a row: n candidates, grouped by step (all_count holds where each step
-// begins), of which top-k, top-p and min-p keep a part; then the draw in index order.
-__device__ __forceinline__ void finish_candidates(const SampleArgs& a, Shared& s, ulonglong2* sorted, int m, uint32_t n,
-                                                  int last_bin, uint32_t k, float p, u64 whole, float floor_w,
-                                                  float top, float rate, float steps, float u) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // rank inside the step, then the sorted place
-  for (uint32_t i = tid; i < n; i += kThreads) {
-    const u64 c = s.cand[i];
-    const float z = key_logit((uint32_t)(c >> 32));
-    const int bin = step_of(z, top, steps);
-    const uint32_t from = s.all_count[bin], to = bin == last_bin ? n : s.all_count[bin + 1];
-    uint32_t r = from;
-    for (uint32_t j = from; j < to; ++j) r += s.cand[j] < c;
-    sorted[r] = make_ulonglong2(c, mass_of(weight_of(z, top, rate)));
-  }
-  for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
+// Sorts the first n of s.cand (larger logit, then lower index, first), by all threads.
+__device__ __noinline__ void sort_candidates(Shared& s, uint32_t n) {
+  uint32_t size = 2;
+  while (size < n) size *= 2;
+  for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) s.cand[i] = ~0ull;
   __syncthreads();
+  // bitonic: pairs (i, i + half) of runs that ascend where bit `run` of i is clear
+#pragma unroll 1
+  for (uint32_t run = 2; run <= size; run *= 2)
+#pragma unroll 1
+    for (uint32_t half = run / 2; half; half /= 2) {
+      for (uint32_t t = threadIdx.x; t < size / 2; t += kThreads) {
+        const uint32_t i = 2 * t - (t & (half - 1));
+        const u64 x = s.cand[i], y = s.cand[i + half];
+        if ((x > y) == ((i & run) == 0)) s.cand[i] = y, s.cand[i + half] = x;
+      }
+      __syncthreads();
+    }
+}
+
+// The first CTA's end of a row: n sorted candidates, of which top-k, top-p and min-p keep a part;
+// then the draw in index order.
+__device__ __forceinline__ void finish_candidates(const SampleArgs& a, Shared& s, ulonglong2* list, int m, uint32_t n,
+                                                  uint32_t k, float p, u64 whole, float floor_w, float top, float rate,
+                                                  float u) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
   // masses before each place; a thread takes four places in a row
   constexpr int kOwn = kCap / kThreads;
   u64 c[kOwn], q[kOwn], sum = 0;
 #pragma unroll
   for (int e = 0; e < kOwn; ++e) {
     const uint32_t i = tid * kOwn + e;
-    const ulonglong2 v = i < n ? sorted[i] : make_ulonglong2(0, 0);
-    c[e] = v.x, q[e] = i < k ? v.y : 0;
+    c[e] = i < n ? s.cand[i] : 0;
+    q[e] = i < n && i < k ? mass_of(weight_of(key_logit((uint32_t)(c[e] >> 32)), top, rate)) : 0;
     sum += q[e];
   }
   const u64 incl = warp_incl(sum, lane);
@@ -299,18 +325,18 @@ __device__ __forceinline__ void finish_candidates(const SampleArgs& a, Shared& s
 #pragma unroll
   for (int e = 0; e < kOwn; ++e)
     if (q[e] && (int)((uint32_t)c[e] >> shift) == bucket)
-      sorted[atomicAdd(&s.found, 1)] = make_ulonglong2(c[e] & 0xFFFFFFFFu, q[e]);
+      list[atomicAdd(&s.found, 1)] = make_ulonglong2(c[e] & 0xFFFFFFFFu, q[e]);
   __syncthreads();
   const int found = s.found;
   for (int i = tid; i < found; i += kThreads) {
-    const ulonglong2 v = sorted[i];
+    const ulonglong2 v = list[i];
     u64 b = base;
-    for (int j = 0; j < found; ++j) b += sorted[j].x < v.x ? sorted[j].y : 0;
+    for (int j = 0; j < found; ++j) b += list[j].x < v.x ? list[j].y : 0;
     if (aim >= b && aim < b + v.y) finish(a, m, (int)v.x, v.y, total, kept);
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool HELD>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
@@ -321,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int local = warp * a.per_warp + lane * 4;              // this lane's first place in the slice
   const int local_end = (warp + 1) * a.per_warp;
   const int index0 = rank * kWarps * a.per_warp;               // of the slice's first element
+  cluster_arrive();  // this CTA runs: the others may write its shared memory
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // the row's settings, asked for before the slice
@@ -337,8 +364,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // ---- the slice comes in, and its largest logit; places past the row hold -inf
   float top = -INFINITY;
-  {
-    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + (long long)m * a.row_stride * kSize;
+  const uint8_t* const row = static_cast<const uint8_t*>(a.logits) + (long long)m * a.row_stride * kSize;
+  const Slice<BF16, HELD> z_of = {HELD ? store : row + (long long)index0 * kSize, max(0, a.V - index0), a.aligned};
+  if (!HELD) {
+#pragma unroll 4
+    for (int i = local; i < local_end; i += 128) {
+      float z[4];
+      z_of.get4(i, z);
+      top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));
+    }
+  } else {
     constexpr int kVec = 16 / kSize;                           // elements of a 16-byte load
     const int first = warp * a.per_warp;
     if (a.aligned) {
@@ -391,18 +426,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
   }
-  Slice<BF16> z_of;
-  z_of.at = reinterpret_cast<decltype(z_of.at)>(store);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) s.warp_max[warp] = top;
   clear_histogram(s);
 
-  cluster_sync();  // every CTA of the cluster runs before its shared memory is written
+  __syncthreads();
   if (warp == 0) {
     top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (lane < C) st_dsmem_f32(map_to_rank(smem_addr(&s.rank_max[rank]), lane), top);
   }
+  cluster_wait();
+  if (warp == 0 && lane < C) st_dsmem_f32(map_to_rank(smem_addr(&s.rank_max[rank]), lane), top);
   cluster_sync();
   top = lane < C ? s.rank_max[lane] : -INFINITY;
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -415,11 +449,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return;
   }
 
-  // Kept mass of this warp's segment when tokens with key < cut stay, and those equal to it are
-  // counted apart; floor_min drops smaller weights.
+  // Kept mass of this warp's segment: without a cut, or of the tokens with key < cut, those equal
+  // to it counted apart; floor_min drops smaller weights.
   u64 seg_mass, seg_tie;
   uint32_t seg_count, seg_ties;
-  auto segment = [&](uint32_t cut, float floor_min) {
+  struct Whole {};  // every token, and no count
+  auto segment = [&](auto with_cut, uint32_t cut, float floor_min) {
+    constexpr bool kCut = std::is_same<decltype(with_cut), std::true_type>::value;
+    constexpr bool kWhole = std::is_same<decltype(with_cut), Whole>::value;
     uint32_t hi = 0, count = 0, ties = 0;
     int lo = 0;
     u64 tie = 0;
@@ -429,27 +466,76 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       z_of.get4(i, z);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t key = down_key(z[e]);
         const float w = weight_of(z[e], top, rate);
         uint32_t h, l;
         split_mass(w, h, l);
-        if (key > cut || w < floor_min) h = l = 0;
-        if (key == cut) {
-          ++ties;
-          tie = (u64)(((long long)(int)h << 20) + (int)l);
-        } else {
-          hi += h, lo += (int)l, count += (h | l) != 0;  // at most 2^9 tokens per lane: 32 bits hold the sums
+        if (!kWhole && w < floor_min) h = l = 0;
+        if (kCut) {
+          const uint32_t key = down_key(z[e]);
+          if (key == cut) ++ties, tie = (u64)(((long long)(int)h << 20) + (int)l);
+          if (key >= cut) h = l = 0;
         }
+        hi += h, lo += (int)l;
+        if (!kWhole) count += (h | l) != 0;  // at most 2^8 tokens per lane: 32 bits hold the sums
       }
     }
     seg_mass = warp_sum((u64)(((long long)hi << 20) + lo));
-    for (int o = 16; o; o >>= 1) {
-      count += __shfl_xor_sync(~0u, count, o);
-      ties += __shfl_xor_sync(~0u, ties, o);
-      const u64 x = __shfl_xor_sync(~0u, tie, o);
-      tie = x > tie ? x : tie;
+    count = __reduce_add_sync(~0u, count);
+    seg_ties = 0, seg_tie = 0;
+    if (kCut) {
+      seg_ties = __reduce_add_sync(~0u, ties);
+      for (int o = 16; o; o >>= 1) {
+        const u64 x = __shfl_xor_sync(~0u, tie, o);
+        tie = x > tie ? x : tie;
+      }
+      seg_tie = tie;
     }
-    seg_count = count, seg_ties = ties, seg_tie = tie;
+    seg_count = count;
+  };
+  // The cluster's sum of seg_mass; once per row.
+  auto cluster_mass = [&]() {
+    if (lane == 0) s.warp_mass[warp] = seg_mass;
+    __syncthreads();
+    if (warp == 0) {
+      const u64 sum = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
+      if (lane < C) st_dsmem_u64(map_to_rank(smem_addr(&s.rank_total[rank]), lane), sum);
+    }
+    cluster_sync();
+    u64 sum = 0;
+    for (int r = 0; r < C; ++r) sum += s.rank_total[r];
+    return sum;
+  };
+  // Tokens of steps from..to (logits >= low) into the first CTA's list, up to kCap of them.
+  auto gather = [&](int from, int to, float low) {
+    low = fmaxf(low, top - (float)(to + 2) / steps);  // a step's width below the last one's end
+    __syncthreads();  // s.found has been read
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = local; i < local_end; i += 128) {
+      float z[4];
+      z_of.get4(i, z);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(z[e] >= low)) continue;
+        const int b = step_of(z[e], top, steps);
+        if (b < from || b > to) continue;
+        const uint32_t at = atomicAdd(&s.found, 1);
+        if (at < kCap) s.cand[at] = ((u64)down_key(z[e]) << 32) | (uint32_t)(index0 + i + e);
+      }
+    }
+    __syncthreads();
+    const uint32_t mine = min((uint32_t)s.found, (uint32_t)kCap);
+    if (tid < C) st_dsmem_u32(map_to_rank(smem_addr(&s.rank_cand[rank]), tid), mine);
+    cluster_sync();
+    if (rank) {
+      uint32_t at = 0;
+      for (int r = 0; r < rank; ++r) at += s.rank_cand[r];
+      const uint32_t cand = map_to_rank(smem_addr(s.cand), 0);
+      for (uint32_t i = tid; i < mine; i += kThreads)
+        if (at + i < kCap) st_dsmem_u64(cand + 8 * (at + i), s.cand[i]);
+    }
+    cluster_sync();
   };
 
   uint32_t cut = 0xFFFFFFFFu, r_keep = 0xFFFFFFFFu;  // tokens past the row have this key, and no mass
@@ -459,15 +545,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 whole = 0, limit = 0;
     float low = -INFINITY;  // logits below it are not looked at
     if (!by_count) {
-      segment(0xFFFFFFFEu, 0.0f);
-      if (lane == 0) s.warp_mass[warp] = seg_mass;
-      __syncthreads();
-      if (warp == 0) {
-        const u64 sum = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
-        if (lane < C) st_dsmem_u64(map_to_rank(smem_addr(&s.rank_total[rank]), lane), sum);
-      }
-      cluster_sync();
-      for (int r = 0; r < C; ++r) whole += s.rank_total[r];
+      segment(Whole(), 0, 0.0f);
+      whole = cluster_mass();
       limit = top_p_limit(p, whole);
       // weights up to (1 - p) S / V: half of it, for the roundings on the way
       const float tau = 0.5f * (1.0f - p) * ((float)whole * 0x1p-40f) / (float)a.V;
@@ -490,39 +569,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     }
     merge_histograms(s, C, rank, !by_count);
-    find_bin(s, !by_count, k, limit, true);
+    find_bin(s, !by_count, k, limit);
     int bin = s.bin;
     uint32_t count_before = s.count_before;
     u64 mass_before = s.mass_before;
     const uint32_t n = count_before + s.found;
     if (n <= kCap) {
-      // ---- the candidates go to the first CTA
-      const int last = bin < kBins ? bin : kBins - 2;
-      for (int i = tid; i < kBins; i += kThreads) s.hi[i] = 0;  // the first CTA's: taken places of a step
-      cluster_sync();
-      const uint32_t taken = map_to_rank(smem_addr(s.hi), 0), cand = map_to_rank(smem_addr(s.cand), 0);
-#pragma unroll 1
-      for (int i = local; i < local_end; i += 128) {
-        float z[4];
-        z_of.get4(i, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!(z[e] >= low)) continue;
-          const int b = step_of(z[e], top, steps);
-          if (b > last) continue;
-          uint32_t place;
-          asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(place) : "r"(taken + 4 * b) : "memory");
-          place += s.all_count[b];
-          if (place < kCap) st_dsmem_u64(cand + 8 * place, ((u64)down_key(z[e]) << 32) | (uint32_t)(index0 + i + e));
-        }
+      gather(0, bin < kBins ? bin : kBins - 2, low);  // after it no CTA touches another's memory
+      if (rank == 0) {
+        sort_candidates(s, n);
+        finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, n, k, p, whole, floor_w, top, rate, u);
       }
-      cluster_sync();  // the last exchange: no CTA touches another's memory after it
-      if (rank == 0)
-        finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, n, last, k, p, whole, floor_w, top, rate, steps, u);
       return;
     }
 
-    // ---- too many: narrow the cut down by digits of the key
+    // ---- too many: the cut itself, for top-k and then for top-p
     u64 total = whole;
 #pragma unroll 1
     for (int turn = by_count ? 0 : 1; turn < 2; ++turn) {
@@ -543,80 +604,109 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             }
           }
           merge_histograms(s, C, rank, true);
-          find_bin(s, true, 0, limit, false);
+          find_bin(s, true, 0, limit);
           bin = s.bin, count_before = s.count_before, mass_before = s.mass_before;
         }
       }
       if (bin == kBins) {  // fewer than k tokens have mass: top-k cuts nothing
         __syncthreads();
         if (turn == 0 && !(p >= 1.0f)) {
-          segment(0xFFFFFFFEu, 0.0f);
-          if (lane == 0) s.warp_mass[warp] = seg_mass;
-          __syncthreads();
-          if (warp == 0) {
-            const u64 sum = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
-            if (lane < C) st_dsmem_u64(map_to_rank(smem_addr(&s.rank_total[rank]), lane), sum);
-          }
-          cluster_sync();
-          total = 0;
-          for (int r = 0; r < C; ++r) total += s.rank_total[r];
+          segment(Whole(), 0, 0.0f);
+          total = cluster_mass();
         }
         continue;
       }
-      // among the tokens of the step: digits of 10, 10, 10 and 2 bits
-      uint32_t prefix = 0;
       u64 one = 0;  // mass of one token at the cut
-#pragma unroll 1
-      for (int level = 0; level < 4; ++level) {
-        const int shift = level < 3 ? 22 - 10 * level : 0, bits = level < 3 ? 10 : 2;
-        __syncthreads();
-        clear_histogram(s);
-        __syncthreads();
-#pragma unroll 1
-        for (int i = local; i < local_end; i += 128) {
-          float z[4];
-          z_of.get4(i, z);
+      const uint32_t here = s.found;
+      if (here <= kCap) {
+        gather(bin, bin, turn == 1 ? low : -INFINITY);
+        if (rank == 0) {
+          sort_candidates(s, here);
+          // a thread takes four places in a row; masses count only for top-p
+          constexpr int kOwn = kCap / kThreads;
+          u64 q[kOwn], sum = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (step_of(z[e], top, steps) != bin) continue;
-            const uint32_t key = down_key(z[e]);
-            if (level && (key >> (shift + bits)) != prefix) continue;
-            const int d = (int)((key >> shift) & ((1u << bits) - 1));
-            atomicAdd(&s.count[d], 1u);
-            add_mass(s, d, mass_of(weight_of(z[e], top, rate)));
+          for (int e = 0; e < kOwn; ++e) {
+            const uint32_t i = tid * kOwn + e;
+            q[e] = i < here ? mass_of(weight_of(key_logit((uint32_t)(s.cand[i] >> 32)), top, rate)) : 0;
+            sum += q[e];
+          }
+          const u64 incl = warp_incl(sum, lane);
+          if (lane == 31) s.warp_mass[warp] = incl;
+          __syncthreads();
+          u64 before = mass_before + incl - sum;
+          for (int w = 0; w < warp; ++w) before += s.warp_mass[w];
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) {
+            const uint32_t i = tid * kOwn + e;
+            // the last token that stays
+            const bool ends = turn == 1 ? before < limit && before + q[e] >= limit : i + 1 == k - count_before;
+            if (i < here && ends) {
+              const uint32_t key = (uint32_t)(s.cand[i] >> 32);
+              uint32_t lo = 0, hi = i;  // the first of its equals
+              while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if ((uint32_t)(s.cand[mid] >> 32) < key) lo = mid + 1;
+                else hi = mid;
+              }
+              s.cut = key, s.stay = i - lo + 1, s.one = q[e];
+            }
+            before += q[e];
+          }
+          __syncthreads();
+          if (tid < C) {
+            st_dsmem_u32(map_to_rank(smem_addr(&s.cut), tid), s.cut);
+            st_dsmem_u32(map_to_rank(smem_addr(&s.stay), tid), s.stay);
+            st_dsmem_u64(map_to_rank(smem_addr(&s.one), tid), s.one);
           }
         }
-        merge_histograms(s, C, rank, true);
-        find_bin(s, turn == 1, k > count_before ? k - count_before : 0, limit - mass_before, false);
-        const int d = s.bin;
-        count_before += s.count_before;
-        if (turn == 1) mass_before += s.mass_before;
-        if (level == 3) one = s.all_mass[d] / s.all_count[d];  // equal keys, equal masses
-        prefix = (prefix << bits) | (uint32_t)d;
-      }
-      cut = prefix;
-      if (turn == 0) {
-        r_keep = k - count_before;
-        // S of what top-k leaves
-        segment(cut, 0.0f);
-        if (lane == 0) s.warp_mass[warp] = seg_mass;
-        __syncthreads();
-        if (warp == 0) {
-          const u64 sum = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
-          if (lane < C) st_dsmem_u64(map_to_rank(smem_addr(&s.rank_total[rank]), lane), sum);
-        }
         cluster_sync();
-        total = 0;
-        for (int r = 0; r < C; ++r) total += s.rank_total[r];
-        total += (u64)r_keep * one;
+        cut = s.cut, r_keep = s.stay, one = s.one;
       } else {
-        r_keep = (uint32_t)((limit - mass_before + one - 1) / one);
+        // digits of 10, 10, 10 and 2 bits
+        uint32_t prefix = 0;
+#pragma unroll 1
+        for (int level = 0; level < 4; ++level) {
+          const int shift = level < 3 ? 22 - 10 * level : 0, bits = level < 3 ? 10 : 2;
+          __syncthreads();
+          clear_histogram(s);
+          __syncthreads();
+#pragma unroll 1
+          for (int i = local; i < local_end; i += 128) {
+            float z[4];
+            z_of.get4(i, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (step_of(z[e], top, steps) != bin) continue;
+              const uint32_t key = down_key(z[e]);
+              if (level && (key >> (shift + bits)) != prefix) continue;
+              const int d = (int)((key >> shift) & ((1u << bits) - 1));
+              atomicAdd(&s.count[d], 1u);
+              add_mass(s, d, mass_of(weight_of(z[e], top, rate)));
+            }
+          }
+          merge_histograms(s, C, rank, true);
+          find_bin(s, turn == 1, k > count_before ? k - count_before : 0, limit - mass_before);
+          const int d = s.bin;
+          count_before += s.count_before;
+          if (turn == 1) mass_before += s.mass_before;
+          if (level == 3) one = s.all_mass[d] / s.all_count[d];  // equal keys, equal masses
+          prefix = (prefix << bits) | (uint32_t)d;
+        }
+        cut = prefix;
+        r_keep = turn == 0 ? k - count_before : (uint32_t)((limit - mass_before + one - 1) / one);
+      }
+      if (turn == 0 && !(p >= 1.0f)) {  // S of what top-k leaves
+        segment(std::true_type(), cut, 0.0f);
+        total = cluster_mass() + (u64)r_keep * one;
       }
     }
   }
 
   // ---- kept mass of every segment
-  segment(cut, floor_w);
+  if (cut == 0xFFFFFFFFu) segment(std::false_type(), 0, floor_w);
+  else segment(std::true_type(), cut, floor_w);
+  __syncthreads();
   if (lane == 0) {
     s.warp_mass[warp] = seg_mass;
     s.warp_count[warp] = seg_count;
@@ -701,25 +791,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
 }
 
-template <bool BF16>
-cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // Slices of up to 32,768 elements (128 KB in fp32), and of about 8,192 and more while the row
-  // is large enough: the phases between the exchanges then take about as long as the exchanges.
-  int C = 1;
-  while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
+template <bool BF16, bool HELD>
+cudaError_t launch(SampleArgs a, int C, cudaStream_t s) {
   a.cluster = C;
   a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128;
   a.aligned = ((uintptr_t)a.logits & 15) == 0 && (a.row_stride * (BF16 ? 2 : 4)) % 16 == 0;
-  const size_t bytes = (sizeof(Shared) + 15) / 16 * 16 +
-                       std::max((size_t)kWarps * a.per_warp * (BF16 ? 2 : 4), (size_t)kCap * 16);
+  const size_t slice = HELD ? (size_t)kWarps * a.per_warp * (BF16 ? 2 : 4) : 0;
+  const size_t bytes = (sizeof(Shared) + 15) / 16 * 16 + std::max(slice, (size_t)kCap * 16);
   static std::atomic<int> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(sample_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<BF16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(sample_kernel<BF16, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(sample_kernel<BF16, HELD>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready[dev].store(1, std::memory_order_relaxed);
   }
@@ -736,7 +823,21 @@ cudaError_t launch(SampleArgs a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, HELD>, a);
+}
+
+template <bool BF16>
+cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
+  // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but past what is
+  // resident at once (about 320 CTAs) rows wait for rows, and four CTAs a row keep the GPU busier
+  // than 16.  V = 248,320, top-k 20 and top-p: one row 17 us on 16 CTAs, 41 on four; 48 rows 65 us on
+  // 16, 61 on eight, 52 on four; 128 rows 149, 124, 104, and 125 us on two.
+  int C = 1;
+  while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
+  while (C > 4 && (long long)C * a.M > 320) C /= 2;
+  // held while two CTAs share an SM: 128 rows on 16 CTAs each take 149 us, 193 us read from L2
+  const long long slice = (long long)((a.V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128 * kWarps * (BF16 ? 2 : 4);
+  return slice <= 65536 ? launch<BF16, true>(a, C, s) : launch<BF16, false>(a, C, s);
 }
 
 }  // namespace
@@ -757,6 +858,6 @@ extern "C" lowbit_status lowbit_sample(const void* logits, int dtype, int64_t ro
   if ((uintptr_t)logits & (dtype == LOWBIT_LOGITS_BF16 ? 1 : 3) || words & 3) return LOWBIT_ERR_ALIGN;
   const SampleArgs a = {logits, row_stride, M, V, 1, 0, 0, temperature, top_k, top_p, min_p, u, id_map, ids, logprob, kept};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == LOWBIT_LOGITS_BF16 ? launch<true>(a, s) : launch<false>(a, s);
+  const cudaError_t e = dtype == LOWBIT_LOGITS_BF16 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
