@@ -58,26 +58,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
       : "r"(taddr)
       : "memory");
 }
-// D[tmem] (+)= A[smem] x B[smem]^T, issued by one thread.
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A x B^T with A in shared memory, or in tensor memory, issued by one thread.  Matrix
+// descriptors are passed as their low words beside constant high words: the thread that issues has
+// 64 cycles per MMA (128 x 128 x 16), and building 64-bit descriptors for each took it 90 to 110.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Matrix descriptor of an operand whose reduction runs over rows of 128 bytes (64 elements of the
-// other dimension, 128-byte swizzle): 8-row groups 1024 bytes apart, the next 64 elements
-// `half_bytes` on.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t half_bytes) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(half_bytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+__device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Both kinds of descriptor have 128-byte rows under the 128-byte swizzle, in 8-row groups 1024
+// bytes apart.  The low word holds the address and, where the reduction runs over rows (V), the
+// distance to the next 64 elements of the other dimension.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t half_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((half_bytes >> 4) << 16);
 }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -216,13 +223,16 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       int stage = 0;
       uint32_t phase = 0;
       uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      // low descriptor words of the queries, and of ring stage 0 as K and as V
+      const uint32_t q_lo = desc_lo(q_at, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, kTcBN * 128);
       auto qk = [&](int slot, int st) {
         if (lane == 0) {
-          const uint32_t qa = q_at + (PAIR ? slot * C::kTile : 0), kb = ring + st * C::kTile;
+          const uint32_t qa = q_lo + (PAIR ? slot * (C::kTile >> 4) : 0), kb = k_lo + st * (C::kTile >> 4);
+          const uint32_t d = tmem + C::kS + 128 * slot;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
-            umma_ss(tmem + C::kS + 128 * slot, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), kIdQK, k > 0);
+            const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+            umma_ss(d, qa + off, kb + off, kDescHi, kIdQK, k > 0);
           }
           umma_commit(smem_addr(&sh.s_full[slot]));
         }
@@ -230,11 +240,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       };
       auto pv = [&](int slot, int st, bool add) {
         if (lane == 0) {
-          const uint32_t vb = ring + st * C::kTile;
+          const uint32_t vb = v_lo + st * (C::kTile >> 4);
+          const uint32_t d = tmem + C::kO + D * slot, pa = tmem + C::kS + 128 * slot;
+          umma_ts_lo(d, pa, vb, kDescHi, kIdPV, add);
 #pragma unroll
-          for (int k = 0; k < kTcBN / 16; ++k)
-            umma_ts(tmem + C::kO + D * slot, tmem + C::kS + 128 * slot + 8 * k,
-                    smem_desc_mn(vb + k * 2048, kTcBN * 128), kIdPV, add || k > 0);
+          for (int k = 1; k < kTcBN / 16; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1);
         }
         __syncwarp();
       };
