@@ -41,7 +41,7 @@ struct Tc {
 
 struct TcShared {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t joined, left;  // both slots' statistics are written; both slots have read both O
   uint32_t tmem;
 };
@@ -140,6 +140,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), PAIR ? 128 : 256);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
+      mbar_init(smem_addr(&sh.p_half[i]), 128);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
     }
@@ -238,13 +239,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         }
         __syncwarp();
       };
-      auto pv = [&](int slot, int st, bool add) {
+      // four of the tile's eight steps of 16 keys
+      auto pv_half = [&](int slot, int st, int half, bool add) {
         if (lane == 0) {
-          const uint32_t vb = v_lo + st * (C::kTile >> 4);
-          const uint32_t d = tmem + C::kO + D * slot, pa = tmem + C::kS + 128 * slot;
+          const uint32_t vb = v_lo + st * (C::kTile >> 4) + half * (4 * 2048 >> 4);
+          const uint32_t d = tmem + C::kO + D * slot, pa = tmem + C::kS + 128 * slot + 32 * half;
           umma_ts_lo(d, pa, vb, kDescHi, kIdPV, add);
 #pragma unroll
-          for (int k = 1; k < kTcBN / 16; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1);
+          for (int k = 1; k < 4; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1);
         }
         __syncwarp();
       };
@@ -294,23 +296,23 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           int st = next_tile();
           if (!ok) break;
           for (int s = 0; s < slots; ++s) qk(s, st);
-          commit(sh.kv_empty[st]);
           for (int j = 0; j < n && ok; ++j) {
             const int sv = next_v(key_first + j * kTcBN);
             int sk = 0;
             for (int s = 0; s < slots && ok; ++s) {
+              WAIT_OR(sh.p_half[s], p_phase[s], { ok = false; break; });
+              tc_fence_after();
+              pv_half(s, sv, 0, j > 0);
               WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
               p_phase[s] ^= 1;
               tc_fence_after();
-              pv(s, sv, j > 0);
-              if (s == slots - 1) commit(sh.kv_empty[sv]);
+              pv_half(s, sv, 1, true);
               if (j + 1 == n) {
                 commit(sh.o_full[s]);
               } else {
                 if (s == 0) sk = next_tile();
                 if (!ok) break;
                 qk(s, sk);
-                if (s == slots - 1) commit(sh.kv_empty[sk]);
               }
             }
           }
@@ -328,7 +330,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
             p_phase[s] ^= 1;
             tc_fence_after();
-            pv(s, sv, j > 1);
+            pv_half(s, sv, 0, j > 1);
+            pv_half(s, sv, 1, true);
             commit(sh.kv_empty[sv]);
             if (j + 2 < n) {
               const int st = next_tile();
@@ -361,6 +364,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       // a scale of zero keeps masked scores at -inf
       const float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
       uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
+      int rel = 0;  // PAIR: ring stage that is released next
       bool first = true, ok = true;
       for (;;) {
         const int kt0 = it.tile, n = walk_take(it, left);
@@ -368,6 +372,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         const int rows = it.q.n * G, r0 = it.qt * kRows;
         const int r_tile = r0 + (PAIR ? slot * 128 : 0);
         const bool active = r_tile < rows;
+        // PAIR: a commit of the MMA thread costs the tensor pipe about 120 cycles, so the tiles are
+        // not released by commits of their own: when the last active slot's scores of tile j have
+        // come, K of tile j and V of tile j - 1 have been read.
+        const bool frees = PAIR && t128 == 0 && (slot == 1 || rows - r0 <= 128);
+        auto release = [&]() {
+          if (frees) mbar_arrive(smem_addr(&sh.kv_empty[rel]));
+          if (++rel == S) rel = 0;
+        };
         const int key_first = it.span.lo / kTcBN * kTcBN + kt0 * kTcBN;
 
         // Q rows into shared memory (swizzled as TMA would leave them)
@@ -415,6 +427,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             WAIT_OR(sh.s_full[slot], s_phase, { ok = false; break; });
             s_phase ^= 1;
             tc_fence_after();
+            if (PAIR) {
+              release();
+              if (j > 0) release();
+            }
             const int key0 = key_first + j * kTcBN;
             // the maximum grew: l and (past the slot's first tile) O follow the new reference
             auto refer = [&](float top) {
@@ -473,8 +489,17 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               }
               refer(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * coef);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) weigh(s + 32 * c, c);
+              for (int c = 0; c < 4; ++c) {
+                weigh(s + 32 * c, c);
+                if (c == 1) {  // the first half's products start while the second is weighed
+                  tmem_st_wait();
+                  tc_fence_before();
+                  mbar_arrive(smem_addr(&sh.p_half[slot]));
+                }
+              }
               tmem_st_wait();
+            } else if (PAIR) {
+              mbar_arrive(smem_addr(&sh.p_half[slot]));
             } else if (work) {
               // 32 scores at a time, read once for the maximum and once for the weights, in a loop
               // that stays rolled: unrolled, a call's first tile waited 5 us for its instructions
@@ -514,6 +539,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           if (active && ok) {
             WAIT_OR(sh.o_full[slot], o_phase, ok = false);
             o_phase ^= 1;
+            release();
+          } else {
+            rel = (rel + 2 * n) % S;
           }
         } else if (ok) {
           ml[128 * slot + row] = make_float2(m, l);
