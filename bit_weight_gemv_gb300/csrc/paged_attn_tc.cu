@@ -62,21 +62,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
 // descriptors are passed as their low words beside constant high words: the thread that issues has
 // 64 cycles per MMA (128 x 128 x 16), and building 64-bit descriptors for each took it 90 to 110.
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
-                                        uint32_t accumulate) {
+                                        uint32_t accumulate, uint32_t issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(issue)
       : "memory");
 }
 __device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
-                                           uint32_t accumulate) {
+                                           uint32_t accumulate, uint32_t issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(issue)
       : "memory");
 }
 // Both kinds of descriptor have 128-byte rows under the 128-byte swizzle, in 8-row groups 1024
@@ -226,28 +226,27 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
       // low descriptor words of the queries, and of ring stage 0 as K and as V
       const uint32_t q_lo = desc_lo(q_at, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, kTcBN * 128);
+      const uint32_t one = lane == 0;
       auto qk = [&](int slot, int st) {
-        if (lane == 0) {
-          const uint32_t qa = q_lo + (PAIR ? slot * (C::kTile >> 4) : 0), kb = k_lo + st * (C::kTile >> 4);
-          const uint32_t d = tmem + C::kS + 128 * slot;
+        st = __shfl_sync(~0u, st, 0);
+        const uint32_t qa = q_lo + (PAIR ? slot * (C::kTile >> 4) : 0), kb = k_lo + st * (C::kTile >> 4);
+        const uint32_t d = C::kS + 128 * slot;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
-            umma_ss(d, qa + off, kb + off, kDescHi, kIdQK, k > 0);
-          }
-          umma_commit(smem_addr(&sh.s_full[slot]));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+          umma_ss(d, qa + off, kb + off, kDescHi, kIdQK, k > 0, one);
         }
+        if (one) umma_commit(smem_addr(&sh.s_full[slot]));
         __syncwarp();
       };
       // four of the tile's eight steps of 16 keys
       auto pv_half = [&](int slot, int st, int half, bool add) {
-        if (lane == 0) {
-          const uint32_t vb = v_lo + st * (C::kTile >> 4) + half * (4 * 2048 >> 4);
-          const uint32_t d = tmem + C::kO + D * slot, pa = tmem + C::kS + 128 * slot + 32 * half;
-          umma_ts_lo(d, pa, vb, kDescHi, kIdPV, add);
+        st = __shfl_sync(~0u, st, 0);
+        const uint32_t vb = v_lo + st * (C::kTile >> 4) + half * (4 * 2048 >> 4);
+        const uint32_t d = C::kO + D * slot, pa = C::kS + 128 * slot + 32 * half;
+        umma_ts_lo(d, pa, vb, kDescHi, kIdPV, add, one);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1);
-        }
+        for (int k = 1; k < 4; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1, one);
         __syncwarp();
       };
       auto commit = [&](uint64_t& bar) {
@@ -299,7 +298,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           for (int j = 0; j < n && ok; ++j) {
             const int sv = next_v(key_first + j * kTcBN);
             int sk = 0;
-            for (int s = 0; s < slots && ok; ++s) {
+            _Pragma("unroll")
+            for (int s = 0; s < 2; ++s) {
+              if (s >= slots || !ok) break;
               WAIT_OR(sh.p_half[s], p_phase[s], { ok = false; break; });
               tc_fence_after();
               pv_half(s, sv, 0, j > 0);
