@@ -15,6 +15,8 @@
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
 // since the value the weights refer to, so most tiles never touch it (weights up to 2^8 round to
 // bf16 with the same relative error, and sums are fp32).
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.cuh"
 #include "paged_attn.cuh"
@@ -41,7 +43,7 @@ struct Tc {
 
 struct TcShared {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t joined, left;  // both slots' statistics are written; both slots have read both O
   uint32_t tmem;
 };
@@ -89,6 +91,11 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t half_bytes)
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -140,7 +147,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), PAIR ? 128 : 256);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_half[i]), 128);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
     }
@@ -160,7 +166,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = sh.tmem;  // an allocation of all 512 columns starts at 0, which the MMA warp builds on
   const int G = a.shape.G;
 
   if (busy) {
@@ -228,7 +234,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       const uint32_t q_lo = desc_lo(q_at, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, kTcBN * 128);
       const uint32_t one = lane == 0;
       auto qk = [&](int slot, int st) {
-        st = __shfl_sync(~0u, st, 0);
+        st = __shfl_sync(~0u, st, 0);  // uniform for the compiler too
         const uint32_t qa = q_lo + (PAIR ? slot * (C::kTile >> 4) : 0), kb = k_lo + st * (C::kTile >> 4);
         const uint32_t d = C::kS + 128 * slot;
 #pragma unroll
@@ -239,14 +245,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         if (one) umma_commit(smem_addr(&sh.s_full[slot]));
         __syncwarp();
       };
-      // four of the tile's eight steps of 16 keys
-      auto pv_half = [&](int slot, int st, int half, bool add) {
+      auto pv = [&](int slot, int st, bool add) {
         st = __shfl_sync(~0u, st, 0);
-        const uint32_t vb = v_lo + st * (C::kTile >> 4) + half * (4 * 2048 >> 4);
-        const uint32_t d = C::kO + D * slot, pa = C::kS + 128 * slot + 32 * half;
+        const uint32_t vb = v_lo + st * (C::kTile >> 4);
+        const uint32_t d = C::kO + D * slot, pa = C::kS + 128 * slot;
         umma_ts_lo(d, pa, vb, kDescHi, kIdPV, add, one);
 #pragma unroll
-        for (int k = 1; k < 4; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1, one);
+        for (int k = 1; k < kTcBN / 16; ++k) umma_ts_lo(d, pa + 8 * k, vb + k * (2048 >> 4), kDescHi, kIdPV, 1, one);
         __syncwarp();
       };
       auto commit = [&](uint64_t& bar) {
@@ -291,28 +296,31 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         }
         tc_fence_after();
         if (!ok) break;
-        if (PAIR) {
-          int st = next_tile();
+        if constexpr (PAIR) {
+          int sk = next_tile();
           if (!ok) break;
-          for (int s = 0; s < slots; ++s) qk(s, st);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (s < slots) qk(s, sk);
+          // Step j multiplies tile j's weights with its V and asks for the scores of tile j + 1.
           for (int j = 0; j < n && ok; ++j) {
             const int sv = next_v(key_first + j * kTcBN);
-            int sk = 0;
-            _Pragma("unroll")
+            const bool more = j + 1 < n;
+            const bool k_ready = more && mbar_try_wait(smem_addr(&sh.kv_full[stage]), phase);
+#pragma unroll
             for (int s = 0; s < 2; ++s) {
               if (s >= slots || !ok) break;
-              WAIT_OR(sh.p_half[s], p_phase[s], { ok = false; break; });
-              tc_fence_after();
-              pv_half(s, sv, 0, j > 0);
               WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
               p_phase[s] ^= 1;
               tc_fence_after();
-              pv_half(s, sv, 1, true);
-              if (j + 1 == n) {
+              pv(s, sv, j > 0);
+              if (!more) {
                 commit(sh.o_full[s]);
               } else {
-                if (s == 0) sk = next_tile();
-                if (!ok) break;
+                if (s == 0) {
+                  if (!k_ready) WAIT_OR(sh.kv_full[stage], phase, { ok = false; break; });
+                  sk = advance();
+                }
                 qk(s, sk);
               }
             }
@@ -331,8 +339,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             WAIT_OR(sh.p_full[s], p_phase[s], { ok = false; break; });
             p_phase[s] ^= 1;
             tc_fence_after();
-            pv_half(s, sv, 0, j > 1);
-            pv_half(s, sv, 1, true);
+            pv(s, sv, j > 1);
             commit(sh.kv_empty[sv]);
             if (j + 2 < n) {
               const int st = next_tile();
@@ -471,7 +478,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               tmem_st16(s_at + 16 * c, w);
               l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             };
-            if (work && PAIR) {
+            if (PAIR && work) {
               // all 128 scores at once, straight through: the prompt kernels run long enough
               float s[128];
 #pragma unroll
@@ -482,26 +489,20 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 for (int i = 0; i < 128; ++i)
                   if (key0 + i < jlo || key0 + i >= jhi) s[i] = -INFINITY;
               }
-              float t4[4] = {s[0], s[1], s[2], s[3]};
+              float t8[8];
 #pragma unroll
-              for (int i = 4; i < 128; i += 8) {
+              for (int e = 0; e < 8; ++e) t8[e] = max3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], i + 4 + e < 128 ? fmaxf(s[i + e], s[i + 4 + e]) : s[i + e]);
-              }
-              refer(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * coef);
+              for (int i = 24; i < 120; i += 16)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                weigh(s + 32 * c, c);
-                if (c == 1) {  // the first half's products start while the second is weighed
-                  tmem_st_wait();
-                  tc_fence_before();
-                  mbar_arrive(smem_addr(&sh.p_half[slot]));
-                }
-              }
+                for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[i + e], s[i + 8 + e]);
+              const float t_a = max3(max3(t8[0], s[120], s[121]), max3(t8[1], s[122], s[123]), t8[2]);
+              const float t_b = max3(max3(t8[3], s[124], s[125]), max3(t8[4], s[126], s[127]), t8[5]);
+              refer(max3(max3(t_a, t_b, t8[6]), t8[7], t8[7]) * coef);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) weigh(s + 32 * c, c);
               tmem_st_wait();
-            } else if (PAIR) {
-              mbar_arrive(smem_addr(&sh.p_half[slot]));
-            } else if (work) {
+            } else if (work && !PAIR) {
               // 32 scores at a time, read once for the maximum and once for the weights, in a loop
               // that stays rolled: unrolled, a call's first tile waited 5 us for its instructions
               const bool masked = __any_sync(~0u, in && (key0 < jlo || key0 + kTcBN > jhi));
