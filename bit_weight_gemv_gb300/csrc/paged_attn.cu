@@ -25,7 +25,7 @@ using namespace ptx;
 
 constexpr int kThreads = 160;
 constexpr int kComputeThreads = 128;
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 constexpr int kBN = 64;  // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -140,7 +140,9 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   __syncthreads();  // the barriers are initialised
   Walk it;
   Share share;
-  if (!start_walk<kThreads>(a, blockIdx.x, it, share)) return;
+  const bool busy = start_walk<kThreads>(a, blockIdx.x, it, share);
+  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
+  if (!busy) return;
   int left = share.left;
   int stage = 0;
   uint32_t phase = 0;
@@ -544,36 +546,30 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
         }
       }
     }
+    if (tid == 0 && kt0 == 0 && kt1 < it.tiles)
+      say_cut(a, blockIdx.x, &it, kt1, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
     if (C::kQShared || MT < 4) named_barrier(1, kComputeThreads);  // s_ml and qs are free again
     first = false;
     if (left <= 0 || !walk_next(a, it)) return;
   }
 }
 
-// Items that the cuts went through: blocks (j, *) look at cut j.  The blocks of one item's cuts
-// share its rows, so the work of joining spreads over as many blocks as there are pieces, times
-// gridDim.y.  A warp takes
-// a row: its lanes hold the pieces' (maximum, sum) 32 at a time, so the weights cost one round
-// trip, and then one part of the row each, whose loads do not wait for one another.
+// Items that the cuts went through: blocks (j, *) finish the item that CTA j began and others went
+// on with, a share of its rows each.  A warp takes a row: its lanes hold the pieces' (maximum, sum)
+// 32 at a time, so the weights cost one round trip, and then one part of the row each, whose loads
+// do not wait for one another.  The attention's CTAs leave behind what there is to join: found
+// again from the batch, as it once was, it took 11 of 34 us for one row of 30,000 keys per head.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const AttnArgs a) {
-  // the schedule reads the batch alone, which no kernel since the attention's start has written
-  Walk it;
-  Share share;
-  // otherwise the cut fell between two items, inside a lead, or past the end
-  const bool cut = start_walk<kJoinThreads>(a, blockIdx.x + 1, it, share) && it.tile > 0;
+__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!cut) return;
-  const long long tiles_at = share.begin - it.tile;           // where the item's tiles begin
-  const long long from = tiles_at - a.shape.lead;            // and its lead
-  const long long c0 = quotient(tiles_at, share.chunk);       // CTAs with a piece: c0..c0 + n
-  const int n = (int)(quotient(tiles_at + it.tiles - 1, share.chunk) - c0);
-  const int shares = n * gridDim.y, mine = (int)(blockIdx.x + 1 - (c0 + 1)) * gridDim.y + blockIdx.y;
-  const long long slot0 = 2 * c0 + (from > c0 * share.chunk ? 1 : 0);
-  const int G = a.shape.G, R = 1 << a.shape.r_shift, r0 = it.qt << a.shape.r_shift;
-  const int rows = min(R, it.q.n * G - r0);
-  const int ra = (int)((long long)rows * mine / shares), rb = (int)((long long)rows * (mine + 1) / shares);
-  const float vscale = a.p.v_scale ? __ldg(a.p.v_scale + it.h) : 1.0f;
+  const int4 lo = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[0];
+  const int n = lo.x;
+  if (n == 0) return;
+  const int4 hi = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[1];
+  const int G = a.shape.G, R = 1 << a.shape.r_shift, rows = lo.z, r0 = lo.w, h = hi.y;
+  const long long c0 = blockIdx.x, slot0 = lo.y;  // pieces: slot0, and slot 2 (c0 + i) for i = 1..n
+  const int ra = rows * blockIdx.y / gridDim.y, rb = rows * (blockIdx.y + 1) / gridDim.y;
+  const float vscale = a.p.v_scale ? __ldg(a.p.v_scale + h) : 1.0f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart);
   for (int row = ra + warp; row < rb; row += kJoinThreads / 32) {
@@ -607,7 +603,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const AttnAr
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
     const int r = r0 + row, tok = token_of(a.shape, r);
-    const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
+    const long long orow = (long long)(hi.x + tok) * a.Hq + h * G + (r - tok * G);
     const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
     for (int q = 0; q < kParts; ++q) {
@@ -679,11 +675,11 @@ void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ct
 }
 
 cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
-  if (a.ctas < 2) return cudaSuccess;
+  if (a.ctas < 2 || tune("NOCOMB", 0)) return cudaSuccess;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, a.ctas - 1, kJoinThreads, 0, s);
-  cfg.gridDim.y = a.shape.r_shift > 6 ? 1u << (a.shape.r_shift - 6) : 1;  // 64 rows of an item each
+  cfg.gridDim.y = 1u << (a.shape.r_shift - 4);  // 16 rows of an item each
   if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
   if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a);
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256>, a);
@@ -727,7 +723,7 @@ size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int 
   if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxBatch || Hk < 1 || Hk > 4096 || Hq < 1 || Hq > 65536 ||
       Hq % Hk || (D != 64 && D != 128 && D != 256))
     return 0;
-  return (size_t)kMaxPieceRows * (size_t)(D + 2) * sizeof(float);
+  return (size_t)kMaxPieceRows * (size_t)(D + 2) * sizeof(float) + (size_t)kMaxCtas * sizeof(CutItem);
 }
 
 lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq,
@@ -760,11 +756,13 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.lse = lse;
   a.piece_o = static_cast<float*>(workspace);
   a.piece_ml = reinterpret_cast<float2*>(a.piece_o + (size_t)kMaxPieceRows * D);
+  a.cuts = reinterpret_cast<CutItem*>(a.piece_ml + kMaxPieceRows);
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Rows that share a request's keys, on average: the host knows the totals only.
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  const cudaError_t e = rows > 32 && attention_tc_fits(a, D, fp8) ? launch_attention_tc(a, D, rows > 128, s)
+  const int kind = tune("KIND", -1);
+  const cudaError_t e = kind >= 0 ? (kind ? launch_attention_tc(a, D, kind > 1, s) : launch_attention_mma(a, D, fp8, s)) : rows > 32 && attention_tc_fits(a, D, fp8) ? launch_attention_tc(a, D, rows > 128, s)
                                                                  : launch_attention_mma(a, D, fp8, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }

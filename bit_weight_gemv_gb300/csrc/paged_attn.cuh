@@ -19,6 +19,14 @@ constexpr int kMaxPieceRows = 2 * 152 * 256;
 
 #include <cstdlib>
 inline int tune(const char* n, int d) { const char* v = getenv(n); return v ? atoi(v) : d; }
+// What a CTA says about the item that its share ends inside of, if it began that item: `more` other
+// CTAs, the ones behind it, have a piece too (0: nothing to join).
+struct CutItem {
+  int more, slot, rows, r0;  // its own piece's slot; the query tile's rows and first row
+  int row0, h, pad0, pad1;   // the request's first row, the key/value head
+};
+constexpr int kMaxCtas = kMaxPieceRows / 2 / 16;
+
 struct AttnArgs {
   PagedArgs p;
   ItemShape shape;
@@ -30,6 +38,7 @@ struct AttnArgs {
   float* lse;
   float* piece_o;   // [slot][R][D], relative to the piece's maximum, not divided by its sum
   float2* piece_ml; // [slot][R]: maximum (of scale * score * log2 e) and sum
+  CutItem* cuts;    // [CTA]
   int ctas;
   int min_chunk;    // tiles a CTA takes at least
 };
@@ -267,6 +276,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 // The cache as [page][head][slot][D], boxes of 128 bytes (64, where a row has no more) by one page's
 // slots, at most `keys`, swizzled over the box's row length.
 bool encode_cache(CUtensorMap* map, const PagedArgs& p, void* at, int D, bool fp8, int keys);
+
+// By one thread: CTA `cta` leaves the walk's item after tile `done`, whose first piece it holds, or
+// (w null) leaves nothing to join.
+__device__ __forceinline__ void say_cut(const AttnArgs& a, int cta, const Walk* w, int done, long long chunk, int slot) {
+  int4 lo = make_int4(0, 0, 0, 0), hi = lo;
+  if (w) {
+    const int R = 1 << a.shape.r_shift, r0 = w->qt << a.shape.r_shift;
+    lo = make_int4((int)quotient(w->tiles - done + chunk - 1, chunk), slot, min(R, w->q.n * a.shape.G - r0), r0);
+    hi = make_int4(w->q.row0, w->h, 0, 0);
+  }
+  reinterpret_cast<int4*>(a.cuts + cta)[0] = lo;
+  reinterpret_cast<int4*>(a.cuts + cta)[1] = hi;
+}
 
 // Launch configuration of an attention kernel of `ctas` resident CTAs, and the combine step behind it.
 void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int threads, int smem,

@@ -163,6 +163,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   Walk it;
   Share share;
   const bool busy = start_walk<kTcThreads>(a, blockIdx.x, it, share);
+  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -536,6 +537,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 
         // ---- the item's rows leave
         const bool whole = kt0 == 0 && n == it.tiles;
+        if (tid == 0 && kt0 == 0 && !whole)
+          say_cut(a, blockIdx.x, &it, n, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * kRows + (PAIR ? slot * 128 : 0) + row;
         if (PAIR) {
           if (active && ok) {
