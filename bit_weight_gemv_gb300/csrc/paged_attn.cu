@@ -586,18 +586,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
         l += f * ml.y;
       }
       const int k1 = min(32, n + 1 - i0);
-#pragma unroll 8
-      for (int k = 0; k < k1; ++k) {
-        const float fk = __shfl_sync(~0u, f, k);
-        const long long slot = i0 + k ? 2 * (c0 + i0 + k) : slot0;
-        const float* src = a.piece_o + (slot * R + row) * D + lane * kPart;
+      constexpr int kBatch = 8 / kParts;  // pieces asked for together
+      for (int k = 0; k < k1; k += kBatch) {
+        float v[kBatch][kParts][kPart];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          float v[kPart];
-          if (kPart == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src + q * 128);
-          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = min(i0 + k + e, n);  // past the last piece: it again, with weight 0
+          const float* src = a.piece_o + ((i ? 2 * (c0 + i) : slot0) * R + row) * D + lane * kPart;
 #pragma unroll
-          for (int e = 0; e < kPart; ++e) acc[q][e] += fk * v[e];
+          for (int q = 0; q < kParts; ++q) {
+            if (kPart == 4) *reinterpret_cast<float4*>(v[e][q]) = *reinterpret_cast<const float4*>(src + q * 128);
+            else *reinterpret_cast<float2*>(v[e][q]) = *reinterpret_cast<const float2*>(src);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const float fk = __shfl_sync(~0u, f, k + e);
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int d = 0; d < kPart; ++d)
+              if (k + e < k1) acc[q][d] += fk * v[e][q][d];
         }
       }
     }
