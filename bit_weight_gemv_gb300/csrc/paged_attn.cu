@@ -56,11 +56,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (the low 16 bits) as two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(w));
-  return d;
+// Four e4m3 codes as two pairs of fp16 values, low bytes first.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -115,6 +115,70 @@ struct RingBars {
   uint64_t full[8], empty[8];
 };
 
+// The copying warp: every key tile of the CTA's share, into the ring as stages come free.
+template <class C, bool FP8>
+__device__ __forceinline__ void copy_tiles(const AttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                           RingBars& bars, uint32_t ring, Walk it, int left) {
+  constexpr int S = C::kStages, RB = C::kRowBytes;
+  const PagedArgs& p = a.p;
+  const int lane = threadIdx.x & 31;
+  int stage = 0;
+  uint32_t phase = 0;
+  const int box = min(p.page_mask + 1, kBN), boxes = kBN / box;  // keys per box
+  int filled = 0;
+  bool ok = true;
+  for (;;) {
+    const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
+    if (kt1 == kt0) break;
+    const int first = (it.span.lo & ~(kBN - 1)) + lane * box;
+    const int32_t* row = p.table + (long long)it.b * p.table_stride;
+    // Page of this lane's box of tile kt (-2: no key of it is seen), looked up one tile ahead.
+    auto page_of = [&](int kt, int extra) {
+      const int key = first + kt * kBN + extra * box;
+      if (lane + extra >= boxes || key >= it.span.hi || key + box <= it.span.lo) return -2;
+      const int page = __ldg(row + (key >> p.page_shift));
+      if (page >= 0 && page < p.pages) return page;
+      record_error(p.err, LOWBIT_ERR_INVALID_ARG);
+      return -1;  // outside the tensor map: the copy fills zeros
+    };
+    int next = page_of(kt0, 0);
+    for (int kt = kt0; kt < kt1; ++kt) {
+      const int page = next;
+      if (kt + 1 < kt1) next = page_of(kt + 1, 0);
+      if (!mbar_wait(smem_addr(&bars.empty[stage]), phase ^ 1)) {
+        record_error(p.err, LOWBIT_ERR_TIMEOUT);
+        ok = false;
+        break;
+      }
+      const uint32_t bar = smem_addr(&bars.full[stage]);
+      const int page2 = boxes > 32 ? page_of(kt, 32) : -2;  // pages of one slot: 64 boxes
+      const int n = __popc(__ballot_sync(~0u, page != -2)) + __popc(__ballot_sync(~0u, page2 != -2));
+      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * RB * 2));
+      __syncwarp();
+      const int slot = (first + kt * kBN) & p.page_mask;
+      auto copy = [&](int pg, int i) {
+        const uint32_t dst = ring + stage * C::kStage + i * box * C::kPart;
+#pragma unroll
+        for (int part = 0; part < C::kParts; ++part) {
+          constexpr int kElems = C::kPart / (FP8 ? 1 : 2);
+          tma_load_4d(dst + part * (kBN * C::kPart), &kmap, part * kElems, slot, it.h, pg, bar);
+          tma_load_4d(dst + C::kHalf + part * (kBN * C::kPart), &vmap, part * kElems, slot, it.h, pg, bar);
+        }
+      };
+      if (page != -2) copy(page, lane);
+      if (page2 != -2) copy(page2, lane + 32);
+      if (++stage == S) stage = 0, phase ^= 1;
+      if (filled < S) ++filled;
+    }
+    if (!ok || left <= 0 || !walk_next(a, it)) break;
+  }
+  // leave only when no copy is in flight
+  for (int i = 0; i < filled; ++i) {
+    if (--stage < 0) stage = S - 1, phase ^= 1;
+    mbar_wait(smem_addr(&bars.full[stage]), phase);
+  }
+}
+
 template <int D, int MT, bool FP8>
 __global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
 attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -148,60 +212,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   uint32_t phase = 0;
 
   if (warp == 4) {
-    // -------------------------------------------------------------------- copies
-    const int box = min(p.page_mask + 1, kBN), boxes = kBN / box;  // keys per box
-    int filled = 0;
-    bool ok = true;
-    for (;;) {
-      const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
-      if (kt1 == kt0) break;
-      const int first = (it.span.lo & ~(kBN - 1)) + lane * box;
-      const int32_t* row = p.table + (long long)it.b * p.table_stride;
-      // Page of this lane's box of tile kt (-2: no key of it is seen), looked up one tile ahead.
-      auto page_of = [&](int kt, int extra) {
-        const int key = first + kt * kBN + extra * box;
-        if (lane + extra >= boxes || key >= it.span.hi || key + box <= it.span.lo) return -2;
-        const int page = __ldg(row + (key >> p.page_shift));
-        if (page >= 0 && page < p.pages) return page;
-        record_error(p.err, LOWBIT_ERR_INVALID_ARG);
-        return -1;  // outside the tensor map: the copy fills zeros
-      };
-      int next = page_of(kt0, 0);
-      for (int kt = kt0; kt < kt1; ++kt) {
-        const int page = next;
-        if (kt + 1 < kt1) next = page_of(kt + 1, 0);
-        if (!mbar_wait(smem_addr(&bars.empty[stage]), phase ^ 1)) {
-          record_error(p.err, LOWBIT_ERR_TIMEOUT);
-          ok = false;
-          break;
-        }
-        const uint32_t bar = smem_addr(&bars.full[stage]);
-        const int page2 = boxes > 32 ? page_of(kt, 32) : -2;  // pages of one slot: 64 boxes
-        const int n = __popc(__ballot_sync(~0u, page != -2)) + __popc(__ballot_sync(~0u, page2 != -2));
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * RB * 2));
-        __syncwarp();
-        const int slot = (first + kt * kBN) & p.page_mask;
-        auto copy = [&](int pg, int i) {
-          const uint32_t dst = ring + stage * C::kStage + i * box * C::kPart;
-#pragma unroll
-          for (int part = 0; part < C::kParts; ++part) {
-            constexpr int kElems = C::kPart / (FP8 ? 1 : 2);
-            tma_load_4d(dst + part * (kBN * C::kPart), &kmap, part * kElems, slot, it.h, pg, bar);
-            tma_load_4d(dst + C::kHalf + part * (kBN * C::kPart), &vmap, part * kElems, slot, it.h, pg, bar);
-          }
-        };
-        if (page != -2) copy(page, lane);
-        if (page2 != -2) copy(page2, lane + 32);
-        if (++stage == S) stage = 0, phase ^= 1;
-        if (filled < S) ++filled;
-      }
-      if (!ok || left <= 0 || !walk_next(a, it)) break;
-    }
-    // leave only when no copy is in flight
-    for (int i = 0; i < filled; ++i) {
-      if (--stage < 0) stage = S - 1, phase ^= 1;
-      mbar_wait(smem_addr(&bars.full[stage]), phase);
-    }
+    copy_tiles<C, FP8>(a, kmap, vmap, bars, ring, it, left);
     return;
   }
 
@@ -354,8 +365,11 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
             const uint4 kw = lds128(ks + chunk_off<RB>(wkey + n * 8 + key_of<RB, FP8>(g), 4 * j + t));
             const uint32_t ww[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma16816<true>(sc[n], qa[e], e4m3x2_f16x2(ww[e]), e4m3x2_f16x2(ww[e] >> 16));
+            for (int e = 0; e < 4; ++e) {
+              uint32_t b0, b1;
+              e4m3x4_f16x4(ww[e], b0, b1);
+              mma16816<true>(sc[n], qa[e], b0, b1);
+            }
           }
         }
       } else {
@@ -435,9 +449,11 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
             // a word holds two keys' bytes of an even and an odd dim: [k0 d0, k0 d1, k1 d0, k1 d1]
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t x0 = __byte_perm(vb[2 * hh], 0, 0x3120), x1 = __byte_perm(vb[2 * hh + 1], 0, 0x3120);
-              mma16816<true>(o[4 * d + 2 * hh], pa[k2], e4m3x2_f16x2(x0), e4m3x2_f16x2(x1));
-              mma16816<true>(o[4 * d + 2 * hh + 1], pa[k2], e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1 >> 16));
+              uint32_t even[2], odd[2];
+              e4m3x4_f16x4(__byte_perm(vb[2 * hh], 0, 0x3120), even[0], odd[0]);
+              e4m3x4_f16x4(__byte_perm(vb[2 * hh + 1], 0, 0x3120), even[1], odd[1]);
+              mma16816<true>(o[4 * d + 2 * hh], pa[k2], even[0], even[1]);
+              mma16816<true>(o[4 * d + 2 * hh + 1], pa[k2], odd[0], odd[1]);
             }
           }
         } else {
@@ -554,6 +570,329 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   }
 }
 
+// Eight rows and fewer (a decode step: one token, up to eight heads a group).  The products change
+// sides, so that the keys, not the rows, fill the MMA's 16: S^T = K Q^T and O^T = V^T P^T, half the MMAs and half
+// the exponentials of the 16-row kernel.  A lane holds two keys' scores of rows 2t and 2t + 1; P^T
+// becomes the other operand by an 8 x 8 transpose of its 16-bit pairs.  64 requests of 1 to 16,384 keys
+// over an e4m3 cache: 47.4 us on the 16-row kernel, whose issue slots were the limit, ROW8_US here.
+template <int D, bool FP8>
+struct Cfg8 {
+  static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  static constexpr int kPart = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kParts = kRowBytes / kPart;
+  static constexpr int kHalf = kBN * kRowBytes;
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kSteps = D / 16;
+  static constexpr int kCtas = kStage <= 8192 ? 4 : (kStage <= 16384 ? 3 : (kStage <= 32768 ? 2 : 1));
+  static constexpr int kFit = (227 * 1024 / kCtas - 3072) / kStage;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kSmem = 1024 + kStages * kStage;
+  static_assert(64 * D <= kStage, "two warps' outputs pass through one stage");
+};
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, Cfg8<D, FP8>::kCtas)
+attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg8<D, FP8>;
+  constexpr int RB = C::kRowBytes, S = C::kStages, kDT = D / 16;
+  extern __shared__ uint8_t raw[];
+  __shared__ RingBars bars;
+  __shared__ float2 s_ml[4][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+  uint8_t* const smem = raw + (ring - smem_addr(raw));
+  const PagedArgs& p = a.p;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 4);
+    fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();  // the barriers are initialised
+  Walk it;
+  Share share;
+  const bool busy = start_walk<kThreads>(a, blockIdx.x, it, share);
+  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
+  if (!busy) return;
+  int left = share.left;
+  if (warp == 4) {
+    copy_tiles<C, FP8>(a, kmap, vmap, bars, ring, it, left);
+    return;
+  }
+
+  int stage = 0;
+  uint32_t phase = 0;
+  const int g = lane >> 2, t = lane & 3;
+  const int wkey = warp * 16;  // this warp's keys inside a tile
+  bool first = true, ok = true;
+  for (;;) {
+    const Request q = it.q;
+    const int kt0 = it.tile, kt1 = kt0 + walk_take(it, left);
+    if (kt1 == kt0) return;
+    const Span span = it.span;
+    const int base_key = span.lo & ~(kBN - 1);
+    const int r0 = it.qt * 8, rows = q.n * a.shape.G;
+
+    // the query operand: row g's elements; over an e4m3 cache scaled by a power of two into fp16
+    uint32_t qf[C::kSteps][2];
+    float row_coef = a.scale * (FP8 && p.k_scale ? __ldg(p.k_scale + it.h) : 1.0f) * kLog2e;
+    {
+      const int r = r0 + g, tok = token_of(a.shape, r);
+      const uint16_t* src = a.q + (long long)(q.row0 + tok) * a.q_stride + (long long)(it.h * a.shape.G + r - tok * a.shape.G) * D;
+#pragma unroll
+      for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = FP8 ? 64 * (st / 4) + 16 * t + 4 * (st % 4) + i * 2 : 16 * st + 2 * t + i * 8;
+          qf[st][i] = r < rows ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+        }
+      if (FP8) {  // as in attn_mma_kernel
+        float top = 0.0f;
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[st][i] << 16)), fabsf(__uint_as_float(qf[st][i] & 0xFFFF0000u))));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+        const int ee = (top > 0.0f && e < 128) ? max(-100, min(100, e)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 - ee) << 23);
+        row_coef *= __uint_as_float((uint32_t)(127 + ee) << 23);
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[st][i] = pack2<true>(__uint_as_float(qf[st][i] << 16) * up, __uint_as_float(qf[st][i] & 0xFFFF0000u) * up);
+      }
+    }
+    // the two rows whose scores this lane holds
+    int jlo[2], jhi[2];
+    long long qrow[2];
+    float coef[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 2 * t + i, tok = token_of(a.shape, r), pos = q.kv - q.n + tok;
+      const bool in = r < rows;
+      jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
+      jlo[i] = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
+      qrow[i] = in ? (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G) : -1;
+      coef[i] = __shfl_sync(~0u, row_coef, (2 * t + i) * 4);
+    }
+    const int last_row = min(r0 + 8, rows) - 1;
+    const int all_lo = a.shape.window ? max(0, q.kv - q.n + token_of(a.shape, last_row) - a.shape.window + 1) : 0;
+    const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
+
+    float o[kDT][4];
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int last = 0;
+
+    for (int kt = kt0; kt < kt1; ++kt) {
+      if (ok && !mbar_wait(smem_addr(&bars.full[stage]), phase)) {
+        record_error(p.err, LOWBIT_ERR_TIMEOUT);
+        ok = false;
+      }
+      const uint32_t ks = ring + stage * C::kStage, vs = ks + C::kHalf;
+      const int key0 = base_key + kt * kBN;
+      if (key0 < span.lo || key0 + kBN > span.hi) {  // values outside the span: as in attn_mma_kernel
+        constexpr int kChunks = RB / 16;
+        for (int i = lane; i < 16 * kChunks; i += 32) {
+          const int r = wkey + i / kChunks;
+          if (key0 + r < span.lo || key0 + r >= span.hi)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + chunk_off<RB>(r, i % kChunks)), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+
+      // scores of keys g and g + 8, rows 2t and 2t + 1; two chains, joined
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+      if (FP8) {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 x = lds128(ks + chunk_off<RB>(wkey + key_of<RB, FP8>(g), 4 * j + t));
+          const uint4 y = lds128(ks + chunk_off<RB>(wkey + 8 + key_of<RB, FP8>(g), 4 * j + t));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t f[4];
+            e4m3x4_f16x4(xw[e], f[0], f[2]);
+            e4m3x4_f16x4(yw[e], f[1], f[3]);
+            mma16816<true>(e & 1 ? sd : sc, f, qf[4 * j + e][0], qf[4 * j + e][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) {
+          uint32_t f[4];  // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
+          ldsm4(f, ks + chunk_off<RB>(wkey + (lane & 15), 2 * st + (lane >> 4)));
+          mma16816<false>(st & 1 ? sd : sc, f, qf[st][0], qf[st][1]);
+        }
+      }
+
+      const bool masked = key0 < all_lo || key0 + kBN > all_hi;
+      float tm[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[e] = (sc[e] + sd[e]) * coef[e & 1];
+        const int key = key0 + wkey + key_of<RB, FP8>(g) + 8 * (e >> 1);
+        if (masked && (key < jlo[e & 1] || key >= jhi[e & 1])) sc[e] = -INFINITY;
+      }
+      float keep[2], base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        tm[i] = fmaxf(sc[i], sc[2 + i]);
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) tm[i] = fmaxf(tm[i], __shfl_xor_sync(~0u, tm[i], x));
+        const float mn = fmaxf(m[i], tm[i]);
+        base[i] = mn == -INFINITY ? 0.0f : mn;
+        keep[i] = ex2(m[i] - base[i]);
+        m[i] = mn;
+        l[i] *= keep[i];
+      }
+      uint32_t pb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // keys g, then keys g + 8
+        const float x = ex2(sc[2 * i] - base[0]), y = ex2(sc[2 * i + 1] - base[1]);
+        l[0] += x;
+        l[1] += y;
+        pb[i] = transpose8x8(pack2<FP8>(x, y));
+      }
+      if (__any_sync(~0u, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) {
+          o[i][0] *= keep[0], o[i][1] *= keep[1];
+          o[i][2] *= keep[0], o[i][3] *= keep[1];
+        }
+      }
+      const int r = wkey + ((lane >> 3) & 1) * 8 + key_of<RB, FP8>(lane & 7);
+      if (FP8) {
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          uint32_t vb[4];
+          ldsm4t(vb, vs + chunk_off<RB>(r, 2 * d + (lane >> 4)));
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            // rows g: even dims, rows g + 8: odd dims, of this group of 16
+            uint32_t f[4];
+            e4m3x4_f16x4(__byte_perm(vb[2 * hh], 0, 0x3120), f[0], f[1]);
+            e4m3x4_f16x4(__byte_perm(vb[2 * hh + 1], 0, 0x3120), f[2], f[3]);
+            mma16816<true>(o[2 * d + hh], f, pb[0], pb[1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) {
+          uint32_t vb[4];
+          ldsm4t(vb, vs + chunk_off<RB>(r, 2 * d + (lane >> 4)));
+          const uint32_t f[4] = {vb[0], vb[2], vb[1], vb[3]};
+          mma16816<false>(o[d], f, pb[0], pb[1]);
+        }
+      }
+      last = stage;
+      if (kt + 1 < kt1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.empty[stage]));
+      }
+      if (++stage == S) stage = 0, phase ^= 1;
+    }
+
+    // ---- join the four warps, through the last tile's stage
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) l[i] += __shfl_xor_sync(~0u, l[i], x);
+      if (g == 0) s_ml[warp][2 * t + i] = make_float2(m[i], l[i]);
+    }
+    named_barrier(1, kComputeThreads);  // also: every warp is done with the last tile
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s_ml[k][2 * t + i].x);
+      const float f = mm == -INFINITY ? 0.0f : ex2(m[i] - mm);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = s_ml[k][2 * t + i];
+        ll += (mm == -INFINITY ? 0.0f : ex2(x.x - mm)) * x.y;
+      }
+      m[i] = mm;
+      l[i] = ll;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) o[d][i] *= f, o[d][2 + i] *= f;
+    }
+    float4* const buf = reinterpret_cast<float4*>(smem + last * C::kStage) + lane;
+    auto give = [&](int place) {
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) buf[(place * kDT + d) * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+    };
+    auto take = [&](int place) {
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) {
+        const float4 v = buf[(place * kDT + d) * 32];
+        o[d][0] += v.x, o[d][1] += v.y, o[d][2] += v.z, o[d][3] += v.w;
+      }
+    };
+    if (warp >= 2) give(warp - 2);
+    named_barrier(1, kComputeThreads);
+    if (warp < 2) take(warp);
+    if (warp == 1) give(1);  // over what it has just read
+    named_barrier(1, kComputeThreads);
+    if (warp == 0) take(1);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&bars.empty[last]));
+
+    if (warp == 0 && ok) {
+      const bool whole = kt0 == 0 && kt1 == it.tiles;
+      const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (qrow[i] < 0) continue;
+        const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * 8 + 2 * t + i;
+        const float f = whole ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
+        uint16_t* const dst = a.out + qrow[i] * D;
+        float* const part = a.piece_o + piece * D;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) {
+          const float x = o[d][i] * f, y = o[d][2 + i] * f;
+          if (FP8) {  // dims 16 d + 2 g and the next
+            if (whole) *reinterpret_cast<uint32_t*>(dst + 16 * d + 2 * g) = pack2<false>(x, y);
+            else *reinterpret_cast<float2*>(part + 16 * d + 2 * g) = make_float2(x, y);
+          } else if (whole) {  // dims 16 d + g and + 8
+            dst[16 * d + g] = float_to_bf16_bits(x);
+            dst[16 * d + g + 8] = float_to_bf16_bits(y);
+          } else {
+            part[16 * d + g] = x;
+            part[16 * d + g + 8] = y;
+          }
+        }
+        if (g == 0) {
+          if (!whole) a.piece_ml[piece] = make_float2(m[i], l[i]);
+          else if (a.lse) a.lse[qrow[i]] = l[i] == 0.0f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
+        }
+      }
+    }
+    if (tid == 0 && kt0 == 0 && kt1 < it.tiles)
+      say_cut(a, blockIdx.x, &it, kt1, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
+    named_barrier(1, kComputeThreads);  // s_ml is free again
+    first = false;
+    if (left <= 0 || !walk_next(a, it)) return;
+  }
+}
+
 // Items that the cuts went through: blocks (j, *) finish the item that CTA j began and others went
 // on with, a share of its rows each.  A warp takes a row: its lanes hold the pieces' (maximum, sum)
 // 32 at a time, so the weights cost one round trip, and then one part of the row each, whose loads
@@ -625,43 +964,54 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
   }
 }
 
-template <int D, int MT, bool FP8>
-cudaError_t launch_mma(AttnArgs a, cudaStream_t s) {
-  using C = Cfg<D, MT, FP8>;
-  static std::atomic<int> ready[kMaxDevices];
+// `kernel` with 1 << r_shift rows per item on a resident grid, and the combine step behind it.
+template <class C>
+cudaError_t launch_ring(void (*kernel)(const AttnArgs, const CUtensorMap, const CUtensorMap), std::atomic<int>* ready,
+                        AttnArgs a, int D, bool fp8, int r_shift, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   int ctas = ready[dev].load(std::memory_order_relaxed);
   if (!ctas) {
-    e = cudaFuncSetAttribute(attn_mma_kernel<D, MT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     int sms = 0, per = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_mma_kernel<D, MT, FP8>, kThreads, C::kSmem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, C::kSmem);
     if (e != cudaSuccess) return e;
-    ctas = std::max(1, std::min(sms * per, kMaxPieceRows / 2 / C::kRows));
+    ctas = std::max(1, std::min(std::min(sms * per, kMaxCtas), kMaxPieceRows / 2 >> r_shift));
     ready[dev].store(ctas, std::memory_order_relaxed);
   }
   CUtensorMap kmap, vmap;
-  if (!encode_cache(&kmap, a.p, a.p.k, D, FP8, kBN) || !encode_cache(&vmap, a.p, a.p.v, D, FP8, kBN))
+  if (!encode_cache(&kmap, a.p, a.p.k, D, fp8, kBN) || !encode_cache(&vmap, a.p, a.p.v, D, fp8, kBN))
     return cudaErrorNotSupported;
   a.ctas = ctas;
-  a.shape.r_shift = MT == 1 ? 4 : (MT == 2 ? 5 : 6);
+  a.shape.r_shift = r_shift;
   a.shape.bn_shift = 6;
   a.shape.lead = tune("LEAD", 4);
   a.min_chunk = tune("MINC", 1);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
-  e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<D, MT, FP8>, a, kmap, vmap);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, kmap, vmap);
   return e != cudaSuccess ? e : launch_combine(a, D, s);
+}
+template <int D, int MT, bool FP8>
+cudaError_t launch_mma(const AttnArgs& a, cudaStream_t s) {
+  static std::atomic<int> ready[kMaxDevices];
+  return launch_ring<Cfg<D, MT, FP8>>(attn_mma_kernel<D, MT, FP8>, ready, a, D, FP8, MT == 1 ? 4 : (MT == 2 ? 5 : 6), s);
+}
+template <int D, bool FP8>
+cudaError_t launch_row8(const AttnArgs& a, cudaStream_t s) {
+  static std::atomic<int> ready[kMaxDevices];
+  return launch_ring<Cfg8<D, FP8>>(attn_row8_kernel<D, FP8>, ready, a, D, FP8, 3, s);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   // Rows that share a request's keys, on average: the host knows the totals only.
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
+  if (rows <= 8 && !tune("NO8", 0)) return launch_row8<D, FP8>(a, s);
   if (rows <= 16) return launch_mma<D, 1, FP8>(a, s);
   if (rows <= 32) return launch_mma<D, 2, FP8>(a, s);
   return launch_mma<D, 4, FP8>(a, s);
@@ -688,7 +1038,7 @@ cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, a.ctas - 1, kJoinThreads, 0, s);
-  cfg.gridDim.y = 1u << (a.shape.r_shift - 4);  // 16 rows of an item each
+  cfg.gridDim.y = a.shape.r_shift > 4 ? 1u << (a.shape.r_shift - 4) : 1;  // 16 rows of an item each
   if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, a);
   if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, a);
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256>, a);

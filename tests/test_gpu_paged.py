@@ -147,7 +147,9 @@ def test_attention(lb, shape, fp8, order):
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 1), (True, 100), (False, 100), (True, 65), (False, 64)])
 @pytest.mark.parametrize("shape", [([16, 1, 40], [900, 513, 130], 16, 4, 64, 32),
                                    ([16, 200], [2000, 450], 8, 2, 128, 64),
-                                   ([3, 20], [333, 140], 4, 2, 256, 16)])
+                                   ([3, 20], [333, 140], 4, 2, 256, 16),
+                                   ([1, 0, 2, 1], [700, 3, 130, 65], 16, 4, 128, 16),
+                                   ([2, 1], [300, 80], 4, 1, 64, 64), ([1, 1], [129, 600], 8, 1, 256, 32)])
 def test_masks(lb, shape, causal, window, fp8):
     new, kv = shape[:2]
     dead = [x - n - window + 1 if window else 0 for n, x in zip(new, kv)]
