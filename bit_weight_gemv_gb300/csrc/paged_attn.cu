@@ -1116,6 +1116,7 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.piece_o = static_cast<float*>(workspace);
   a.piece_ml = reinterpret_cast<float2*>(a.piece_o + (size_t)kMaxPieceRows * D);
   a.cuts = reinterpret_cast<CutItem*>(a.piece_ml + kMaxPieceRows);
+  a.wide = (((uintptr_t)out | (uintptr_t)workspace) & 31) == 0;
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Rows that share a request's keys, on average: the host knows the totals only.

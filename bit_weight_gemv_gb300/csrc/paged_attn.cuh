@@ -41,6 +41,7 @@ struct AttnArgs {
   CutItem* cuts;    // [CTA]
   int ctas;
   int min_chunk;    // tiles a CTA takes at least
+  bool wide;        // out and the pieces start on 32-byte boundaries
 };
 
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);

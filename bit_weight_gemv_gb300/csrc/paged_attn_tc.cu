@@ -7,9 +7,9 @@
 //       tensor memory, fold them into (m, l) and write the weights back as bf16 over the scores,
 //       where they are the A operand of the product with V;
 //   warp 8 -- copies: K and V tiles of 128 keys by TMA, one box per page and 64-element half;
-//   (warps 10 and 11 only fill their warpgroup, whose registers go to the softmax);
 //   warp 9 -- issues the MMAs: S = Q K^T (both in shared memory) and O += P V (P in tensor memory,
-//       V as it lies in the cache, keys along the reduction).
+//       V as it lies in the cache, keys along the reduction);
+//   warps 10 and 11 -- the queries of the next item.
 // PAIR: the slots hold different rows and share every tile (256 rows per item).  Otherwise both
 // slots hold the same 128 rows and take alternate tiles; their (m, l, O) are joined at the end.
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
@@ -43,7 +43,7 @@ struct Tc {
 
 struct TcShared {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_free, s_full[2], p_full[2], o_full[2];
   uint64_t joined, left;  // both slots' statistics are written; both slots have read both O
   uint32_t tmem;
 };
@@ -103,6 +103,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// 32 bytes: at once where addresses allow (`wide`), since each thread has a row of its own and a
+// whole sector per store halves their cost; else as two stores of 16.
+__device__ __forceinline__ void st_global_32(void* at, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // Two fp32 operations at once, each rounded as the single one.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -145,11 +157,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   if (tid == 0) {
     for (int i = 0; i < S; ++i) mbar_init(smem_addr(&sh.kv_full[i]), 1), mbar_init(smem_addr(&sh.kv_empty[i]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.q_full[i]), PAIR ? 128 : 256);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.o_full[i]), 1);
     }
+    mbar_init(smem_addr(&sh.q_full), 64);
+    mbar_init(smem_addr(&sh.q_free), 1);
     mbar_init(smem_addr(&sh.joined), 256);
     mbar_init(smem_addr(&sh.left), 256);
     fence_mbar_init();
@@ -230,7 +243,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       constexpr uint32_t kIdPV = umma_idesc_bf16(128, D) | (1u << 16);  // B with rows along the reduction
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      uint32_t q_phase = 0, p_phase[2] = {0, 0};
       // low descriptor words of the queries, and of ring stage 0 as K and as V
       const uint32_t q_lo = desc_lo(q_at, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, kTcBN * 128);
       const uint32_t one = lane == 0;
@@ -291,10 +304,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           }
           return advance();
         };
-        for (int s = 0; s < (PAIR ? slots : 1) && ok; ++s) {
-          WAIT_OR(sh.q_full[s], q_phase[s], ok = false);
-          q_phase[s] ^= 1;
-        }
+        WAIT_OR(sh.q_full, q_phase, ok = false);
+        q_phase ^= 1;
         tc_fence_after();
         if (!ok) break;
         if constexpr (PAIR) {
@@ -303,6 +314,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
           for (int s = 0; s < 2; ++s)
             if (s < slots) qk(s, sk);
+          if (n == 1) commit(sh.q_free);
           // Step j multiplies tile j's weights with its V and asks for the scores of tile j + 1.
           for (int j = 0; j < n && ok; ++j) {
             const int sv = next_v(key_first + j * kTcBN);
@@ -323,6 +335,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                   sk = advance();
                 }
                 qk(s, sk);
+                if (j + 2 == n && s + 1 == slots) commit(sh.q_free);
               }
             }
           }
@@ -333,6 +346,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             qk(s, st);
             commit(sh.kv_empty[st]);
           }
+          if (ok && n <= 2) commit(sh.q_free);
           for (int j = 0; j < n && ok; ++j) {
             const int s = j & 1;
             const int sv = next_v(key_first + j * kTcBN);
@@ -347,6 +361,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               if (!ok) break;
               qk(s, st);
               commit(sh.kv_empty[st]);
+              if (j + 3 == n) commit(sh.q_free);
             } else {
               commit(sh.o_full[s]);
             }
@@ -362,14 +377,36 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         while (clock64() - t0 < 20000000LL) {}
       }
     } else if (warp > kMmaWarp) {
+      // ------------------------------------------------------------------ queries
+      // The item's rows into shared memory, swizzled as TMA would leave them, as soon as the last
+      // scores of the item before are there: the copy then hides behind its last weights and its
+      // way out (loaded at the item's start by the softmax warps, the rows took 10,000 cycles).
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      uint32_t free_phase = 1;  // the place is free to begin with
+      for (;;) {
+        if (walk_take(it, left) == 0) break;
+        WAIT_OR(sh.q_free, free_phase, break);
+        free_phase ^= 1;
+        constexpr int kChunks = D / 8;
+        const int r0 = it.qt * kRows, rows = min(kRows, it.q.n * G - r0);
+        for (int i = tid - 32 * (kMmaWarp + 1); i < rows * kChunks; i += 64) {
+          const int rr = i / kChunks, c = i % kChunks, r = r0 + rr, tok = token_of(a.shape, r);
+          const uint16_t* src = a.q + (long long)(it.q.row0 + tok) * a.q_stride + (long long)(it.h * G + r - tok * G) * D + c * 8;
+          const uint32_t dst = q_at + (rr >> 7) * C::kTile + (c / 8) * (128 * 128) + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(smem_addr(&sh.q_full));
+        if (left <= 0 || !walk_next(a, it)) break;
+      }
     } else {
       // ------------------------------------------------------------------ softmax
       asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
       const int slot = warp >> 2, row = (warp & 3) * 32 + lane, t128 = tid & 127;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + C::kS + 128 * slot + lanes;
-      const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // of the scale, given to q
+      const bool negative = a.scale < 0.0f;  // the scores change sign, so that the largest stays the largest
       // a scale of zero keeps masked scores at -inf
       const float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
       uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
@@ -390,36 +427,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           if (++rel == S) rel = 0;
         };
         const int key_first = it.span.lo / kTcBN * kTcBN + kt0 * kTcBN;
-
-        // Q rows into shared memory (swizzled as TMA would leave them)
-        if (active) {
-          constexpr int kChunks = D / 8, kAll = PAIR ? 128 : 256, kMine = 128 * kChunks / kAll, kBatch = 8;
-          const uint32_t dst = q_at + (PAIR ? slot * C::kTile : 0);
-          const int t0 = PAIR ? t128 : tid;
-#pragma unroll
-          for (int i0 = 0; i0 < kMine; i0 += kBatch) {
-            uint4 v[kBatch];  // loaded together, then stored: one round trip per batch
-#pragma unroll
-            for (int i = 0; i < kBatch && i0 + i < kMine; ++i) {
-              const int rr = (t0 + (i0 + i) * kAll) / kChunks, c = (t0 + (i0 + i) * kAll) % kChunks, r = r_tile + rr;
-              const int tok = token_of(a.shape, r);
-              v[i] = make_uint4(0, 0, 0, 0);
-              if (r < rows)
-                v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.q.row0 + tok) * a.q_stride +
-                                                       (long long)(it.h * G + r - tok * G) * D + c * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch && i0 + i < kMine; ++i) {
-              const int rr = (t0 + (i0 + i) * kAll) / kChunks, c = (t0 + (i0 + i) * kAll) % kChunks;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               dst + (c / 8) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
-                           "r"(v[i].x ^ sign), "r"(v[i].y ^ sign), "r"(v[i].z ^ sign), "r"(v[i].w ^ sign)
-                           : "memory");
-            }
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(smem_addr(&sh.q_full[PAIR ? slot : 0]));
-        }
 
         // the keys this row sees
         const int r = r_tile + row, tok = token_of(a.shape, r);
@@ -485,6 +492,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
               for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
               tmem_ld_wait();
+              if (negative) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) s[i] = -s[i];
+              }
               if (__any_sync(~0u, in && (key0 < jlo || key0 + kTcBN > jhi))) {
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
@@ -514,6 +525,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 float s[32];
                 tmem_ld32(s_at + 32 * c, s);
                 tmem_ld_wait();
+                if (negative) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) s[k] = -s[k];
+                }
                 if (masked) {
                   const int from = jlo - key0 - 32 * c, to = jhi - key0 - 32 * c;
 #pragma unroll
@@ -587,13 +602,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               v[i] *= inv;
             }
             if (in && whole) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0 + c);
-              dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-              dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
-            } else if (in) {
-              float4* dst = reinterpret_cast<float4*>(a.piece_o + piece * D + c0 + c);
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+              st_global_32(a.out + orow * D + c0 + c, w, a.wide);
+            } else if (in) {
+              const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+              st_global_32(a.piece_o + piece * D + c0 + c, w, a.wide);
+              st_global_32(a.piece_o + piece * D + c0 + c + 8, w + 8, a.wide);
             }
           }
           if (in && (PAIR || slot == 0)) {
