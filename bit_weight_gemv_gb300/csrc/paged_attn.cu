@@ -988,8 +988,7 @@ cudaError_t launch_ring(void (*kernel)(const AttnArgs, const CUtensorMap, const 
   a.ctas = ctas;
   a.shape.r_shift = r_shift;
   a.shape.bn_shift = 6;
-  a.shape.lead = tune("LEAD", 4);
-  a.min_chunk = tune("MINC", 1);
+  a.shape.lead = 3;  // 64 ragged requests over e4m3: 42.6 us with 2 tiles' worth, 38.4 with 3, 39.6 with 6
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
@@ -1011,7 +1010,7 @@ template <int D, bool FP8>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
   // Rows that share a request's keys, on average: the host knows the totals only.
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  if (rows <= 8 && !tune("NO8", 0)) return launch_row8<D, FP8>(a, s);
+  if (rows <= 8) return launch_row8<D, FP8>(a, s);
   if (rows <= 16) return launch_mma<D, 1, FP8>(a, s);
   if (rows <= 32) return launch_mma<D, 2, FP8>(a, s);
   return launch_mma<D, 4, FP8>(a, s);
@@ -1034,7 +1033,7 @@ void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ct
 }
 
 cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s) {
-  if (a.ctas < 2 || tune("NOCOMB", 0)) return cudaSuccess;
+  if (a.ctas < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, a.ctas - 1, kJoinThreads, 0, s);
@@ -1119,11 +1118,16 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.wide = (((uintptr_t)out | (uintptr_t)workspace) & 31) == 0;
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Rows that share a request's keys, on average: the host knows the totals only.
+  // By the rows that share a request's keys, on average (the host knows the totals only).  Heads of
+  // 128, one request of 30,000 keys, us on the warp-level MMA / tcgen05 with 128 rows an item / with
+  // 256: 32 rows 38.7 / 36.3 / 51.8, 64 rows 47.8 / 37.6 / 59.8, 400 rows 189 / 81 / 101; of 500 keys
+  // 9.6 / 11 / 13 with 32 rows.  Heads of 64: 48 rows 29.8 / 26.1, 32 requests of up to 16,000 keys 48.0 /
+  // 49.0.  256 rows an item pay when there are many: one request of 16,000 keys, 800 rows 71 with 128 and
+  // 69 with 256, 1,600 rows 116 and 103, 3,200 rows 200 and 171 (of 4,000 keys 33 and 37, 48 and 50, 69 and 69).
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  const int kind = tune("KIND", -1);
-  const cudaError_t e = kind >= 0 ? (kind ? launch_attention_tc(a, D, kind > 1, s) : launch_attention_mma(a, D, fp8, s)) : rows > 32 && attention_tc_fits(a, D, fp8) ? launch_attention_tc(a, D, rows > 128, s)
-                                                                 : launch_attention_mma(a, D, fp8, s);
+  const cudaError_t e = rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D, fp8)
+                            ? launch_attention_tc(a, D, rows > 1024, s)
+                            : launch_attention_mma(a, D, fp8, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 

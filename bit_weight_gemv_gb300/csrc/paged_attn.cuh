@@ -17,8 +17,6 @@ constexpr int kMaxDevices = 64;
 // limited so that 2 * CTAs * rows stays within it.
 constexpr int kMaxPieceRows = 2 * 152 * 256;
 
-#include <cstdlib>
-inline int tune(const char* n, int d) { const char* v = getenv(n); return v ? atoi(v) : d; }
 // What a CTA says about the item that its share ends inside of, if it began that item: `more` other
 // CTAs, the ones behind it, have a piece too (0: nothing to join).
 struct CutItem {
@@ -40,7 +38,6 @@ struct AttnArgs {
   float2* piece_ml; // [slot][R]: maximum (of scale * score * log2 e) and sum
   CutItem* cuts;    // [CTA]
   int ctas;
-  int min_chunk;    // tiles a CTA takes at least
   bool wide;        // out and the pieces start on 32-byte boundaries
 };
 
@@ -117,7 +114,7 @@ __device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk
     if (lane >= o) incl += v;
   }
   const uint32_t total = __shfl_sync(~0u, incl, 31);
-  const uint32_t chunk = max((uint32_t)a.min_chunk, (total + a.ctas - 1) / a.ctas);
+  const uint32_t chunk = (total + a.ctas - 1) / a.ctas;
   const uint32_t begin = cta * chunk;
   if (begin >= total) return -1;
   sh.begin = begin;
@@ -153,7 +150,7 @@ __device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, 
   const bool tall = (long long)a.p.T * a.shape.G > (4LL << a.shape.r_shift) * a.p.B;
   long long total, off = 0;
   auto share = [&]() {
-    sh.chunk = max((long long)a.min_chunk, quotient(total + a.ctas - 1, a.ctas));
+    sh.chunk = quotient(total + a.ctas - 1, a.ctas);
     sh.begin = (long long)cta * sh.chunk;
     sh.left = (int)(min(sh.begin + sh.chunk, total) - sh.begin);
     return sh.left > 0;

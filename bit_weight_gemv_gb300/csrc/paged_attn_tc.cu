@@ -656,8 +656,10 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   a.ctas = ctas;
   a.shape.r_shift = PAIR ? 8 : 7;
   a.shape.bn_shift = 7;
-  a.shape.lead = tune("LEADTC", PAIR ? 2 : 4);
-  a.min_chunk = tune("MINCTC", 1);
+  // what an item costs beside its tiles, measured: 24 ragged draft blocks take 50.7 us with 3 tiles'
+  // worth, 53 with 8 (and 190 with none, on an earlier form); 3,200 rows over 4,000 keys 154 us with
+  // 2, 143 with 6
+  a.shape.lead = PAIR ? 6 : 3;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   attention_config(&cfg, &attr, ctas, kTcThreads, C::kSmem, s);
