@@ -3,7 +3,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -13,6 +12,8 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m bit_weight_gemv_gb300.build`")
 
 lib = ctypes.CDLL(LIB_PATH)
+
+from . import _binding  # noqa: E402  (built beside the library; its absence is an ImportError too)
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -65,10 +66,6 @@ _SIGS["lowbit_gemm_int4_grouped"] = (_i, [ctypes.POINTER(lowbit_gemm_desc), _i, 
 _SIGS["lmhead_argmax_verify_noalloc"] = (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp])
 
 
-# lowbit_paged_batch, packed field by field (a ctypes.Structure costs three times the host time)
-_PAGED_BATCH = struct.Struct("@PPPqiii0q")
-
-
 class _PagedCache(ctypes.Structure):
     """lowbit_paged_cache (mirrors the C struct)."""
     _fields_ = [("k", _vp), ("v", _vp), ("page_stride", ctypes.c_int64),
@@ -91,6 +88,10 @@ for _name, (_res, _args) in _SIGS.items():
     _f.argtypes = _args
 
 
+_binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
+                for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample")))
+
+
 class LowbitError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = int(status)
@@ -106,16 +107,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# The handle of torch's current stream without building a Stream object around it (a third of a
-# small call's host time); the public way where a torch build lacks it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+        return _binding.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -448,6 +442,11 @@ def lowbit_draft_argmax_q8(H, packed_head, M, N, K, id_map, ids, workspace, stre
            "lowbit_draft_argmax_q8")
 
 
+def _handle(stream):
+    """A stream's handle for the compiled binding, which finds the current one itself."""
+    return None if stream is None else _stream(stream)
+
+
 class lowbit_paged_cache:
     """A paged key/value cache as the library takes it: k and v of shape
     [num_pages][page_size][heads][head_dim], bf16 or float8_e4m3fn, head_dim dense, the other
@@ -478,44 +477,7 @@ class lowbit_paged_cache:
                                   k.shape[0], k.shape[1], k.shape[2], k.shape[3], 1 if fp8 else 0,
                                   None if k_scale is None else k_scale.data_ptr(),
                                   None if v_scale is None else v_scale.data_ptr())
-        self.ref = ctypes.byref(self.struct)
-
-
-def _rows(t, dim, name):
-    """(rows, heads, row stride) of a bf16 CUDA tensor [T][heads][dim] whose rows may be apart (a
-    slice of a wider product)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != dim:
-        raise ValueError(f"{name} must have shape [T][heads][{dim}]")
-    T, heads, _ = shape
-    row, head, one = t.stride()
-    if T <= 1:
-        row = heads * dim if row < heads * dim or row % 8 else row
-    if row < heads * dim or one != 1 or (heads > 1 and head != dim):
-        raise ValueError(f"{name}: heads must be dense within a row")
-    return T, heads, row
-
-
-def _batch(cu_q, kv_lens, block_table, T):
-    """A lowbit_paged_batch as bytes."""
-    _need(cu_q, torch.int32, "cu_q")
-    _need(kv_lens, torch.int32, "kv_lens")
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 \
-            or not block_table.is_cuda:
-        raise TypeError("block_table must be an int32 CUDA tensor")
-    shape = block_table.shape
-    B = kv_lens.numel()
-    if len(shape) != 2 or shape[0] != B or cu_q.numel() != B + 1:
-        raise ValueError("cu_q [requests + 1], kv_lens [requests] and block_table [requests][pages] "
-                         "must describe the same requests")
-    row, one = block_table.stride()
-    width = shape[1]
-    if width > 1 and one != 1:
-        raise ValueError("block_table: rows must be dense")
-    return _PAGED_BATCH.pack(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
-                             row if B > 1 else max(row, width), B, T, width)
+        self.address = ctypes.addressof(self.struct)
 
 
 def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved=False,
@@ -523,27 +485,8 @@ def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, in
     """Rotary positions on q [T][Hq][D] (into q_out; both may be None) and k [T][heads][D], and
     k and v into `cache` (a lowbit_paged_cache) at the positions that cu_q, kv_lens and
     block_table give.  rope: fp32 [positions][rot], cos then sin, or None."""
-    D = cache.head_dim
-    T, H, ks = _rows(k, D, "k")
-    Tv, Hv, vs = _rows(v, D, "v")
-    if Tv != T or H != cache.heads or Hv != H:
-        raise ValueError("k and v must have the same rows and the cache's heads")
-    qs = Hq = qp = op = rp = rows = rot = 0
-    if q is not None and q_out is not None:
-        Tq, Hq, qs = _rows(q, D, "q")
-        _need(q_out, torch.bfloat16, "q_out")
-        if Tq != T or q_out.numel() != T * Hq * D:
-            raise ValueError("q and q_out must have k's rows")
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q is not q_out:
-        raise ValueError("q and q_out go together")
-    if rope is not None:
-        _need(rope, torch.float32, "rope")
-        rows, rot = rope.shape
-        rp = rope.data_ptr()
-    st = lib.lowbit_kv_append(qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, Hq, rp, rows, rot,
-                              1 if interleaved else 0, _batch(cu_q, kv_lens, block_table, T),
-                              cache.ref, op, _stream(stream))
+    st = _binding.kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache.address, q_out, interleaved,
+                            _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_kv_append")
 
@@ -556,22 +499,9 @@ def lowbit_paged_attention(q, cache, cu_q, kv_lens, block_table, out, workspace,
                            causal=True, window=0, lse=None, stream=None):
     """out [T][Hq][D] = attention of q [T][Hq][D] over each request's keys in `cache` (a
     lowbit_paged_cache); scale None = 1/sqrt(D); lse fp32 [T][Hq] or None."""
-    D = cache.head_dim
-    T, Hq, qs = _rows(q, D, "q")
-    _need(out, torch.bfloat16, "out")
-    _need(workspace, torch.uint8, "workspace")
-    if out.numel() != T * Hq * D:
-        raise ValueError("out must have q's shape")
-    lp = 0
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if lse.numel() != T * Hq:
-            raise ValueError("lse must have shape [T][Hq]")
-        lp = lse.data_ptr()
-    st = lib.lowbit_paged_attention(q.data_ptr(), qs, Hq, _batch(cu_q, kv_lens, block_table, T),
-                                    cache.ref, D ** -0.5 if scale is None else scale,
-                                    1 if causal else 0, window, out.data_ptr(), lp,
-                                    workspace.data_ptr(), workspace.numel(), _stream(stream))
+    st = _binding.paged_attention(q, cache.address, cu_q, kv_lens, block_table, out, workspace,
+                                  cache.head_dim ** -0.5 if scale is None else scale, causal, window, lse,
+                                  _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_paged_attention")
 
@@ -580,27 +510,7 @@ def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_
                   logprob=None, kept=None, stream=None):
     """One token per row of logits [M][V] (fp32 or bf16, rows may be apart) from the uniform
     numbers u [M]; every other argument may be None (see include/lowbit.h)."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2 \
-            or logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("logits must be an fp32 or bf16 CUDA tensor [M][V]")
-    M, V = logits.shape
-    row, one = logits.stride()
-    if V > 1 and one != 1:
-        raise ValueError("logits: rows must be dense")
-
-    def at(t, dtype, n, name):
-        if t is None:
-            return 0
-        _need(t, dtype, name)
-        if t.numel() != n:
-            raise ValueError(f"{name} must hold {n} values")
-        return t.data_ptr()
-
-    f, i = torch.float32, torch.int32
-    st = lib.lowbit_sample(logits.data_ptr(), 1 if logits.dtype is torch.bfloat16 else 0,
-                           row if M > 1 else max(row, V), M, V, at(temperature, f, M, "temperature"),
-                           at(top_k, i, M, "top_k"), at(top_p, f, M, "top_p"), at(min_p, f, M, "min_p"),
-                           at(u, f, M, "u"), at(id_map, i, V, "id_map"), at(ids, i, M, "ids"),
-                           at(logprob, f, M, "logprob"), at(kept, i, M, "kept"), _stream(stream))
+    st = _binding.sample(logits, u, ids, temperature, top_k, top_p, min_p, id_map, logprob, kept,
+                         _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_sample")

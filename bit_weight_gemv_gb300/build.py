@@ -1,8 +1,10 @@
 """Build liblowbit.so in-tree with nvcc for sm_103a (GB300).
 
 Each CUDA translation unit under csrc/ is compiled in parallel to an object file in
-_build/, then the objects are linked into bit_weight_gemv_gb300/liblowbit.so.  Objects are
-rebuilt only when a source or header is newer.  Usage: ``python -m bit_weight_gemv_gb300.build``.
+_build/, then the objects are linked into bit_weight_gemv_gb300/liblowbit.so; beside them the host
+compiler builds csrc/binding.cpp into bit_weight_gemv_gb300/_binding.so (tensor arguments of the
+small calls, see there).  Objects are rebuilt only when a source or header is newer.
+Usage: ``python -m bit_weight_gemv_gb300.build``.
 """
 from __future__ import annotations
 
@@ -12,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblowbit.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -42,6 +46,19 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command():
+    """The host compiler's command for _binding.so (torch's own libraries carry the symbols)."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
+    return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"],
+            "-I" + os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+            os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+            "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every csrc/*.cu for sm_103a and link liblowbit.so; returns its path."""
     nvcc = _nvcc()
@@ -59,6 +76,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    stale_binding = _stale(BINDING, [os.path.join(CSRC, "binding.cpp")] + headers)
+    if stale_binding:
+        jobs.append(_binding_command())
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -69,7 +90,9 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 if verbose or ptxas_info or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                    raise RuntimeError("compilation failed: " + " ".join(cmd))
+    if stale_binding:
+        os.replace(BINDING + ".tmp", BINDING)
     if jobs or not os.path.exists(LIB) or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]

@@ -1,6 +1,7 @@
 """CPU pins of the oracle for the paged-cache operators and sampling, the host-side refusals of
 their entry points, and the binding's checks."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -112,7 +113,7 @@ P = 0x10000      # never dereferenced: every call below is refused on the host
 def batch(n, **kw):
     f = dict(cu_q=P, kv_lens=P, block_table=P, table_stride=8, B=2, T=4, width=8)
     f |= kw
-    return n._PAGED_BATCH.pack(*(f[x] or 0 for x in ("cu_q", "kv_lens", "block_table", "table_stride", "B", "T", "width")))
+    return struct.pack("@PPPqiii0q", *(f[x] or 0 for x in ("cu_q", "kv_lens", "block_table", "table_stride", "B", "T", "width")))
 
 
 def cache(n, **kw):
