@@ -92,6 +92,27 @@ def test_settings(lb, V, bf16):
     check(lb, z[:, 1:V + 1], rows)
 
 
+@pytest.mark.parametrize("M,V", [(1, 248320), (6, 100003), (40, 248320), (40, 33000), (3, 5000)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_prefix_lengths(lb, M, V, bf16):
+    """Prefixes on both sides of what the first list, the candidates and a step can hold, over every
+    split of a row, with ties, hot tokens and masked ones."""
+    g = torch.Generator("cuda").manual_seed(M * 7 + V + bf16)
+    z = 2.0 * torch.randn((M, V), device="cuda", generator=g)
+    z[:, ::97] += 3.0
+    z[0, :V // 2] = 4.0                                   # more equal logits than any list holds
+    if M > 1:
+        z[1, 200:] = -torch.inf                           # fewer tokens than the bound asks for
+        z[2, ::3] = z[2, 5].item()
+    z = z.to(torch.bfloat16) if bf16 else z
+    kinds = [(0.8, 0, 0.9, 0.0), (1.0, 0, 0.5, 0.0), (1.5, 0, 0.97, 0.0), (0.5, 0, 0.9999, 0.01), (1.0, 255, 1.0, 0.0),
+             (1.0, 256, 0.9, 0.0), (1.2, 1024, 0.99, 0.0), (1.2, 1025, 0.99, 0.001), (0.7, 2048, 1.0, 0.0),
+             (1.0, 2049, 0.8, 0.0), (1.0, V - 1, 1.0, 0.0), (1.0, 0, 0.02, 0.0), (1.0, 0, 1.0, 1e-3)]
+    n = len(kinds) if M < 8 else 1
+    for i in range(n):
+        check(lb, z, [kinds[(i + m) % len(kinds)] + (((m * 37 + i * 11) % 101) / 101,) for m in range(M)])
+
+
 @pytest.mark.parametrize("V", [7, 5000, 100003])
 def test_edge_rows(lb, V):
     inf, nan = float("inf"), float("nan")
