@@ -11,6 +11,11 @@
 // copying warp walks the items on its own, so the next item's tiles arrive while one is finished.
 // The grid is resident and the work is cut evenly over it (see paged.cuh); attn_combine_kernel
 // joins items that were cut.
+//
+// Bound: few rows per key/value head read the cache once and are bound by HBM, plus what a call pays
+// whatever its size (start, an empty pipeline, the combine step: 7.4 us for one row over 777 keys).
+// 64 ragged requests of one token over an e4m3 cache: 38.4 us, 176 MB, 4.6 TB/s; 32 rows of one
+// request over 30,000 bf16 keys: 38.7 us, 123 MB, 3.2 TB/s (the copy rate is 6.8).
 #include "common.cuh"
 #include "paged.cuh"
 #include "paged_attn.cuh"
@@ -574,7 +579,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
 // sides, so that the keys, not the rows, fill the MMA's 16: S^T = K Q^T and O^T = V^T P^T, half the MMAs and half
 // the exponentials of the 16-row kernel.  A lane holds two keys' scores of rows 2t and 2t + 1; P^T
 // becomes the other operand by an 8 x 8 transpose of its 16-bit pairs.  64 requests of 1 to 16,384 keys
-// over an e4m3 cache: 47.4 us on the 16-row kernel, whose issue slots were the limit, ROW8_US here.
+// over an e4m3 cache: 47.4 us on the 16-row kernel, whose issue slots were the limit, 38.4 us here.
 template <int D, bool FP8>
 struct Cfg8 {
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);

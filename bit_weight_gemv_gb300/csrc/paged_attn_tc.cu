@@ -15,6 +15,12 @@
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
 // since the value the weights refer to, so most tiles never touch it (weights up to 2^8 round to
 // bf16 with the same relative error, and sums are fp32).
+//
+// Bound: the tensor pipe, shared memory and the issuing thread together.  A prompt chunk of 4,001
+// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 654 us, 1,436 TFLOP/s, 75% of a
+// large library product; S = Q K^T reads both operands from shared memory, and an MMA comes every
+// 81 cycles for 64 of work.  Few rows are bound by HBM: one request's 64 rows over 32,765 keys 33.3 us,
+// 134 MB, 4.0 TB/s; 24 ragged requests of 64 rows 50.4 us, 246 MB, 4.9 TB/s.
 #include <type_traits>
 
 #include "common.cuh"

@@ -403,9 +403,10 @@ size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int 
  *   workspace : lowbit_paged_attention_workspace_bytes() bytes, 16-byte aligned, any contents.
  *   Scores, softmax statistics and outputs are held in fp32; the softmax weights enter their
  *   product with v rounded to bf16 (bf16 cache) or fp16 (e4m3 cache).  Slots outside a request's
- *   span are never used, whatever they hold.  A non-finite value inside the span may reach every
- *   row of the token's tile (up to 128 rows) that is computed with it.  The result does not
- *   depend on timing: the same call gives the same bits. */
+ *   span are never used, whatever they hold.  A key that the mask hides from a token does not reach
+ *   it, whatever it holds; a non-finite value v inside the span may (0 * inf is NaN), through the
+ *   up to 256 rows of one request and head that are computed together.  The result does not depend
+ *   on timing: the same call gives the same bits. */
 lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq,
                                      const lowbit_paged_batch* batch,
                                      const lowbit_paged_cache* cache, float scale, int causal,
