@@ -51,7 +51,7 @@ struct SampleArgs {
   const void* logits;
   long long row_stride;
   int M, V, cluster;
-  int per_warp;   // elements of a warp's segment, a multiple of 128
+  int per_warp;   // elements of a warp's segment, a multiple of 128, or of 512 read from L2
   int aligned;    // every row starts on a 16-byte boundary
   const float* temperature;
   const int32_t* top_k;
@@ -222,21 +222,19 @@ struct Slice {
   const uint8_t* at;   // HELD: the slice in shared memory; else the slice in the row
   int end;             // places of the slice inside the row
   int aligned;
-  __device__ __forceinline__ void load4(int i, float (&z)[4]) const {
-    if (HELD && !BF16) {
-      const float4 v = *reinterpret_cast<const float4*>(at + 4 * i);
+  __device__ __forceinline__ void vector4(int i, float (&z)[4]) const {
+    if (BF16) {
+      const uint2 v = HELD ? *reinterpret_cast<const uint2*>(at + 2 * i) : __ldg(reinterpret_cast<const uint2*>(at + 2 * i));
+      z[0] = __uint_as_float(v.x << 16), z[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      z[2] = __uint_as_float(v.y << 16), z[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    } else {
+      const float4 v = HELD ? *reinterpret_cast<const float4*>(at + 4 * i) : __ldg(reinterpret_cast<const float4*>(at + 4 * i));
       z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
-      return;
     }
+  }
+  __device__ __forceinline__ void load4(int i, float (&z)[4]) const {
     if (HELD || (aligned && i + 4 <= end)) {
-      if (BF16) {
-        const uint2 v = HELD ? *reinterpret_cast<const uint2*>(at + 2 * i) : __ldg(reinterpret_cast<const uint2*>(at + 2 * i));
-        z[0] = __uint_as_float(v.x << 16), z[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        z[2] = __uint_as_float(v.y << 16), z[3] = __uint_as_float(v.y & 0xFFFF0000u);
-      } else {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(at + 4 * i));
-        z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
-      }
+      vector4(i, z);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -253,25 +251,33 @@ struct Slice {
       for (int e = 0; e < 4; ++e) z[e] = clean(z[e]);
     }
   }
-  // f(place, logits) for every 128th place, until it returns true.  Out of L2 four loads of a lane are
-  // under way at a time (top-k 20, 128 fp32 rows of 248,320: 63 us, 72 with two, 79 with one); the loop
-  // over shared memory stays short, since few rows spend their time on instructions read for the
-  // first time.
+  // f(place, logits) for every fourth place of from..to (a multiple of 128 apart) and the lane's, until
+  // it returns true.  Out of L2 four loads of a lane are under way at a time (top-k 20, 128 fp32 rows
+  // of 248,320: 63 us, 72 with two, 79 with one); the loop over shared memory stays short, since few
+  // rows spend their time on instructions read for the first time.
   template <class F>
   __device__ __forceinline__ void each4(int from, int to, F&& f) const {
-    constexpr int kDeep = HELD ? 1 : 4;
+    const int lane4 = (threadIdx.x & 31) * 4;
+    if constexpr (!HELD) {
+      const int whole = aligned ? min(to, end) : 0;
 #pragma unroll 1
-    for (int i = from; i < to; i += 128 * kDeep) {
-      float z[kDeep][4];
+      for (; from + 512 <= whole; from += 512) {
+        float z[4][4];
 #pragma unroll
-      for (int j = 0; j < kDeep; ++j)
-        if (i + 128 * j < to) load4(i + 128 * j, z[j]);
+        for (int j = 0; j < 4; ++j) vector4(from + lane4 + 128 * j, z[j]);
 #pragma unroll
-      for (int j = 0; j < kDeep; ++j)
-        if (i + 128 * j < to) {
+        for (int j = 0; j < 4; ++j) {
           clean4(z[j]);
-          if (f(i + 128 * j, z[j])) return;
+          if (f(from + lane4 + 128 * j, z[j])) return;
         }
+      }
+    }
+#pragma unroll 1
+    for (; from < to; from += 128) {
+      float z[4];
+      load4(from + lane4, z);
+      clean4(z);
+      if (f(from + lane4, z)) return;
     }
   }
 };
@@ -283,8 +289,8 @@ __device__ __forceinline__ u64 keep_of_pair(u64 x, int half, bool lower) {
 }
 // Sorts the first n of s.cand (larger logit, then lower index, first), by all threads: bitonic, runs
 // that ascend where bit `run` of a place is clear.  A warp does the exchanges within 64 places in
-// registers, two places a lane, and wider ones go through shared memory (2,048 candidates: 8 us,
-// 20 with every exchange in shared memory; up to 64 need no barrier).
+// registers, two places a lane, and wider ones go through shared memory (about 2,048 candidates with
+// the search of the cut in them: 13.7 us, 19.7 with every exchange in shared memory).
 __device__ __noinline__ void sort_candidates(Shared& s, uint32_t n) {
   const uint32_t lane = threadIdx.x & 31;
   uint32_t size = 64;
@@ -413,8 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   constexpr int kSize = BF16 ? 2 : 4;
   const int C = a.cluster, rank = blockIdx.x % C, m = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int local = warp * a.per_warp + lane * 4;              // this lane's first place in the slice
-  const int local_end = (warp + 1) * a.per_warp;
+  const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;  // this warp's places in the slice
   const int index0 = rank * kWarps * a.per_warp;               // of the slice's first element
   cluster_arrive();  // this CTA runs: the others may write its shared memory
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -436,16 +441,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const uint8_t* const row = static_cast<const uint8_t*>(a.logits) + (long long)m * a.row_stride * kSize;
   const Slice<BF16, HELD> z_of = {HELD ? store : row + (long long)index0 * kSize, max(0, a.V - index0), a.aligned};
   if (!HELD) {
-    z_of.each4(local, local_end, [&](int, float (&z)[4]) {
+    z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
       top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));
       return false;
     });
   } else {
     constexpr int kVec = 16 / kSize;                           // elements of a 16-byte load
-    const int first = warp * a.per_warp;
     if (a.aligned) {
 #pragma unroll 4
-      for (int i = first + lane * kVec; i < local_end; i += 32 * kVec) {
+      for (int i = seg_from + lane * kVec; i < seg_to; i += 32 * kVec) {
         const int at = index0 + i;
         uint4 v;
         if (at + kVec <= a.V) {
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
     } else {
 #pragma unroll 8
-      for (int i = first + lane; i < local_end; i += 32) {
+      for (int i = seg_from + lane; i < seg_to; i += 32) {
         const int at = index0 + i;
         if (BF16) {
           const uint16_t x = at < a.V ? reinterpret_cast<const uint16_t*>(row)[at] : 0xFF80u;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // below this exponent the mass is zero, or the weight under the floor (expf and logf are good to
     // 2 ulp, a part in 2^21)
     const float least = !kWhole && floor_min > 0.0f ? fmaxf(logf(floor_min) - 1e-3f, -kReach) : -kReach;
-    z_of.each4(from + lane * 4, to, [&](int, float (&z)[4]) {
+    z_of.each4(from, to, [&](int, float (&z)[4]) {
       if ((fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) - top) * rate < least) return false;
       parts += 4;  // at most 2^8 tokens per lane: 32 bits hold the sums
 #pragma unroll
@@ -562,7 +566,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   using Plain = std::integral_constant<int, 0>;
   using WithCut = std::integral_constant<int, 1>;
   using Whole = std::integral_constant<int, 2>;  // every token, and no count
-  const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;
   // The cluster's sum of seg_mass; once per row.
   auto cluster_mass = [&]() {
     if (lane == 0) s.warp_mass[warp] = seg_mass;
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();  // s.found has been read
     if (tid == 0) s.found = 0;
     __syncthreads();
-    z_of.each4(local, local_end, [&](int i, float (&z)[4]) {
+    z_of.each4(seg_from, seg_to, [&](int i, float (&z)[4]) {
       const float most = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
       if (kMasses && (most - top) * rate >= -kReach) {  // as in `segment`
         parts += 4;
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
 
     // ---- the step in which the prefix ends
-    z_of.each4(local, local_end, [&](int, float (&z)[4]) {
+    z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (!(z[e] >= low)) continue;
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           limit = top_p_limit(p, total);
           clear_histogram(s);
           __syncthreads();
-          z_of.each4(local, local_end, [&](int, float (&z)[4]) {
+          z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int b = step_of(z[e], origin, steps);
@@ -814,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           __syncthreads();
           clear_histogram(s);
           __syncthreads();
-          z_of.each4(local, local_end, [&](int, float (&z)[4]) {
+          z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (step_of(z[e], origin, steps) != bin) continue;
@@ -912,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       to = min(from + each, to);
     }
   }
-  z_of.each4(from + lane * 4, to, [&](int i, float (&z)[4]) {
+  z_of.each4(from, to, [&](int i, float (&z)[4]) {
     u64 q[4], sum = 0;
     uint32_t at_cut = 0;
 #pragma unroll
@@ -949,7 +952,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 template <bool BF16, bool HELD>
 cudaError_t launch(SampleArgs a, int C, cudaStream_t s) {
   a.cluster = C;
-  a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128;
+  const int step = HELD ? 128 : 512;
+  a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step;
   a.aligned = ((uintptr_t)a.logits & 15) == 0 && (a.row_stride * (BF16 ? 2 : 4)) % 16 == 0;
   const size_t slice = HELD ? (size_t)kWarps * a.per_warp * (BF16 ? 2 : 4) : 0;
   const size_t bytes = (sizeof(Shared) + 15) / 16 * 16 + std::max(slice, (size_t)kCap * 16);
@@ -984,22 +988,19 @@ cudaError_t launch(SampleArgs a, int C, cudaStream_t s) {
 template <bool BF16>
 cudaError_t launch_rows(const SampleArgs& a, cudaStream_t s) {
   // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16
-  // find room at once.  V = 248,320, top-k 20 and top-p / no truncation, fp32: four rows 15.8 / 10.4 us
-  // on 16 CTAs and 16.4 / 12.9 on eight, eight rows 19.8 / 15.1 and 16.7 / 13.3.
+  // find room at once, and rows that wait for room are done soonest by fours.  V = 248,320, fp32,
+  // top-k 20 and top-p / no truncation, us: six rows on 16 CTAs 15.7 / 10.9, on eight 16.6 / 13.3; eight
+  // rows 19.4 / 15.2 and 16.8 / 13.1; 32 rows on eight 22.8 / 22.6, on four 23.0 / 23.1; 48 rows 35.7 / 33.4
+  // and 27.4 / 33.2, on two 31.3 / 36.4; 192 rows 101 / 105, 73 / 89 and 89 / 91.
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
-  if (C == 16 && a.M > 4) C = 8;
-  // A slice is held in shared memory where two CTAs still share an SM (bf16, 64 rows on eight CTAs:
-  // 37 us, 58 read from L2), and a larger one where every CTA has an SM of its own (fp32, 12 rows on
-  // eight: 17.0 us and 19.9; 16 rows: 27.1 and 22.7).
-  auto held = [&](int c) {
-    const long long slice = (long long)((a.V + c * kWarps - 1) / (c * kWarps) + 127) / 128 * 128 * kWarps * (BF16 ? 2 : 4);
-    return slice <= (c * a.M <= 96 ? 163840 : 65536);
-  };
-  // Rows that wait for room and are read from L2 go by fours: 48 fp32 rows 31 us, 41 on eight (32
-  // rows: 25.5 on either); held ones do not (bf16, 192 rows: 91 us on eight, 108 on four).
-  if (C == 8 && a.M > 32 && !held(C)) C = 4;
-  return held(C) ? launch<BF16, true>(a, C, s) : launch<BF16, false>(a, C, s);
+  if (C == 16 && a.M * 16 > 96) C = 8;
+  if (C == 8 && a.M * 8 > 256) C = 4;
+  // A slice is held in shared memory where two CTAs still share an SM (fp32, one row on 16: 14.7 / 9.4 us,
+  // 15.0 / 10.4 read from L2), and a larger one where every CTA has an SM of its own (12 rows on eight:
+  // 17.0 / 13.9 and 17.9 / 15.4; 16 rows: 27.0 / 23.9 and 19.9 / 20.6).
+  const long long slice = (long long)((a.V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128 * kWarps * (BF16 ? 2 : 4);
+  return slice <= (a.M * C <= 96 ? 163840 : 65536) ? launch<BF16, true>(a, C, s) : launch<BF16, false>(a, C, s);
 }
 
 }  // namespace
