@@ -8,7 +8,7 @@
 // CTAs share an SM (the row is then read once), else read again from L2, which holds the rows in
 // flight.  Truncation keeps a prefix of the order (larger logit, then lower index):
 //   1. the largest logit, over the cluster;
-//   2. a bound from the lanes' own maxima, of which k (or 256, for top-p alone) lie above it: a count of
+//   2. a bound from the lanes' own maxima, of which k (or 512, for top-p alone) lie above it: a count of
 //      them in 1024 equal steps of (max - z) / T (28.5 covers every weight that does not round to
 //      zero).  The tokens down to that step, little more than k, go to the first CTA; for top-p the same
 //      pass takes the whole mass S.  Where they hold all that stays, the first CTA sorts them and
@@ -24,7 +24,7 @@
 //
 // Few rows wait on latency: one row of 248,320 takes 14.9 us with top-k 20 and top-p 0.95, of which the
 // merges and exchanges over 16 CTAs take 9, and 9.7 us without truncation.  Many rows are bound by
-// instructions, about 20 for each weight that is summed: 192 rows of mixed settings take 176 us, 28
+// instructions, about 30 for each weight that is summed: 192 rows of mixed settings take 145 us, 28
 // of them for reading the logits once at the copy rate.
 #include <algorithm>
 #include <atomic>
@@ -651,13 +651,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return n;
   };
 
+  // In the first CTA: of its n candidates only those down to the step in which their mass reaches
+  // `limit`, still unsorted; their number.
+  auto trim = [&](uint32_t n, u64 limit) {
+    constexpr int kOwn = kCap / kThreads;
+    clear_histogram(s);
+    __syncthreads();
+    u64 c[kOwn];
+    int step[kOwn];
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const uint32_t i = tid + e * kThreads;
+      c[e] = i < n ? s.cand[i] : 0;
+      step[e] = kBins;
+      if (i < n) {
+        const float x = key_logit((uint32_t)(c[e] >> 32));
+        step[e] = step_of(x, origin, steps);
+        add_mass(s, step[e], mass_of(weight_of(x, top, rate)));
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0, s.all_mass[i] = s.lo[i] + ((u64)s.hi[i] << 32);
+    __syncthreads();
+    find_bin(s, true, 0, limit);
+    const int last = s.bin;
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e)
+      if (step[e] <= last && step[e] < kBins) s.cand[atomicAdd(&s.found, 1)] = c[e];
+    __syncthreads();
+    return (uint32_t)s.found;
+  };
+
   uint32_t cut = 0xFFFFFFFFu, r_keep = 0xFFFFFFFFu;  // a key that no token has
   const bool by_count = k < (uint32_t)a.V;
   if (by_count || !(p >= 1.0f)) {
     // ---- the lanes' own maxima first: at least k tokens lie in the steps down to the k-th largest
     // of them, and with k up to half the lanes not many more.  Where they number kCap at most and
     // hold all that top-k or top-p leaves, they finish the row, and no histogram of it is taken (one
-    // row of 248,320 with top-k 20: 14.9 us, 17.5 by the histogram; with top-p 0.8: 19.6 and 25.7).
+    // row of 248,320 with top-k 20: 14.9 us, 17.5 by the histogram; with top-p 0.8: 19.8 and 25.7).  For
+    // top-p the bound is that of 512 lanes (16 rows with top-p 0.8: 29 us, 46 with 256 and 30 with 1,024;
+    // 192 rows of mixed settings 145, 147 and 152).
     const uint32_t reach = min(C * kThreads / 2, kCap / 2);
     u64 limit = 0;
     bool have_whole = false, beyond = false;
@@ -665,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int own = step_of(lane_max, origin, steps);
       if (own < kBins - 1) atomicAdd(&s.count[own], 1u);
       merge_histograms(s, C, rank, false);
-      find_bin(s, false, by_count ? k : 256u, 0);
+      find_bin(s, false, by_count ? k : min(reach, 512u), 0);
       const int bin = min(s.bin, kBins - 2);
       uint32_t n = kCap + 1;
       bool all = true;
@@ -680,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (n <= kCap && all) {
         if (rank == 0) {
+          if (!by_count && n > 64) n = trim(n, limit);
           sort_candidates(s, n);
           finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, n, k, p, whole, floor_w, top, rate, u);
         }
