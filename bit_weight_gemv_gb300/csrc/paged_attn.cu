@@ -899,33 +899,82 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
 }
 
 // Items that the cuts went through: blocks (j, *) finish the item that CTA j began and others went
-// on with, a share of its rows each.  A warp takes a row: its lanes hold the pieces' (maximum, sum)
-// 32 at a time, so the weights cost one round trip, and then one part of the row each, whose loads
-// do not wait for one another.  The attention's CTAs leave behind what there is to join: found
+// on with, a share of its rows each.  The attention's CTAs leave behind what there is to join: found
 // again from the batch, as it once was, it took 11 of 34 us for one row of 30,000 keys per head.
+// Bound by round trips to L2, so everything a row needs is asked for at once where its pieces are few
+// (1,200 tokens over 4,000 keys, most items cut once: 80 us with the attention, 86 when the weights came
+// first and then pieces by eights).  Four blocks an SM: most blocks have nothing to join, and with
+// fewer at a time the others wait for them (16 tokens over 32,765 keys: 34.5 us, 35.4 with three).
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 lo = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[0];
-  const int n = lo.x;
-  if (n == 0) return;
-  const int4 hi = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[1];
-  const int G = a.shape.G, R = 1 << a.shape.r_shift, rows = lo.z, r0 = lo.w, h = hi.y;
-  const long long c0 = blockIdx.x, slot0 = lo.y;  // pieces: slot0, and slot 2 (c0 + i) for i = 1..n
-  const int ra = rows * blockIdx.y / gridDim.y, rb = rows * (blockIdx.y + 1) / gridDim.y;
-  const float vscale = a.p.v_scale ? __ldg(a.p.v_scale + h) : 1.0f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart);
-  for (int row = ra + warp; row < rb; row += kJoinThreads / 32) {
+struct Join {
+  static constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart);  // a lane's elements of a row
+  const AttnArgs& a;
+  long long slot0, c0;  // pieces: slot0, and slot 2 (c0 + i) for i = 1..n
+  int n, R, r0, h, row_base, lane;
+  float vscale;
+
+  __device__ __forceinline__ long long place(int i, int row) const { return (i ? 2 * (c0 + i) : slot0) * R + row; }
+  __device__ __forceinline__ void load(int i, int row, float (&v)[kParts][kPart]) const {
+    const float* src = a.piece_o + place(i, row) * D + lane * kPart;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      if (kPart == 4) *reinterpret_cast<float4*>(v[q]) = *reinterpret_cast<const float4*>(src + q * 128);
+      else *reinterpret_cast<float2*>(v[q]) = *reinterpret_cast<const float2*>(src);
+    }
+  }
+  __device__ __forceinline__ void store(int row, float m, float l, const float (&acc)[kParts][kPart]) const {
+    const int G = a.shape.G, r = r0 + row, tok = token_of(a.shape, r);
+    const long long orow = (long long)(row_base + tok) * a.Hq + h * G + (r - tok * G);
+    const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      uint16_t* dst = a.out + orow * D + q * 128 + lane * kPart;
+      const uint32_t lo = pack2<false>(acc[q][0] * s, acc[q][1] * s);
+      if (kPart == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2<false>(acc[q][kPart - 2] * s, acc[q][kPart - 1] * s));
+      else *reinterpret_cast<uint32_t*>(dst) = lo;
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+  // ROWS rows of up to PIECES pieces, by one warp.
+  template <int ROWS, int PIECES>
+  __device__ __forceinline__ void few(int row, int end) const {
+    float2 ml[ROWS][PIECES];
+    float v[ROWS][PIECES][kParts][kPart];
+#pragma unroll
+    for (int e = 0; e < ROWS; ++e)
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {  // past the last: it again, with weight 0
+        ml[e][k] = a.piece_ml[place(min(k, n), min(row + e, end - 1))];
+        load(min(k, n), min(row + e, end - 1), v[e][k]);
+      }
+#pragma unroll
+    for (int e = 0; e < ROWS; ++e) {
+      float m = ml[e][0].x, l = 0.0f, acc[kParts][kPart] = {};
+#pragma unroll
+      for (int k = 1; k < PIECES; ++k) m = fmaxf(m, ml[e][k].x);
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        if (k > n) break;
+        const float f = m == -INFINITY ? 0.0f : ex2(ml[e][k].x - m);
+        l += f * ml[e][k].y;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int d = 0; d < kPart; ++d) acc[q][d] += f * v[e][k][q][d];
+      }
+      if (row + e < end) store(row + e, m, l, acc);
+    }
+  }
+  // One row of any number of pieces: the lanes hold the pieces' (maximum, sum), 32 at a time.
+  __device__ __forceinline__ void many(int row) const {
     float m = -INFINITY;
-    for (int i = lane; i <= n; i += 32) m = fmaxf(m, a.piece_ml[(i ? 2 * (c0 + i) : slot0) * R + row].x);
+    for (int i = lane; i <= n; i += 32) m = fmaxf(m, a.piece_ml[place(i, row)].x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.0f, acc[kParts][kPart] = {};
     for (int i0 = 0; i0 <= n; i0 += 32) {
       float f = 0.0f;
       if (i0 + lane <= n) {
-        const int i = i0 + lane;
-        const float2 ml = a.piece_ml[(i ? 2 * (c0 + i) : slot0) * R + row];
+        const float2 ml = a.piece_ml[place(i0 + lane, row)];
         f = m == -INFINITY ? 0.0f : ex2(ml.x - m);
         l += f * ml.y;
       }
@@ -934,15 +983,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
       for (int k = 0; k < k1; k += kBatch) {
         float v[kBatch][kParts][kPart];
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int i = min(i0 + k + e, n);  // past the last piece: it again, with weight 0
-          const float* src = a.piece_o + ((i ? 2 * (c0 + i) : slot0) * R + row) * D + lane * kPart;
-#pragma unroll
-          for (int q = 0; q < kParts; ++q) {
-            if (kPart == 4) *reinterpret_cast<float4*>(v[e][q]) = *reinterpret_cast<const float4*>(src + q * 128);
-            else *reinterpret_cast<float2*>(v[e][q]) = *reinterpret_cast<const float2*>(src);
-          }
-        }
+        for (int e = 0; e < kBatch; ++e) load(min(i0 + k + e, n), row, v[e]);
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
           const float fk = __shfl_sync(~0u, f, k + e);
@@ -955,17 +996,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
       }
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    const int r = r0 + row, tok = token_of(a.shape, r);
-    const long long orow = (long long)(hi.x + tok) * a.Hq + h * G + (r - tok * G);
-    const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) {
-      uint16_t* dst = a.out + orow * D + q * 128 + lane * kPart;
-      const uint32_t lo = pack2<false>(acc[q][0] * s, acc[q][1] * s);
-      if (kPart == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2<false>(acc[q][kPart - 2] * s, acc[q][kPart - 1] * s));
-      else *reinterpret_cast<uint32_t*>(dst) = lo;
-    }
-    if (lane == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    store(row, m, l, acc);
+  }
+};
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 4) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 lo = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[0];
+  const int n = lo.x;
+  if (n == 0) return;
+  const int4 hi = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[1];
+  const int rows = lo.z, warp = threadIdx.x >> 5;
+  const int ra = rows * blockIdx.y / gridDim.y, rb = rows * (blockIdx.y + 1) / gridDim.y;
+  const Join<D> j = {a, lo.y, (long long)blockIdx.x, n, 1 << a.shape.r_shift, lo.w, hi.y, hi.x, (int)(threadIdx.x & 31),
+                     a.p.v_scale ? __ldg(a.p.v_scale + hi.y) : 1.0f};
+  constexpr int kWide = D == 256 ? 4 : 8;
+  if (n < 2) {
+    for (int row = ra + 2 * warp; row < rb; row += kJoinThreads / 16) j.template few<2, 2>(row, rb);
+  } else if (n < kWide) {
+    for (int row = ra + warp; row < rb; row += kJoinThreads / 32) j.template few<1, kWide>(row, rb);
+  } else {
+    for (int row = ra + warp; row < rb; row += kJoinThreads / 32) j.many(row);
   }
 }
 
