@@ -166,6 +166,26 @@ def test_rows_that_see_nothing(lb, new, kv, fp8):
     pr.check(*pr.run(lb, False), False)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,kv,Hq,Hk,D", [([4, 2], [70, 33], 4, 2, 128), ([9], [200], 8, 4, 64), ([30], [500], 8, 2, 256),
+                                            ([90], [300], 8, 2, 128), ([700], [900], 8, 2, 128), ([700], [700], 4, 1, 64)])
+def test_hidden_keys_may_hold_anything(lb, new, kv, Hq, Hk, D, fp8):
+    """A key that is NaN reaches the tokens that see it and no others (its value is finite)."""
+    pr = Problem(14, new, kv, Hq, Hk, D, 16, fp8=fp8)
+    bad = [n // 2 for n in new]                                   # the new token whose key is NaN
+    for b, i in enumerate(bad):
+        j = kv[b] - new[b] + i
+        at = pr.kc[int(pr.table[b, j // 16]), j % 16]
+        at.view(torch.uint8 if fp8 else torch.int16).fill_(0x7F if fp8 else 0x7FC0)
+    out, lse = (x.double().cpu().numpy() for x in pr.run(lb))
+    clean = Problem(14, new, kv, Hq, Hk, D, 16, fp8=fp8)
+    out0, lse0 = (x.double().cpu().numpy() for x in clean.run(lb))
+    for b, i in enumerate(bad):
+        before, after = slice(pr.cu[b], pr.cu[b] + i), slice(pr.cu[b] + i, pr.cu[b + 1])
+        assert np.array_equal(out[before], out0[before]) and np.array_equal(lse[before], lse0[before])
+        assert np.isnan(out[after]).all()
+
+
 def test_sharp_and_flat_scores(lb):
     """Scores far apart (one key takes all) and all equal; scale negative and zero."""
     for scale in (4.0, 0.0, -0.3):

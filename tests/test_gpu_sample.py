@@ -92,7 +92,7 @@ def test_settings(lb, V, bf16):
     check(lb, z[:, 1:V + 1], rows)
 
 
-@pytest.mark.parametrize("M,V", [(1, 248320), (6, 100003), (40, 248320), (40, 33000), (3, 5000)])
+@pytest.mark.parametrize("M,V", [(1, 248320), (6, 100003), (40, 248320), (40, 248309), (40, 33000), (3, 5000), (17, 131073)])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_prefix_lengths(lb, M, V, bf16):
     """Prefixes on both sides of what the first list, the candidates and a step can hold, over every
@@ -105,6 +105,9 @@ def test_prefix_lengths(lb, M, V, bf16):
         z[1, 200:] = -torch.inf                           # fewer tokens than the bound asks for
         z[2, ::3] = z[2, 5].item()
     z = z.to(torch.bfloat16) if bf16 else z
+    wide = torch.full((M, -(-V // 8) * 8 + 8 * (M % 2)), 99.0, dtype=z.dtype, device="cuda")  # whole vectors, rows apart
+    wide[:, :V] = z
+    z = wide[:, :V]
     kinds = [(0.8, 0, 0.9, 0.0), (1.0, 0, 0.5, 0.0), (1.5, 0, 0.97, 0.0), (0.5, 0, 0.9999, 0.01), (1.0, 255, 1.0, 0.0),
              (1.0, 256, 0.9, 0.0), (1.2, 1024, 0.99, 0.0), (1.2, 1025, 0.99, 0.001), (0.7, 2048, 1.0, 0.0),
              (1.0, 2049, 0.8, 0.0), (1.0, V - 1, 1.0, 0.0), (1.0, 0, 0.02, 0.0), (1.0, 0, 1.0, 1e-3)]
