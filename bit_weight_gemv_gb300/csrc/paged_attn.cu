@@ -1181,8 +1181,8 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   // 49.0.  256 rows an item pay when there are many: one request of 16,000 keys, 800 rows 71 with 128 and
   // 69 with 256, 1,600 rows 116 and 103, 3,200 rows 200 and 171 (of 4,000 keys 33 and 37, 48 and 50, 69 and 69).
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  const cudaError_t e = rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D, fp8)
-                            ? launch_attention_tc(a, D, rows > 1024, s)
+  const cudaError_t e = rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D)
+                            ? launch_attention_tc(a, D, fp8, rows > 1024, s)
                             : launch_attention_mma(a, D, fp8, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }

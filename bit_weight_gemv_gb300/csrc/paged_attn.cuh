@@ -295,7 +295,7 @@ cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s);
 
 // The tensor-core kernel (paged_attn_tc.cu): whether it can take the call, and its launch with 256
 // (`pair`) or 128 query rows per item.
-bool attention_tc_fits(const AttnArgs& a, int D, bool fp8);
-cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool pair, cudaStream_t s);
+bool attention_tc_fits(const AttnArgs& a, int D);
+cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool fp8, bool pair, cudaStream_t s);
 
 }  // namespace lowbit

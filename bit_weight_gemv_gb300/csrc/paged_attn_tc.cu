@@ -21,6 +21,8 @@
 // large library product; S = Q K^T reads both operands from shared memory, and an MMA comes every
 // 81 cycles for 64 of work.  Few rows are bound by HBM: one request's 64 rows over 32,765 keys 33.3 us,
 // 134 MB, 4.0 TB/s; 24 ragged requests of 64 rows 50.4 us, 246 MB, 4.9 TB/s.
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -33,22 +35,24 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTcThreads = 384;
 constexpr int kTcBN = 128;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
 constexpr float kGrow = 8.0f;
 
-template <int D>
+template <int D, bool PAIR, bool FP8>
 struct Tc {
+  static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kTile = 128 * D * 2;   // 128 rows of Q, K or V
   static constexpr int kHalves = D / 64;      // 64-element (128-byte) halves of a row
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+  // e4m3: tiles arrive in a ring of their own, deep where HBM is the bound
+  static constexpr int kRaw = 128 * D, kRawStages = !FP8 ? 0 : (D == 64 ? 6 : (PAIR ? 2 : 4));
+  static constexpr int kStages = D == 64 ? (FP8 ? 6 : 8) : (!FP8 ? 5 : (PAIR ? 4 : 3));
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTile + kRawStages * kRaw;
   static constexpr uint32_t kS = 0, kO = 256;  // tensor memory columns: S (and P) of slot s at 128 s,
 };                                             // O at 256 + D s
 
 struct TcShared {
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t kv_full[8], kv_empty[8], raw_full[8], raw_empty[8];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_full[2];
   uint64_t joined, left;  // both slots' statistics are written; both slots have read both O
   uint32_t tmem;
@@ -109,6 +113,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two e4m3 codes as fp16, and two fp16 values as bf16: both exact, since e4m3 has four bits of
+// significand and an exponent that either type holds.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(d) : "r"(two));
+  return d;
+}
+__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t h) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16x2(x.x, x.y);
+}
 // 32 bytes: at once where addresses allow (`wide`), since each thread has a row of its own and a
 // whole sector per store halves their cost; else as two stores of 16.
 __device__ __forceinline__ void st_global_32(void* at, const uint32_t* w, bool wide) {
@@ -144,11 +164,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     what;                                          \
   }
 
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int D, bool PAIR, bool FP8>
+__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
 attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
-  using C = Tc<D>;
+  using C = Tc<D, PAIR, FP8>;
   constexpr int S = C::kStages;
   constexpr int kRows = PAIR ? 256 : 128;
   extern __shared__ uint8_t raw[];
@@ -161,7 +181,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   const PagedArgs& p = a.p;
 
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&sh.kv_full[i]), 1), mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&sh.kv_full[i]), FP8 ? 128 : 1), mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+    for (int i = 0; i < C::kRawStages; ++i) mbar_init(smem_addr(&sh.raw_full[i]), 1), mbar_init(smem_addr(&sh.raw_empty[i]), 128);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
@@ -181,7 +202,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk it;
   Share share;
-  const bool busy = start_walk<kTcThreads>(a, blockIdx.x, it, share);
+  const bool busy = start_walk<C::kThreads>(a, blockIdx.x, it, share);
   if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
   tc_fence_before();
   __syncthreads();
@@ -193,17 +214,39 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
     int left = share.left;
 
     // Registers: 384 threads launch with 168 each (64,512); 256 softmax threads take 208 and the
-    // other 128 keep 80 (63,488).
+    // other 128 keep 80 (63,488).  512 threads launch with 128 each (65,536): 200 and 56, or 168 and 88,
+    // are as many.
+    constexpr int kSide = !FP8 ? 80 : (PAIR ? 56 : 88), kSoftmax = !FP8 ? 208 : (PAIR ? 200 : 168);
+    // The tiles of the share, in the order in which the MMA warp takes them: tile(key tile, is V).
+    auto in_order = [&](const bool& ok, auto&& tile) {
+      for (;;) {
+        const int kt0 = it.tile, n = walk_take(it, left);
+        if (n == 0) break;
+        tile(kt0, false);
+        if (!PAIR && ok && n > 1) tile(kt0 + 1, false);
+        for (int j = 0; j < n && ok; ++j) {
+          tile(kt0 + j, true);
+          const int next = j + (PAIR ? 1 : 2);
+          if (next < n && ok) tile(kt0 + next, false);
+        }
+        if (!ok || left <= 0 || !walk_next(a, it)) break;
+      }
+    };
     if (warp == kLoadWarp) {
       // ------------------------------------------------------------------ copies
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
+      constexpr int kDepth = FP8 ? C::kRawStages : S, kBytes = FP8 ? C::kRaw : C::kTile;
+      uint64_t* const full = FP8 ? sh.raw_full : sh.kv_full;
+      uint64_t* const empty = FP8 ? sh.raw_empty : sh.kv_empty;
+      const uint32_t dst = FP8 ? ring + S * C::kTile : ring;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int filled = 0;  // loads issued, up to S
+      int filled = 0;  // loads issued, up to kDepth
       const int box = min(p.page_mask + 1, kTcBN), boxes = kTcBN / box;  // keys per box
-      auto load = [&](const CUtensorMap* map, int kt) {
-        WAIT_OR(sh.kv_empty[stage], phase ^ 1, { ok = false; return; });
+      in_order(ok, [&](int kt, bool value) {
+        const CUtensorMap* map = value ? &vmap : &kmap;
+        WAIT_OR(empty[stage], phase ^ 1, { ok = false; return; });
         const int key0 = it.span.lo / kTcBN * kTcBN + kt * kTcBN + lane * box;
         const bool mine = lane < boxes && key0 < it.span.hi && key0 + box > it.span.lo;
         int page = 0;
@@ -213,40 +256,78 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
           if (page < 0 || page >= p.pages) record_error(p.err, LOWBIT_ERR_INVALID_ARG), page = -1;
         }
         const int n = __popc(__ballot_sync(~0u, mine));
-        const uint32_t bar = smem_addr(&sh.kv_full[stage]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * 128 * C::kHalves));
+        const uint32_t bar = smem_addr(&full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * box * (kBytes / 128)));
         __syncwarp();
-        if (mine)
+        if (mine) {
+          if (FP8) {
+            tma_load_4d(dst + stage * kBytes + lane * box * D, map, 0, key0 & p.page_mask, it.h, page, bar);
+          } else {
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_4d(ring + stage * C::kTile + h * (kTcBN * 128) + lane * box * 128, map, 64 * h,
-                        key0 & p.page_mask, it.h, page, bar);
-        if (++stage == S) stage = 0, phase ^= 1;
-        if (filled < S) ++filled;
-      };
-      for (;;) {
-        const int kt0 = it.tile, n = walk_take(it, left);
-        if (n == 0) break;
-        load(&kmap, kt0);
-        if (!PAIR && ok && n > 1) load(&kmap, kt0 + 1);
-        for (int j = 0; j < n && ok; ++j) {
-          load(&vmap, kt0 + j);
-          const int next = j + (PAIR ? 1 : 2);
-          if (next < n && ok) load(&kmap, kt0 + next);
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(dst + stage * kBytes + h * (kTcBN * 128) + lane * box * 128, map, 64 * h,
+                          key0 & p.page_mask, it.h, page, bar);
+          }
         }
-        if (!ok || left <= 0 || !walk_next(a, it)) break;
-      }
+        if (++stage == kDepth) stage = 0, phase ^= 1;
+        if (filled < kDepth) ++filled;
+      });
       // Leave only when no copy is in flight and every release has arrived.
       for (int i = 0; i < filled; ++i) {
+        if (--stage < 0) stage = kDepth - 1, phase ^= 1;
+        mbar_wait(smem_addr(&full[stage]), phase);
+        if (ok) mbar_wait(smem_addr(&empty[stage]), phase);
+      }
+    } else if (FP8 && warp >= kConvertWarp) {
+      // ------------------------------------------------------------------ e4m3 to 16 bits
+      // A thread takes a row: K becomes bf16, as the queries are, and V fp16, as the weights are over
+      // such a cache, in the layout that TMA gives a 16-bit tile.
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
+      const int row = tid - 32 * kConvertWarp;
+      int stage = 0, raw_stage = 0, filled = 0;
+      uint32_t phase = 0, raw_phase = 0;
+      bool ok = true;
+      in_order(ok, [&](int, bool value) {
+        WAIT_OR(sh.raw_full[raw_stage], raw_phase, { ok = false; return; });
+        WAIT_OR(sh.kv_empty[stage], phase ^ 1, { ok = false; return; });
+        const uint32_t from = ring + S * C::kTile + raw_stage * C::kRaw + row * D;
+        const uint32_t to = ring + stage * C::kTile + row * 128;
+        const int from_turn = D == 128 ? row & 7 : (row >> 1) & 3;
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t w[4], x[8];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(from + ((c ^ from_turn) << 4)));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = e4m3x2_f16x2(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+          if (!value) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = f16x2_bf16x2(x[i]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             to + (c / 4) * (128 * 128) + (((((c & 3) * 2 + h)) ^ (row & 7)) << 4)),
+                         "r"(x[4 * h]), "r"(x[4 * h + 1]), "r"(x[4 * h + 2]), "r"(x[4 * h + 3])
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_addr(&sh.kv_full[stage]));
+        mbar_arrive(smem_addr(&sh.raw_empty[raw_stage]));
+        if (++stage == S) stage = 0, phase ^= 1;
+        if (++raw_stage == C::kRawStages) raw_stage = 0, raw_phase ^= 1;
+        if (filled < S) ++filled;
+      });
+      for (int i = 0; i < filled; ++i) {  // every release has arrived
         if (--stage < 0) stage = S - 1, phase ^= 1;
-        mbar_wait(smem_addr(&sh.kv_full[stage]), phase);
         if (ok) mbar_wait(smem_addr(&sh.kv_empty[stage]), phase);
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------ MMA issue
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
       constexpr uint32_t kIdQK = umma_idesc_bf16(128, 128);
-      constexpr uint32_t kIdPV = umma_idesc_bf16(128, D) | (1u << 16);  // B with rows along the reduction
+      constexpr uint32_t kIdPV = (FP8 ? umma_idesc_f16(128, D) : umma_idesc_bf16(128, D)) | (1u << 16);  // B with rows along the reduction
       int stage = 0;
       uint32_t phase = 0;
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
@@ -387,7 +468,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       // The item's rows into shared memory, swizzled as TMA would leave them, as soon as the last
       // scores of the item before are there: the copy then hides behind its last weights and its
       // way out (loaded at the item's start by the softmax warps, the rows took 10,000 cycles).
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
       uint32_t free_phase = 1;  // the place is free to begin with
       for (;;) {
         if (walk_take(it, left) == 0) break;
@@ -408,19 +489,26 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       }
     } else {
       // ------------------------------------------------------------------ softmax
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmax));
       const int slot = warp >> 2, row = (warp & 3) * 32 + lane, t128 = tid & 127;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + C::kS + 128 * slot + lanes;
-      const bool negative = a.scale < 0.0f;  // the scores change sign, so that the largest stays the largest
+      bool negative = a.scale < 0.0f;  // the scores change sign, so that the largest stays the largest
       // a scale of zero keeps masked scores at -inf
-      const float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+      float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
       uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
       int rel = 0;  // PAIR: ring stage that is released next
       bool first = true, ok = true;
       for (;;) {
         const int kt0 = it.tile, n = walk_take(it, left);
         if (n == 0) break;
+        float vscale = 1.0f;
+        if (FP8) {
+          const float scale = a.scale * (p.k_scale ? __ldg(p.k_scale + it.h) : 1.0f);
+          negative = scale < 0.0f;
+          coef = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
+          if (p.v_scale) vscale = __ldg(p.v_scale + it.h);
+        }
         const int rows = it.q.n * G, r0 = it.qt * kRows;
         const int r_tile = r0 + (PAIR ? slot * 128 : 0);
         const bool active = r_tile < rows;
@@ -476,7 +564,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 }
               }
             };
-            // weights of 32 scores, as bf16 pairs, and their sum into l
+            // weights of 32 scores, as 16-bit pairs, and their sum into l
             auto weigh = [&](const float* s, int c) {
               const float ref = m == -INFINITY ? 0.0f : -m;
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -487,7 +575,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 x.x = exp2_approx(x.x);
                 x.y = exp2_approx(x.y);
                 sum[i & 1] = add2(sum[i & 1], x);
-                w[i] = pack_bf16x2(x.x, x.y);
+                w[i] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
               }
               tmem_st16(s_at + 16 * c, w);
               l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -590,7 +678,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             l = f0 * x.y + f1 * y.y;
           }
           const bool two = !PAIR && n > 1;
-          const float inv = whole ? (l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l)) : 1.0f;
+          const float inv = whole ? (l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l)) : 1.0f;
           const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
           constexpr int kCols = PAIR ? D : D / 2;
           const int c0 = PAIR ? 0 : slot * kCols;
@@ -640,9 +728,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool FP8>
 cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
-  using C = Tc<D>;
+  using C = Tc<D, PAIR, FP8>;
   static std::atomic<int> ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -650,7 +738,7 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   int ctas = ready[dev].load(std::memory_order_relaxed);
   if (!ctas) {
-    e = cudaFuncSetAttribute(attn_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attn_tc_kernel<D, PAIR, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     int sms = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -658,7 +746,7 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
     ready[dev].store(ctas, std::memory_order_relaxed);
   }
   CUtensorMap kmap, vmap;
-  if (!encode_cache(&kmap, a.p, a.p.k, D, false, kTcBN) || !encode_cache(&vmap, a.p, a.p.v, D, false, kTcBN)) return cudaErrorNotSupported;
+  if (!encode_cache(&kmap, a.p, a.p.k, D, FP8, kTcBN) || !encode_cache(&vmap, a.p, a.p.v, D, FP8, kTcBN)) return cudaErrorNotSupported;
   a.ctas = ctas;
   a.shape.r_shift = PAIR ? 8 : 7;
   a.shape.bn_shift = 7;
@@ -668,22 +756,23 @@ cudaError_t launch_tc(AttnArgs a, cudaStream_t s) {
   a.shape.lead = PAIR ? 6 : 3;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
-  attention_config(&cfg, &attr, ctas, kTcThreads, C::kSmem, s);
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, PAIR>, a, kmap, vmap);
+  attention_config(&cfg, &attr, ctas, C::kThreads, C::kSmem, s);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, PAIR, FP8>, a, kmap, vmap);
   return e != cudaSuccess ? e : launch_combine(a, D, s);
 }
 
 }  // namespace
 
-// True where the kernel can run: bf16, heads of 64 or 128, pages that TMA can box, strides and
-// addresses within its limits.
-bool attention_tc_fits(const AttnArgs& a, int D, bool fp8) {
-  return !fp8 && D <= 128 && a.p.page_mask + 1 >= 16;
-}
+// True where the kernel can run: heads of 64 or 128, pages that TMA can box.
+bool attention_tc_fits(const AttnArgs& a, int D) { return D <= 128 && a.p.page_mask + 1 >= 16; }
 
-cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool pair, cudaStream_t s) {
-  if (D == 64) return pair ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
-  return pair ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
+template <int D, bool PAIR>
+cudaError_t launch_type(const AttnArgs& a, bool fp8, cudaStream_t s) {
+  return fp8 ? launch_tc<D, PAIR, true>(a, s) : launch_tc<D, PAIR, false>(a, s);
+}
+cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool fp8, bool pair, cudaStream_t s) {
+  if (D == 64) return pair ? launch_type<64, true>(a, fp8, s) : launch_type<64, false>(a, fp8, s);
+  return pair ? launch_type<128, true>(a, fp8, s) : launch_type<128, false>(a, fp8, s);
 }
 
 }  // namespace lowbit
