@@ -1180,6 +1180,10 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   // 9.6 / 11 / 13 with 32 rows.  Heads of 64: 48 rows 29.8 / 26.1, 32 requests of up to 16,000 keys 48.0 /
   // 49.0.  256 rows an item pay when there are many: one request of 16,000 keys, 800 rows 71 with 128 and
   // 69 with 256, 1,600 rows 116 and 103, 3,200 rows 200 and 171 (of 4,000 keys 33 and 37, 48 and 50, 69 and 69).
+  // Over e4m3 caches the same limits hold: heads of 128, 30,000 keys, warp-level MMA / tcgen05: 32 rows 35.3 /
+  // 29.5, 40 rows 48.2 / 32.2 (500 keys 10.4 / 10.8), 16 requests of up to 8,000 keys and 32 rows 28.7 / 29.8, 40
+  // rows 33.7 / 27.5; heads of 64, 48 rows 31.2 / 27.0 and 20.9 / 22.7; 256 rows an item: 16,000 keys, 1,600 rows
+  // 137 with 128 and 114 with 256 (of 4,000 keys 49 and 52).
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
   const cudaError_t e = rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D)
                             ? launch_attention_tc(a, D, fp8, rows > 1024, s)

@@ -9,7 +9,9 @@
 //   warp 8 -- copies: K and V tiles of 128 keys by TMA, one box per page and 64-element half;
 //   warp 9 -- issues the MMAs: S = Q K^T (both in shared memory) and O += P V (P in tensor memory,
 //       V as it lies in the cache, keys along the reduction);
-//   warps 10 and 11 -- the queries of the next item.
+//   warps 10 and 11 -- the queries of the next item;
+//   warps 12-15, over an e4m3 cache only -- tiles into 16 bits on their way from the copies to the MMAs:
+//       keys as bf16, which the queries are, values as fp16, which the weights then are; both exact.
 // PAIR: the slots hold different rows and share every tile (256 rows per item).  Otherwise both
 // slots hold the same 128 rows and take alternate tiles; their (m, l, O) are joined at the end.
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
@@ -17,10 +19,12 @@
 // bf16 with the same relative error, and sums are fp32).
 //
 // Bound: the tensor pipe, shared memory and the issuing thread together.  A prompt chunk of 4,001
-// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 654 us, 1,436 TFLOP/s, 75% of a
+// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 638 us, 1,472 TFLOP/s, 77% of a
 // large library product; S = Q K^T reads both operands from shared memory, and an MMA comes every
 // 81 cycles for 64 of work.  Few rows are bound by HBM: one request's 64 rows over 32,765 keys 33.3 us,
-// 134 MB, 4.0 TB/s; 24 ragged requests of 64 rows 50.4 us, 246 MB, 4.9 TB/s.
+// 134 MB, 4.0 TB/s; 24 ragged requests of 64 rows 50.4 us, 246 MB, 4.9 TB/s.  Over e4m3 caches the
+// conversion takes issue slots from the softmax: 1,200 tokens over 4,000 keys 92 us (79 in bf16, 250 on the
+// warp-level MMA); 64 rows over 32,765 keys 33.4 us (54 on the warp-level MMA).
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -44,10 +48,11 @@ struct Tc {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kTile = 128 * D * 2;   // 128 rows of Q, K or V
   static constexpr int kHalves = D / 64;      // 64-element (128-byte) halves of a row
-  // e4m3: tiles arrive in a ring of their own, deep where HBM is the bound
-  static constexpr int kRaw = 128 * D, kRawStages = !FP8 ? 0 : (D == 64 ? 6 : (PAIR ? 2 : 4));
-  static constexpr int kStages = D == 64 ? (FP8 ? 6 : 8) : (!FP8 ? 5 : (PAIR ? 4 : 3));
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTile + kRawStages * kRaw;
+  // e4m3: tiles arrive in a ring of their own
+  static constexpr int kRaw = 128 * D, kRawStages = !FP8 ? 0 : (D == 64 ? 6 : (PAIR ? 2 : 3));
+  static constexpr int kStages = D == 64 ? (FP8 ? 6 : 8) : (FP8 ? 4 : 5);
+  static constexpr int kQ = PAIR ? 2 * kTile : kTile + 2048;  // queries; or one tile and the slots' statistics
+  static constexpr int kSmem = 1024 + kQ + kStages * kTile + kRawStages * kRaw;
   static constexpr uint32_t kS = 0, kO = 256;  // tensor memory columns: S (and P) of slot s at 128 s,
 };                                             // O at 256 + D s
 
@@ -174,8 +179,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
   extern __shared__ uint8_t raw[];
   __shared__ TcShared sh;
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t q_at = base, ring = base + 2 * C::kTile;
-  // the second Q tile's place holds the two slots' statistics when they share the first
+  const uint32_t q_at = base, ring = base + C::kQ;
   float2* const ml = reinterpret_cast<float2*>(raw + (base - smem_addr(raw)) + C::kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedArgs& p = a.p;
@@ -293,7 +297,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         const uint32_t from = ring + S * C::kTile + raw_stage * C::kRaw + row * D;
         const uint32_t to = ring + stage * C::kTile + row * 128;
         const int from_turn = D == 128 ? row & 7 : (row >> 1) & 3;
-#pragma unroll 2
+        // 3,000 tokens (PAIR): 118 us with one, 120 with two, 127 with four; 24 draft blocks 53.1 with
+        // four, 57.1 with eight
+#pragma unroll(PAIR ? 1 : 4)
         for (int c = 0; c < D / 16; ++c) {
           uint32_t w[4], x[8];
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -327,7 +333,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       // ------------------------------------------------------------------ MMA issue
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
       constexpr uint32_t kIdQK = umma_idesc_bf16(128, 128);
-      constexpr uint32_t kIdPV = (FP8 ? umma_idesc_f16(128, D) : umma_idesc_bf16(128, D)) | (1u << 16);  // B with rows along the reduction
+      // B with rows along the reduction; operand formats bf16 (1), or f16 (0)
+      constexpr uint32_t kIdPV = (umma_idesc_bf16(128, D) & (FP8 ? ~((1u << 7) | (1u << 10)) : ~0u)) | (1u << 16);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
@@ -493,22 +500,17 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       const int slot = warp >> 2, row = (warp & 3) * 32 + lane, t128 = tid & 127;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + C::kS + 128 * slot + lanes;
-      bool negative = a.scale < 0.0f;  // the scores change sign, so that the largest stays the largest
-      // a scale of zero keeps masked scores at -inf
-      float coef = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
       uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
       int rel = 0;  // PAIR: ring stage that is released next
       bool first = true, ok = true;
       for (;;) {
         const int kt0 = it.tile, n = walk_take(it, left);
         if (n == 0) break;
-        float vscale = 1.0f;
-        if (FP8) {
-          const float scale = a.scale * (p.k_scale ? __ldg(p.k_scale + it.h) : 1.0f);
-          negative = scale < 0.0f;
-          coef = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
-          if (p.v_scale) vscale = __ldg(p.v_scale + it.h);
-        }
+        const float scale = FP8 && p.k_scale ? a.scale * __ldg(p.k_scale + it.h) : a.scale;
+        const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
+        const bool negative = scale < 0.0f;  // the scores change sign, so that the largest stays the largest
+        // a scale of zero keeps masked scores at -inf
+        const float coef = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
         const int rows = it.q.n * G, r0 = it.qt * kRows;
         const int r_tile = r0 + (PAIR ? slot * 128 : 0);
         const bool active = r_tile < rows;

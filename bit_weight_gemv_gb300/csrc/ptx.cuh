@@ -149,10 +149,6 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N) {
          | ((uint32_t)(N >> 3) << 17)    // N / 8
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
-// The same with both operands f16 (format 0).
-__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
-  return umma_idesc_bf16(M, N) & ~((1u << 7) | (1u << 10));
-}
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle (rows of 128 B, 8-row core
 // groups 1024 B apart).  The start address may sit at a 32-byte step inside a swizzle atom.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
