@@ -13,14 +13,14 @@
 //      zero).  The tokens down to that step, little more than k, go to the first CTA; for top-p the same
 //      pass takes the whole mass S.  Where they hold all that stays, the first CTA sorts them and
 //      finishes the row;
-//   3. else a histogram over 1024 steps, of counts, or of counts and masses, merged over the cluster:
-//      the step in which the prefix ends, and how many tokens (n) lie up to it.  For top-p alone the
-//      steps are laid below the list of 2, down to the weight (1 - p) S / V: what lies below sums to
-//      (1 - p) S at most, so the prefix ends above it;
-//   4. n <= 2048: those tokens go to the first CTA as in 2; else only the tokens of that step do, which
-//      gives the threshold key and the number of tokens equal to it that stay, and the draw walks the
-//      segments that the warps own.  (A step with more than 2048 tokens, such as a row of equal
-//      logits, is narrowed down by its keys' digits.)
+//   3. else a histogram over 1024 steps, of counts for top-k and of masses for top-p, merged over the
+//      cluster: the step in which the prefix ends, and for top-k how many tokens (n) lie up to it.  For
+//      top-p alone the steps are laid below the list of 2, down to the weight (1 - p) S / V: what lies
+//      below sums to (1 - p) S at most, so the prefix ends above it;
+//   4. top-k with n <= 2048: those tokens go to the first CTA as in 2; else only the tokens of that step
+//      do, which gives the threshold key and the number of tokens equal to it that stay, and the draw
+//      walks the segments that the warps own.  (A step with more than 2048 tokens, such as a row of
+//      equal logits, is narrowed down by its keys' digits.)
 //
 // Few rows wait on latency: one row of 248,320 takes 14.9 us with top-k 20 and top-p 0.95, of which the
 // merges and exchanges over 16 CTAs take 9, and 9.7 us without truncation.  Many rows are bound by
@@ -585,7 +585,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   float origin = top;  // where the steps begin
   auto gather = [&](auto with_masses, int from, int to, float low) {
     constexpr bool kMasses = decltype(with_masses)::value;
-    low = fmaxf(low, origin - (float)(to + 2) / steps);  // a step's width below the last one's end
+    // a step's width below the last one's end, and above the first one's start
+    low = fmaxf(low, origin - (float)(to + 2) / steps);
+    const float high = from ? origin - (float)(from - 1) / steps : INFINITY;
     uint32_t hi = 0, lo = 0, parts = 0;
     __syncthreads();  // s.found has been read
     if (tid == 0) s.found = 0;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (most >= low) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (!(z[e] >= low)) continue;
+          if (!(z[e] >= low && z[e] <= high)) continue;
           const int b = step_of(z[e], origin, steps);
           if (b < from || b > to) continue;
           const uint32_t at = atomicAdd(&s.found, 1);
@@ -649,6 +651,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     cluster_sync();
     return n;
+  };
+
+  // Four tokens' masses, those with logits >= low, into the histogram; the additions to the low words
+  // are all under way before the first one's carry is looked at (128 rows with top-p 0.9 that keep 90,000
+  // tokens each: 226 us, 236 one after another).
+  auto add_masses = [&](const float (&z)[4], float low) {
+    if (!(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low)) return;
+    int bin[4];
+    uint32_t lo[4], up[4], old[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bin[e] = step_of(z[e], origin, steps);
+      const u64 mass = z[e] >= low && bin[e] < kBins - 1 ? mass_of(weight_of(z[e], top, rate)) : 0;
+      lo[e] = (uint32_t)mass, up[e] = (uint32_t)(mass >> 32), old[e] = 0;
+      if (lo[e]) old[e] = atomicAdd(&s.lo[bin[e]], lo[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (lo[e] && old[e] > 0xFFFFFFFFu - lo[e]) ++up[e];
+      if (up[e]) atomicAdd(&s.hi[bin[e]], up[e]);
+    }
   };
 
   // In the first CTA: of its n candidates only those down to the step in which their mass reaches
@@ -726,9 +749,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     float low = -INFINITY;  // logits below it are not looked at
     if (have_whole) {
-      // weights up to (1 - p) S / V: half of it, for the roundings on the way
-      const float tau = 0.5f * (1.0f - p) * ((float)whole * 0x1p-40f) / (float)a.V;
-      low = top + logf(fmaxf(tau, 1e-30f)) / rate;
+      // Tokens of weights up to (1 - p) S / V sum to (1 - p) S at most.  Less a thousandth for expf and
+      // logf, half a unit of 2^-40 for each mass's rounding, and a few ulps of the logits.
+      const float tau = 0.999f * (1.0f - p) * ((float)whole * 0x1p-40f) / (float)a.V - 0x1p-41f;
+      const float deep = logf(fmaxf(tau, 1e-30f)) / rate;
+      low = top + deep - 4e-7f * (fabsf(top) + fabsf(deep));
       // the prefix ends between it and the list's last step: the steps are laid there, which leaves
       // a sixth of the tokens in the one that is searched (T = 1.5, p = 0.9)
       const float from = top - (float)min(s.bin, kBins - 2) / steps;
@@ -742,13 +767,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
     // ---- the step in which the prefix ends
     z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
+      if (by_count) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (!(z[e] >= low)) continue;
-        const int bin = step_of(z[e], origin, steps);
-        if (bin >= kBins - 1) continue;  // no mass past the last step: a cut there cuts nothing
-        atomicAdd(&s.count[bin], 1u);
-        if (!by_count) add_mass(s, bin, mass_of(weight_of(z[e], top, rate)));
+        for (int e = 0; e < 4; ++e) {
+          const int bin = step_of(z[e], origin, steps);
+          if (bin < kBins - 1) atomicAdd(&s.count[bin], 1u);  // no mass past the last step: a cut there cuts nothing
+        }
+      } else {
+        add_masses(z, low);
       }
       return false;
     });
@@ -758,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     uint32_t count_before = s.count_before;
     u64 mass_before = s.mass_before;
     const uint32_t n = count_before + s.found;
-    if (n <= kCap) {
+    if (by_count && n <= kCap) {
       gather(std::false_type(), 0, bin < kBins ? bin : kBins - 2, low);  // after it no CTA touches another's memory
       if (rank == 0) {
         sort_candidates(s, n);
@@ -778,11 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           clear_histogram(s);
           __syncthreads();
           z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int b = step_of(z[e], origin, steps);
-              if (b < kBins - 1) atomicAdd(&s.count[b], 1u), add_mass(s, b, mass_of(weight_of(z[e], top, rate)));
-            }
+            add_masses(z, -INFINITY);
             return false;
           });
           merge_histograms(s, C, rank, true);
@@ -799,9 +821,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         continue;
       }
       u64 one = 0;  // mass of one token at the cut
-      const uint32_t here = s.found;
+      const uint32_t here = gather(std::false_type(), bin, bin, turn == 1 ? low : -INFINITY);
       if (here <= kCap) {
-        gather(std::false_type(), bin, bin, turn == 1 ? low : -INFINITY);
         if (rank == 0) {
           sort_candidates(s, here);
           // a thread takes four places in a row; masses count only for top-p
