@@ -12,6 +12,10 @@
 namespace lowbit {
 
 constexpr int kMaxDevices = 64;
+// Scores (in powers of two) past it are rounded to more than an eighth in fp32: their weights then refer to
+// the largest itself.
+constexpr float kFarScore = 1048576.0f;
+__device__ __forceinline__ bool far_score(float x) { return fabsf(x) > kFarScore && fabsf(x) != INFINITY; }
 // Query rows of all pieces together: every CTA may leave two (the item it starts inside of and
 // the one it ends inside of).  The workspace holds D + 2 floats for each; a kernel's grid is
 // limited so that 2 * CTAs * rows stays within it.

@@ -16,7 +16,9 @@
 // slots hold the same 128 rows and take alternate tiles; their (m, l, O) are joined at the end.
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
 // since the value the weights refer to, so most tiles never touch it (weights up to 2^8 round to
-// bf16 with the same relative error, and sums are fp32).
+// bf16 with the same relative error, and sums are fp32).  Scores past 2^20 are rounded to fp32 before the reference
+// is taken off (the difference of a fused product and a rounded one would be an eighth and more), and
+// refer to the largest itself.
 //
 // Bound: the tensor pipe, shared memory and the issuing thread together.  A prompt chunk of 4,001
 // tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 638 us, 1,472 TFLOP/s, 77% of a
@@ -509,9 +511,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         if (n == 0) break;
         const float scale = FP8 && p.k_scale ? a.scale * __ldg(p.k_scale + it.h) : a.scale;
         const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
-        const bool negative = scale < 0.0f;  // the scores change sign, so that the largest stays the largest
         // a scale of zero keeps masked scores at -inf
         const float coef = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
+        const float signed_coef = copysignf(coef, scale);
         const int rows = it.q.n * G, r0 = it.qt * kRows;
         const int r_tile = r0 + (PAIR ? slot * 128 : 0);
         const bool active = r_tile < rows;
@@ -534,6 +536,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         const bool work = __any_sync(~0u, in);  // a warp without rows only keeps the pace
 
         float m = -INFINITY, l = 0.0f;  // m: what the weights so far refer to
+        float slack = kGrow;    // a maximum this far above m moves it
+        // The scores in powers of two are s * sign * unit, the first product rounded and the second fused with
+        // the subtraction of m: sign is 1 or -1, so that the largest stays the largest under a negative
+        // scale, and unit is coef, until m of some row of the warp is past 2^20.  Then coef is part of the first
+        // (of sign, or PAIR, whose loop is straight, of a product of its own: 117.5 us for 3,000 tokens over
+        // e4m3, 120.5 with the tile's scores read again where that changes).
+        float sign = copysignf(1.0f, scale), unit = coef;
         int steps = 0;
         if (active && ok) {
           for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2, ++steps) {
@@ -547,8 +556,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             const int key0 = key_first + j * kTcBN;
             // the maximum grew: l and (past the slot's first tile) O follow the new reference
             auto refer = [&](float top) {
-              const bool grow = top > m + kGrow;  // from -inf: any finite maximum
+              const bool grow = top > m + slack;  // from -inf: any finite maximum
               if (__any_sync(~0u, grow)) {
+                const bool far = __any_sync(~0u, in && far_score(fmaxf(m, top)));
+                slack = far ? 0.0f : kGrow;
+                unit = far ? 1.0f : coef;
+                if (!PAIR) sign = far ? signed_coef : copysignf(1.0f, signed_coef);
                 const float f = grow ? exp2_approx(m - top) : 1.0f;
                 if (grow) m = top;
                 l *= f;
@@ -567,14 +580,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 }
               }
             };
-            // weights of 32 scores, as 16-bit pairs, and their sum into l
+            // weights of 32 scores (times `unit`), as 16-bit pairs, and their sum into l
             auto weigh = [&](const float* s, int c) {
               const float ref = m == -INFINITY ? 0.0f : -m;
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               uint32_t w[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(coef, coef), make_float2(ref, ref));
+                float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), make_float2(unit, unit), make_float2(ref, ref));
                 x.x = exp2_approx(x.x);
                 x.y = exp2_approx(x.y);
                 sum[i & 1] = add2(sum[i & 1], x);
@@ -589,9 +602,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
               for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
               tmem_ld_wait();
-              if (negative) {
+              if (sign != 1.0f) {
 #pragma unroll
-                for (int i = 0; i < 128; ++i) s[i] = -s[i];
+                for (int i = 0; i < 128; ++i) s[i] *= sign;
               }
               if (__any_sync(~0u, in && (key0 < jlo || key0 + kTcBN > jhi))) {
 #pragma unroll
@@ -608,6 +621,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               const float t_a = max3(max3(t8[0], s[120], s[121]), max3(t8[1], s[122], s[123]), t8[2]);
               const float t_b = max3(max3(t8[3], s[124], s[125]), max3(t8[4], s[126], s[127]), t8[5]);
               refer(max3(max3(t_a, t_b, t8[6]), t8[7], t8[7]) * coef);
+              if (unit != coef) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) s[i] *= coef;
+              }
 #pragma unroll
               for (int c = 0; c < 4; ++c) weigh(s + 32 * c, c);
               tmem_st_wait();
@@ -622,9 +639,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 float s[32];
                 tmem_ld32(s_at + 32 * c, s);
                 tmem_ld_wait();
-                if (negative) {
+                if (sign != 1.0f) {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) s[k] = -s[k];
+                  for (int k = 0; k < 32; ++k) s[k] *= sign;
                 }
                 if (masked) {
                   const int from = jlo - key0 - 32 * c, to = jhi - key0 - 32 * c;
@@ -635,7 +652,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 if (i < 4) {
 #pragma unroll
                   for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(s[k], s[k + 1]));
-                  if (i == 3) refer(top * coef);
+                  if (i == 3) refer(top * unit);
                 } else {
                   weigh(s, c);
                 }
