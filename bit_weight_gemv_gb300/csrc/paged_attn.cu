@@ -72,6 +72,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// What a row's weights refer to when the largest of its scores so far (in powers of two) is `top`.  Over an
+// e4m3 cache they enter their product as fp16, which has no values below 2^-24: there the largest
+// weight is 2^15 instead of 1, so a weight loses bits only below 2^-29 of the largest and becomes zero
+// below 2^-40.  (With 1 as the largest, a tail of keys 2^26 times below one leading key left the output
+// although it counted in the sum.)  Scores past 2^20, whose own rounding approaches the shift, keep 1.
+template <bool F16>
+__device__ __forceinline__ float reference(float top) {
+  return F16 && !far_score(top) ? top - 15.0f : top;
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t d;
@@ -417,7 +426,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
       for (int i = 0; i < 2; ++i) {
         tm[i] = fmaxf(tm[i], __shfl_xor_sync(~0u, tm[i], 1));
         tm[i] = fmaxf(tm[i], __shfl_xor_sync(~0u, tm[i], 2));
-        const float mn = fmaxf(m[i], tm[i]);
+        const float mn = fmaxf(m[i], reference<FP8>(tm[i]));
         base[i] = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every weight is 2^-inf = 0
         keep[i] = ex2(m[i] - base[i]);
         m[i] = mn;
@@ -761,7 +770,7 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         tm[i] = fmaxf(sc[i], sc[2 + i]);
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) tm[i] = fmaxf(tm[i], __shfl_xor_sync(~0u, tm[i], x));
-        const float mn = fmaxf(m[i], tm[i]);
+        const float mn = fmaxf(m[i], reference<FP8>(tm[i]));
         base[i] = mn == -INFINITY ? 0.0f : mn;
         keep[i] = ex2(m[i] - base[i]);
         m[i] = mn;

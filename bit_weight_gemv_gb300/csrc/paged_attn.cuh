@@ -38,8 +38,8 @@ struct AttnArgs {
   float scale;
   uint16_t* out;
   float* lse;
-  float* piece_o;   // [slot][R][D], relative to the piece's maximum, not divided by its sum
-  float2* piece_ml; // [slot][R]: maximum (of scale * score * log2 e) and sum
+  float* piece_o;   // [slot][R][D], weights relative to the piece's reference, not divided by their sum
+  float2* piece_ml; // [slot][R]: reference (of scale * score * log2 e; about the maximum) and sum
   CutItem* cuts;    // [CTA]
   int ctas;
   bool wide;        // out and the pieces start on 32-byte boundaries

@@ -16,7 +16,10 @@
 // slots hold the same 128 rows and take alternate tiles; their (m, l, O) are joined at the end.
 // O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than 2^8
 // since the value the weights refer to, so most tiles never touch it (weights up to 2^8 round to
-// bf16 with the same relative error, and sums are fp32).  Scores past 2^20 are rounded to fp32 before the reference
+// bf16 with the same relative error, and sums are fp32).  Over an e4m3 cache the weights are fp16, which ends
+// at 2^16 and has no values below 2^-24: they refer to 2^-7 of the maximum, so the largest is 2^7 to 2^15, and
+// a weight becomes zero only below 2^-32 of it (24 draft blocks 54.0 us; with rescaling from a growth of 2^3 on
+// and 2^-12 of the maximum 56.9).  Scores past 2^20 are rounded to fp32 before the reference
 // is taken off (the difference of a fused product and a rounded one would be an eighth and more), and
 // refer to the largest itself.
 //
@@ -535,8 +538,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         const int jlo = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
         const bool work = __any_sync(~0u, in);  // a warp without rows only keeps the pace
 
+        constexpr float kLift = FP8 ? 7.0f : 0.0f;
         float m = -INFINITY, l = 0.0f;  // m: what the weights so far refer to
-        float slack = kGrow;    // a maximum this far above m moves it
+        float slack = kGrow + kLift;    // a maximum this far above m moves it
         // The scores in powers of two are s * sign * unit, the first product rounded and the second fused with
         // the subtraction of m: sign is 1 or -1, so that the largest stays the largest under a negative
         // scale, and unit is coef, until m of some row of the warp is past 2^20.  Then coef is part of the first
@@ -559,11 +563,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
               const bool grow = top > m + slack;  // from -inf: any finite maximum
               if (__any_sync(~0u, grow)) {
                 const bool far = __any_sync(~0u, in && far_score(fmaxf(m, top)));
-                slack = far ? 0.0f : kGrow;
+                slack = far ? 0.0f : kGrow + kLift;
                 unit = far ? 1.0f : coef;
                 if (!PAIR) sign = far ? signed_coef : copysignf(1.0f, signed_coef);
-                const float f = grow ? exp2_approx(m - top) : 1.0f;
-                if (grow) m = top;
+                const float ref = far ? top : top - kLift;
+                const float f = grow ? exp2_approx(m - ref) : 1.0f;
+                if (grow) m = ref;
                 l *= f;
                 // the product before this one is complete: its tensor work came before these scores'
                 if (steps > 0) {

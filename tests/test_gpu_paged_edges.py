@@ -1,4 +1,5 @@
-"""GPU checks of the paged calls at their edges: scores far beyond those of a model.
+"""GPU checks of the paged calls at their edges: weights far below the largest one, scores far
+beyond those of a model.
 
 Row counts choose the kernels: tokens times grouped heads per request of up to 8, 16, 32, then 128
 rows an item and, past 1,024, 256."""
@@ -37,6 +38,35 @@ def attend(lb, q, kc, vc, new, kv, table, causal=True, window=0, scale=1.0):
 
 
 ROWS = [(2, 64), (2, 128), (2, 256), (4, 128), (8, 64), (8, 128), (16, 256), (16, 128), (40, 64), (300, 128), (300, 64)]
+
+
+@pytest.mark.parametrize("below", [25.4, 26.5, 28.0])
+@pytest.mark.parametrize("new,D", ROWS)
+def test_a_tail_of_tiny_weights_over_e4m3(lb, new, D, below):
+    """One leading key whose value is 0, and 2,999 keys 2^below under it whose value is 1: the output is
+    the tail's share.  Weights are fp16, good to 2^-11 of themselves or to half of fp16's smallest step,
+    2^-25, with the largest at 2^15 (up to 32 rows, and heads of 256) or between 2^7 and 2^15; the output is
+    rounded to bf16 (2^-8); scores of below * ln 2 in fp32 move a weight by less than 1e-4.  These times
+    1.05.  So many requests that most are not cut: a piece of the keys without the leading one refers to
+    its own largest."""
+    B, G, kv, page = 300, 4, 3000, 64
+    pages = -(-kv // page)
+    kc = torch.zeros((pages, page, 1, D), device="cuda")
+    vc = torch.ones((pages, page, 1, D), device="cuda")
+    kc[0, 0, 0, 0] = 8.0
+    vc[0, 0] = 0.0
+    kc, vc = kc.to(torch.float8_e4m3fn), vc.to(torch.float8_e4m3fn)
+    q = torch.zeros((B * new, G, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0
+    scale = float(np.float32(below * np.log(2.0) / 16.0))
+    out, lse = attend(lb, q, kc, vc, [new] * B, [kv] * B, [list(range(pages))] * B, causal=False, scale=scale)
+    tail = (kv - 1) * np.exp(-16.0 * scale)
+    want = tail / (1.0 + tail)
+    step = 2.0 ** (below - 25 - (15 if D == 256 or new * G <= 32 else 7))
+    tol = 1.05 * (max(2.0 ** -11, step) + 2.0 ** -8 + 1e-4) * want
+    assert float((out.double() - want).abs().max()) <= tol
+    assert float((lse.double() - (16.0 * scale + np.log1p(tail))).abs().max()) <= 1e-4
+    assert lb.lowbit_device_error() == 0
 
 
 @pytest.mark.parametrize("fp8", [False, True])
