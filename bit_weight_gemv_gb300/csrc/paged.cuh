@@ -76,11 +76,16 @@ __device__ __forceinline__ int token_of(const ItemShape& s, int r) {
   const uint32_t q = __umulhi((uint32_t)r, s.g_inv);
   return (int)(q + ((uint32_t)r - q * s.G >= (uint32_t)s.G ? 1u : 0u));
 }
+// First key that the window leaves a token at `pos`.  More new tokens than keys put the first ones at positions
+// below zero, where window and position together may pass 32 bits: they lose no key to the window.
+__device__ __forceinline__ int first_key(const ItemShape& s, int pos) {
+  return s.window ? max(0, max(pos + 1, 0) - s.window) : 0;
+}
 __device__ __forceinline__ Span tile_span(const ItemShape& s, const Request& q, int qt) {
   const int r0 = qt << s.r_shift, r1 = min(r0 + (1 << s.r_shift), q.n * s.G) - 1;
   Span k;
   k.hi = s.causal ? max(0, min(q.kv, q.kv - q.n + token_of(s, r1) + 1)) : q.kv;
-  k.lo = s.window ? max(0, q.kv - q.n + token_of(s, r0) - s.window + 1) : 0;
+  k.lo = first_key(s, q.kv - q.n + token_of(s, r0));
   if (k.lo >= k.hi) k.lo = k.hi = 0;
   return k;
 }

@@ -253,12 +253,12 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
       const bool in = r < rows;
       const int pos = q.kv - q.n + tok;
       jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
-      jlo[i] = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
+      jlo[i] = first_key(a.shape, pos);
       qrow[i] = in ? (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G) : -1;
     }
     // keys that every row of the CTA's tile sees need no mask
     const int last_row = min(r0 + C::kRows, rows) - 1;
-    const int all_lo = a.shape.window ? max(0, q.kv - q.n + token_of(a.shape, last_row) - a.shape.window + 1) : 0;
+    const int all_lo = first_key(a.shape, q.kv - q.n + token_of(a.shape, last_row));
     const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
 
     // ---- query fragments; with an e4m3 cache the row is scaled by a power of two into fp16
@@ -697,12 +697,12 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
       const int r = r0 + 2 * t + i, tok = token_of(a.shape, r), pos = q.kv - q.n + tok;
       const bool in = r < rows;
       jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
-      jlo[i] = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
+      jlo[i] = first_key(a.shape, pos);
       qrow[i] = in ? (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G) : -1;
       coef[i] = __shfl_sync(~0u, row_coef, (2 * t + i) * 4);
     }
     const int last_row = min(r0 + 8, rows) - 1;
-    const int all_lo = a.shape.window ? max(0, q.kv - q.n + token_of(a.shape, last_row) - a.shape.window + 1) : 0;
+    const int all_lo = first_key(a.shape, q.kv - q.n + token_of(a.shape, last_row));
     const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
 
     float o[kDT][4];

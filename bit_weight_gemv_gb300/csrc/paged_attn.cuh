@@ -105,7 +105,7 @@ __device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk
   Request q = {0, 0, 0};
   if (lane < a.p.B) q = load_request(a.p, lane);
   // one tile holds every row: its keys end with the request's, whatever the mask
-  const int lo = a.shape.window ? max(0, q.kv - q.n - a.shape.window + 1) : 0;
+  const int lo = first_key(a.shape, q.kv - q.n);
   const bool none = lo >= q.kv;
   const int tiles = none ? 1 : ((q.kv - 1) >> a.shape.bn_shift) - (lo >> a.shape.bn_shift) + 1;
   const uint32_t cost = q.n ? (uint32_t)(tiles + a.shape.lead) : 0;

@@ -535,7 +535,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         const bool in = r < rows;
         const int pos = it.q.kv - it.q.n + tok;
         const int jhi = in ? (a.shape.causal ? min(it.q.kv, pos + 1) : it.q.kv) : 0;
-        const int jlo = a.shape.window ? max(0, pos - a.shape.window + 1) : 0;
+        const int jlo = first_key(a.shape, pos);
         const bool work = __any_sync(~0u, in);  // a warp without rows only keeps the pace
 
         constexpr float kLift = FP8 ? 7.0f : 0.0f;

@@ -1,5 +1,5 @@
 """GPU checks of the paged calls at their edges: weights far below the largest one, scores far
-beyond those of a model.
+beyond those of a model, descriptions of a batch that do not hold together.
 
 Row counts choose the kernels: tokens times grouped heads per request of up to 8, 16, 32, then 128
 rows an item and, past 1,024, 256."""
@@ -91,3 +91,25 @@ def test_scores_past_whole_numbers(lb, new, D, scale, fp8):
     want = vc[lead // page, lead % page, 0].expand_as(out)
     assert bool(((out.float() - want).abs() <= 1.05 * 2.0 ** -7 * want.abs()).all())
     assert float((lse.double() / (21.0 * scale) - 1.0).abs().max()) <= 2.0 ** -21
+
+
+# ------------------------------------------------------------------------------------ descriptions
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 50, 2 ** 30, 200])
+@pytest.mark.parametrize("new,kv,G,D", [(100, 3, 1, 64), (100, 60, 4, 128), (6, 2, 4, 128), (2, 1, 4, 64), (9, 4, 4, 256),
+                                        (400, 90, 4, 128)])
+def test_windows_past_every_length(lb, window, new, kv, G, D):
+    """A window that no key falls out of changes nothing, whatever its size, also for a request whose
+    first tokens come before every key (more new tokens than keys: positions below zero)."""
+    g = torch.Generator(device="cuda").manual_seed(window % 1000 + new)
+    page = 16
+    pages = -(-kv // page)
+    kc, vc = (torch.randn((pages, page, 1, D), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((new, G, D), device="cuda", generator=g).to(torch.bfloat16)
+    args = (lb, q, kc, vc, [new], [kv], [list(range(pages))])
+    for causal in (True, False):
+        want, norm = attend(*args, causal=causal, scale=D ** -0.5)
+        out, lse = attend(*args, causal=causal, window=window, scale=D ** -0.5)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, norm)
+    assert lb.lowbit_device_error() == 0
