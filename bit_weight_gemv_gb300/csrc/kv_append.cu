@@ -68,15 +68,22 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
   // a warp looks up each token's place
   if (tid < 32 * TOKENS) {
     const int t = t0 + (tid >> 5);
-    // its request: as many requests end at or before row t as precede it
-    int b = 0;
+    // its request: the first one whose rows it is among
+    int b = p.B, row0 = 0, end = 0, kv = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const bool before = b0 + lane < p.B && p.cu_q[b0 + lane + 1] <= t;
-      b += __popc(__ballot_sync(~0u, before));
+      int from = 0, to = 0, len = 0;
+      if (b0 + lane < p.B) from = p.cu_q[b0 + lane], to = p.cu_q[b0 + lane + 1], len = p.kv_lens[b0 + lane];
+      if (to < from) record_error(p.err, LOWBIT_ERR_INVALID_ARG);
+      const uint32_t in = __ballot_sync(~0u, from <= t && t < to);
+      if (in && b == p.B) {
+        const int src = __ffs(in) - 1;
+        b = b0 + src;
+        row0 = __shfl_sync(~0u, from, src), end = __shfl_sync(~0u, to, src), kv = __shfl_sync(~0u, len, src);
+      }
     }
     int pos = -1, page = -1;
-    if (t < p.T && b < p.B && t >= p.cu_q[b]) {
-      const Request r = load_request(p, b);
+    if (t < p.T && b < p.B) {
+      const Request r = check_request(p, row0, end, kv);
       if (t - r.row0 < r.n) {
         pos = r.kv - r.n + (t - r.row0);
         const bool in = pos >= 0 && (a.rot == 0 || pos < a.rope_rows);

@@ -38,17 +38,17 @@ lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_page
 struct Request {
   int row0, n, kv;
 };
-__device__ __forceinline__ Request load_request(const PagedArgs& a, int b) {
-  Request r;
-  r.row0 = a.cu_q[b];
-  r.n = a.cu_q[b + 1] - r.row0;
-  r.kv = a.kv_lens[b];
+__device__ __forceinline__ Request check_request(const PagedArgs& a, int from, int to, int kv) {
+  Request r = {from, to - from, kv};
   if (r.row0 < 0 || r.n < 0 || r.row0 > a.T - r.n || r.kv < 0 ||
       (long long)r.kv > ((long long)a.width << a.page_shift)) {
     record_error(a.err, LOWBIT_ERR_INVALID_ARG);
     r.row0 = r.n = r.kv = 0;
   }
   return r;
+}
+__device__ __forceinline__ Request load_request(const PagedArgs& a, int b) {
+  return check_request(a, a.cu_q[b], a.cu_q[b + 1], a.kv_lens[b]);
 }
 
 // ---------------------------------------------------------------------- attention schedule

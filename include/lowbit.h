@@ -339,7 +339,9 @@ lowbit_status lmhead_accept_keys(const uint64_t* keys, int W, int M, const int32
  * The kernels check what they read: a request whose cu_q decreases or passes T, or whose
  * kv_lens is negative or passes width * page_size, is skipped; a token whose page is outside
  * 0..num_pages-1 is not appended, and a key in such a page is read as zeros.  Each records
- * LOWBIT_ERR_INVALID_ARG in the device error word. */
+ * LOWBIT_ERR_INVALID_ARG in the device error word (lowbit_kv_append looks at the lengths of requests with
+ * rows only).  Where offsets decrease, requests may claim the same row: it is appended for the first
+ * of them, and attention writes it for each. */
 typedef struct lowbit_paged_batch {
   const int32_t* cu_q;         /* device, [B + 1] */
   const int32_t* kv_lens;      /* device, [B] */

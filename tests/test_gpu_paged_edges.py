@@ -113,3 +113,30 @@ def test_windows_past_every_length(lb, window, new, kv, G, D):
         out, lse = attend(*args, causal=causal, window=window, scale=D ** -0.5)
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, norm)
     assert lb.lowbit_device_error() == 0
+
+
+def test_append_finds_requests_whatever_the_order_of_the_rows(lb):
+    """Offsets that decrease somewhere are recorded; the requests that are consistent are appended (a row
+    that two of them claim, for the earlier one)."""
+    D = 64
+    for cu, kv, want in (
+            ([0, 5, 3, 8], [5, 9, 9], {0: [0, 1, 2, 3, 4], 2: [6, 7, 8]}),
+            ([0, 3, 8, 6], [3, 5, 9], {0: [0, 1, 2], 1: [0, 1, 2, 3, 4]}),
+            ([3, 1, 8], [4, 7], {1: list(range(7))}),
+            ([0] * 40 + [3, 2, 6], [6] * 42, {39: [3, 4, 5], 41: [3, 4, 5]})):
+        T, B = 8, len(kv)
+        x = torch.arange(1, T + 1, device="cuda").to(torch.bfloat16).view(T, 1, 1).expand(T, 1, D).contiguous()
+        kc = torch.zeros((B, 16, 1, D), dtype=torch.bfloat16, device="cuda")
+        vc = kc.clone()
+        q_out = torch.zeros_like(x)
+        lb.lowbit_kv_append(x, x, x, None, i32(cu), i32(kv), i32([[b] for b in range(B)]), lb.lowbit_paged_cache(kc, vc), q_out)
+        assert lb.lowbit_device_error() == 1
+        ref = torch.zeros_like(kc)
+        seen = torch.zeros(T, dtype=torch.bool)
+        for b, places in want.items():
+            for p in places:
+                row = cu[b] + p - (kv[b] - (cu[b + 1] - cu[b]))
+                ref[b, p] = x[row]
+                seen[row] = True
+        assert torch.equal(kc, ref) and torch.equal(vc, ref)
+        assert torch.equal((q_out[:, 0, 0] != 0).cpu(), seen)
