@@ -175,6 +175,12 @@ cudaError_t launch_tokens(const AppendArgs& a, bool fp8, bool inter, cudaStream_
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// True where the `bytes` bytes at `p` meet one of T rows of `row` bytes, `stride` bytes apart from `first` on.
+inline bool meets(const void* p, __int128 bytes, const void* first, __int128 row, __int128 stride, int T) {
+  const __int128 at = (__int128)(uintptr_t)p - (__int128)(uintptr_t)first;
+  const __int128 t = at < row ? 0 : (at - row) / stride + 1;  // the first row that ends behind p
+  return t < T && t * stride < at + bytes;
+}
 
 }  // namespace
 
@@ -232,6 +238,14 @@ extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, c
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(rope) || !aligned16(q_out) ||
       (q && q_stride % 8) || k_stride % 8 || v_stride % 8)
     return LOWBIT_ERR_ALIGN;
+  if (q) {  // a block that writes its token's queries must not meet what another one has yet to read
+    const __int128 row = (__int128)Hq * D * 2, kv = (__int128)cache->heads * D * 2;
+    const bool in_place = q_out == q && (a.p.T == 1 || q_stride == (int64_t)Hq * D);
+    if ((!in_place && meets(q_out, row * a.p.T, q, row, (__int128)q_stride * 2, a.p.T)) ||
+        meets(q_out, row * a.p.T, k, kv, (__int128)k_stride * 2, a.p.T) ||
+        meets(q_out, row * a.p.T, v, kv, (__int128)v_stride * 2, a.p.T))
+      return LOWBIT_ERR_INVALID_ARG;
+  }
   a.p.err = device_error_word();
   if (!a.p.err) return LOWBIT_ERR_CUDA;
   a.q = q;

@@ -379,7 +379,8 @@ typedef struct lowbit_paged_cache {
  *       Element pair j is (x[j], x[j + rot/2]), or (x[2j], x[2j + 1]) when `interleaved`:
  *         a' = a cos - b sin,  b' = b cos + a sin   (fp32, every product and sum rounded).
  *       Elements from rot on, and values, are not rotated.
- *   q_out : bf16 [T][Hq][D], dense, 16-byte aligned (NULL with q); may be q itself.
+ *   q_out : bf16 [T][Hq][D], dense, 16-byte aligned (NULL with q).  It may be q itself where q is dense
+ *       too; any other overlap with a row of q, k or v is refused (LOWBIT_ERR_INVALID_ARG).
  *   In the cache a bf16 element is rounded once; an e4m3 element is x / scale rounded to
  *   nearest-even and clipped to +-448 (NaN stays NaN).  Slots of other positions keep their
  *   contents.  A position at or past rope_rows is not appended and recorded in the device
