@@ -543,9 +543,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         float slack = kGrow + kLift;    // a maximum this far above m moves it
         // The scores in powers of two are s * sign * unit, the first product rounded and the second fused with
         // the subtraction of m: sign is 1 or -1, so that the largest stays the largest under a negative
-        // scale, and unit is coef, until m of some row of the warp is past 2^20.  Then coef is part of the first
-        // (of sign, or PAIR, whose loop is straight, of a product of its own: 117.5 us for 3,000 tokens over
-        // e4m3, 120.5 with the tile's scores read again where that changes).
+        // scale, and unit is coef, until m of some row of the warp is past 2^20: then sign takes coef.
         float sign = copysignf(1.0f, scale), unit = coef;
         int steps = 0;
         if (active && ok) {
@@ -559,13 +557,20 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
             }
             const int key0 = key_first + j * kTcBN;
             // the maximum grew: l and (past the slot's first tile) O follow the new reference
-            auto refer = [&](float top) {
+            auto refer = [&](float top, float* s) {
               const bool grow = top > m + slack;  // from -inf: any finite maximum
               if (__any_sync(~0u, grow)) {
                 const bool far = __any_sync(~0u, in && far_score(fmaxf(m, top)));
-                slack = far ? 0.0f : kGrow + kLift;
-                unit = far ? 1.0f : coef;
-                if (!PAIR) sign = far ? signed_coef : copysignf(1.0f, signed_coef);
+                if (far != (slack == 0.0f)) {
+                  if (PAIR) {
+                    const float turn = far ? coef : 1.0f / coef;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) s[i] *= turn;
+                  }
+                  slack = far ? 0.0f : kGrow + kLift;
+                  unit = far ? 1.0f : coef;
+                  sign = far ? signed_coef : copysignf(1.0f, signed_coef);
+                }
                 const float ref = far ? top : top - kLift;
                 const float f = grow ? exp2_approx(m - ref) : 1.0f;
                 if (grow) m = ref;
@@ -625,11 +630,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 for (int e = 0; e < 8; ++e) t8[e] = max3(t8[e], s[i + e], s[i + 8 + e]);
               const float t_a = max3(max3(t8[0], s[120], s[121]), max3(t8[1], s[122], s[123]), t8[2]);
               const float t_b = max3(max3(t8[3], s[124], s[125]), max3(t8[4], s[126], s[127]), t8[5]);
-              refer(max3(max3(t_a, t_b, t8[6]), t8[7], t8[7]) * coef);
-              if (unit != coef) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i) s[i] *= coef;
-              }
+              refer(max3(max3(t_a, t_b, t8[6]), t8[7], t8[7]) * unit, s);
 #pragma unroll
               for (int c = 0; c < 4; ++c) weigh(s + 32 * c, c);
               tmem_st_wait();
@@ -657,7 +658,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 if (i < 4) {
 #pragma unroll
                   for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(s[k], s[k + 1]));
-                  if (i == 3) refer(top * unit);
+                  if (i == 3) refer(top * unit, nullptr);  // the scores are read again
                 } else {
                   weigh(s, c);
                 }

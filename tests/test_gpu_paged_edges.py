@@ -71,9 +71,9 @@ def test_a_tail_of_tiny_weights_over_e4m3(lb, new, D, below):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("new,D", ROWS)
-@pytest.mark.parametrize("scale", [1e3, 3e4, 1e6, 4e7, 3e9])
+@pytest.mark.parametrize("scale", [1e3, 3e4, 1e6, 4e7, 3e9, -1e6, -3e9])
 def test_scores_past_whole_numbers(lb, new, D, scale, fp8):
-    """Scores of 21 * scale for one key and 3 * scale for the others: its value is the output, however
+    """Scores of 21 * |scale| for one key and 3 * |scale| for the others: its value is the output, however
     coarse fp32 is there, but for the rounding of its weight (to bf16 at worst) and of the output, 2^-8
     each, times 1.05.  The logarithm of the sum is the score, good to the few roundings of 2^-24 that
     take it to powers of two and back."""
@@ -83,6 +83,7 @@ def test_scores_past_whole_numbers(lb, new, D, scale, fp8):
     kc = torch.zeros((pages, page, 1, D), device="cuda")
     kc[..., 0] = 1.0
     kc[lead // page, lead % page, 0, 0] = 7.0
+    kc *= 1 if scale > 0 else -1
     vc = torch.randint(-8, 9, (pages, page, 1, D), device="cuda", generator=g).float()
     dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
     q = torch.zeros((B * new, G, D), dtype=torch.bfloat16, device="cuda")
@@ -90,7 +91,39 @@ def test_scores_past_whole_numbers(lb, new, D, scale, fp8):
     out, lse = attend(lb, q, kc.to(dt), vc.to(dt), [new] * B, [kv] * B, [list(range(pages))] * B, causal=False, scale=scale)
     want = vc[lead // page, lead % page, 0].expand_as(out)
     assert bool(((out.float() - want).abs() <= 1.05 * 2.0 ** -7 * want.abs()).all())
-    assert float((lse.double() / (21.0 * scale) - 1.0).abs().max()) <= 2.0 ** -21
+    assert float((lse.double() / (21.0 * abs(scale)) - 1.0).abs().max()) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,D", ROWS)
+@pytest.mark.parametrize("scale", [1e3, -1e3, -2e5])
+def test_scores_that_come_back_from_afar(lb, new, D, scale, fp8):
+    """The first 300 keys score -1,344 |scale|, past whole numbers, and the others next to nothing: their
+    weights are those of ordinary scores (weights and output rounded to 2^-8 each, 1e-4 for fp32 scores,
+    times 1.05; over e4m3 the weights of a warp that comes back are taken as they come, still 2^-8)."""
+    B, G, kv, page = 3, 4, 1000, 32
+    pages = -(-kv // page)
+    g = torch.Generator(device="cuda").manual_seed(new + D)
+    near = torch.randint(-2, 3, (kv,), device="cuda", generator=g) * (2.0 ** -9 if abs(scale) < 1e4 else 2.0 ** -17)
+    if fp8 and abs(scale) > 1e4:
+        near = near * 0                                  # below e4m3's smallest
+    near[:300] = -448.0
+    near = near * (1 if scale > 0 else -1)
+    kc = torch.zeros((pages * page, 1, D), device="cuda")
+    kc[:kv, 0, 0] = near
+    vc = torch.randn((pages * page, 1, D), device="cuda", generator=g)
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    kc, vc = (x.view(pages, page, 1, D).to(dt) for x in (kc, vc))
+    q = torch.zeros((B * new, G, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 3.0
+    out, lse = attend(lb, q, kc, vc, [new] * B, [kv] * B, [list(range(pages))] * B, causal=False, scale=scale)
+    x = 3.0 * scale * near.double()
+    p = torch.softmax(x, 0)
+    v = vc.double().view(-1, D)[:kv]
+    want, spread = p @ v, p @ v.abs()
+    tol = 1.05 * ((2.0 ** -8 + 1e-4) * spread + 2.0 ** -8 * want.abs())
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert float((lse.double() - torch.logsumexp(x, 0)).abs().max()) <= 1e-4
 
 
 # ------------------------------------------------------------------------------------ descriptions
