@@ -127,7 +127,22 @@ __device__ __forceinline__ int key_of(int i) {
 
 struct RingBars {
   uint64_t full[8], empty[8];
+  volatile int failed;  // some lane of the compute warps has given up a wait
 };
+__device__ __forceinline__ void init_bars(RingBars& bars, int stages) {
+  for (int i = 0; i < stages; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 4);
+  bars.failed = 0;
+  fence_mbar_init();
+}
+// A compute warp's wait; after the first one that gives up the warp takes no data and releases no stage, so
+// that the copying warp finds none free and gives up too, and its rows are not stored.
+__device__ __forceinline__ void take_or_fail(const AttnArgs& a, RingBars& bars, uint64_t& bar, uint32_t phase, bool& ok) {
+  if (ok && !mbar_wait(smem_addr(&bar), phase)) {
+    record_error(a.p.err, LOWBIT_ERR_TIMEOUT);
+    bars.failed = 1;
+    ok = false;
+  }
+}
 
 // The copying warp: every key tile of the CTA's share, into the ring as stages come free.
 template <class C, bool FP8>
@@ -163,6 +178,10 @@ __device__ __forceinline__ void copy_tiles(const AttnArgs& a, const CUtensorMap&
         record_error(p.err, LOWBIT_ERR_TIMEOUT);
         ok = false;
         break;
+      }
+      if (a.stall) {  // nothing is copied
+        if (++stage == S) stage = 0, phase ^= 1;
+        continue;
       }
       const uint32_t bar = smem_addr(&bars.full[stage]);
       const int page2 = boxes > 32 ? page_of(kt, 32) : -2;  // pages of one slot: 64 boxes
@@ -210,8 +229,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
   const PagedArgs& p = a.p;
 
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 4);
-    fence_mbar_init();
+    init_bars(bars, S);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -334,10 +352,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
     int last = 0;  // stage of the item's last tile, released after the join
 
     for (int kt = kt0; kt < kt1; ++kt) {
-      if (ok && !mbar_wait(smem_addr(&bars.full[stage]), phase)) {
-        record_error(p.err, LOWBIT_ERR_TIMEOUT);
-        ok = false;
-      }
+      take_or_fail(a, bars, bars.full[stage], phase, ok);
       const uint32_t ks = ring + stage * C::kStage, vs = ks + C::kHalf;
       const int key0 = base_key + kt * kBN;
 
@@ -483,7 +498,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
       last = stage;
       if (kt + 1 < kt1 || MT == 4) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.empty[stage]));
+        if (lane == 0 && ok) mbar_arrive(smem_addr(&bars.empty[stage]));
       }
       if (++stage == S) stage = 0, phase ^= 1;
     }
@@ -542,17 +557,23 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&bars.empty[last]));
+      if (lane == 0 && ok) mbar_arrive(smem_addr(&bars.empty[last]));
     }
 
     // ---- store: the row group's first warp holds its rows
-    if (wk == 0 && ok) {
+    if (wk == 0) {
+      // what other warps added: their failures came before the join's barriers
+      const bool good = MT < 4 ? !bars.failed : __all_sync(~0u, ok);
       const bool whole = kt0 == 0 && kt1 == it.tiles;
       const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (qrow[i] < 0) continue;
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * C::kRows + wr * 16 + g + 8 * i;
+        if (!good) {
+          if (t == 0 && !whole) a.piece_ml[piece] = make_float2(0.0f, kNoPiece);
+          continue;
+        }
         const float f = whole ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
         uint16_t* const dst = a.out + qrow[i] * D;
         float* const part = a.piece_o + piece * D;
@@ -625,8 +646,7 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
   const PagedArgs& p = a.p;
 
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_addr(&bars.full[i]), 1), mbar_init(smem_addr(&bars.empty[i]), 4);
-    fence_mbar_init();
+    init_bars(bars, S);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -714,10 +734,7 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     int last = 0;
 
     for (int kt = kt0; kt < kt1; ++kt) {
-      if (ok && !mbar_wait(smem_addr(&bars.full[stage]), phase)) {
-        record_error(p.err, LOWBIT_ERR_TIMEOUT);
-        ok = false;
-      }
+      take_or_fail(a, bars, bars.full[stage], phase, ok);
       const uint32_t ks = ring + stage * C::kStage, vs = ks + C::kHalf;
       const int key0 = base_key + kt * kBN;
       if (key0 < span.lo || key0 + kBN > span.hi) {  // values outside the span: as in attn_mma_kernel
@@ -818,7 +835,7 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
       last = stage;
       if (kt + 1 < kt1) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.empty[stage]));
+        if (lane == 0 && ok) mbar_arrive(smem_addr(&bars.empty[stage]));
       }
       if (++stage == S) stage = 0, phase ^= 1;
     }
@@ -867,15 +884,20 @@ attn_row8_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     if (warp == 0) take(1);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&bars.empty[last]));
+    if (lane == 0 && ok) mbar_arrive(smem_addr(&bars.empty[last]));
 
-    if (warp == 0 && ok) {
+    if (warp == 0) {
+      const bool good = !bars.failed;  // as in attn_mma_kernel
       const bool whole = kt0 == 0 && kt1 == it.tiles;
       const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (qrow[i] < 0) continue;
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * 8 + 2 * t + i;
+        if (!good) {
+          if (g == 0 && !whole) a.piece_ml[piece] = make_float2(0.0f, kNoPiece);
+          continue;
+        }
         const float f = whole ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
         uint16_t* const dst = a.out + qrow[i] * D;
         float* const part = a.piece_o + piece * D;
@@ -959,8 +981,9 @@ struct Join {
 #pragma unroll
     for (int e = 0; e < ROWS; ++e) {
       float m = ml[e][0].x, l = 0.0f, acc[kParts][kPart] = {};
+      bool all = ml[e][0].y != kNoPiece;
 #pragma unroll
-      for (int k = 1; k < PIECES; ++k) m = fmaxf(m, ml[e][k].x);
+      for (int k = 1; k < PIECES; ++k) m = fmaxf(m, ml[e][k].x), all &= ml[e][k].y != kNoPiece;
 #pragma unroll
       for (int k = 0; k < PIECES; ++k) {
         if (k > n) break;
@@ -971,7 +994,7 @@ struct Join {
 #pragma unroll
           for (int d = 0; d < kPart; ++d) acc[q][d] += f * v[e][k][q][d];
       }
-      if (row + e < end) store(row + e, m, l, acc);
+      if (row + e < end && all) store(row + e, m, l, acc);
     }
   }
   // One row of any number of pieces: the lanes hold the pieces' (maximum, sum), 32 at a time.
@@ -980,10 +1003,12 @@ struct Join {
     for (int i = lane; i <= n; i += 32) m = fmaxf(m, a.piece_ml[place(i, row)].x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     float l = 0.0f, acc[kParts][kPart] = {};
+    bool all = true;
     for (int i0 = 0; i0 <= n; i0 += 32) {
       float f = 0.0f;
       if (i0 + lane <= n) {
         const float2 ml = a.piece_ml[place(i0 + lane, row)];
+        all &= ml.y != kNoPiece;
         f = m == -INFINITY ? 0.0f : ex2(ml.x - m);
         l += f * ml.y;
       }
@@ -1005,7 +1030,7 @@ struct Join {
       }
     }
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    store(row, m, l, acc);
+    if (__all_sync(~0u, all)) store(row, m, l, acc);
   }
 };
 template <int D>
@@ -1181,6 +1206,7 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.piece_ml = reinterpret_cast<float2*>(a.piece_o + (size_t)kMaxPieceRows * D);
   a.cuts = reinterpret_cast<CutItem*>(a.piece_ml + kMaxPieceRows);
   a.wide = (((uintptr_t)out | (uintptr_t)workspace) & 31) == 0;
+  a.stall = debug_stall();
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // By the rows that share a request's keys, on average (the host knows the totals only).  Heads of

@@ -23,6 +23,9 @@ constexpr int kMaxPieceRows = 2 * 152 * 256;
 
 // What a CTA says about the item that its share ends inside of, if it began that item: `more` other
 // CTAs, the ones behind it, have a piece too (0: nothing to join).
+// A piece whose CTA gave up a wait has a sum of -1 in its rows: the combine step leaves what it is part of
+// unwritten.
+constexpr float kNoPiece = -1.0f;
 struct CutItem {
   int more, slot, rows, r0;  // its own piece's slot; the query tile's rows and first row
   int row0, h, pad0, pad1;   // the request's first row, the key/value head
@@ -43,6 +46,8 @@ struct AttnArgs {
   CutItem* cuts;    // [CTA]
   int ctas;
   bool wide;        // out and the pieces start on 32-byte boundaries
+  int stall;        // test-only stall setting (lowbit_debug_inject_stall), under which the first data (tiles,
+                    // or queries on tcgen05) never come, so that every role's wait gives up; 0 in normal use
 };
 
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);

@@ -286,7 +286,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       for (int i = 0; i < filled; ++i) {
         if (--stage < 0) stage = kDepth - 1, phase ^= 1;
         mbar_wait(smem_addr(&full[stage]), phase);
-        if (ok) mbar_wait(smem_addr(&empty[stage]), phase);
+        if (ok) WAIT_OR(empty[stage], phase, ok = false);
       }
     } else if (FP8 && warp >= kConvertWarp) {
       // ------------------------------------------------------------------ e4m3 to 16 bits
@@ -333,7 +333,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       });
       for (int i = 0; i < filled; ++i) {  // every release has arrived
         if (--stage < 0) stage = S - 1, phase ^= 1;
-        if (ok) mbar_wait(smem_addr(&sh.kv_empty[stage]), phase);
+        if (ok) WAIT_OR(sh.kv_empty[stage], phase, ok = false);
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------ MMA issue
@@ -484,7 +484,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSide));
       uint32_t free_phase = 1;  // the place is free to begin with
       for (;;) {
-        if (walk_take(it, left) == 0) break;
+        if (a.stall || walk_take(it, left) == 0) break;
         WAIT_OR(sh.q_free, free_phase, break);
         free_phase ^= 1;
         constexpr int kChunks = D / 8;
@@ -745,6 +745,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         }
         first = false;
         if (left <= 0 || !walk_next(a, it)) break;
+      }
+      if (!ok) {  // neither piece of this row is to be joined
+        for (int i = 0; i < 2; ++i)
+          a.piece_ml[(2LL * blockIdx.x + i) * kRows + (PAIR ? slot * 128 : 0) + row] = make_float2(0.0f, kNoPiece);
       }
     }
   }

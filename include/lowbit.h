@@ -511,8 +511,10 @@ lowbit_status lowbit_draft_argmax_path(const uint16_t* H, const void* packed_hea
  * wait then ends after about a millisecond instead of about a second.  Such a call writes no
  * output (Y, argmax, n_accept, bonus, ids keep their previous contents), leaves the LM-head
  * workspace zeroed, and records LOWBIT_ERR_TIMEOUT in the device error word.  A CTA still
- * waits for its own copies in flight before it exits.  The tcgen05 and CUDA-core kernels are
- * not affected.  The setting is process-wide; pass 0 to restore normal operation. */
+ * waits for its own copies in flight before it exits.  lowbit_paged_attention's kernels then get no data
+ * (no key tiles, or on tcgen05 no queries): every role's wait runs out, after about a second, and
+ * neither out nor lse is written.  The other tcgen05 kernels and the CUDA-core kernels are not
+ * affected.  The setting is process-wide; pass 0 to restore normal operation. */
 lowbit_status lowbit_debug_inject_stall(int on);
 
 /* Synchronises `stream`, then returns (in *status_out) and clears the current device's
