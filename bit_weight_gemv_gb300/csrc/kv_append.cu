@@ -17,6 +17,8 @@
 
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 namespace lowbit {
 namespace {
 
@@ -171,7 +173,13 @@ cudaError_t launch(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
 }
 template <int D>
 cudaError_t launch_tokens(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
-  return a.p.T > 1520 ? launch<D, 8>(a, fp8, inter, s) : launch<D, 1>(a, fp8, inter, s);
+  // One token per block finishes soonest while the blocks come in few waves of 760; eight share the lookup
+  // and fill the block where a token has few units of 16 elements.  us with one / eight, bf16: 40 units a
+  // token, 608 tokens 2.4 / 3.4, 1,216 3.8 / 3.5; 96 units, 1,216 4.1 / 4.1, 1,824 5.5 / 4.5; 192 units, 2,432
+  // 8.5 / 9.1, 3,648 13.5 / 12.1; 256 units, 3,040 12.8 / 15.2, 4,864 19.0 / 19.6; 384 units, 1,824 12.3 / 17.1,
+  // 3,648 20.9 / 21.1, 6,080 31.9 / 27.1; 640 units, 3,952 32.1 / 34.4, 4,864 38.3 / 37.8.
+  const long long units = (long long)((a.q ? a.Hq : 0) + 2 * a.p.Hk) * (D / 16);
+  return a.p.T > std::max(1000LL, std::min(16 * units, 4000LL)) ? launch<D, 8>(a, fp8, inter, s) : launch<D, 1>(a, fp8, inter, s);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
