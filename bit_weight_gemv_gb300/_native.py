@@ -2,9 +2,12 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
+
+from .build import binding_path
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblowbit.so")
 
@@ -13,7 +16,36 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-from . import _binding  # noqa: E402  (built beside the library; its absence is an ImportError too)
+
+class _NoBinding:
+    """Stands for the compiled binding where it is missing or does not load: the calls that go through it
+    raise ImportError, the others only look their stream up in torch."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._why}: build it with `python -m bit_weight_gemv_gb300.build`")
+
+    @staticmethod
+    def current_stream():
+        return torch.cuda.current_stream().cuda_stream
+
+
+def _load_binding():
+    path = binding_path()
+    if not os.path.exists(path):
+        return _NoBinding(f"{path} is missing")
+    spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        return _NoBinding(f"{path} does not load ({e})")
+
+
+_binding = _load_binding()
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -88,8 +120,9 @@ for _name, (_res, _args) in _SIGS.items():
     _f.argtypes = _args
 
 
-_binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
-                for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample")))
+if not isinstance(_binding, _NoBinding):
+    _binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
+                    for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample")))
 
 
 class LowbitError(RuntimeError):

@@ -2,8 +2,8 @@
 
 Each CUDA translation unit under csrc/ is compiled in parallel to an object file in
 _build/, then the objects are linked into bit_weight_gemv_gb300/liblowbit.so; beside them the host
-compiler builds csrc/binding.cpp into bit_weight_gemv_gb300/_binding.so (tensor arguments of the
-small calls, see there).  Objects are rebuilt only when a source or header is newer.
+compiler builds csrc/binding.cpp (tensor arguments of the small calls, see there) into a module that
+is named after the torch and the Python it reads the tensors of.  Objects are rebuilt only when a source or header is newer.
 Usage: ``python -m bit_weight_gemv_gb300.build``.
 """
 from __future__ import annotations
@@ -21,7 +21,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblowbit.so")
-BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -46,8 +45,15 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_path() -> str:
+    """The compiled binding for the torch and the Python that run now: its inline accessors know one
+    layout of a tensor, so another version's file is never loaded, and never taken as up to date."""
+    import torch
+    return os.path.join(PKG, f"_binding-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _binding_command():
-    """The host compiler's command for _binding.so (torch's own libraries carry the symbols)."""
+    """The host compiler's command for the binding (torch's own libraries carry the symbols)."""
     import torch
     home = os.path.dirname(torch.__file__)
     inc, libs = os.path.join(home, "include"), os.path.join(home, "lib")
@@ -55,7 +61,7 @@ def _binding_command():
             "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
             "-I" + sysconfig.get_paths()["include"],
             "-I" + os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
-            os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+            os.path.join(CSRC, "binding.cpp"), "-o", binding_path() + ".tmp",
             "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
@@ -76,9 +82,12 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    stale_binding = _stale(BINDING, [os.path.join(CSRC, "binding.cpp")] + headers)
-    if stale_binding:
-        jobs.append(_binding_command())
+    binding = binding_path()
+    binding_job = None
+    if _stale(binding, [os.path.join(CSRC, "binding.cpp")] + headers):
+        binding_job = _binding_command()
+        jobs.append(binding_job)
+    binding_error = None
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -89,10 +98,12 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             for cmd, r in ex.map(run, jobs):
                 if verbose or ptxas_info or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
-                if r.returncode != 0:
+                if r.returncode != 0 and cmd is binding_job:  # the library does without
+                    binding_error = "compilation failed: " + " ".join(cmd)
+                elif r.returncode != 0:
                     raise RuntimeError("compilation failed: " + " ".join(cmd))
-    if stale_binding:
-        os.replace(BINDING + ".tmp", BINDING)
+    if binding_job and not binding_error:
+        os.replace(binding + ".tmp", binding)
     if jobs or not os.path.exists(LIB) or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
@@ -101,6 +112,8 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    if binding_error:
+        raise RuntimeError(binding_error)
     return LIB
 
 
