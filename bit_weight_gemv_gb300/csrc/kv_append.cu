@@ -8,8 +8,8 @@
 // Bound: memory.  Each of q, k and v is read once and written once, plus 4 * rot bytes of table
 // per token; nothing is shared between tokens, so a thread takes 16 elements of one head of one
 // token: the two 8-element vectors that hold 8 whole pairs, as 16-byte accesses.  A block takes one
-// token, or eight in long calls.  16,665 tokens of 32 + 8 + 8 heads of 128, bf16: 49.5 us, 261 MB,
-// 5.3 TB/s of 6.8 copied (57 us with one token per block); 512 tokens into an e4m3 cache 4.0 us, one
+// token, or eight in long calls.  16,665 tokens of 32 + 8 + 8 heads of 128, bf16: 49.4 us, 261 MB,
+// 5.3 TB/s of 6.8 copied (57 us with one token per block); 512 tokens into an e4m3 cache 3.9 us, one
 // token 2.9 us, which is a launch and two dependent loads (the page, then the data).
 #include "common.cuh"
 #include "paged.cuh"

@@ -12,9 +12,14 @@
 // The grid is resident and the work is cut evenly over it (see paged.cuh); attn_combine_kernel
 // joins items that were cut.
 //
+// The weights exp(s_j - m) enter their product as bf16, or over an e4m3 cache as fp16: the MMA takes 16-bit
+// operands, and of the two each goes with a type that holds the values exactly.  l sums the weights
+// as they were in fp32, so the rounding (at most 2^-8, or 2^-11, of a weight) shows in the output alone: an error of
+// 0.0023 of it over 32,765 bf16 keys, of which 0.0017 is the output's own rounding.
+//
 // Bound: few rows per key/value head read the cache once and are bound by HBM, plus what a call pays
-// whatever its size (start, an empty pipeline, the combine step: 7.4 us for one row over 777 keys).
-// 64 ragged requests of one token over an e4m3 cache: 38.4 us, 176 MB, 4.6 TB/s; 32 rows of one
+// whatever its size (start, an empty pipeline, the combine step: 7.8 us for one row over 777 keys).
+// 64 ragged requests of one token over an e4m3 cache: 39.2 us, 176 MB, 4.5 TB/s; 32 rows of one
 // request over 30,000 bf16 keys: 38.7 us, 123 MB, 3.2 TB/s (the copy rate is 6.8).
 #include "common.cuh"
 #include "paged.cuh"
@@ -609,7 +614,7 @@ attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUte
 // sides, so that the keys, not the rows, fill the MMA's 16: S^T = K Q^T and O^T = V^T P^T, half the MMAs and half
 // the exponentials of the 16-row kernel.  A lane holds two keys' scores of rows 2t and 2t + 1; P^T
 // becomes the other operand by an 8 x 8 transpose of its 16-bit pairs.  64 requests of 1 to 16,384 keys
-// over an e4m3 cache: 47.4 us on the 16-row kernel, whose issue slots were the limit, 38.4 us here.
+// over an e4m3 cache: 47.4 us on the 16-row kernel, whose issue slots were the limit, 39.2 us here.
 template <int D, bool FP8>
 struct Cfg8 {
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
@@ -1209,7 +1214,9 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
   a.stall = debug_stall();
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // By the rows that share a request's keys, on average (the host knows the totals only).  Heads of
+  // By the rows that share a request's keys, on average (the host knows the totals only; a request that
+  // differs from the average is computed right and slowly).  At 32 rows each side wins somewhere, the warp-level
+  // MMA on short contexts and where the start counts, tcgen05 on long ones; above, tcgen05 nearly always.  Heads of
   // 128, one request of 30,000 keys, us on the warp-level MMA / tcgen05 with 128 rows an item / with
   // 256: 32 rows 38.7 / 36.3 / 51.8, 64 rows 47.8 / 37.6 / 59.8, 400 rows 189 / 81 / 101; of 500 keys
   // 9.6 / 11 / 13 with 32 rows.  Heads of 64: 48 rows 29.8 / 26.1, 32 requests of up to 16,000 keys 48.0 /

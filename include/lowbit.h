@@ -392,7 +392,8 @@ lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16
                                uint16_t* q_out, void* stream);
 
 /* Bytes of lowbit_paged_attention's workspace for up to T rows and B requests of Hq query and
- * Hk key/value heads of D (0 for invalid shapes). */
+ * Hk key/value heads of D (0 for invalid shapes): enough for the pieces of the largest grid, so it
+ * depends on D alone (21, 40 or 80 MB for heads of 64, 128 or 256); one serves every call on a stream. */
 size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D);
 
 /* Attention of every request's new tokens over its cached keys, grouped heads (query head h
@@ -400,6 +401,8 @@ size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int 
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j over the keys j the token sees:
  *   j < kv_lens[b]; j <= its position when `causal`; j > its position - window when window > 0.
  *   A token that sees no key gets zeros, and -inf as lse.
+ *   Requests should be alike in new tokens: the kernel is chosen by their average (T / B).  width *
+ *   page_size is at most 2^31 - 256 here.
  *   q   : bf16 [T][Hq][D], token stride q_stride (elements, a multiple of 8), 16-byte aligned.
  *   out : bf16 [T][Hq][D] dense, 16-byte aligned.    lse : fp32 [T][Hq] or NULL: the natural
  *   logarithm of the softmax's denominator (log sum_j exp(scale * q . k_j)).
