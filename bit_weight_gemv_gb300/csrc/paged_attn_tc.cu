@@ -24,13 +24,14 @@
 // refer to the largest itself.
 //
 // Bound: the tensor pipe, shared memory and the issuing thread together.  A prompt chunk of 4,001
-// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 666 to 675 us call after call under the power
-// limit, 1,400 TFLOP/s, 81% of a large library product there; 638 us in bursts, 1,472 TFLOP/s, 77%. S = Q K^T reads both operands from shared memory, and an MMA comes every
-// 81 cycles for 64 of work.  Few rows are bound by the chain of a tile (scores, softmax, product, 3 us on
-// two slots in turn): one request's 64 rows over 32,765 keys 34.6 us, 134 MB, 3.9 TB/s; 24 ragged requests of
-// 64 rows 51.8 us, 246 MB, 4.7 TB/s.  Over e4m3 caches the
-// conversion takes issue slots from the softmax: 1,200 tokens over 4,000 keys 91 us (80 in bf16, 250 on the
-// warp-level MMA); 64 rows over 32,765 keys 34.0 us (54 on the warp-level MMA).
+// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 666 to 675 us call after call under
+// the power limit, 1,400 TFLOP/s, 81% of a large library product there; 638 us in bursts, 1,472 TFLOP/s,
+// 77%.  S = Q K^T reads both operands from shared memory, and an MMA comes every 81 cycles for 64 of
+// work.  Few rows are bound by the chain of a tile (scores, softmax, product, 3 us on two slots in turn):
+// one request's 64 rows over 32,765 keys 34.6 us, 134 MB, 3.9 TB/s; 24 ragged requests of 64 rows 51.8 us,
+// 246 MB, 4.7 TB/s.  Over e4m3 caches the conversion takes issue slots from the softmax: 1,200 tokens over
+// 4,000 keys 91 us (80 in bf16, 250 on the warp-level MMA); 64 rows over 32,765 keys 34.0 us (54 on the
+// warp-level MMA).
 #include <cuda_fp16.h>
 
 #include <type_traits>

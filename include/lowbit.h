@@ -410,8 +410,8 @@ size_t lowbit_paged_attention_workspace_bytes(int T, int B, int Hq, int Hk, int 
  *   Scores, softmax statistics and outputs are held in fp32; the softmax weights enter their
  *   product with v rounded to bf16 (bf16 cache) or fp16 (e4m3 cache), 2^-8 or 2^-11 of themselves at
  *   most (over an e4m3 cache, weights under 2^-21 of the row's largest by 2^-32 of that one).  Slots
- *   outside a request's span are never used, whatever they hold.  A key that the mask hides from a token does not reach
- *   it, whatever it holds; a non-finite value v inside the span may (0 * inf is NaN), through the
+ *   outside a request's span are never used, whatever they hold.  A key that the mask hides from a
+ *   token does not reach it, whatever it holds; a non-finite value v inside the span may (0 * inf is NaN), through the
  *   up to 256 rows of one request and head that are computed together.  The result does not depend
  *   on timing: the same call gives the same bits. */
 lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq,
