@@ -24,7 +24,7 @@
 // refer to the largest itself.
 //
 // Bound: the tensor pipe, shared memory and the issuing thread together.  A prompt chunk of 4,001
-// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 666 to 675 us call after call under
+// tokens over 16,331 keys (32 heads on 8 of 128, causal, 939 GFLOP): 664 to 675 us call after call under
 // the power limit, 1,400 TFLOP/s, 81% of a large library product there; 638 us in bursts, 1,472 TFLOP/s,
 // 77%.  S = Q K^T reads both operands from shared memory, and an MMA comes every 81 cycles for 64 of
 // work.  Few rows are bound by the chain of a tile (scores, softmax, product, 3 us on two slots in turn):
@@ -546,6 +546,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
         // the subtraction of m: sign is 1 or -1, so that the largest stays the largest under a negative
         // scale, and unit is coef, until m of some row of the warp is past 2^20: then sign takes coef.
         float sign = copysignf(1.0f, scale), unit = coef;
+        bool turned = scale < 0.0f;
         int steps = 0;
         if (active && ok) {
           for (int j = PAIR ? 0 : slot; j < n; j += PAIR ? 1 : 2, ++steps) {
@@ -571,6 +572,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                   slack = far ? 0.0f : kGrow + kLift;
                   unit = far ? 1.0f : coef;
                   sign = far ? signed_coef : copysignf(1.0f, signed_coef);
+                  turned = far || scale < 0.0f;
                 }
                 const float ref = far ? top : top - kLift;
                 const float f = grow ? exp2_approx(m - ref) : 1.0f;
@@ -613,7 +615,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
 #pragma unroll
               for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
               tmem_ld_wait();
-              if (sign != 1.0f) {
+              if (turned) {
 #pragma unroll
                 for (int i = 0; i < 128; ++i) s[i] *= sign;
               }
@@ -646,7 +648,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUten
                 float s[32];
                 tmem_ld32(s_at + 32 * c, s);
                 tmem_ld_wait();
-                if (sign != 1.0f) {
+                if (turned) {
 #pragma unroll
                   for (int k = 0; k < 32; ++k) s[k] *= sign;
                 }
