@@ -24,7 +24,7 @@ __all__ = [
     "lmhead_argmax_partial", "lmhead_accept_keys",
     "lowbit_q8_packed_bytes", "lowbit_pack_q8", "lowbit_gemm_q8", "lowbit_gemm_q8_path",
     "lowbit_draft_argmax_q8",
-    "lowbit_paged_cache", "lowbit_kv_append", "lowbit_paged_attention",
+    "lowbit_paged_cache", "lowbit_kv_append", "lowbit_kv_append_norm", "lowbit_paged_attention",
     "lowbit_paged_attention_workspace_bytes", "lowbit_sample",
 ]
 

@@ -109,6 +109,8 @@ class _PagedCache(ctypes.Structure):
 _i64 = ctypes.c_int64
 _SIGS["lowbit_kv_append"] = (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _i, _i, _i,
                                   _vp, ctypes.POINTER(_PagedCache), _vp, _vp])
+_SIGS["lowbit_kv_append_norm"] = (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _vp, _vp, ctypes.c_float, _vp, _i, _i,
+                                       _i, _vp, ctypes.POINTER(_PagedCache), _vp, _vp])
 _SIGS["lowbit_paged_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
 _SIGS["lowbit_paged_attention"] = (_i, [_vp, _i64, _i, _vp,
                                         ctypes.POINTER(_PagedCache), ctypes.c_float, _i, _i, _vp,
@@ -122,7 +124,8 @@ for _name, (_res, _args) in _SIGS.items():
 
 if not isinstance(_binding, _NoBinding):
     _binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
-                    for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample")))
+                    for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample",
+                                  "lowbit_kv_append_norm")))
 
 
 class LowbitError(RuntimeError):
@@ -522,6 +525,16 @@ def lowbit_kv_append(q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, in
                             _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_kv_append")
+
+
+def lowbit_kv_append_norm(q, k, v, q_weight, k_weight, eps, rope, cu_q, kv_lens, block_table, cache, q_out,
+                          interleaved=False, stream=None):
+    """lowbit_kv_append with each head of q and k divided by its root mean square (plus eps under the
+    root) and multiplied by q_weight or k_weight, fp32 [D] (None: not normalised), before the rotation."""
+    st = _binding.kv_append_norm(q, k, v, q_weight, k_weight, eps, rope, cu_q, kv_lens, block_table, cache.address,
+                                 q_out, interleaved, _handle(stream))
+    if st:
+        raise LowbitError(st, "lowbit_kv_append_norm")
 
 
 def lowbit_paged_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int) -> int:

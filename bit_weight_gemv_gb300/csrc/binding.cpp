@@ -22,6 +22,7 @@ using at::ScalarType;
 using at::Tensor;
 
 decltype(&lowbit_kv_append) g_append;
+decltype(&lowbit_kv_append_norm) g_append_norm;
 decltype(&lowbit_paged_attention) g_attention;
 decltype(&lowbit_sample) g_sample;
 
@@ -97,35 +98,63 @@ bool count_is(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
-// q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved, stream
-PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void *cache_at, *stream;
-  if (!count_is(n, 11) || !address(a[7], &cache_at)) return nullptr;
-  const lowbit_paged_cache* cache = static_cast<const lowbit_paged_cache*>(cache_at);
-  const int64_t D = cache->head_dim;
+// What both append calls take: q, k, v and, from `rest` on, rope, cu_q, kv_lens, block_table, cache, q_out,
+// interleaved, stream.
+struct Append {
   Rows q = {nullptr, 0, 0, 0}, k, v;
-  if (!rows(a[1], D, "k", &k) || !rows(a[2], D, "v", &v)) return nullptr;
-  if (v.T != k.T || k.heads != cache->heads || v.heads != k.heads)
-    return fail(PyExc_ValueError, "k and v", "must have the same rows and the cache's heads"), nullptr;
-  uint16_t* q_out = nullptr;
-  if ((a[0] == Py_None) != (a[8] == Py_None)) return fail(PyExc_ValueError, "q and q_out", "go together"), nullptr;
-  if (a[0] != Py_None) {
-    if (!rows(a[0], D, "q", &q) || !dense(a[8], ScalarType::BFloat16, k.T * q.heads * D, "q_out", false, &q_out)) return nullptr;
-    if (q.T != k.T) return fail(PyExc_ValueError, "q", "must have k's rows"), nullptr;
-  }
   const float* rope = nullptr;
   int64_t positions = 0, rot = 0;
-  if (a[3] != Py_None) {
-    if (!dense(a[3], ScalarType::Float, -1, "rope", false, &rope)) return nullptr;
-    const Tensor& t = THPVariable_Unpack(a[3]);
-    if (t.dim() != 2) return fail(PyExc_ValueError, "rope", "must have shape [positions][rot]"), nullptr;
-    positions = std::min<int64_t>(t.size(0), INT32_MAX), rot = std::min<int64_t>(t.size(1), INT32_MAX);
-  }
-  const int interleaved = PyObject_IsTrue(a[9]);
   lowbit_paged_batch b;
-  if (interleaved < 0 || !batch(a[4], a[5], a[6], k.T, &b) || !stream_of(a[10], &stream)) return nullptr;
-  return PyLong_FromLong(g_append(q.at, q.stride, k.at, k.stride, v.at, v.stride, (int)q.heads, rope, (int)positions,
-                                  (int)rot, interleaved, &b, cache, q_out, stream));
+  const lowbit_paged_cache* cache;
+  uint16_t* q_out = nullptr;
+  int interleaved;
+  void* stream;
+};
+bool append_args(PyObject* const* a, PyObject* const* rest, Append* s) {
+  void* cache_at;
+  if (!address(rest[4], &cache_at)) return false;
+  s->cache = static_cast<const lowbit_paged_cache*>(cache_at);
+  const int64_t D = s->cache->head_dim;
+  if (!rows(a[1], D, "k", &s->k) || !rows(a[2], D, "v", &s->v)) return false;
+  if (s->v.T != s->k.T || s->k.heads != s->cache->heads || s->v.heads != s->k.heads)
+    return fail(PyExc_ValueError, "k and v", "must have the same rows and the cache's heads");
+  if ((a[0] == Py_None) != (rest[5] == Py_None)) return fail(PyExc_ValueError, "q and q_out", "go together");
+  if (a[0] != Py_None) {
+    if (!rows(a[0], D, "q", &s->q) || !dense(rest[5], ScalarType::BFloat16, s->k.T * s->q.heads * D, "q_out", false, &s->q_out))
+      return false;
+    if (s->q.T != s->k.T) return fail(PyExc_ValueError, "q", "must have k's rows");
+  }
+  if (rest[0] != Py_None) {
+    if (!dense(rest[0], ScalarType::Float, -1, "rope", false, &s->rope)) return false;
+    const Tensor& t = THPVariable_Unpack(rest[0]);
+    if (t.dim() != 2) return fail(PyExc_ValueError, "rope", "must have shape [positions][rot]");
+    s->positions = std::min<int64_t>(t.size(0), INT32_MAX), s->rot = std::min<int64_t>(t.size(1), INT32_MAX);
+  }
+  s->interleaved = PyObject_IsTrue(rest[6]);
+  return s->interleaved >= 0 && batch(rest[1], rest[2], rest[3], s->k.T, &s->b) && stream_of(rest[7], &s->stream);
+}
+
+// q, k, v, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved, stream
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Append s;
+  if (!count_is(n, 11) || !append_args(a, a + 3, &s)) return nullptr;
+  return PyLong_FromLong(g_append(s.q.at, s.q.stride, s.k.at, s.k.stride, s.v.at, s.v.stride, (int)s.q.heads, s.rope,
+                                  (int)s.positions, (int)s.rot, s.interleaved, &s.b, s.cache, s.q_out, s.stream));
+}
+
+// q, k, v, q_weight, k_weight, eps, rope, cu_q, kv_lens, block_table, cache, q_out, interleaved, stream
+PyObject* kv_append_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Append s;
+  const float *q_weight, *k_weight;
+  if (!count_is(n, 14)) return nullptr;
+  const double eps = PyFloat_AsDouble(a[5]);
+  if (PyErr_Occurred() || !append_args(a, a + 6, &s) ||
+      !dense(a[3], ScalarType::Float, s.cache->head_dim, "q_weight", true, &q_weight) ||
+      !dense(a[4], ScalarType::Float, s.cache->head_dim, "k_weight", true, &k_weight))
+    return nullptr;
+  return PyLong_FromLong(g_append_norm(s.q.at, s.q.stride, s.k.at, s.k.stride, s.v.at, s.v.stride, (int)s.q.heads,
+                                       q_weight, k_weight, (float)eps, s.rope, (int)s.positions, (int)s.rot,
+                                       s.interleaved, &s.b, s.cache, s.q_out, s.stream));
 }
 
 // q, cache, cu_q, kv_lens, block_table, out, workspace, scale, causal, window, lse, stream
@@ -187,15 +216,16 @@ PyObject* current_stream(PyObject*, PyObject* const*, Py_ssize_t n) {
   return count_is(n, 0) && stream_of(Py_None, &stream) ? PyLong_FromVoidPtr(stream) : nullptr;
 }
 
-// The three entry points' addresses in the loaded library.
+// The entry points' addresses in the loaded library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[3];
-  if (!count_is(n, 3)) return nullptr;
-  for (int i = 0; i < 3; ++i)
+  void* p[4];
+  if (!count_is(n, 4)) return nullptr;
+  for (int i = 0; i < 4; ++i)
     if (!address(a[i], &p[i])) return nullptr;
   g_append = reinterpret_cast<decltype(g_append)>(p[0]);
   g_attention = reinterpret_cast<decltype(g_attention)>(p[1]);
   g_sample = reinterpret_cast<decltype(g_sample)>(p[2]);
+  g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[3]);
   Py_RETURN_NONE;
 }
 
@@ -217,6 +247,7 @@ PyCFunction entry() {
 PyMethodDef kMethods[] = {{"bind", entry<bind>(), METH_FASTCALL, nullptr},
                           {"current_stream", entry<current_stream>(), METH_FASTCALL, nullptr},
                           {"kv_append", entry<kv_append>(), METH_FASTCALL, nullptr},
+                          {"kv_append_norm", entry<kv_append_norm>(), METH_FASTCALL, nullptr},
                           {"paged_attention", entry<paged_attention>(), METH_FASTCALL, nullptr},
                           {"sample", entry<sample>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

@@ -31,6 +31,9 @@ struct AppendArgs {
   const float* rope;
   int rope_rows, rot, Hq;
   uint16_t* q_out;
+  const float* q_weight;  // of the norm (kv_append_norm_kernel alone)
+  const float* k_weight;
+  float eps;
 };
 
 __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
@@ -57,6 +60,69 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
   return make_uint2(w[0], w[1]);
 }
 
+// Where token t goes, found by a warp: its position and page, or position -1 for a row that belongs to no
+// request or has no place (which the device error word then says).
+struct Spot {
+  int pos, page;
+};
+__device__ __forceinline__ Spot find_spot(const AppendArgs& a, int t, int lane) {
+  const PagedArgs& p = a.p;
+  // its request: the first one whose rows it is among
+  int b = p.B, row0 = 0, end = 0, kv = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int from = 0, to = 0, len = 0;
+    if (b0 + lane < p.B) from = p.cu_q[b0 + lane], to = p.cu_q[b0 + lane + 1], len = p.kv_lens[b0 + lane];
+    if (to < from) record_error(p.err, LOWBIT_ERR_INVALID_ARG);
+    const uint32_t in = __ballot_sync(~0u, from <= t && t < to);
+    if (in && b == p.B) {
+      const int src = __ffs(in) - 1;
+      b = b0 + src;
+      row0 = __shfl_sync(~0u, from, src), end = __shfl_sync(~0u, to, src), kv = __shfl_sync(~0u, len, src);
+    }
+  }
+  Spot s = {-1, -1};
+  if (t < p.T && b < p.B) {
+    const Request r = check_request(p, row0, end, kv);
+    if (t - r.row0 < r.n) {
+      s.pos = r.kv - r.n + (t - r.row0);
+      const bool in = s.pos >= 0 && (a.rot == 0 || s.pos < a.rope_rows);
+      if (in) s.page = p.table[(long long)b * p.table_stride + (s.pos >> p.page_shift)];
+      if (!in || s.page < 0 || s.page >= p.pages) {
+        record_error(p.err, LOWBIT_ERR_INVALID_ARG);
+        s.pos = -1;
+      }
+    }
+  }
+  return s;
+}
+// Eight pairs of a thread turned: (x[i], y[i]), or neighbours of x and then of y.
+template <bool INTER>
+__device__ __forceinline__ void turn8(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& e = INTER ? (i < 4 ? x[2 * i] : y[2 * (i - 4)]) : x[i];
+    float& f = INTER ? (i < 4 ? x[2 * i + 1] : y[2 * (i - 4) + 1]) : y[i];
+    const float e0 = e, f0 = f;
+    e = __fsub_rn(__fmul_rn(e0, c[i]), __fmul_rn(f0, s[i]));
+    f = __fadd_rn(__fmul_rn(f0, c[i]), __fmul_rn(e0, s[i]));
+  }
+}
+// A thread's 16 elements of head h into the slot at byte `slot` of the keys or values.
+template <bool FP8>
+__device__ __forceinline__ void store_cache(const PagedArgs& p, bool key, long long slot, int h, int ia, int ib,
+                                            const float (&x)[8], const float (&y)[8]) {
+  uint8_t* dst = (key ? p.k : p.v) + slot + (long long)h * p.head_stride;
+  if (FP8) {
+    const float* sc = key ? p.k_scale : p.v_scale;
+    const float scale = sc ? __ldg(sc + h) : 1.0f;
+    *reinterpret_cast<uint2*>(dst + ia) = pack8_e4m3(x, scale);
+    *reinterpret_cast<uint2*>(dst + ib) = pack8_e4m3(y, scale);
+  } else {
+    *reinterpret_cast<uint4*>(dst + 2 * ia) = pack8(x);
+    *reinterpret_cast<uint4*>(dst + 2 * ib) = pack8(y);
+  }
+}
+
 template <int D, bool FP8, bool INTER, int TOKENS>
 __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kPer = D / 16;  // threads per head
@@ -69,34 +135,8 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
 
   // a warp looks up each token's place
   if (tid < 32 * TOKENS) {
-    const int t = t0 + (tid >> 5);
-    // its request: the first one whose rows it is among
-    int b = p.B, row0 = 0, end = 0, kv = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int from = 0, to = 0, len = 0;
-      if (b0 + lane < p.B) from = p.cu_q[b0 + lane], to = p.cu_q[b0 + lane + 1], len = p.kv_lens[b0 + lane];
-      if (to < from) record_error(p.err, LOWBIT_ERR_INVALID_ARG);
-      const uint32_t in = __ballot_sync(~0u, from <= t && t < to);
-      if (in && b == p.B) {
-        const int src = __ffs(in) - 1;
-        b = b0 + src;
-        row0 = __shfl_sync(~0u, from, src), end = __shfl_sync(~0u, to, src), kv = __shfl_sync(~0u, len, src);
-      }
-    }
-    int pos = -1, page = -1;
-    if (t < p.T && b < p.B) {
-      const Request r = check_request(p, row0, end, kv);
-      if (t - r.row0 < r.n) {
-        pos = r.kv - r.n + (t - r.row0);
-        const bool in = pos >= 0 && (a.rot == 0 || pos < a.rope_rows);
-        if (in) page = p.table[(long long)b * p.table_stride + (pos >> p.page_shift)];
-        if (!in || page < 0 || page >= p.pages) {
-          record_error(p.err, LOWBIT_ERR_INVALID_ARG);
-          pos = -1;
-        }
-      }
-    }
-    if (lane == 0) s_pos[tid >> 5] = pos, s_page[tid >> 5] = page;
+    const Spot s = find_spot(a, t0 + (tid >> 5), lane);
+    if (lane == 0) s_pos[tid >> 5] = s.pos, s_page[tid >> 5] = s.page;
   }
   __syncthreads();
 
@@ -126,14 +166,7 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
       *reinterpret_cast<float4*>(c + 4) = __ldg(pc + 1);
       *reinterpret_cast<float4*>(s) = __ldg(ps);
       *reinterpret_cast<float4*>(s + 4) = __ldg(ps + 1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float& e = INTER ? (i < 4 ? x[2 * i] : y[2 * (i - 4)]) : x[i];
-        float& f = INTER ? (i < 4 ? x[2 * i + 1] : y[2 * (i - 4) + 1]) : y[i];
-        const float e0 = e, f0 = f;
-        e = __fsub_rn(__fmul_rn(e0, c[i]), __fmul_rn(f0, s[i]));
-        f = __fadd_rn(__fmul_rn(f0, c[i]), __fmul_rn(e0, s[i]));
-      }
+      turn8<INTER>(x, y, c, s);
     }
     if (kind == 0) {
       uint16_t* dst = a.q_out + ((long long)t * a.Hq + h) * D;
@@ -141,15 +174,106 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
       *reinterpret_cast<uint4*>(dst + ib) = pack8(y);
       continue;
     }
-    uint8_t* dst = (kind == 1 ? p.k : p.v) + slot + (long long)h * p.head_stride;
-    if (FP8) {
-      const float* sc = kind == 1 ? p.k_scale : p.v_scale;
-      const float scale = sc ? __ldg(sc + h) : 1.0f;
-      *reinterpret_cast<uint2*>(dst + ia) = pack8_e4m3(x, scale);
-      *reinterpret_cast<uint2*>(dst + ib) = pack8_e4m3(y, scale);
-    } else {
-      *reinterpret_cast<uint4*>(dst + 2 * ia) = pack8(x);
-      *reinterpret_cast<uint4*>(dst + 2 * ib) = pack8(y);
+    store_cache<FP8>(p, kind == 1, slot, h, ia, ib, x, y);
+  }
+}
+
+// With a norm of each head of q and k before the rotation:
+//   y = x * r * w,  r = 1 / sqrt(sum x^2 / D + eps),
+// everything in fp32 from the bf16 elements to the one rounding of what is stored.
+//
+// WARPS warps take a token, or one does (WARPS = 1): 32 lanes hold 512 elements, D / 16 lanes a head, so that
+// a head's sum of squares is a few exchanges between neighbouring lanes, the lane's part of the angles stays in
+// registers over the token's heads, and no warp waits for another.  The first heads are asked for before the
+// token's place is known.
+template <int D, bool FP8, bool INTER, int WARPS>
+__global__ void __launch_bounds__(256, 3) kv_append_norm_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kPer = D / 16, kHeads = 32 / kPer;  // lanes per head, heads per step of a warp
+  constexpr int kBatch = WARPS == 1 ? 2 : 1;        // steps asked for together
+  const PagedArgs& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (8 / WARPS) + warp / WARPS, part = warp % WARPS;
+  if (t >= p.T) return;
+  const int j = lane % kPer, nq = a.q ? a.Hq : 0;
+  const int q_steps = (nq + kHeads - 1) / kHeads, kv_steps = (p.Hk + kHeads - 1) / kHeads;
+  const int steps = q_steps + 2 * kv_steps;
+  const bool turned = 16 * j < a.rot;
+  const int ia = !INTER && turned ? 8 * j : 16 * j, ib = !INTER && turned ? a.rot / 2 + 8 * j : 16 * j + 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // the steps' heads: first those of q, then of k, then of v
+  struct Place {
+    int kind, h;
+    bool in;
+  };
+  auto locate = [&](int step) {
+    Place w;
+    w.kind = step < q_steps ? 0 : (step < q_steps + kv_steps ? 1 : 2);
+    w.h = (step - (w.kind == 0 ? 0 : q_steps + (w.kind - 1) * kv_steps)) * kHeads + lane / kPer;
+    w.in = step < steps && w.h < (w.kind == 0 ? nq : p.Hk);
+    return w;
+  };
+  uint4 va[kBatch], vb[kBatch];
+  auto load = [&](int step0) {
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const Place w = locate(step0 + e * WARPS);
+      va[e] = vb[e] = make_uint4(0, 0, 0, 0);
+      if (!w.in) continue;
+      const uint16_t* src = (w.kind == 0 ? a.q + (long long)t * a.q_stride
+                           : w.kind == 1 ? a.k + (long long)t * a.k_stride
+                                         : a.v + (long long)t * a.v_stride) + (long long)w.h * D;
+      va[e] = *reinterpret_cast<const uint4*>(src + ia);
+      vb[e] = *reinterpret_cast<const uint4*>(src + ib);
+    }
+  };
+  load(part);
+
+  const Spot s = find_spot(a, t, lane);
+  if (s.pos < 0) return;
+  float c[8], sn[8];
+  if (turned) {
+    const float* row = a.rope + (long long)s.pos * a.rot + 8 * j;
+    *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(row));
+    *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(row) + 1);
+    *reinterpret_cast<float4*>(sn) = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2));
+    *reinterpret_cast<float4*>(sn + 4) = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2) + 1);
+  }
+  const long long slot = (long long)s.page * p.page_stride + (long long)(s.pos & p.page_mask) * p.token_stride;
+
+  for (int step0 = part; step0 < steps; step0 += WARPS * kBatch) {
+    if (step0 != part) load(step0);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const Place w = locate(step0 + e * WARPS);
+      float x[8], y[8];
+      unpack8(va[e], x);
+      unpack8(vb[e], y);
+      const float* weight = w.kind == 0 ? a.q_weight : (w.kind == 1 ? a.k_weight : nullptr);
+      if (weight) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
+#pragma unroll
+        for (int o = kPer / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        const float r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 wa = __ldg(reinterpret_cast<const float4*>(weight + ia + i));
+          const float4 wb = __ldg(reinterpret_cast<const float4*>(weight + ib + i));
+          x[i] *= r * wa.x, x[i + 1] *= r * wa.y, x[i + 2] *= r * wa.z, x[i + 3] *= r * wa.w;
+          y[i] *= r * wb.x, y[i + 1] *= r * wb.y, y[i + 2] *= r * wb.z, y[i + 3] *= r * wb.w;
+        }
+      }
+      if (turned && w.kind != 2) turn8<INTER>(x, y, c, sn);
+      if (!w.in) continue;
+      if (w.kind == 0) {
+        uint16_t* dst = a.q_out + ((long long)t * a.Hq + w.h) * D;
+        *reinterpret_cast<uint4*>(dst + ia) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + ib) = pack8(y);
+      } else {
+        store_cache<FP8>(p, w.kind == 1, slot, w.h, ia, ib, x, y);
+      }
     }
   }
 }
@@ -180,6 +304,29 @@ cudaError_t launch_tokens(const AppendArgs& a, bool fp8, bool inter, cudaStream_
   // 3,648 20.9 / 21.1, 6,080 31.9 / 27.1; 640 units, 3,952 32.1 / 34.4, 4,864 38.3 / 37.8.
   const long long units = (long long)((a.q ? a.Hq : 0) + 2 * a.p.Hk) * (D / 16);
   return a.p.T > std::max(1000LL, std::min(16 * units, 4000LL)) ? launch<D, 8>(a, fp8, inter, s) : launch<D, 1>(a, fp8, inter, s);
+}
+
+
+template <int D, int WARPS>
+cudaError_t launch_norm(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.p.T + 8 / WARPS - 1) / (8 / WARPS)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (fp8)
+    return inter ? cudaLaunchKernelEx(&cfg, kv_append_norm_kernel<D, true, true, WARPS>, a)
+                 : cudaLaunchKernelEx(&cfg, kv_append_norm_kernel<D, true, false, WARPS>, a);
+  return inter ? cudaLaunchKernelEx(&cfg, kv_append_norm_kernel<D, false, true, WARPS>, a)
+               : cudaLaunchKernelEx(&cfg, kv_append_norm_kernel<D, false, false, WARPS>, a);
+}
+template <int D>
+cudaError_t launch_norm_warps(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
+  return a.p.T > 2000 ? launch_norm<D, 1>(a, fp8, inter, s) : launch_norm<D, 8>(a, fp8, inter, s);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -222,19 +369,16 @@ lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_page
   return LOWBIT_OK;
 }
 
-}  // namespace lowbit
-
-using namespace lowbit;
-
-extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
-                                          int64_t k_stride, const uint16_t* v, int64_t v_stride,
-                                          int Hq, const float* rope, int rope_rows, int rot,
-                                          int interleaved, const lowbit_paged_batch* batch,
-                                          const lowbit_paged_cache* cache, uint16_t* q_out,
-                                          void* stream) {
+namespace {
+// The checks of both append calls; fills `a` (all but the norm's part).  LOWBIT_OK with T = 0: nothing to do.
+lowbit_status make_append_args(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, int Hq, const float* rope, int rope_rows, int rot,
+                               const lowbit_paged_batch* batch, const lowbit_paged_cache* cache, uint16_t* q_out,
+                               AppendArgs* out) {
   AppendArgs a = {};
   const lowbit_status st = make_paged_args(batch, cache, &a.p);
   if (st != LOWBIT_OK) return st;
+  *out = a;
   if (a.p.T == 0) return LOWBIT_OK;  // the token arrays may then be null
   if (!k || !v || !q != !q_out) return LOWBIT_ERR_INVALID_ARG;
   const int D = cache->head_dim;
@@ -254,8 +398,6 @@ extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, c
         meets(q_out, row * a.p.T, v, kv, (__int128)v_stride * 2, a.p.T))
       return LOWBIT_ERR_INVALID_ARG;
   }
-  a.p.err = device_error_word();
-  if (!a.p.err) return LOWBIT_ERR_CUDA;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -267,6 +409,28 @@ extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, c
   a.rot = rot;
   a.Hq = Hq;
   a.q_out = q_out;
+  *out = a;
+  return LOWBIT_OK;
+}
+}  // namespace
+
+}  // namespace lowbit
+
+using namespace lowbit;
+
+extern "C" {
+
+lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, int Hq, const float* rope, int rope_rows,
+                               int rot, int interleaved, const lowbit_paged_batch* batch,
+                               const lowbit_paged_cache* cache, uint16_t* q_out, void* stream) {
+  AppendArgs a = {};
+  const lowbit_status st = make_append_args(q, q_stride, k, k_stride, v, v_stride, Hq, rope, rope_rows, rot, batch,
+                                            cache, q_out, &a);
+  if (st != LOWBIT_OK || a.p.T == 0) return st;
+  a.p.err = device_error_word();
+  if (!a.p.err) return LOWBIT_ERR_CUDA;
+  const int D = cache->head_dim;
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3, inter = interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 64 ? launch_tokens<64>(a, fp8, inter, s)
@@ -274,3 +438,30 @@ extern "C" lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, c
                                  : launch_tokens<256>(a, fp8, inter, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
+
+lowbit_status lowbit_kv_append_norm(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                    const uint16_t* v, int64_t v_stride, int Hq, const float* q_weight,
+                                    const float* k_weight, float eps, const float* rope, int rope_rows, int rot,
+                                    int interleaved, const lowbit_paged_batch* batch,
+                                    const lowbit_paged_cache* cache, uint16_t* q_out, void* stream) {
+  AppendArgs a = {};
+  const lowbit_status st = make_append_args(q, q_stride, k, k_stride, v, v_stride, Hq, rope, rope_rows, rot, batch,
+                                            cache, q_out, &a);
+  if (st != LOWBIT_OK || a.p.T == 0) return st;
+  if ((q_weight && !q) || !(eps >= 0.0f) || eps > 3.402823466e38f) return LOWBIT_ERR_INVALID_ARG;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return LOWBIT_ERR_ALIGN;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.p.err = device_error_word();
+  if (!a.p.err) return LOWBIT_ERR_CUDA;
+  const int D = cache->head_dim;
+  const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3, inter = interleaved != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 64 ? launch_norm_warps<64>(a, fp8, inter, s)
+                      : D == 128 ? launch_norm_warps<128>(a, fp8, inter, s)
+                                 : launch_norm_warps<256>(a, fp8, inter, s);
+  return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -391,6 +391,22 @@ lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16
                                const lowbit_paged_batch* batch, const lowbit_paged_cache* cache,
                                uint16_t* q_out, void* stream);
 
+/* lowbit_kv_append with a norm of each head of q and k before the rotation:
+ *   y = x * w / sqrt(sum_d x_d^2 / D + eps)   over the head's D elements,
+ * in fp32 from the bf16 elements up to the one rounding of what is stored (q_out, or the cache as there).
+ *   q_weight, k_weight : fp32 [D], 16-byte aligned; NULL leaves q's, or k's, heads as they are (q_weight
+ *       is NULL where q is).  Values are never normalised.
+ *   eps : finite, >= 0; with 0, a head of zeros becomes NaN.
+ *   The squares are summed in fp32, so a head whose sum of squares passes 3.4e38 (elements past 2^60) becomes
+ *   zeros, or NaN where it holds an infinity.  All else is as in lowbit_kv_append. */
+lowbit_status lowbit_kv_append_norm(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                    int64_t k_stride, const uint16_t* v, int64_t v_stride, int Hq,
+                                    const float* q_weight, const float* k_weight, float eps,
+                                    const float* rope, int rope_rows, int rot, int interleaved,
+                                    const lowbit_paged_batch* batch,
+                                    const lowbit_paged_cache* cache, uint16_t* q_out,
+                                    void* stream);
+
 /* Bytes of lowbit_paged_attention's workspace for up to T rows and B requests of Hq query and
  * Hk key/value heads of D (0 for invalid shapes): enough for the pieces of the largest grid, so it
  * depends on D alone (21, 40 or 80 MB for heads of 64, 128 or 256); one serves every call on a stream. */

@@ -32,6 +32,26 @@ def rotate(x, rows, interleaved):
     return y
 
 
+def normalise(x, weight, eps):
+    """Every head [..., D] over its root mean square (eps under the root), times weight [D], in fp64."""
+    x = np.asarray(x, dtype=np.float64)
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, dtype=np.float64)
+
+
+def rotate64(x, rows, interleaved):
+    """`rotate` in fp64, and the sum of its two products' magnitudes (0 where nothing turns)."""
+    x = np.array(x, dtype=np.float64)
+    rot = rows.shape[1]
+    c, s = rows[:, None, :rot // 2].astype(np.float64), rows[:, None, rot // 2:].astype(np.float64)
+    ia = np.arange(0, rot, 2) if interleaved else np.arange(rot // 2)
+    ib = ia + (1 if interleaved else rot // 2)
+    a, b = x[..., ia], x[..., ib]
+    y, size = x.copy(), np.abs(x)
+    y[..., ia], size[..., ia] = a * c - b * s, np.abs(a * c) + np.abs(b * s)
+    y[..., ib], size[..., ib] = b * c + a * s, np.abs(b * c) + np.abs(a * s)
+    return y, size
+
+
 def gather(cache, table, n, page_size):
     """The first n slots of one request: cache [pages][page_size][H][D] -> [n][H][D]."""
     j = np.arange(n)
