@@ -25,7 +25,8 @@ __all__ = [
     "lowbit_q8_packed_bytes", "lowbit_pack_q8", "lowbit_gemm_q8", "lowbit_gemm_q8_path",
     "lowbit_draft_argmax_q8",
     "lowbit_paged_cache", "lowbit_kv_append", "lowbit_kv_append_norm", "lowbit_paged_attention",
-    "lowbit_paged_attention_workspace_bytes", "lowbit_sample",
+    "lowbit_paged_attention_workspace_bytes", "lowbit_prefix_attention",
+    "lowbit_prefix_attention_workspace_bytes", "lowbit_sample",
 ]
 
 

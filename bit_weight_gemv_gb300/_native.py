@@ -115,6 +115,9 @@ _SIGS["lowbit_paged_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
 _SIGS["lowbit_paged_attention"] = (_i, [_vp, _i64, _i, _vp,
                                         ctypes.POINTER(_PagedCache), ctypes.c_float, _i, _i, _vp,
                                         _vp, _vp, _sz, _vp])
+_SIGS["lowbit_prefix_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
+_SIGS["lowbit_prefix_attention"] = (_i, [_vp, _i64, _i, _vp, ctypes.POINTER(_PagedCache), _vp, _vp, _i,
+                                         ctypes.c_float, _i, _vp, _vp, _vp, _sz, _vp])
 _SIGS["lowbit_sample"] = (_i, [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -125,7 +128,7 @@ for _name, (_res, _args) in _SIGS.items():
 if not isinstance(_binding, _NoBinding):
     _binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
                     for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample",
-                                  "lowbit_kv_append_norm")))
+                                  "lowbit_kv_append_norm", "lowbit_prefix_attention")))
 
 
 class LowbitError(RuntimeError):
@@ -550,6 +553,21 @@ def lowbit_paged_attention(q, cache, cu_q, kv_lens, block_table, out, workspace,
                                   _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_paged_attention")
+
+
+def lowbit_prefix_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int) -> int:
+    return lib.lowbit_prefix_attention_workspace_bytes(T, B, Hq, Hk, D)
+
+
+def lowbit_prefix_attention(q, cache, cu_q, kv_lens, block_table, cu_groups, prefix_lens, out, workspace,
+                            scale=None, causal=True, lse=None, stream=None):
+    """lowbit_paged_attention for requests whose first pages are the same ones, read once for each group:
+    group g is the requests cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [groups + 1]), whose first
+    prefix_lens[g] positions (int32 [groups]) are shared."""
+    st = _binding.prefix_attention(q, cache.address, cu_q, kv_lens, block_table, cu_groups, prefix_lens, out, workspace,
+                                   cache.head_dim ** -0.5 if scale is None else scale, causal, lse, _handle(stream))
+    if st:
+        raise LowbitError(st, "lowbit_prefix_attention")
 
 
 def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=None, id_map=None,

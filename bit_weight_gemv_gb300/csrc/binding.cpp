@@ -25,6 +25,7 @@ decltype(&lowbit_kv_append) g_append;
 decltype(&lowbit_kv_append_norm) g_append_norm;
 decltype(&lowbit_paged_attention) g_attention;
 decltype(&lowbit_sample) g_sample;
+decltype(&lowbit_prefix_attention) g_prefix;
 
 bool fail(PyObject* kind, const char* name, const char* what) {
   PyErr_Format(kind, "%s %s", name, what);
@@ -157,29 +158,63 @@ PyObject* kv_append_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        s.interleaved, &s.b, s.cache, s.q_out, s.stream));
 }
 
-// q, cache, cu_q, kv_lens, block_table, out, workspace, scale, causal, window, lse, stream
-PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void *cache_at, *stream;
-  if (!count_is(n, 12) || !address(a[1], &cache_at)) return nullptr;
-  const lowbit_paged_cache* cache = static_cast<const lowbit_paged_cache*>(cache_at);
+// What both attention calls take: q, cache, cu_q, kv_lens, block_table, and the rest by name.
+struct Attention {
   Rows q;
-  if (!rows(a[0], cache->head_dim, "q", &q)) return nullptr;
+  lowbit_paged_batch b;
+  const lowbit_paged_cache* cache;
   uint16_t* out;
   float* lse;
   void* workspace;
-  if (!dense(a[5], ScalarType::BFloat16, q.T * q.heads * cache->head_dim, "out", false, &out) ||
-      !dense(a[6], ScalarType::Byte, -1, "workspace", false, &workspace) ||
-      !dense(a[10], ScalarType::Float, q.T * q.heads, "lse", true, &lse))
-    return nullptr;
-  const double scale = PyFloat_AsDouble(a[7]);
-  const int causal = PyObject_IsTrue(a[8]);
+  size_t bytes;
+  double scale;
+  int causal;
+};
+bool attention_args(PyObject* const* a, PyObject* out, PyObject* workspace, PyObject* scale, PyObject* causal,
+                    PyObject* lse, Attention* s) {
+  void* cache_at;
+  if (!address(a[1], &cache_at)) return false;
+  s->cache = static_cast<const lowbit_paged_cache*>(cache_at);
+  const int64_t D = s->cache->head_dim;
+  if (!rows(a[0], D, "q", &s->q)) return false;
+  if (!dense(out, ScalarType::BFloat16, s->q.T * s->q.heads * D, "out", false, &s->out) ||
+      !dense(workspace, ScalarType::Byte, -1, "workspace", false, &s->workspace) ||
+      !dense(lse, ScalarType::Float, s->q.T * s->q.heads, "lse", true, &s->lse))
+    return false;
+  s->bytes = (size_t)THPVariable_Unpack(workspace).numel();
+  s->scale = PyFloat_AsDouble(scale);
+  s->causal = PyObject_IsTrue(causal);
+  return !PyErr_Occurred() && s->causal >= 0 && batch(a[2], a[3], a[4], s->q.T, &s->b);
+}
+
+// q, cache, cu_q, kv_lens, block_table, out, workspace, scale, causal, window, lse, stream
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Attention s;
+  void* stream;
+  if (!count_is(n, 12) || !attention_args(a, a[5], a[6], a[7], a[8], a[10], &s)) return nullptr;
   const long window = PyLong_AsLong(a[9]);
-  lowbit_paged_batch b;
-  if (PyErr_Occurred() || causal < 0 || !batch(a[2], a[3], a[4], q.T, &b)) return nullptr;
+  if (PyErr_Occurred()) return nullptr;
   if (window < INT32_MIN || window > INT32_MAX) return fail(PyExc_ValueError, "window", "is out of range"), nullptr;
   if (!stream_of(a[11], &stream)) return nullptr;
-  return PyLong_FromLong(g_attention(q.at, q.stride, (int)q.heads, &b, cache, (float)scale, causal, (int)window, out, lse,
-                                     workspace, (size_t)THPVariable_Unpack(a[6]).numel(), stream));
+  return PyLong_FromLong(g_attention(s.q.at, s.q.stride, (int)s.q.heads, &s.b, s.cache, (float)s.scale, s.causal,
+                                     (int)window, s.out, s.lse, s.workspace, s.bytes, stream));
+}
+
+// q, cache, cu_q, kv_lens, block_table, cu_groups, prefix_lens, out, workspace, scale, causal, lse, stream
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Attention s;
+  void* stream;
+  const Tensor* lens;
+  const int32_t *cu_groups, *prefix_lens;
+  if (!count_is(n, 13) || !attention_args(a, a[7], a[8], a[9], a[10], a[11], &s) ||
+      !tensor(a[6], ScalarType::Int, "prefix_lens", &lens) ||
+      !dense(a[6], ScalarType::Int, -1, "prefix_lens", false, &prefix_lens) ||
+      !dense(a[5], ScalarType::Int, lens->numel() + 1, "cu_groups [groups + 1]", false, &cu_groups))
+    return nullptr;
+  if (lens->numel() > INT32_MAX) return fail(PyExc_ValueError, "prefix_lens", "has too many values"), nullptr;
+  if (!stream_of(a[12], &stream)) return nullptr;
+  return PyLong_FromLong(g_prefix(s.q.at, s.q.stride, (int)s.q.heads, &s.b, s.cache, cu_groups, prefix_lens,
+                                  (int)lens->numel(), (float)s.scale, s.causal, s.out, s.lse, s.workspace, s.bytes, stream));
 }
 
 // logits, u, ids, temperature, top_k, top_p, min_p, id_map, logprob, kept, stream
@@ -218,14 +253,15 @@ PyObject* current_stream(PyObject*, PyObject* const*, Py_ssize_t n) {
 
 // The entry points' addresses in the loaded library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[4];
-  if (!count_is(n, 4)) return nullptr;
-  for (int i = 0; i < 4; ++i)
+  void* p[5];
+  if (!count_is(n, 5)) return nullptr;
+  for (int i = 0; i < 5; ++i)
     if (!address(a[i], &p[i])) return nullptr;
   g_append = reinterpret_cast<decltype(g_append)>(p[0]);
   g_attention = reinterpret_cast<decltype(g_attention)>(p[1]);
   g_sample = reinterpret_cast<decltype(g_sample)>(p[2]);
   g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[3]);
+  g_prefix = reinterpret_cast<decltype(g_prefix)>(p[4]);
   Py_RETURN_NONE;
 }
 
@@ -249,6 +285,7 @@ PyMethodDef kMethods[] = {{"bind", entry<bind>(), METH_FASTCALL, nullptr},
                           {"kv_append", entry<kv_append>(), METH_FASTCALL, nullptr},
                           {"kv_append_norm", entry<kv_append_norm>(), METH_FASTCALL, nullptr},
                           {"paged_attention", entry<paged_attention>(), METH_FASTCALL, nullptr},
+                          {"prefix_attention", entry<prefix_attention>(), METH_FASTCALL, nullptr},
                           {"sample", entry<sample>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

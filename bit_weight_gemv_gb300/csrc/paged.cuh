@@ -37,18 +37,16 @@ lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_page
 // without tokens, and the device error word says so.
 struct Request {
   int row0, n, kv;
+  int skip;  // keys of its pages that come before those counted by kv (lowbit_prefix_attention's own part)
 };
 __device__ __forceinline__ Request check_request(const PagedArgs& a, int from, int to, int kv) {
-  Request r = {from, to - from, kv};
+  Request r = {from, to - from, kv, 0};
   if (r.row0 < 0 || r.n < 0 || r.row0 > a.T - r.n || r.kv < 0 ||
       (long long)r.kv > ((long long)a.width << a.page_shift)) {
     record_error(a.err, LOWBIT_ERR_INVALID_ARG);
     r.row0 = r.n = r.kv = 0;
   }
   return r;
-}
-__device__ __forceinline__ Request load_request(const PagedArgs& a, int b) {
-  return check_request(a, a.cu_q[b], a.cu_q[b + 1], a.kv_lens[b]);
 }
 
 // ---------------------------------------------------------------------- attention schedule

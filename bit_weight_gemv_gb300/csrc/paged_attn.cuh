@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "paged.cuh"
@@ -50,7 +51,67 @@ struct AttnArgs {
                     // or queries on tcgen05) never come, so that every role's wait gives up; 0 in normal use
 };
 
+// lowbit_prefix_attention makes two launches of the same kernels.  The shared part: a "request" is all rows of a
+// group (p.B counts groups) over the keys that its requests share; every row leaves as a piece does.  The own
+// part: the requests over their own keys, each row joined with what the first part left.
+struct PrefixArgs : AttnArgs {
+  bool shared;
+  int groups, requests;
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  float* base_o;    // [row of out][D]
+  float2* base_ml;  // [row of out]: a sum of kNoPiece where the row was not computed
+};
+template <class A>
+constexpr bool kPrefix = std::is_same<A, PrefixArgs>::value;
+
+__device__ __forceinline__ Request load_request(const AttnArgs& a, int b) {
+  return check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
+}
+// All rows of group g over the whole pages of its shared length.
+__device__ __forceinline__ Request load_group(const PrefixArgs& a, int g) {
+  const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
+  if (from < 0 || to < from || to > a.requests || len < 0) {
+    record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
+    return Request{0, 0, 0, 0};
+  }
+  return check_request(a.p, a.p.cu_q[from], a.p.cu_q[to], len & ~a.p.page_mask);
+}
+// Request b without the keys that its group shares.  One that has new tokens among these, or rows
+// outside its group's, counts as inconsistent.
+__device__ __forceinline__ Request load_own(const PrefixArgs& a, int b) {
+  int g = 0;
+#pragma unroll 1
+  for (int end = a.groups; end - g > 1;) {  // the last group that begins at b or before it
+    const int mid = (g + end) / 2;
+    if (a.cu_groups[mid] <= b) g = mid;
+    else end = mid;
+  }
+  const Request s = load_group(a, g);
+  Request r = check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
+  if (r.n == 0) return r;
+  if (b < a.cu_groups[g] || b >= a.cu_groups[g + 1] || r.row0 < s.row0 || r.row0 + r.n > s.row0 + s.n ||
+      r.kv - r.n < s.kv) {
+    record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
+    return Request{0, 0, 0, 0};
+  }
+  r.kv -= s.kv;
+  r.skip = s.kv;
+  return r;
+}
+__device__ __forceinline__ Request load_request(const PrefixArgs& a, int b) {
+  return a.shared ? load_group(a, b) : load_own(a, b);
+}
+// The block table from the page of the request's first counted key on.
+__device__ __forceinline__ const int32_t* table_of(const AttnArgs& a, int b, const Request&) {
+  return a.p.table + (long long)b * a.p.table_stride;
+}
+__device__ __forceinline__ const int32_t* table_of(const PrefixArgs& a, int b, const Request& r) {
+  return a.p.table + (long long)(a.shared ? a.cu_groups[b] : b) * a.p.table_stride + (r.skip >> a.p.page_shift);
+}
+
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);
+cudaError_t launch_attention_mma(const PrefixArgs& a, int D, bool fp8, cudaStream_t s);
 
 // a / b of nonnegative numbers: 32-bit where both fit (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -104,11 +165,12 @@ struct Share {
 // CTA touches for the first time are a large part (about 6 cycles each when they come from
 // memory), so this way is kept apart from the general one: 0 = not applicable, 1 = found,
 // -1 = the CTA has no share.
-__device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk& w, Share& sh) {
+template <class A>
+__device__ __forceinline__ int start_walk_short(const A& a, int cta, Walk& w, Share& sh) {
   const int lane = threadIdx.x & 31;
   if (a.p.B > 32) return 0;
-  Request q = {0, 0, 0};
-  if (lane < a.p.B) q = load_request(a.p, lane);
+  Request q = {0, 0, 0, 0};
+  if (lane < a.p.B) q = load_request(a, lane);
   // one tile holds every row: its keys end with the request's, whatever the mask
   const int lo = first_key(a.shape, q.kv - q.n);
   const bool none = lo >= q.kv;
@@ -136,6 +198,7 @@ __device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk
   w.q.row0 = __shfl_sync(~0u, q.row0, src);
   w.q.n = __shfl_sync(~0u, q.n, src);
   w.q.kv = __shfl_sync(~0u, q.kv, src);
+  w.q.skip = __shfl_sync(~0u, q.skip, src);
   w.span.lo = __shfl_sync(~0u, none ? 0 : lo, src);
   w.span.hi = __shfl_sync(~0u, none ? 0 : q.kv, src);
   w.h = (int)(off / each);
@@ -149,8 +212,8 @@ __device__ __forceinline__ int start_walk_short(const AttnArgs& a, int cta, Walk
 }
 // Up to 32 requests every warp sums them on its own (one per lane, or one after another where each
 // has many query tiles), so that nothing waits for a barrier; above, the block does.
-template <int NT>
-__device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, Share& sh) {
+template <int NT, class A>
+__device__ __forceinline__ bool start_walk(const A& a, int cta, Walk& w, Share& sh) {
   __shared__ long long s_warp[NT / 32], s_off;
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -170,11 +233,11 @@ __device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, 
     if (tall) {
 #pragma unroll 1
       for (int b = 0; b < a.p.B; ++b) {
-        const long long c = head_cost(a.shape, load_request(a.p, b), lane) * a.p.Hk;
+        const long long c = head_cost(a.shape, load_request(a, b), lane) * a.p.Hk;
         if (lane == b) sum = c;
       }
     } else if (lane < a.p.B) {
-      sum = head_cost(a.shape, load_request(a.p, lane), -1) * a.p.Hk;
+      sum = head_cost(a.shape, load_request(a, lane), -1) * a.p.Hk;
     }
     const long long incl = warp_inclusive(sum, lane);
     total = __shfl_sync(~0u, incl, 31);
@@ -192,7 +255,7 @@ __device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, 
       for (int b0 = 0; b0 < a.p.B; b0 += step) {
         const int b = b0 + (tall ? warp : tid);
         long long c = 0;
-        if (b < a.p.B) c = head_cost(a.shape, load_request(a.p, b), tall ? lane : -1) * a.p.Hk;
+        if (b < a.p.B) c = head_cost(a.shape, load_request(a, b), tall ? lane : -1) * a.p.Hk;
         const long long incl = tall ? c : warp_inclusive(c, lane);
         if (b0 || pass) __syncthreads();
         if (lane == 31) s_warp[warp] = incl;
@@ -220,7 +283,7 @@ __device__ __forceinline__ bool start_walk(const AttnArgs& a, int cta, Walk& w, 
     w.b = s_b;
     off = s_off;
   }
-  w.q = load_request(a.p, w.b);
+  w.q = load_request(a, w.b);
 
   // the head, the query tile and the place inside the item
   w.nq = query_tiles(a.shape, w.q);
@@ -254,20 +317,53 @@ __device__ __forceinline__ int walk_take(Walk& w, int& left) {
   return max(0, n);
 }
 // To the next item; false past the last request.
-__device__ __forceinline__ bool walk_next(const AttnArgs& a, Walk& w) {
+template <class A>
+__device__ __forceinline__ bool walk_next(const A& a, Walk& w) {
   if (++w.qt == w.nq) {
     w.qt = 0;
     if (++w.h == a.p.Hk) {
       w.h = 0;
       do {
         if (++w.b >= a.p.B) return false;
-        w.q = load_request(a.p, w.b);
+        w.q = load_request(a, w.b);
         w.nq = query_tiles(a.shape, w.q);
       } while (w.nq == 0);
     }
   }
   walk_item(a, w, 0);
   return true;
+}
+
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// What the shared keys of output row `at` left, joined with (m, l): the factors of the own part's output and of
+// the base's.  False where the base was not computed.
+__device__ __forceinline__ bool join_base(const PrefixArgs& a, long long at, float& m, float& l, float& f_own, float& f_base) {
+  const float2 b = a.base_ml[at];
+  const float top = fmaxf(m, b.x);
+  f_own = top == -INFINITY ? 0.0f : pow2(m - top);
+  f_base = top == -INFINITY ? 0.0f : pow2(b.x - top);
+  l = f_own * l + f_base * b.y;
+  m = top;
+  return b.y != kNoPiece;
+}
+
+// Whether a row whose keys this CTA saw all of goes to out, and where it goes else: to its piece, or (the shared
+// part) to its base.
+__device__ __forceinline__ bool to_out(const AttnArgs&) { return true; }
+__device__ __forceinline__ bool to_out(const PrefixArgs& a) { return !a.shared; }
+__device__ __forceinline__ float2* part_ml_of(const AttnArgs& a, bool, long long, long long piece) { return a.piece_ml + piece; }
+__device__ __forceinline__ float2* part_ml_of(const PrefixArgs& a, bool whole, long long row, long long piece) {
+  return whole ? a.base_ml + row : a.piece_ml + piece;
+}
+template <int D>
+__device__ __forceinline__ float* part_o_of(const AttnArgs& a, bool, long long, long long piece) { return a.piece_o + piece * D; }
+template <int D>
+__device__ __forceinline__ float* part_o_of(const PrefixArgs& a, bool whole, long long row, long long piece) {
+  return whole ? a.base_o + row * D : a.piece_o + piece * D;
 }
 
 // 4-D tiled tensor copy (TMA) global -> shared.
@@ -297,14 +393,53 @@ __device__ __forceinline__ void say_cut(const AttnArgs& a, int cta, const Walk* 
   reinterpret_cast<int4*>(a.cuts + cta)[1] = hi;
 }
 
-// Launch configuration of an attention kernel of `ctas` resident CTAs, and the combine step behind it.
+// Launch configuration of an attention kernel of `ctas` resident CTAs.
 void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ctas, int threads, int smem,
                       cudaStream_t s);
-cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s);
 
 // The tensor-core kernel (paged_attn_tc.cu): whether it can take the call, and its launch with 256
 // (`pair`) or 128 query rows per item.
 bool attention_tc_fits(const AttnArgs& a, int D);
 cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool fp8, bool pair, cudaStream_t s);
+cudaError_t launch_attention_tc(const PrefixArgs& a, int D, bool fp8, bool pair, cudaStream_t s);
+// The combine step behind either.
+cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s);
+cudaError_t launch_combine(const PrefixArgs& a, int D, cudaStream_t s);
+
+
+// Checks of the arguments that both attention calls take; fills `a` all but the workspace and the error word.
+// LOWBIT_OK with T = 0: nothing to do.
+lowbit_status make_attn_args(const uint16_t* q, int64_t q_stride, int Hq, const lowbit_paged_batch* batch,
+                             const lowbit_paged_cache* cache, float scale, int causal, int window, uint16_t* out,
+                             float* lse, AttnArgs* a);
+
+// The pieces of a launch, and what its CTAs say about them, from `at` on (a multiple of 32 bytes in all).
+inline size_t pieces_bytes(int D) {
+  return (size_t)kMaxPieceRows * (size_t)(D + 2) * sizeof(float) + (size_t)kMaxCtas * sizeof(CutItem);
+}
+inline void use_pieces(AttnArgs* a, void* at, int D) {
+  a->piece_o = static_cast<float*>(at);
+  a->piece_ml = reinterpret_cast<float2*>(a->piece_o + (size_t)kMaxPieceRows * D);
+  a->cuts = reinterpret_cast<CutItem*>(a->piece_ml + kMaxPieceRows);
+}
+
+// By the rows that share a request's keys, on average (the host knows the totals only; a request that
+// differs from the average is computed right and slowly).  At 32 rows each side wins somewhere, the warp-level
+// MMA on short contexts and where the start counts, tcgen05 on long ones; above, tcgen05 nearly always.  Heads of
+// 128, one request of 30,000 keys, us on the warp-level MMA / tcgen05 with 128 rows an item / with
+// 256: 32 rows 38.7 / 36.3 / 51.8, 64 rows 47.8 / 37.6 / 59.8, 400 rows 189 / 81 / 101; of 500 keys
+// 9.6 / 11 / 13 with 32 rows.  Heads of 64: 48 rows 29.8 / 26.1, 32 requests of up to 16,000 keys 48.0 /
+// 49.0.  256 rows an item pay when there are many: one request of 16,000 keys, 800 rows 71 with 128 and
+// 69 with 256, 1,600 rows 116 and 103, 3,200 rows 200 and 171 (of 4,000 keys 33 and 37, 48 and 50, 69 and 69).
+// Over e4m3 caches the same limits hold: heads of 128, 30,000 keys, warp-level MMA / tcgen05: 32 rows 35.3 /
+// 29.5, 40 rows 48.2 / 32.2 (500 keys 10.4 / 10.8), 16 requests of up to 8,000 keys and 32 rows 28.7 / 29.8, 40
+// rows 33.7 / 27.5; heads of 64, 48 rows 31.2 / 27.0 and 20.9 / 22.7; 256 rows an item: 16,000 keys, 1,600 rows
+// 137 with 128 and 114 with 256 (of 4,000 keys 49 and 52).
+template <class A>
+cudaError_t launch_attention(const A& a, int D, bool fp8, cudaStream_t s) {
+  const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
+  return rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D) ? launch_attention_tc(a, D, fp8, rows > 1024, s)
+                                                               : launch_attention_mma(a, D, fp8, s);
+}
 
 }  // namespace lowbit

@@ -436,6 +436,38 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
                                      int window, uint16_t* out, float* lse, void* workspace,
                                      size_t ws_bytes, void* stream);
 
+/* Bytes of lowbit_prefix_attention's workspace for up to T rows and B requests of Hq query and Hk
+ * key/value heads of D (0 for invalid shapes): twice lowbit_paged_attention's, and 4 (D + 2) for each row
+ * and query head. */
+size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D);
+
+/* lowbit_paged_attention (without a window) for requests whose first pages are the same ones: a long system
+ * prompt, a document that many ask about, several answers to one prompt.  The shared pages are read once
+ * for all rows of a group of requests, instead of once for each request.
+ *   cu_groups   : int32 [groups + 1] on the device: group g is the requests cu_groups[g] ..
+ *                 cu_groups[g + 1] - 1; 0 first, B last.  A group may be empty, or one request.
+ *   prefix_lens : int32 [groups] on the device: the first prefix_lens[g] positions of the group's
+ *                 requests hold the same keys and values.  The whole pages of it are taken from the
+ *                 block table row of the group's first request (which may have no new tokens; its row is
+ *                 read all the same); what lies behind the last whole page each request has on its
+ *                 own.  0: nothing is shared.  New tokens come after the shared positions:
+ *                 kv_lens[b] - new tokens >= the length of the whole pages.
+ * kv_lens and block_table describe the whole requests, as for lowbit_kv_append and lowbit_paged_attention,
+ * whose result over the same arguments is this one's but for rounding.  A group or request that the
+ * arrays describe inconsistently counts as one without tokens and is recorded in the device error
+ * word; its rows are not written.  Pages are compared by nobody: rows of different pages under the same
+ * prefix give each request the first one's.
+ *   workspace : lowbit_prefix_attention_workspace_bytes() bytes, 16-byte aligned, any contents; calls that
+ *   may run at the same time need one each.
+ * All else (rounding, non-finite values, alignment) is as in lowbit_paged_attention; a non-finite v in
+ * the shared pages reaches the rows of the whole group. */
+lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int Hq,
+                                      const lowbit_paged_batch* batch,
+                                      const lowbit_paged_cache* cache, const int32_t* cu_groups,
+                                      const int32_t* prefix_lens, int groups, float scale,
+                                      int causal, uint16_t* out, float* lse, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
 #define LOWBIT_LOGITS_FP32 0
 #define LOWBIT_LOGITS_BF16 1
 
