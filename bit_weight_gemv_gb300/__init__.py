@@ -26,7 +26,8 @@ __all__ = [
     "lowbit_draft_argmax_q8",
     "lowbit_paged_cache", "lowbit_kv_append", "lowbit_kv_append_norm", "lowbit_paged_attention",
     "lowbit_paged_attention_workspace_bytes", "lowbit_prefix_attention",
-    "lowbit_prefix_attention_workspace_bytes", "lowbit_sample",
+    "lowbit_prefix_attention_workspace_bytes", "lowbit_sample", "lowbit_verify_drafts",
+    "lowbit_verify_drafts_workspace_bytes",
 ]
 
 

@@ -119,6 +119,8 @@ _SIGS["lowbit_prefix_attention_workspace_bytes"] = (_sz, [_i, _i, _i, _i, _i])
 _SIGS["lowbit_prefix_attention"] = (_i, [_vp, _i64, _i, _vp, ctypes.POINTER(_PagedCache), _vp, _vp, _i,
                                          ctypes.c_float, _i, _vp, _vp, _vp, _sz, _vp])
 _SIGS["lowbit_sample"] = (_i, [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
+_SIGS["lowbit_verify_drafts_workspace_bytes"] = (_sz, [_i, _i])
+_SIGS["lowbit_verify_drafts"] = (_i, [_vp, _vp, _i, _i] + [_vp] * 9 + [_sz, _vp])
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
     _f.restype = _res
@@ -128,7 +130,7 @@ for _name, (_res, _args) in _SIGS.items():
 if not isinstance(_binding, _NoBinding):
     _binding.bind(*(ctypes.cast(getattr(lib, _name), _vp).value
                     for _name in ("lowbit_kv_append", "lowbit_paged_attention", "lowbit_sample",
-                                  "lowbit_kv_append_norm", "lowbit_prefix_attention")))
+                                  "lowbit_kv_append_norm", "lowbit_prefix_attention", "lowbit_verify_drafts")))
 
 
 class LowbitError(RuntimeError):
@@ -578,3 +580,23 @@ def lowbit_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_
                          _handle(stream))
     if st:
         raise LowbitError(st, "lowbit_sample")
+
+
+def lowbit_verify_drafts_workspace_bytes(M: int, N: int) -> int:
+    return lib.lowbit_verify_drafts_workspace_bytes(M, N)
+
+
+def lowbit_verify_drafts(logits, cu_drafts, drafts, u, v, n_accept, ids, workspace, draft_logits=None,
+                         draft_index=None, temperature=None, top_k=None, top_p=None, min_p=None,
+                         draft_temperature=None, draft_top_k=None, draft_top_p=None, draft_min_p=None,
+                         accept=None, stream=None):
+    """Drafts [N] accepted against the target's logits [M][V] (a row for every draft and one more for each
+    request) from the uniform numbers u [N], and the token that follows them from v [B]: n_accept [B] and
+    ids [M], a request's tokens in its rows.  draft_logits [N][Vd]: what the drafts were drawn from (None:
+    proposed with certainty), draft_index int32 [V] the column of a token there.  Settings per request, as
+    in lowbit_sample; accept fp32 [N] (None) gets every draft's probability of being accepted."""
+    st = _binding.verify_drafts(logits, cu_drafts, drafts, u, v, n_accept, ids, workspace, draft_logits, draft_index,
+                                temperature, top_k, top_p, min_p, draft_temperature, draft_top_k, draft_top_p,
+                                draft_min_p, accept, _handle(stream))
+    if st:
+        raise LowbitError(st, "lowbit_verify_drafts")

@@ -1,6 +1,6 @@
-// Argument marshalling of the calls between the products (lowbit_kv_append,
-// lowbit_paged_attention, lowbit_sample) from torch tensors to the C ABI.  These calls take eight to
-// thirteen tensors and a kernel of a few microseconds; checked and unpacked in Python, the tensors
+// Argument marshalling of the calls between the products (appends, attention, sampling, verification of
+// drafts) from torch tensors to the C ABI.  These calls take eight to
+// twenty tensors and a kernel of a few microseconds; checked and unpacked in Python, the tensors
 // cost more than the kernel (an append of one token: 10.9 us of host time a call, 3.8 from here;
 // attention of one short request 12.0 against 6.0, sampling one row 9.5 against 8.4).  Same checks as the rest
 // of the binding: TypeError or ValueError for what the library could not see (dtype, device,
@@ -26,6 +26,7 @@ decltype(&lowbit_kv_append_norm) g_append_norm;
 decltype(&lowbit_paged_attention) g_attention;
 decltype(&lowbit_sample) g_sample;
 decltype(&lowbit_prefix_attention) g_prefix;
+decltype(&lowbit_verify_drafts) g_verify;
 
 bool fail(PyObject* kind, const char* name, const char* what) {
   PyErr_Format(kind, "%s %s", name, what);
@@ -217,18 +218,33 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   (int)lens->numel(), (float)s.scale, s.causal, s.out, s.lse, s.workspace, s.bytes, stream));
 }
 
+// fp32 or bf16 logits [M][V] with dense rows.
+struct Logits {
+  void* at;
+  int64_t M, V, stride;
+  int dtype;
+};
+bool logits_of(PyObject* o, const char* name, Logits* l) {
+  if (!THPVariable_Check(o)) return fail(PyExc_TypeError, name, "must be a torch tensor");
+  const Tensor& z = THPVariable_Unpack(o);
+  const bool bf16 = z.scalar_type() == ScalarType::BFloat16;
+  if (!z.is_cuda() || z.dim() != 2 || (!bf16 && z.scalar_type() != ScalarType::Float))
+    return fail(PyExc_TypeError, name, "must be an fp32 or bf16 CUDA tensor [M][V]");
+  l->M = z.size(0), l->V = z.size(1);
+  if ((l->V > 1 && z.stride(1) != 1) || l->M > INT32_MAX || l->V > INT32_MAX) return fail(PyExc_ValueError, name, "must have dense rows");
+  l->at = z.data_ptr();
+  l->stride = l->M > 1 ? z.stride(0) : std::max(z.stride(0), l->V);
+  l->dtype = bf16 ? LOWBIT_LOGITS_BF16 : LOWBIT_LOGITS_FP32;
+  return true;
+}
+
 // logits, u, ids, temperature, top_k, top_p, min_p, id_map, logprob, kept, stream
 PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* stream;
   if (!count_is(n, 11)) return nullptr;
-  if (!THPVariable_Check(a[0])) return fail(PyExc_TypeError, "logits", "must be a torch tensor"), nullptr;
-  const Tensor& z = THPVariable_Unpack(a[0]);
-  const bool bf16 = z.scalar_type() == ScalarType::BFloat16;
-  if (!z.is_cuda() || z.dim() != 2 || (!bf16 && z.scalar_type() != ScalarType::Float))
-    return fail(PyExc_TypeError, "logits", "must be an fp32 or bf16 CUDA tensor [M][V]"), nullptr;
-  const int64_t M = z.size(0), V = z.size(1);
-  if ((V > 1 && z.stride(1) != 1) || M > INT32_MAX || V > INT32_MAX)
-    return fail(PyExc_ValueError, "logits", "must have dense rows"), nullptr;
+  Logits z;
+  if (!logits_of(a[0], "logits", &z)) return nullptr;
+  const int64_t M = z.M, V = z.V;
   const float *temperature, *top_p, *min_p, *u;
   const int32_t *top_k, *id_map;
   int32_t *ids, *kept;
@@ -240,9 +256,51 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !dense(a[7], i, V, "id_map", true, &id_map) || !dense(a[8], f, M, "logprob", true, &logprob) ||
       !dense(a[9], i, M, "kept", true, &kept) || !stream_of(a[10], &stream))
     return nullptr;
-  return PyLong_FromLong(g_sample(z.data_ptr(), bf16 ? LOWBIT_LOGITS_BF16 : LOWBIT_LOGITS_FP32,
-                                  M > 1 ? z.stride(0) : std::max(z.stride(0), V), (int)M, (int)V, temperature, top_k,
-                                  top_p, min_p, u, id_map, ids, logprob, kept, stream));
+  return PyLong_FromLong(g_sample(z.at, z.dtype, z.stride, (int)M, (int)V, temperature, top_k, top_p, min_p, u, id_map,
+                                  ids, logprob, kept, stream));
+}
+
+// A row's settings, one per request: a[0..3] temperature, top_k, top_p, min_p.
+bool settings_of(PyObject* const* a, const Logits& z, int64_t B, lowbit_row_settings* r) {
+  const ScalarType f = ScalarType::Float;
+  *r = lowbit_row_settings{z.at, z.stride, z.dtype, (int)z.M, (int)z.V, nullptr, nullptr, nullptr, nullptr};
+  return dense(a[0], f, B, "temperature", true, &r->temperature) && dense(a[1], ScalarType::Int, B, "top_k", true, &r->top_k) &&
+         dense(a[2], f, B, "top_p", true, &r->top_p) && dense(a[3], f, B, "min_p", true, &r->min_p);
+}
+
+// logits, cu_drafts, drafts, u, v, n_accept, ids, workspace, draft_logits, draft_index, then temperature, top_k,
+// top_p, min_p of the target and of the drafter, accept, stream
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 20)) return nullptr;
+  Logits z, y = {nullptr, 0, 0, 0, 0};
+  const Tensor *last, *tokens;
+  if (!logits_of(a[0], "logits", &z) || !tensor(a[4], ScalarType::Float, "v", &last) || !tensor(a[2], ScalarType::Int, "drafts", &tokens)) return nullptr;
+  const int64_t B = last->numel(), N = tokens->numel();
+  if (B > INT32_MAX || N > INT32_MAX) return fail(PyExc_ValueError, "the batch", "is too large"), nullptr;
+  const ScalarType f = ScalarType::Float, i = ScalarType::Int;
+  const int32_t *cu, *drafts, *index;
+  const float *u, *v;
+  int32_t *n_accept, *ids;
+  float* accept;
+  void *workspace, *stream;
+  lowbit_row_settings target, draft;
+  const bool has_draft = a[8] != Py_None;
+  if (!dense(a[1], i, B + 1, "cu_drafts [requests + 1]", false, &cu) || !dense(a[2], i, N, "drafts", false, &drafts) ||
+      !dense(a[3], f, N, "u", false, &u) || !dense(a[4], f, B, "v", false, &v) ||
+      !dense(a[5], i, B, "n_accept", false, &n_accept) || !dense(a[6], i, z.M, "ids", false, &ids) ||
+      !dense(a[7], ScalarType::Byte, -1, "workspace", false, &workspace) || !dense(a[18], f, N, "accept", true, &accept) ||
+      !settings_of(a + 10, z, B, &target))
+    return nullptr;
+  if (has_draft) {
+    if (!logits_of(a[8], "draft_logits", &y) || !settings_of(a + 14, y, B, &draft)) return nullptr;
+    if (y.M != N) return fail(PyExc_ValueError, "draft_logits", "must have a row for every draft"), nullptr;
+  } else {
+    for (int k = 14; k < 18; ++k)
+      if (a[k] != Py_None) return fail(PyExc_ValueError, "the drafter's settings", "need draft_logits"), nullptr;
+  }
+  if (!dense(a[9], i, z.V, "draft_index", true, &index) || !stream_of(a[19], &stream)) return nullptr;
+  return PyLong_FromLong(g_verify(&target, has_draft ? &draft : nullptr, (int)B, (int)N, cu, drafts, index, u, v, n_accept, ids,
+                                  accept, workspace, (size_t)THPVariable_Unpack(a[7]).numel(), stream));
 }
 
 // The handle of torch's current stream, without a Stream object around it.
@@ -253,15 +311,16 @@ PyObject* current_stream(PyObject*, PyObject* const*, Py_ssize_t n) {
 
 // The entry points' addresses in the loaded library.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[5];
-  if (!count_is(n, 5)) return nullptr;
-  for (int i = 0; i < 5; ++i)
+  void* p[6];
+  if (!count_is(n, 6)) return nullptr;
+  for (int i = 0; i < 6; ++i)
     if (!address(a[i], &p[i])) return nullptr;
   g_append = reinterpret_cast<decltype(g_append)>(p[0]);
   g_attention = reinterpret_cast<decltype(g_attention)>(p[1]);
   g_sample = reinterpret_cast<decltype(g_sample)>(p[2]);
   g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[3]);
   g_prefix = reinterpret_cast<decltype(g_prefix)>(p[4]);
+  g_verify = reinterpret_cast<decltype(g_verify)>(p[5]);
   Py_RETURN_NONE;
 }
 
@@ -287,6 +346,7 @@ PyMethodDef kMethods[] = {{"bind", entry<bind>(), METH_FASTCALL, nullptr},
                           {"paged_attention", entry<paged_attention>(), METH_FASTCALL, nullptr},
                           {"prefix_attention", entry<prefix_attention>(), METH_FASTCALL, nullptr},
                           {"sample", entry<sample>(), METH_FASTCALL, nullptr},
+                          {"verify_drafts", entry<verify_drafts>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -494,6 +494,60 @@ lowbit_status lowbit_sample(const void* logits, int dtype, int64_t row_stride, i
                             const float* min_p, const float* u, const int32_t* id_map,
                             int32_t* ids, float* logprob, int32_t* kept, void* stream);
 
+/* Rows of logits and the settings that say what of them may be drawn, as in lowbit_sample, but one setting
+ * per request (NULL = 1, 0, 1, 0). */
+typedef struct lowbit_row_settings {
+  const void* logits;          /* [rows][V], row stride row_stride elements */
+  int64_t row_stride;
+  int dtype, rows, V;          /* LOWBIT_LOGITS_FP32 or LOWBIT_LOGITS_BF16; 1 <= V <= 2^19 */
+  const float* temperature;    /* [B] */
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} lowbit_row_settings;
+
+/* Bytes of lowbit_verify_drafts's workspace for M rows of the target and N drafts: 32 each (0 for invalid
+ * shapes). */
+size_t lowbit_verify_drafts_workspace_bytes(int M, int N);
+
+/* Drafted tokens accepted or rejected against the target's probabilities, and the token that follows, so
+ * that the outcome is distributed as sampling from the target alone (lmhead_argmax_verify is the greedy
+ * case).  Request b of B has the drafts cu_drafts[b] .. cu_drafts[b + 1] - 1, any number down to none,
+ * and one row of the target more than drafts: rows cu_drafts[b] + b .. cu_drafts[b + 1] + b, of which row i
+ * judges the request's draft i and the last one follows them all.
+ *   target    : the target's rows; at least N + B of them where all are used.
+ *   draft     : the drafter's rows, row r of the N that draft r was drawn from, or NULL: every draft was
+ *               proposed with certainty (a greedy drafter, looked-up tokens).
+ *   drafts    : int32 [N], tokens of the target's vocabulary.
+ *   draft_index : int32 [target V]: the column of the drafter's rows that stands for a token, -1 for none (a
+ *               trimmed vocabulary), or NULL: the token itself.  Needs draft.
+ *   u : fp32 [N], v : fp32 [B], in [0, 1) (others are clamped, NaN counts as 0).
+ * With p and q the shares m / S of lowbit_sample's masses, under the request's settings, in the target's
+ * and the drafter's row (q = 1 for the draft and 0 else where draft is NULL; a token without column has
+ * q = 0, a row without a finite logit p = 0 or q = 0 throughout):
+ *   draft i is accepted where u q(d) < p(d), both shares, product and comparison in 64-bit floating point;
+ *   n is the number of accepted drafts before the first that is not; a draft outside the vocabulary
+ *   is never accepted.
+ *   The next token comes from row n with v.  Where n is all of them: as lowbit_sample draws it.  Else
+ *   from the masses r_i * 2^40 rounded, r_i = max(0, w_i * f - w'_i * f') over the tokens that p keeps, with
+ *   w, w' the weights (0 of a token dropped or without mass), f = 2^40 / S rounded to fp32, and each
+ *   product and the difference rounded to fp32:
+ *   the first token in index order whose inclusive mass exceeds floor(v * their sum).  Where that sum is
+ *   zero, as lowbit_sample draws from p.
+ *   n_accept : int32 [B] out: n.
+ *   ids    : int32 [target rows] out: a request's tokens in its rows: the n accepted drafts, the next token (-1
+ *            where its row has no finite logit), and -1 in the rows behind it.
+ *   accept : fp32 [N] out or NULL: min(1, p(d) / q(d)) of every draft, whatever became of it.
+ * A request that cu_drafts describes inconsistently (decreasing, or outside the arrays) gets n = 0, no ids and
+ * is recorded in the device error word.  Rows of no request are neither read nor written.
+ *   workspace : lowbit_verify_drafts_workspace_bytes() bytes, 16-byte aligned, any contents; calls that may
+ *   run at the same time need one each.  The result does not depend on timing. */
+lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowbit_row_settings* draft,
+                                   int B, int N, const int32_t* cu_drafts, const int32_t* drafts,
+                                   const int32_t* draft_index, const float* u, const float* v,
+                                   int32_t* n_accept, int32_t* ids, float* accept,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------------------------
  * For callers that cannot allocate device memory.
  */
