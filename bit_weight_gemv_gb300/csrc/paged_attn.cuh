@@ -435,10 +435,13 @@ inline void use_pieces(AttnArgs* a, void* at, int D) {
 // 29.5, 40 rows 48.2 / 32.2 (500 keys 10.4 / 10.8), 16 requests of up to 8,000 keys and 32 rows 28.7 / 29.8, 40
 // rows 33.7 / 27.5; heads of 64, 48 rows 31.2 / 27.0 and 20.9 / 22.7; 256 rows an item: 16,000 keys, 1,600 rows
 // 137 with 128 and 114 with 256 (of 4,000 keys 49 and 52).
+// The shared part of a prefix takes 256 rows an item from 500 on: there the keys are long.
+inline int pair_rows(const AttnArgs&) { return 1024; }
+inline int pair_rows(const PrefixArgs& a) { return a.shared ? 500 : 1024; }
 template <class A>
 cudaError_t launch_attention(const A& a, int D, bool fp8, cudaStream_t s) {
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  return rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D) ? launch_attention_tc(a, D, fp8, rows > 1024, s)
+  return rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D) ? launch_attention_tc(a, D, fp8, rows > pair_rows(a), s)
                                                                : launch_attention_mma(a, D, fp8, s);
 }
 

@@ -53,7 +53,7 @@ struct SampleArgs {
   const void* logits;
   long long row_stride;
   int M, V, cluster;
-  int per_warp;   // elements of a warp's segment, a multiple of 128, or of 512 read from L2
+  int per_warp;   // elements of a warp's segment, a multiple of 128 (bf16: 256), or of 512 read from L2
   int aligned;    // every row starts on a 16-byte boundary
   const float* temperature;
   const int32_t* top_k;
@@ -71,12 +71,16 @@ struct SampleArgs {
 // without a finite logit.
 struct RowState {
   u64 total, cut;
-  float top, rate, floor_w, pad;
+  float top, rate, floor_w;
+  int listed;  // the first this many entries of the row's list are all the tokens that stay; 0: no list
 };
+constexpr int kList = 256;  // entries (key << 32 | index) of a row's list
 // The same kernel for that: settings by request; request b has the rows cu_drafts[b] + extra * b up to
 // cu_drafts[b + 1] + extra * (b + 1), and rows of none are skipped.
 struct StateArgs : SampleArgs {
   RowState* state;
+  u64* lists;           // [row][kList], or NULL
+  int behind;           // launched behind another call of this kernel that does not concern it (see there)
   const int32_t* cu_drafts;
   int B, N, rows, extra;  // requests, drafts and target rows of the arrays
 };
@@ -88,6 +92,8 @@ __device__ __forceinline__ bool request_fits(int b, int c0, int c1, int N, int r
 __device__ __forceinline__ float clean(float z) {
   return fminf(fmaxf(z, -INFINITY), 3.402823466e38f);  // NaN to -inf
 }
+// Of two pairs of bf16 the larger ones; a number against NaN.
+__device__ __forceinline__ void max_bf16x2(uint32_t& a, uint32_t b) { asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b)); }
 // Ascending with descending z, and back.
 __device__ __forceinline__ uint32_t down_key(float z) {
   const uint32_t b = __float_as_uint(z + 0.0f);  // -0 to +0
@@ -108,6 +114,33 @@ __device__ __forceinline__ void split_mass(float w, uint32_t& hi, uint32_t& lo) 
   const float f = w * 1048576.0f, t = f + kMagic;
   hi = __float_as_uint(t);
   lo = __float_as_uint(fmaf(f - (t - kMagic), 1048576.0f, kMagic));
+}
+// Two at once (each operation rounded as the single one), summed into hi and lo.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<u64&>(d)) : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<u64&>(d)) : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<u64&>(d))
+      : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)), "l"(reinterpret_cast<u64&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void add_masses2(float2 w, uint32_t& hi, uint32_t& lo) {
+  const float2 f = mul2(w, both(1048576.0f)), t = add2(f, both(kMagic));
+  const float2 l = fma2(fma2(add2(t, both(-kMagic)), both(-1.0f), f), both(1048576.0f), both(kMagic));
+  hi += __float_as_uint(t.x) + __float_as_uint(t.y);
+  lo += __float_as_uint(l.x) + __float_as_uint(l.y);
 }
 __device__ __forceinline__ u64 join_mass(uint32_t hi, uint32_t lo, uint32_t parts) {
   return (u64)(((long long)(hi - parts * kMagicBits) << 20) + (int)(lo - parts * kMagicBits));
@@ -272,11 +305,12 @@ struct Slice {
       for (int e = 0; e < 4; ++e) z[e] = clean(z[e]);
     }
   }
+  // (!CLEAN: the logits may be as they were given, NaN and infinities among them.)
   // f(place, logits) for every fourth place of from..to (a multiple of 128 apart) and the lane's, until
   // it returns true.  Out of L2 four loads of a lane are under way at a time (top-k 20, 128 fp32 rows
   // of 248,320: 63 us, 72 with two, 79 with one); the loop over shared memory stays short, since few
   // rows spend their time on instructions read for the first time.
-  template <class F>
+  template <bool CLEAN = true, class F>
   __device__ __forceinline__ void each4(int from, int to, F&& f) const {
     const int lane4 = (threadIdx.x & 31) * 4;
     if constexpr (!HELD) {
@@ -288,7 +322,7 @@ struct Slice {
         for (int j = 0; j < 4; ++j) vector4(from + lane4 + 128 * j, z[j]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          clean4(z[j]);
+          if (CLEAN) clean4(z[j]);
           if (f(from + lane4 + 128 * j, z[j])) return;
         }
       }
@@ -297,7 +331,7 @@ struct Slice {
     for (; from < to; from += 128) {
       float z[4];
       load4(from + lane4, z);
-      clean4(z);
+      if (CLEAN) clean4(z);
       if (f(from + lane4, z)) return;
     }
   }
@@ -393,21 +427,21 @@ __device__ __forceinline__ void finish_candidates(const A& a, Shared& s, ulonglo
     if (q[e]) ++kept, mine += q[e], add_mass(s, (int)((uint32_t)c[e] >> shift), q[e]);
   }
   if constexpr (std::is_same<A, StateArgs>::value) {  // the last one that stays
-    u64 last = 0;
+    int last = -1;
 #pragma unroll
-    for (int e = 0; e < kOwn; ++e) last = q[e] && c[e] > last ? c[e] : last;
-    for (int o = 16; o; o >>= 1) {
-      const u64 x = __shfl_xor_sync(~0u, last, o);
-      last = x > last ? x : last;
+    for (int e = 0; e < kOwn; ++e) {
+      if (q[e]) last = tid * kOwn + e;
+      if (a.lists && tid * kOwn + e < kList) a.lists[(long long)m * kList + tid * kOwn + e] = c[e];
     }
+    last = __reduce_max_sync(~0u, last);
     mine = warp_sum(mine);
     __syncthreads();  // warp_mass has been read
-    if (lane == 0) s.warp_mass[warp] = mine, s.warp_tie[warp] = last;
+    if (lane == 0) s.warp_mass[warp] = mine, s.warp_count[warp] = (uint32_t)last;
     __syncthreads();
-    if (tid == 0) {
-      total = 0, last = 0;
-      for (int w = 0; w < kWarps; ++w) total += s.warp_mass[w], last = s.warp_tie[w] > last ? s.warp_tie[w] : last;
-      a.state[m] = RowState{total, last, top, rate, floor_w, 0.0f};
+    if (warp == 0) {
+      total = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
+      last = __reduce_max_sync(~0u, lane < kWarps ? (int)s.warp_count[lane] : -1);
+      if (lane == 0) a.state[m] = RowState{total, s.cand[last], top, rate, floor_w, a.lists && last < kList ? last + 1 : 0};
     }
     return;
   }
@@ -453,7 +487,7 @@ __device__ __forceinline__ void finish_candidates(const A& a, Shared& s, ulonglo
 }
 
 template <bool BF16, bool HELD, class A>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ A a) {
+__device__ __forceinline__ void sample_row(const A& a) {
   constexpr bool kState = std::is_same<A, StateArgs>::value;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
@@ -464,7 +498,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;  // this warp's places in the slice
   const int index0 = rank * kWarps * a.per_warp;               // of the slice's first element
   cluster_arrive();  // this CTA runs: the others may write its shared memory
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   int of = m;  // where its settings are
   if constexpr (kState) {
@@ -499,12 +532,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const uint8_t* const row = static_cast<const uint8_t*>(a.logits) + (long long)m * a.row_stride * kSize;
   const Slice<BF16, HELD> z_of = {HELD ? store : row + (long long)index0 * kSize, max(0, a.V - index0), a.aligned};
   if (!HELD) {
-    z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
-      top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));
+    int from = seg_from;  // a lane takes every 32nd unit of eight bf16 or four fp32
+    if (BF16 && a.aligned) {  // two at a maximum
+      uint32_t top2[4] = {0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+      const int whole = min(seg_to, z_of.end);
+#pragma unroll 1
+      for (; from + 1024 <= whole; from += 1024) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __ldg(reinterpret_cast<const uint4*>(z_of.at + 2 * (from + 256 * j + 8 * lane)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          max_bf16x2(top2[0], v[j].x), max_bf16x2(top2[1], v[j].y);
+          max_bf16x2(top2[2], v[j].z), max_bf16x2(top2[3], v[j].w);
+        }
+      }
+      for (; from < seg_to; from += 256) {
+        float z[4], y[4];
+        z_of.load4(from + 8 * lane, z);
+        z_of.load4(from + 8 * lane + 4, y);
+        top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));
+        top = fmaxf(fmaxf(fmaxf(top, y[0]), y[1]), fmaxf(y[2], y[3]));
+      }
+#pragma unroll
+      for (int j = 1; j < 4; ++j) max_bf16x2(top2[0], top2[j]);
+      top = fmaxf(top, fmaxf(__uint_as_float(top2[0] << 16), __uint_as_float(top2[0] & 0xFFFF0000u)));
+    }
+    z_of.template each4<false>(from, seg_to, [&](int, float (&z)[4]) {
+      top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));  // not NaN, which loses against any number
       return false;
     });
+    top = clean(top);
   } else {
     constexpr int kVec = 16 / kSize;                           // elements of a 16-byte load
+    uint32_t top2 = 0xFF80FF80u;                               // two bf16 at a time
     if (a.aligned) {
 #pragma unroll 4
       for (int i = seg_from + lane * kVec; i < seg_to; i += 32 * kVec) {
@@ -530,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (BF16) {
-            top = fmaxf(top, fmaxf(clean(__uint_as_float(w[e] << 16)), clean(__uint_as_float(w[e] & 0xFFFF0000u))));
+            max_bf16x2(top2, w[e]);
           } else {
             const float z = clean(__uint_as_float(w[e]));
             top = fmaxf(top, z);
@@ -539,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         *reinterpret_cast<uint4*>(store + (size_t)i * kSize) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if (BF16) top = clean(fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xFFFF0000u)));
     } else {
 #pragma unroll 8
       for (int i = seg_from + lane; i < seg_to; i += 32) {
@@ -559,20 +621,84 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) s.warp_max[warp] = top;
   clear_histogram(s);
-
+  for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
   __syncthreads();
-  if (warp == 0) {
-    top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+
+  // ---- top-k with a small k: every CTA's own k largest and little more, by a bound from its own lanes' maxima,
+  // go to the first CTA with its largest logit: one exchange in all
+  const bool by_count = k < (uint32_t)a.V;
+  const bool alone = by_count && k <= kThreads / 2 && k * C <= kCap * 5 / 8;  // about k + k^2 / 1024 tokens a CTA
+  const uint32_t room = kCap / C;                                             // of the list, for each CTA
+  if (alone) {
+    if (lane_max > -INFINITY) {
+      const int own = step_of(lane_max, top, steps);
+      if (own < kBins - 1) atomicAdd(&s.all_count[own], 1u);
+    }
+    __syncthreads();
+    find_bin(s, false, k, 0);
+    // steps past the last hold no mass, whatever the other CTAs' largest
+    const int bin = min(s.bin, kBins - 2);
+    if (tid == 0) s.found = 0;  // which the search has used
+    __syncthreads();
+    const float low = top - (float)(bin + 2) / steps;
+    auto list = [&](int i, float z) {
+      z = clean(z);
+      if (!(z >= low) || step_of(z, top, steps) > bin) return;
+      const uint32_t at = atomicAdd(&s.found, 1);
+      if (at < room) s.cand[at] = ((u64)down_key(z) << 32) | (uint32_t)(index0 + i);
+    };
+    // Such tokens lie with lanes whose own maximum is one: where they are few, the warp looks through a
+    // lane's units together, one load for 32 of them, and the segment as a whole is not read again.
+    uint32_t hits = __ballot_sync(~0u, top > -INFINITY && lane_max >= low);
+    if (__popc(hits) > 8) {
+      z_of.template each4<false>(seg_from, seg_to, [&](int i, float (&z)[4]) {
+        if (fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) list(i + e, z[e]);
+        }
+        return false;
+      });
+    } else {
+      const int unit = !a.aligned && HELD ? 1 : (BF16 && a.aligned ? 8 : 4);  // as the lanes took them above
+#pragma unroll 1
+      for (; hits; hits &= hits - 1) {
+        const int of_lane = seg_from + (__ffs(hits) - 1) * unit;
+#pragma unroll 1
+        for (int i = of_lane + lane * 32 * unit; i < seg_to; i += 1024 * unit) {
+          if (unit == 1) {
+            list(i, HELD ? (BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(z_of.at)[i])
+                                 : reinterpret_cast<const float*>(z_of.at)[i]) : -INFINITY);
+          } else {
+            for (int g = 0; g < unit; g += 4) {
+              float z[4];
+              z_of.load4(i + g, z);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) list(i + g + e, z[e]);
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const uint32_t mine = (uint32_t)s.found;
+    cluster_wait();
+    if (rank) {
+      const uint32_t to = map_to_rank(smem_addr(s.cand + rank * room), 0);
+      for (uint32_t i = tid; i < min(mine, room); i += kThreads) st_dsmem_u64(to + 8 * i, s.cand[i]);
+    }
+    if (warp == 0 && lane < C) st_dsmem_u32(map_to_rank(smem_addr(&s.rank_cand[rank]), lane), mine);
+  } else {
+    cluster_wait();
   }
-  cluster_wait();
   if (warp == 0 && lane < C) st_dsmem_f32(map_to_rank(smem_addr(&s.rank_max[rank]), lane), top);
   cluster_sync();
   top = lane < C ? s.rank_max[lane] : -INFINITY;
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (top == -INFINITY) {  // no finite logit; the whole cluster agrees
     if constexpr (kState) {
-      if (rank == 0 && tid == 0) a.state[m] = RowState{0, 0, 0.0f, 1.0f, 0.0f, 0.0f};
+      if (rank == 0 && tid == 0) a.state[m] = RowState{0, 0, 0.0f, 1.0f, 0.0f, 0};
     } else if (rank == 0 && tid == 0) {
       a.ids[m] = -1;
       if (a.logprob) a.logprob[m] = -INFINITY;
@@ -585,6 +711,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // it counted apart; floor_min drops smaller weights.
   u64 seg_mass, seg_tie;
   uint32_t seg_count, seg_ties;
+  // The masses of four logits as they were given: clipped to 0..1, the weight of NaN is 0 and that of an infinity
+  // 1, as those of cleaned logits.
+  auto add_weights4 = [&](const float (&z)[4], uint32_t& hi, uint32_t& lo) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float2 x = mul2(add2(make_float2(z[e], z[e + 1]), both(-top)), both(rate));
+      add_masses2(make_float2(__saturatef(expf(x.x)), __saturatef(expf(x.y))), hi, lo);
+    }
+  };
   auto segment = [&](auto with_cut, int from, int to, uint32_t cut, float floor_min) {
     constexpr bool kCut = decltype(with_cut)::value == 1, kWhole = decltype(with_cut)::value == 2;
     uint32_t hi = 0, lo = 0, parts = 0, count = 0, ties = 0;
@@ -592,22 +727,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // below this exponent the mass is zero, or the weight under the floor (expf and logf are good to
     // 2 ulp, a part in 2^21)
     const float least = !kWhole && floor_min > 0.0f ? fmaxf(logf(floor_min) - 1e-3f, -kReach) : -kReach;
-    z_of.each4(from, to, [&](int, float (&z)[4]) {
+    z_of.template each4<!kWhole>(from, to, [&](int, float (&z)[4]) {
       if ((fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) - top) * rate < least) return false;
       parts += 4;  // at most 2^8 tokens per lane: 32 bits hold the sums
+      if constexpr (kWhole) {
+        add_weights4(z, hi, lo);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float w = weight_of(z[e], top, rate);
-        if (!kWhole && w < floor_min) w = 0.0f;
-        if (kCut) {
-          const uint32_t key = down_key(z[e]);
-          if (key == cut) ++ties, tie = mass_of(w);
-          if (key >= cut) w = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          float w = weight_of(z[e], top, rate);
+          if (!kWhole && w < floor_min) w = 0.0f;
+          if (kCut) {
+            const uint32_t key = down_key(z[e]);
+            if (key == cut) ++ties, tie = mass_of(w);
+            if (key >= cut) w = 0.0f;
+          }
+          uint32_t h, l;
+          split_mass(w, h, l);
+          hi += h, lo += l;
+          if (!kWhole) count += w > kLeast;
         }
-        uint32_t h, l;
-        split_mass(w, h, l);
-        hi += h, lo += l;
-        if (!kWhole) count += w > kLeast;
       }
       return false;
     });
@@ -652,25 +791,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();  // s.found has been read
     if (tid == 0) s.found = 0;
     __syncthreads();
-    z_of.each4(seg_from, seg_to, [&](int i, float (&z)[4]) {
+    z_of.template each4<false>(seg_from, seg_to, [&](int i, float (&z)[4]) {
       const float most = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-      if (kMasses && (most - top) * rate >= -kReach) {  // as in `segment`
+      if (kMasses && (most - top) * rate >= -kReach) {
         parts += 4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t h, l;
-          split_mass(weight_of(z[e], top, rate), h, l);
-          hi += h, lo += l;
-        }
+        add_weights4(z, hi, lo);
       }
       if (most >= low) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (!(z[e] >= low && z[e] <= high)) continue;
-          const int b = step_of(z[e], origin, steps);
+          const float x = clean(z[e]);
+          if (!(x >= low && x <= high)) continue;
+          const int b = step_of(x, origin, steps);
           if (b < from || b > to) continue;
           const uint32_t at = atomicAdd(&s.found, 1);
-          if (at < kCap) s.cand[at] = ((u64)down_key(z[e]) << 32) | (uint32_t)(index0 + i + e);
+          if (at < kCap) s.cand[at] = ((u64)down_key(x) << 32) | (uint32_t)(index0 + i + e);
         }
       }
       return false;
@@ -767,9 +902,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return (uint32_t)s.found;
   };
 
+  // The lists of `alone` in the first CTA: of them the k largest and what shares their last step, unsorted.
+  auto pick = [&]() {
+    constexpr int kOwn = kCap / kThreads;
+    for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
+    __syncthreads();
+    u64 c[kOwn];
+    int step[kOwn];
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const uint32_t i = tid + e * kThreads, r = i / room;
+      step[e] = kBins;
+      if (i - r * room < s.rank_cand[r]) {
+        c[e] = s.cand[i];
+        step[e] = step_of(key_logit((uint32_t)(c[e] >> 32)), top, steps);
+        if (step[e] < kBins - 1) atomicAdd(&s.all_count[step[e]], 1u);
+      }
+    }
+    __syncthreads();
+    find_bin(s, false, k, 0);
+    const int last = min(s.bin, kBins - 2);
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e)
+      if (step[e] <= last) s.cand[atomicAdd(&s.found, 1)] = c[e];
+    __syncthreads();
+    return (uint32_t)s.found;
+  };
+
   uint32_t cut = 0xFFFFFFFFu, r_keep = 0xFFFFFFFFu;  // a key that no token has
-  const bool by_count = k < (uint32_t)a.V;
-  if (by_count || !(p >= 1.0f)) {
+  constexpr uint32_t kNone = 0xFFFFFFFFu;
+  uint32_t ready = kNone;  // candidates in the first CTA that hold all that stays
+  if (by_count || !(p >= 1.0f)) do {
+    if (alone) {
+      bool fits = true;
+      for (int r = 0; r < C; ++r) fits &= s.rank_cand[r] <= room;
+      if (fits) {  // no CTA touches another's memory from here on
+        ready = rank == 0 ? pick() : 0;
+        break;
+      }
+      __syncthreads();  // rank_cand has been read
+    }
     // ---- the lanes' own maxima first: at least k tokens lie in the steps down to the k-th largest
     // of them, and with k up to half the lanes not many more.  Where they number kCap at most and
     // hold all that top-k or top-p leaves, they finish the row, and no histogram of it is taken (one
@@ -797,12 +971,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         beyond = n <= kCap && !all;
       }
       if (n <= kCap && all) {
-        if (rank == 0) {
-          if (!by_count && n > 64) n = trim(n, limit);
-          sort_candidates(s, n);
-          finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, n, k, p, whole, floor_w, top, rate, u);
-        }
-        return;
+        ready = rank == 0 && !by_count && n > 64 ? trim(n, limit) : n;
+        break;
       }
       clear_histogram(s);
       __syncthreads();
@@ -846,11 +1016,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint32_t n = count_before + s.found;
     if (by_count && n <= kCap) {
       gather(std::false_type(), 0, bin < kBins ? bin : kBins - 2, low);  // after it no CTA touches another's memory
-      if (rank == 0) {
-        sort_candidates(s, n);
-        finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, n, k, p, whole, floor_w, top, rate, u);
-      }
-      return;
+      ready = n;
+      break;
     }
 
     // ---- too many: the cut itself, for top-k and then for top-p
@@ -913,6 +1080,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 else hi = mid;
               }
               s.cut = key, s.stay = i - lo + 1, s.one = q[e];
+              if constexpr (kState)  // what precedes it and itself are all that stays, unless min-p drops more
+                if (turn == 1) a.state[m] = RowState{before + q[e], s.cand[i], top, rate, floor_w, 0};
             }
             before += q[e];
           }
@@ -925,6 +1094,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         cluster_sync();
         cut = s.cut, r_keep = s.stay, one = s.one;
+        if constexpr (kState)
+          if (turn == 1 && !(weight_of(key_logit(cut), top, rate) < floor_w)) return;  // the whole cluster agrees
       } else {
         // digits of 10, 10, 10 and 2 bits
         uint32_t prefix = 0;
@@ -962,6 +1133,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         total = cluster_mass() + (u64)r_keep * one;
       }
     }
+  } while (false);
+  if (ready != kNone) {
+    if (rank == 0) {
+      sort_candidates(s, ready);
+      finish_candidates(a, s, reinterpret_cast<ulonglong2*>(store), m, ready, k, p, whole, floor_w, top, rate, u);
+    }
+    return;
   }
 
   // ---- kept mass of every warp's segment, over the cluster; then, in the CTA whose slice holds the
@@ -1016,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         seen += s.rank_ties[r];
       }
       if constexpr (kState) {
-        const RowState row = {total, ((u64)cut << 32) | 0xFFFFFFFFu, top, rate, floor_w, 0.0f};
+        const RowState row = {total, ((u64)cut << 32) | 0xFFFFFFFFu, top, rate, floor_w, 0};
         if (cut == 0xFFFFFFFFu || seen <= r_keep) {  // every token at the cut stays
           if (rank == 0 && tid == 0) a.state[m] = row;
           return;
@@ -1095,9 +1273,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 }
 
 template <bool BF16, bool HELD, class A>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ A a) {
+  if constexpr (std::is_same<A, StateArgs>::value) {
+    // Two of these in a row (the drafter's rows, then the target's) do not depend on each other, so the second one
+    // does not wait for the first to end, which it follows as soon as all of the first's CTAs run: these
+    // have waited for everything before.  It waits at its own end, so that what comes behind it, which waits for
+    // it alone, finds both done.
+    if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    sample_row<BF16, HELD>(a);
+    if (a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    sample_row<BF16, HELD>(a);
+  }
+}
+
+template <bool BF16, bool HELD, class A>
 cudaError_t launch(A a, int C, cudaStream_t s) {
   a.cluster = C;
-  const int step = HELD ? 128 : 512;
+  const int step = HELD ? (BF16 ? 256 : 128) : 512;
   a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step;
   a.aligned = ((uintptr_t)a.logits & 15) == 0 && (a.row_stride * (BF16 ? 2 : 4)) % 16 == 0;
   const size_t slice = HELD ? (size_t)kWarps * a.per_warp * (BF16 ? 2 : 4) : 0;
@@ -1144,7 +1339,8 @@ cudaError_t launch_rows(const A& a, cudaStream_t s) {
   // A slice is held in shared memory where two CTAs still share an SM (fp32, one row on 16: 14.7 / 9.4 us,
   // 15.0 / 10.4 read from L2), and a larger one where every CTA has an SM of its own (12 rows on eight:
   // 17.0 / 13.9 and 17.9 / 15.4; 16 rows: 27.0 / 23.9 and 19.9 / 20.6).
-  const long long slice = (long long)((a.V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128 * kWarps * (BF16 ? 2 : 4);
+  const int step = BF16 ? 256 : 128;
+  const long long slice = (long long)((a.V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step * kWarps * (BF16 ? 2 : 4);
   return slice <= (a.M * C <= 96 ? 163840 : 65536) ? launch<BF16, true>(a, C, s) : launch<BF16, false>(a, C, s);
 }
 

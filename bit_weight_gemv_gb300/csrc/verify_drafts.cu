@@ -7,9 +7,10 @@
 //
 // Two steps.  sample_kernel (sample.cuh), in the form that keeps a row's settled state instead of drawing
 // from it, takes every row of the target and of the drafter: the largest logit, the cut that top-k, top-p and
-// min-p come to, and the mass of what stays, in 32 bytes.  Then a cluster of CTAs per request looks up the
-// drafted tokens' shares, which needs two logits each, finds the first rejection, and draws once: it sums
-// the differences of its slice, the CTA that holds the aim takes it apart again, as in lowbit_sample.
+// min-p come to, and the mass of what stays, in 32 bytes, with a list of the target's tokens that stay where
+// they are few.  Then a cluster of CTAs per request looks up the drafted tokens' shares, which needs two logits
+// each, finds the first rejection, and draws once: from the list, or it sums the differences of its
+// slices, and the CTA that holds the aim takes its own apart again, as in lowbit_sample.
 //
 // Differences are taken in fp32 of the two probabilities, each product and the difference rounded by
 // itself, and become whole numbers (2^-40 each) before they are summed, so the sums are exact, in any order.
@@ -32,6 +33,7 @@ struct VerifyArgs {
   const float* v;
   const RowState* target;
   const RowState* draft;
+  const u64* lists;  // [target row][kList]
   int32_t* n_accept;
   int32_t* ids;
   float* accept;
@@ -39,32 +41,66 @@ struct VerifyArgs {
 };
 
 __device__ __forceinline__ float logit_at(const void* row, bool bf16, int i) {
-  return clean(bf16 ? bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(row) + i)) : __ldg(static_cast<const float*>(row) + i));
+  return bf16 ? bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(row) + i)) : __ldg(static_cast<const float*>(row) + i);
 }
-// The weight of a token that the row's settings leave, 0 of another and of one without mass (where a cut through
-// such tokens falls depends on the way that it was found).
-__device__ __forceinline__ float kept_weight(const RowState& s, float z, int i) {
-  const float w = weight_of(z, s.top, s.rate);
-  return (((u64)down_key(z) << 32) | (uint32_t)i) <= s.cut && w > kLeast && !(w < s.floor_w) && s.total ? w : 0.0f;
-}
+// A row's state in the form that a token is tested in: its weight counts where the logit is above cut, or equal to
+// it with an index up to `last`, and the weight is at least `least`, which leaves out those that min-p drops and
+// those without mass (where a cut through such tokens falls depends on the way that it was found).
+struct Kept {
+  float top, rate, cut, least;
+  uint32_t last;
+  __device__ __forceinline__ explicit Kept(const RowState& s) : top(s.top), rate(s.rate) {
+    const uint32_t key = (uint32_t)(s.cut >> 32);
+    cut = !s.total ? INFINITY : (key == 0xFFFFFFFFu ? -INFINITY : key_logit(key));
+    last = s.total ? (uint32_t)s.cut : 0u;
+    least = s.total ? fmaxf(s.floor_w, __uint_as_float(__float_as_uint(kLeast) + 1)) : INFINITY;
+  }
+  // The logit as it was given: clipped to 0..1, the weight of an infinity is that of the largest number.
+  __device__ __forceinline__ float weight(float z, int i) const {
+    const float w = __saturatef(weight_of(z, top, rate));
+    return (z > cut || (z == cut && (uint32_t)i <= last)) && w >= least ? w : 0.0f;
+  }
+  // Of four neighbours, from token i on; a row that nothing is cut off takes the short way.
+  __device__ __forceinline__ void weights4(const float (&z)[4], int i, float (&w)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float2 x = mul2(add2(make_float2(z[e], z[e + 1]), both(-top)), both(rate));
+      w[e] = __saturatef(expf(x.x)), w[e + 1] = __saturatef(expf(x.y));
+    }
+    if (cut == -INFINITY) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = w[e] >= least ? w[e] : 0.0f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (z[e] > cut || (z[e] == cut && (uint32_t)(i + e) <= last)) && w[e] >= least ? w[e] : 0.0f;
+    }
+  }
+};
 // 2^40 / total: what a weight is multiplied by to become a probability.
 __device__ __forceinline__ float inverse(const RowState& s) {
   return s.total ? (float)(0x1p40 / (double)s.total) : 0.0f;
 }
 
+// A thousand threads a CTA, so that few requests, which have 16 CTAs each at most, keep their SMs busy.
+constexpr int kDrawThreads = 1024, kDrawWarps = kDrawThreads / 32;
+
 struct VerifyShared {
-  u64 warp_mass[kWarps], rank_mass[2][kMaxCluster];
+  u64 warp_mass[kDrawWarps], rank_mass[2][kMaxCluster];
+  u64 token[kList], mass[kList];  // a listed row's
+  u64 aim;
+  float ip, iq;
   int first;
 };
 
 template <bool BF16, bool DRAFT_BF16>
-__global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ VerifyShared s;
   constexpr int kSize = BF16 ? 2 : 4, kDraftSize = DRAFT_BF16 ? 2 : 4;
   const int C = a.cluster, rank = blockIdx.x % C, b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;
-  const int index0 = rank * kWarps * a.per_warp;
+  const int index0 = rank * kDrawWarps * a.per_warp;
   cluster_arrive();  // this CTA runs: the others may write its shared memory
   if (tid == 0) s.first = INT32_MAX;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -83,14 +119,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
   const uint8_t* const draft_rows = static_cast<const uint8_t*>(a.draft_logits);
 
   // ---- which drafts are accepted: every CTA finds out for itself
-  for (int i = tid; i < n; i += kThreads) {
+  for (int i = tid; i < n; i += kDrawThreads) {
     const int r = c0 + i, d = a.drafts[r];
     const bool inside = d >= 0 && d < a.V;
     double share = 0.0, given = 1.0;
     if (inside) {
       const RowState p = a.target[r + b];
       const float z = logit_at(rows + (long long)(r + b) * a.row_stride * kSize, BF16, d);
-      share = p.total ? (double)mass_of(kept_weight(p, z, d)) / (double)p.total : 0.0;
+      share = p.total ? (double)mass_of(Kept(p).weight(z, d)) / (double)p.total : 0.0;
     }
     if (draft_rows) {
       given = 0.0;
@@ -98,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
       if (col >= 0 && col < a.Vd) {
         const RowState q = a.draft[r];
         const float z = logit_at(draft_rows + (long long)r * a.draft_stride * kDraftSize, DRAFT_BF16, col);
-        if (q.total) given = (double)mass_of(kept_weight(q, z, col)) / (double)q.total;
+        if (q.total) given = (double)mass_of(Kept(q).weight(z, col)) / (double)q.total;
       }
     }
     float u = a.u[r];
@@ -111,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
   const RowState p = a.target[t];
   const bool rejected = j < n;
   if (rank == 0) {
-    for (int i = tid; i <= n; i += kThreads)
+    for (int i = tid; i <= n; i += kDrawThreads)
       if (i != j) a.ids[c0 + b + i] = i < j ? a.drafts[c0 + i] : -1;
     if (tid == 0) {
       a.n_accept[b] = j;
@@ -122,39 +158,78 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
     cluster_wait();
     return;
   }
+  if (p.listed && rank != 0) {  // the first CTA does it alone, and the whole cluster agrees
+    cluster_wait();
+    return;
+  }
   RowState q = {};
   if (rejected && draft_rows) q = a.draft[c0 + j];
   const int out = rejected && !draft_rows ? a.drafts[c0 + j] : -1;  // proposed with certainty
-  const float ip = inverse(p), iq = inverse(q);
-  // tokens below it have no mass, or are cut off
-  const float cut_z = (uint32_t)(p.cut >> 32) == 0xFFFFFFFFu ? -INFINITY : key_logit((uint32_t)(p.cut >> 32));
+  // 64-bit floating point is slow here (two a clock and SM): one warp's worth of it
+  if (warp == 0) {
+    const float x = inverse(lane == 0 ? p : q);
+    if (lane == 0) s.ip = x;
+    if (lane == 1) s.iq = x;
+  }
+  __syncthreads();
+  const float ip = s.ip, iq = s.iq;
+  const uint8_t* const draft_row = draft_rows + (long long)(c0 + j) * a.draft_stride * kDraftSize;
+  const Kept by_p(p), by_q(q);
+  // What is left of a token's probability once the drafter's is taken off.
+  auto left_of = [&](float w, float drafted) { return fmaxf(__fsub_rn(__fmul_rn(w, ip), __fmul_rn(drafted, iq)), 0.0f); };
+
+  if (p.listed) {
+    cluster_wait();
+    const u64 entry = tid < p.listed ? a.lists[(long long)t * kList + tid] : 0;
+    const int token = (int)(uint32_t)entry;
+    float w = 0.0f, x = 0.0f;
+    if (tid < p.listed) {
+      w = by_p.weight(key_logit((uint32_t)(entry >> 32)), token);
+      x = w;
+      if (rejected && draft_rows) {
+        const int col = a.draft_index ? __ldg(a.draft_index + token) : token;
+        x = left_of(w, col >= 0 && col < a.Vd ? by_q.weight(logit_at(draft_row, DRAFT_BF16, col), col) : 0.0f);
+      } else if (rejected) {
+        x = token == out ? 0.0f : __fmul_rn(w, ip);
+      }
+    }
+    u64 mine = mass_of(x);
+    if (rejected && !__syncthreads_or(mine != 0)) mine = mass_of(w);
+    if (tid < kList) s.token[tid] = token, s.mass[tid] = mine;
+    const u64 sum = warp_sum(mine);
+    if (lane == 0) s.warp_mass[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const u64 all = warp_sum(s.warp_mass[lane]);
+      const u64 aim = aim_of(a.v[b], all);
+      if (lane == 0) s.aim = aim;
+    }
+    __syncthreads();
+    if (!mine) return;
+    u64 before = 0;  // of the tokens with lower indices
+    for (int i = 0; i < p.listed; ++i) before += s.token[i] < (u64)token ? s.mass[i] : 0;
+    if (s.aim >= before && s.aim < before + mine) a.ids[t] = token;
+    return;
+  }
 
   const Slice<BF16, false> z_of = {rows + (long long)t * a.row_stride * kSize + (long long)index0 * kSize,
                                    max(0, a.V - index0), a.aligned};
-  const uint8_t* const draft_row = draft_rows + (long long)(c0 + j) * a.draft_stride * kDraftSize;
   const Slice<DRAFT_BF16, false> y_of = {draft_row + (long long)index0 * kDraftSize, max(0, a.Vd - index0), a.draft_aligned};
 
   // What four neighbouring tokens are drawn with, in units of 1: false where all of it is zero.
   bool differ = rejected;  // else p itself
   auto values = [&](int i, const float (&z)[4], float (&x)[4]) {
     const float most = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-    if (!(most >= cut_z) || (most - p.top) * p.rate < -kReach) return false;
-    bool any = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = kept_weight(p, z[e], index0 + i + e);
-      any |= x[e] > 0.0f;
-    }
-    if (!differ || !any) return any;
+    if (!(most >= by_p.cut) || (most - p.top) * p.rate < -kReach) return false;
+    by_p.weights4(z, index0 + i, x);
+    if (!differ) return true;
     if (draft_rows) {
       if (!a.draft_index) {
-        float y[4];
-        y_of.load4(i, y);
+        float y[4], w[4];
+        y_of.load4(i, y);  // -inf past the row
+        by_q.weights4(y, index0 + i, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = index0 + i + e < a.Vd ? kept_weight(q, clean(y[e]), index0 + i + e) : 0.0f;
-          x[e] = fmaxf(__fsub_rn(__fmul_rn(x[e], ip), __fmul_rn(w, iq)), 0.0f);
-        }
+        for (int e = 0; e < 4; ++e) x[e] = left_of(x[e], w[e]);
       } else {
         int col[4];
         if (a.index_aligned && index0 + i + 4 <= a.V) {
@@ -166,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float w = 0.0f;
-          if (x[e] > 0.0f && col[e] >= 0 && col[e] < a.Vd) w = kept_weight(q, logit_at(draft_row, DRAFT_BF16, col[e]), col[e]);
-          x[e] = fmaxf(__fsub_rn(__fmul_rn(x[e], ip), __fmul_rn(w, iq)), 0.0f);
+          if (x[e] > 0.0f && col[e] >= 0 && col[e] < a.Vd) w = by_q.weight(logit_at(draft_row, DRAFT_BF16, col[e]), col[e]);
+          x[e] = left_of(x[e], w);
         }
       }
     } else {
@@ -178,16 +253,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
   };
   auto sum_of = [&](int from, int to) {
     uint32_t hi = 0, lo = 0, parts = 0;
-    z_of.each4(from, to, [&](int i, float (&z)[4]) {
+    z_of.template each4<false>(from, to, [&](int i, float (&z)[4]) {
       float x[4];
       if (!values(i, z, x)) return false;
       parts += 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t h, l;
-        split_mass(x[e], h, l);
-        hi += h, lo += l;
-      }
+      add_masses2(make_float2(x[0], x[1]), hi, lo);
+      add_masses2(make_float2(x[2], x[3]), hi, lo);
       return false;
     });
     return warp_sum(join_mass(hi, lo, parts));
@@ -203,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
     if (lane == 0) s.warp_mass[warp] = mine;
     __syncthreads();
     if (warp == 0) {
-      const u64 sum = warp_sum(lane < kWarps ? s.warp_mass[lane] : 0);
+      const u64 sum = warp_sum(s.warp_mass[lane]);
       if (lane < C) st_dsmem_u64(map_to_rank(smem_addr(&s.rank_mass[turn][rank]), lane), sum);
     }
     cluster_sync();
@@ -214,16 +285,21 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
     if (total || !differ) break;
     differ = false;
   }
-  const u64 aim = aim_of(a.v[b], total);
+  if (warp == 0) {
+    const u64 at = aim_of(a.v[b], total);
+    if (lane == 0) s.aim = at;
+  }
+  __syncthreads();
+  const u64 aim = s.aim;
   const u64 slice = s.rank_mass[rejected && !differ ? 1 : 0][rank];
   if (aim < before || aim >= before + slice) return;
 
-  // ---- the warp's segment that holds the aim, its sixteenth, then the token
+  // ---- the warp's segment that holds the aim, of its parts the one that does, then the token
   int from = seg_from, to = seg_to;
 #pragma unroll 1
   for (int level = 0; level < 2; ++level) {
     int owner = 0;
-    for (; owner < kWarps; ++owner) {
+    for (; owner < kDrawWarps; ++owner) {
       if (aim < before + s.warp_mass[owner]) break;
       before += s.warp_mass[owner];
     }
@@ -231,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
       if (owner != warp) return;
       break;
     }
-    const int each = ((a.per_warp / 128 + kWarps - 1) / kWarps) * 128;
+    const int each = ((a.per_warp / 128 + kDrawWarps - 1) / kDrawWarps) * 128;
     to = (owner + 1) * a.per_warp;
     from = min(owner * a.per_warp + warp * each, to);
     to = min(from + each, to);
@@ -240,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const __grid_c
     if (lane == 0) s.warp_mass[warp] = mine;
     __syncthreads();
   }
-  z_of.each4(from, to, [&](int i, float (&z)[4]) {
+  z_of.template each4<false>(from, to, [&](int i, float (&z)[4]) {
     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     u64 m[4], sum = 0;
     const bool some = values(i, z, x);
@@ -269,9 +345,9 @@ cudaError_t launch_draw(VerifyArgs a, cudaStream_t s) {
   // Slices of 16,384 elements and more, and no more CTAs than fit at a time.
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
-  while (C > 4 && (long long)a.B * C > 256) C /= 2;
+  while (C > 2 && (long long)a.B * C > 152) C /= 2;
   a.cluster = C;
-  a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + 511) / 512 * 512;
+  a.per_warp = ((a.V + C * kDrawWarps - 1) / (C * kDrawWarps) + 511) / 512 * 512;
   a.aligned = ((uintptr_t)a.logits & 15) == 0 && (a.row_stride * (BF16 ? 2 : 4)) % 16 == 0;
   a.draft_aligned = ((uintptr_t)a.draft_logits & 15) == 0 && (a.draft_stride * (DRAFT_BF16 ? 2 : 4)) % 16 == 0;
   a.index_aligned = ((uintptr_t)a.draft_index & 15) == 0;
@@ -287,7 +363,7 @@ cudaError_t launch_draw(VerifyArgs a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kDrawThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -314,7 +390,7 @@ extern "C" {
 
 size_t lowbit_verify_drafts_workspace_bytes(int M, int N) {
   if (M < 1 || M > 1 << 24 || N < 0 || N > 1 << 24) return 0;
-  return ((size_t)M + (size_t)N) * sizeof(RowState);
+  return ((size_t)M + (size_t)N) * sizeof(RowState) + (size_t)M * kList * sizeof(u64);
 }
 
 lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowbit_row_settings* draft, int B, int N,
@@ -342,9 +418,11 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   if (!err) return LOWBIT_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RowState* const states = static_cast<RowState*>(workspace);
+  u64* const lists = reinterpret_cast<u64*>(states + target->rows + N);
+  const bool drafter = draft && N > 0;
 
   for (const lowbit_row_settings* r : {draft, target}) {
-    if (!r || (r == draft && N == 0)) continue;
+    if (!r || (r == draft && !drafter)) continue;
     StateArgs st = {};
     st.logits = r->logits;
     st.row_stride = r->row_stride;
@@ -355,6 +433,8 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
     st.top_p = r->top_p;
     st.min_p = r->min_p;
     st.state = r == target ? states : states + target->rows;
+    st.lists = r == target ? lists : nullptr;
+    st.behind = r == target && drafter;
     st.cu_drafts = cu_drafts;
     st.B = B;
     st.N = N;
@@ -381,6 +461,7 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   a.v = v;
   a.target = states;
   a.draft = states + target->rows;
+  a.lists = lists;
   a.n_accept = n_accept;
   a.ids = ids;
   a.accept = accept;

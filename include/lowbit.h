@@ -506,8 +506,8 @@ typedef struct lowbit_row_settings {
   const float* min_p;
 } lowbit_row_settings;
 
-/* Bytes of lowbit_verify_drafts's workspace for M rows of the target and N drafts: 32 each (0 for invalid
- * shapes). */
+/* Bytes of lowbit_verify_drafts's workspace for M rows of the target and N drafts: 2,080 and 32 each (0 for
+ * invalid shapes). */
 size_t lowbit_verify_drafts_workspace_bytes(int M, int N);
 
 /* Drafted tokens accepted or rejected against the target's probabilities, and the token that follows, so

@@ -102,7 +102,7 @@ def call(n, target=None, draft=None, **kw):
     (dict(draft=rows(rows=5)), SHAPE), (dict(draft=rows(rows=6, V=101)), SHAPE), (dict(draft=rows(rows=6, V=0)), SHAPE),
     (dict(target=rows(logits=P + 2)), ALIGN), (dict(target=rows(logits=P + 1, dtype=1)), ALIGN), (dict(ids=P + 2), ALIGN),
     (dict(draft=rows(rows=6, top_p=P + 1)), ALIGN), (dict(accept=P + 1), ALIGN), (dict(ws=P + 8), ALIGN), (dict(ws=None), WORKSPACE),
-    (dict(bytes=14 * 32 - 1), WORKSPACE)])
+    (dict(bytes=8 * 2080 + 6 * 32 - 1), WORKSPACE)])
 def test_refusals(native, kw, status):  # noqa: F811
     assert call(native, **kw) == status
 
@@ -114,7 +114,7 @@ def test_no_rows_at_all(native):  # noqa: F811
 
 def test_workspace_sizes(native):  # noqa: F811
     f = native.lowbit_verify_drafts_workspace_bytes
-    assert f(8, 6) == 14 * 32 and f(1, 0) == 32
+    assert f(8, 6) == 8 * 2080 + 6 * 32 and f(1, 0) == 2080
     assert f(0, 0) == f(4, -1) == f((1 << 24) + 1, 0) == 0
 
 
