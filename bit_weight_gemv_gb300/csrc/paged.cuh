@@ -38,9 +38,10 @@ lowbit_status make_paged_args(const lowbit_paged_batch* batch, const lowbit_page
 struct Request {
   int row0, n, kv;
   int skip;  // keys of its pages that come before those counted by kv (lowbit_prefix_attention's own part)
+  int all;   // every row sees every key (its shared part), whatever the mask
 };
 __device__ __forceinline__ Request check_request(const PagedArgs& a, int from, int to, int kv) {
-  Request r = {from, to - from, kv, 0};
+  Request r = {from, to - from, kv, 0, 0};
   if (r.row0 < 0 || r.n < 0 || r.row0 > a.T - r.n || r.kv < 0 ||
       (long long)r.kv > ((long long)a.width << a.page_shift)) {
     record_error(a.err, LOWBIT_ERR_INVALID_ARG);
@@ -82,7 +83,7 @@ __device__ __forceinline__ int first_key(const ItemShape& s, int pos) {
 __device__ __forceinline__ Span tile_span(const ItemShape& s, const Request& q, int qt) {
   const int r0 = qt << s.r_shift, r1 = min(r0 + (1 << s.r_shift), q.n * s.G) - 1;
   Span k;
-  k.hi = s.causal ? max(0, min(q.kv, q.kv - q.n + token_of(s, r1) + 1)) : q.kv;
+  k.hi = s.causal && !q.all ? max(0, min(q.kv, q.kv - q.n + token_of(s, r1) + 1)) : q.kv;
   k.lo = first_key(s, q.kv - q.n + token_of(s, r0));
   if (k.lo >= k.hi) k.lo = k.hi = 0;
   return k;

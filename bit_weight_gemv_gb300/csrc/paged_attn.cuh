@@ -51,67 +51,81 @@ struct AttnArgs {
                     // or queries on tcgen05) never come, so that every role's wait gives up; 0 in normal use
 };
 
-// lowbit_prefix_attention makes two launches of the same kernels.  The shared part: a "request" is all rows of a
-// group (p.B counts groups) over the keys that its requests share; every row leaves as a piece does.  The own
-// part: the requests over their own keys, each row joined with what the first part left.
+// lowbit_prefix_attention runs the same kernels over a longer list of "requests": first its groups (all rows of a
+// group over the keys that its requests share), then the requests over their own keys; a launch takes
+// a part of that list.  Every row leaves as a piece does, from whichever of the two, and the join step
+// (prefix_attn.cu) finds by `found` where its pieces are.
 struct PrefixArgs : AttnArgs {
-  bool shared;
+  int first;        // the launch's part of the list: p.B entries from here on
   int groups, requests;
   const int32_t* cu_groups;
   const int32_t* prefix_lens;
-  float* base_o;    // [row of out][D]
-  float2* base_ml;  // [row of out]: a sum of kNoPiece where the row was not computed
+  long long rows;   // rows of out, T * Hq; of the arrays below first the shared part's, then the own part's
+  float* base_o;    // [2][row][D]: rows that one CTA saw all keys of
+  float2* base_ml;  // [2][row]
+  int4* found;      // [2][row]: {kInBase or kLost}, or {more, first, next, apart}: places of the first piece and of
+                    // the `more` that follow it, the second at `next` and the others `apart` behind one another
+  int behind;       // launched behind another part, which it does not wait for before its end
 };
+constexpr int kInBase = -1, kLost = -2;
 template <class A>
 constexpr bool kPrefix = std::is_same<A, PrefixArgs>::value;
 
 __device__ __forceinline__ Request load_request(const AttnArgs& a, int b) {
   return check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
 }
-// All rows of group g over the whole pages of its shared length.
+// All rows of group g over the whole pages of its shared length; no rows where there are none.
 __device__ __forceinline__ Request load_group(const PrefixArgs& a, int g) {
   const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
   if (from < 0 || to < from || to > a.requests || len < 0) {
     record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
-    return Request{0, 0, 0, 0};
+    return Request{0, 0, 0, 0, 1};
   }
-  return check_request(a.p, a.p.cu_q[from], a.p.cu_q[to], len & ~a.p.page_mask);
+  Request r = check_request(a.p, a.p.cu_q[from], a.p.cu_q[to], len & ~a.p.page_mask);
+  r.all = 1;
+  if (r.kv == 0) r.n = 0;
+  return r;
 }
-// Request b without the keys that its group shares.  One that has new tokens among these, or rows
-// outside its group's, counts as inconsistent.
-__device__ __forceinline__ Request load_own(const PrefixArgs& a, int b) {
+// The last group that begins at request b or before it.
+__device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
   int g = 0;
 #pragma unroll 1
-  for (int end = a.groups; end - g > 1;) {  // the last group that begins at b or before it
+  for (int end = a.groups; end - g > 1;) {
     const int mid = (g + end) / 2;
     if (a.cu_groups[mid] <= b) g = mid;
     else end = mid;
   }
-  const Request s = load_group(a, g);
+  return g;
+}
+// Request b without the keys that its group shares.  One that has new tokens among these counts as inconsistent;
+// what else can be wrong with it the join step looks for, which keeps its loads out of the way here.
+__device__ __forceinline__ Request load_own(const PrefixArgs& a, int b) {
+  const int g = group_of(a, b), skip = a.prefix_lens[g] & ~a.p.page_mask;
   Request r = check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
   if (r.n == 0) return r;
-  if (b < a.cu_groups[g] || b >= a.cu_groups[g + 1] || r.row0 < s.row0 || r.row0 + r.n > s.row0 + s.n ||
-      r.kv - r.n < s.kv) {
+  if (skip < 0 || r.kv - r.n < skip) {
     record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
-    return Request{0, 0, 0, 0};
+    return Request{0, 0, 0, 0, 0};
   }
-  r.kv -= s.kv;
-  r.skip = s.kv;
+  r.kv -= skip;
+  r.skip = skip;
   return r;
 }
 __device__ __forceinline__ Request load_request(const PrefixArgs& a, int b) {
-  return a.shared ? load_group(a, b) : load_own(a, b);
+  b += a.first;
+  return b < a.groups ? load_group(a, b) : load_own(a, b - a.groups);
 }
 // The block table from the page of the request's first counted key on.
 __device__ __forceinline__ const int32_t* table_of(const AttnArgs& a, int b, const Request&) {
   return a.p.table + (long long)b * a.p.table_stride;
 }
 __device__ __forceinline__ const int32_t* table_of(const PrefixArgs& a, int b, const Request& r) {
-  return a.p.table + (long long)(a.shared ? a.cu_groups[b] : b) * a.p.table_stride + (r.skip >> a.p.page_shift);
+  b += a.first;
+  b = b < a.groups ? a.cu_groups[b] : b - a.groups;
+  return a.p.table + (long long)b * a.p.table_stride + (r.skip >> a.p.page_shift);
 }
 
 cudaError_t launch_attention_mma(const AttnArgs& a, int D, bool fp8, cudaStream_t s);
-cudaError_t launch_attention_mma(const PrefixArgs& a, int D, bool fp8, cudaStream_t s);
 
 // a / b of nonnegative numbers: 32-bit where both fit (a 64-bit division is a hundred instructions).
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -169,7 +183,7 @@ template <class A>
 __device__ __forceinline__ int start_walk_short(const A& a, int cta, Walk& w, Share& sh) {
   const int lane = threadIdx.x & 31;
   if (a.p.B > 32) return 0;
-  Request q = {0, 0, 0, 0};
+  Request q = {0, 0, 0, 0, 0};
   if (lane < a.p.B) q = load_request(a, lane);
   // one tile holds every row: its keys end with the request's, whatever the mask
   const int lo = first_key(a.shape, q.kv - q.n);
@@ -199,6 +213,7 @@ __device__ __forceinline__ int start_walk_short(const A& a, int cta, Walk& w, Sh
   w.q.n = __shfl_sync(~0u, q.n, src);
   w.q.kv = __shfl_sync(~0u, q.kv, src);
   w.q.skip = __shfl_sync(~0u, q.skip, src);
+  w.q.all = __shfl_sync(~0u, q.all, src);
   w.span.lo = __shfl_sync(~0u, none ? 0 : lo, src);
   w.span.hi = __shfl_sync(~0u, none ? 0 : q.kv, src);
   w.h = (int)(off / each);
@@ -334,36 +349,47 @@ __device__ __forceinline__ bool walk_next(const A& a, Walk& w) {
   return true;
 }
 
-__device__ __forceinline__ float pow2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// The first and the last step of an attention kernel.  A part of lowbit_prefix_attention that is launched behind another
+// one starts as soon as all of the other's CTAs run, which have waited for everything before; it waits for them at
+// its own end, so that the step behind it, which waits for it alone, finds both done.
+__device__ __forceinline__ void begin_launch(const AttnArgs&) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// What the shared keys of output row `at` left, joined with (m, l): the factors of the own part's output and of
-// the base's.  False where the base was not computed.
-__device__ __forceinline__ bool join_base(const PrefixArgs& a, long long at, float& m, float& l, float& f_own, float& f_base) {
-  const float2 b = a.base_ml[at];
-  const float top = fmaxf(m, b.x);
-  f_own = top == -INFINITY ? 0.0f : pow2(m - top);
-  f_base = top == -INFINITY ? 0.0f : pow2(b.x - top);
-  l = f_own * l + f_base * b.y;
-  m = top;
-  return b.y != kNoPiece;
+__device__ __forceinline__ void end_launch(const AttnArgs&) {}
+__device__ __forceinline__ void begin_launch(const PrefixArgs& a) {
+  if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void end_launch(const PrefixArgs& a) {
+  if (a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Whether a row whose keys this CTA saw all of goes to out, and where it goes else: to its piece, or (the shared
-// part) to its base.
-__device__ __forceinline__ bool to_out(const AttnArgs&) { return true; }
-__device__ __forceinline__ bool to_out(const PrefixArgs& a) { return !a.shared; }
-__device__ __forceinline__ float2* part_ml_of(const AttnArgs& a, bool, long long, long long piece) { return a.piece_ml + piece; }
-__device__ __forceinline__ float2* part_ml_of(const PrefixArgs& a, bool whole, long long row, long long piece) {
-  return whole ? a.base_ml + row : a.piece_ml + piece;
+// Where a row's (reference, sum) and output go that do not go to out: to its piece, or to its base.
+struct Part {
+  float2* ml;
+  float* o;
+};
+template <int D>
+__device__ __forceinline__ Part part_of(const AttnArgs& a, const Walk&, bool, long long, long long piece) {
+  return Part{a.piece_ml + piece, a.piece_o + piece * D};
 }
 template <int D>
-__device__ __forceinline__ float* part_o_of(const AttnArgs& a, bool, long long, long long piece) { return a.piece_o + piece * D; }
-template <int D>
-__device__ __forceinline__ float* part_o_of(const PrefixArgs& a, bool whole, long long row, long long piece) {
-  return whole ? a.base_o + row * D : a.piece_o + piece * D;
+__device__ __forceinline__ Part part_of(const PrefixArgs& a, const Walk& w, bool whole, long long row, long long piece) {
+  if (!whole) return Part{a.piece_ml + piece, a.piece_o + piece * D};
+  if (a.first + w.b >= a.groups) row += a.rows;
+  return Part{a.base_ml + row, a.base_o + row * D};
+}
+// By the CTA that holds the first piece of a row, place `in_tile` of its item, done up to key tile `done`.
+__device__ __forceinline__ void say_found(const AttnArgs&, const Walk&, long long, bool, int, int, long long, long long) {}
+__device__ __forceinline__ void say_found(const PrefixArgs& a, const Walk& w, long long row, bool good, int done, int in_tile,
+                                          long long chunk, long long piece) {
+  if (a.first + w.b >= a.groups) row += a.rows;
+  int4 f = make_int4(good ? kInBase : kLost, 0, 0, 0);
+  if (good && done < w.tiles)
+    f = make_int4((int)quotient(w.tiles - done + chunk - 1, chunk), (int)piece,
+                  (2 * ((int)blockIdx.x + 1) << a.shape.r_shift) + in_tile, 2 << a.shape.r_shift);
+  a.found[row] = f;
 }
 
 // 4-D tiled tensor copy (TMA) global -> shared.
@@ -402,9 +428,8 @@ void attention_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int ct
 bool attention_tc_fits(const AttnArgs& a, int D);
 cudaError_t launch_attention_tc(const AttnArgs& a, int D, bool fp8, bool pair, cudaStream_t s);
 cudaError_t launch_attention_tc(const PrefixArgs& a, int D, bool fp8, bool pair, cudaStream_t s);
-// The combine step behind either.
+// The combine step behind lowbit_paged_attention's.
 cudaError_t launch_combine(const AttnArgs& a, int D, cudaStream_t s);
-cudaError_t launch_combine(const PrefixArgs& a, int D, cudaStream_t s);
 
 
 // Checks of the arguments that both attention calls take; fills `a` all but the workspace and the error word.
@@ -435,13 +460,9 @@ inline void use_pieces(AttnArgs* a, void* at, int D) {
 // 29.5, 40 rows 48.2 / 32.2 (500 keys 10.4 / 10.8), 16 requests of up to 8,000 keys and 32 rows 28.7 / 29.8, 40
 // rows 33.7 / 27.5; heads of 64, 48 rows 31.2 / 27.0 and 20.9 / 22.7; 256 rows an item: 16,000 keys, 1,600 rows
 // 137 with 128 and 114 with 256 (of 4,000 keys 49 and 52).
-// The shared part of a prefix takes 256 rows an item from 500 on: there the keys are long.
-inline int pair_rows(const AttnArgs&) { return 1024; }
-inline int pair_rows(const PrefixArgs& a) { return a.shared ? 500 : 1024; }
-template <class A>
-cudaError_t launch_attention(const A& a, int D, bool fp8, cudaStream_t s) {
+inline cudaError_t launch_attention(const AttnArgs& a, int D, bool fp8, cudaStream_t s) {
   const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  return rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D) ? launch_attention_tc(a, D, fp8, rows > pair_rows(a), s)
+  return rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D) ? launch_attention_tc(a, D, fp8, rows > 1024, s)
                                                                : launch_attention_mma(a, D, fp8, s);
 }
 

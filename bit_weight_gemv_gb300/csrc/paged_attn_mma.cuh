@@ -220,9 +220,7 @@ __device__ __forceinline__ void copy_tiles(const A& a, const CUtensorMap& kmap, 
 }
 
 template <int D, int MT, bool FP8, class A>
-__global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
-attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void attn_mma_items(const A& a, const CUtensorMap& kmap, const CUtensorMap& vmap) {
   using C = Cfg<D, MT, FP8>;
   constexpr int RB = C::kRowBytes, S = C::kStages;
   constexpr int kNT = 2 * MT;       // 8-key tiles per warp
@@ -238,13 +236,12 @@ attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap
   if (tid == 0) {
     init_bars(bars, S);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_launch(a);
   __syncthreads();  // the barriers are initialised
   Walk it;
   Share share;
   const bool busy = start_walk<kThreads>(a, blockIdx.x, it, share);
-  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
+  if (!kPrefix<A> && tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
   if (!busy) return;
   int left = share.left;
   int stage = 0;
@@ -277,14 +274,14 @@ attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap
       const int tok = token_of(a.shape, r);
       const bool in = r < rows;
       const int pos = q.kv - q.n + tok;
-      jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
+      jhi[i] = in ? (a.shape.causal && !q.all ? min(q.kv, pos + 1) : q.kv) : 0;
       jlo[i] = first_key(a.shape, pos);
       qrow[i] = in ? (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G) : -1;
     }
     // keys that every row of the CTA's tile sees need no mask
     const int last_row = min(r0 + C::kRows, rows) - 1;
     const int all_lo = first_key(a.shape, q.kv - q.n + token_of(a.shape, last_row));
-    const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
+    const int all_hi = a.shape.causal && !q.all ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
 
     // ---- query fragments; with an e4m3 cache the row is scaled by a power of two into fp16
     uint32_t qf[C::kQShared ? 1 : C::kSteps][4];
@@ -571,36 +568,18 @@ attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap
     if (wk == 0) {
       // what other warps added: their failures came before the join's barriers
       const bool good = MT < 4 ? !bars.failed : __all_sync(~0u, ok);
-      const bool whole = kt0 == 0 && kt1 == it.tiles, final = whole && to_out(a);
+      const bool whole = kt0 == 0 && kt1 == it.tiles, final = whole && !kPrefix<A>;
       const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (qrow[i] < 0) continue;
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * C::kRows + wr * 16 + g + 8 * i;
-        float2* const part_ml = part_ml_of(a, whole, qrow[i], piece);
-        float* const part = part_o_of<D>(a, whole, qrow[i], piece);
+        const Part to = part_of<D>(a, it, whole, qrow[i], piece);
+        float* const part = to.o;
+        if (t == 0 && kt0 == 0) say_found(a, it, qrow[i], good, kt1, wr * 16 + g + 8 * i, share.chunk, piece);
         if (!good) {
-          if (t == 0 && !final) *part_ml = make_float2(0.0f, kNoPiece);
+          if (t == 0 && !final) *to.ml = make_float2(0.0f, kNoPiece);
           continue;
-        }
-        if constexpr (kPrefix<A>) if (final) {
-          float f_own, f_base;
-          if (!join_base(a, qrow[i], m[i], l[i], f_own, f_base)) continue;
-          // in the order of the stores below
-#pragma unroll
-          for (int d = 0; d < kDT; d += 2) {
-            float4 b;
-            if (FP8) {
-              b = *reinterpret_cast<const float4*>(part + 8 * d + 4 * t);
-            } else {
-              const float2 lo = *reinterpret_cast<const float2*>(part + 8 * d + 2 * t);
-              const float2 hi = *reinterpret_cast<const float2*>(part + 8 * d + 8 + 2 * t);
-              b = make_float4(lo.x, hi.x, lo.y, hi.y);
-            }
-            o[d][2 * i] = o[d][2 * i] * f_own + b.x * f_base, o[d + 1][2 * i] = o[d + 1][2 * i] * f_own + b.y * f_base;
-            o[d][2 * i + 1] = o[d][2 * i + 1] * f_own + b.z * f_base;
-            o[d + 1][2 * i + 1] = o[d + 1][2 * i + 1] * f_own + b.w * f_base;
-          }
         }
         const float f = final ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
         uint16_t* const dst = a.out + qrow[i] * D;
@@ -619,17 +598,25 @@ attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap
           }
         }
         if (t == 0) {
-          if (!final) *part_ml = make_float2(m[i], l[i]);
+          if (!final) *to.ml = make_float2(m[i], l[i]);
           else if (a.lse) a.lse[qrow[i]] = l[i] == 0.0f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
         }
       }
     }
-    if (tid == 0 && kt0 == 0 && kt1 < it.tiles)
+    if (!kPrefix<A> && tid == 0 && kt0 == 0 && kt1 < it.tiles)
       say_cut(a, blockIdx.x, &it, kt1, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
     if (C::kQShared || MT < 4) named_barrier(1, kComputeThreads);  // s_ml and qs are free again
     first = false;
     if (left <= 0 || !walk_next(a, it)) return;
   }
+}
+
+template <int D, int MT, bool FP8, class A>
+__global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
+attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
+  attn_mma_items<D, MT, FP8>(a, kmap, vmap);
+  end_launch(a);
 }
 
 // Eight rows and fewer (a decode step: one token, up to eight heads a group).  The products change
@@ -659,9 +646,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 template <int D, bool FP8, class A>
-__global__ void __launch_bounds__(kThreads, Cfg8<D, FP8>::kCtas)
-attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
-                 const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void attn_row8_items(const A& a, const CUtensorMap& kmap, const CUtensorMap& vmap) {
   using C = Cfg8<D, FP8>;
   constexpr int RB = C::kRowBytes, S = C::kStages, kDT = D / 16;
   extern __shared__ uint8_t raw[];
@@ -675,13 +660,12 @@ attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMa
   if (tid == 0) {
     init_bars(bars, S);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_launch(a);
   __syncthreads();  // the barriers are initialised
   Walk it;
   Share share;
   const bool busy = start_walk<kThreads>(a, blockIdx.x, it, share);
-  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
+  if (!kPrefix<A> && tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
   if (!busy) return;
   int left = share.left;
   if (warp == 4) {
@@ -743,14 +727,14 @@ attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMa
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 2 * t + i, tok = token_of(a.shape, r), pos = q.kv - q.n + tok;
       const bool in = r < rows;
-      jhi[i] = in ? (a.shape.causal ? min(q.kv, pos + 1) : q.kv) : 0;
+      jhi[i] = in ? (a.shape.causal && !q.all ? min(q.kv, pos + 1) : q.kv) : 0;
       jlo[i] = first_key(a.shape, pos);
       qrow[i] = in ? (long long)(q.row0 + tok) * a.Hq + it.h * a.shape.G + (r - tok * a.shape.G) : -1;
       coef[i] = __shfl_sync(~0u, row_coef, (2 * t + i) * 4);
     }
     const int last_row = min(r0 + 8, rows) - 1;
     const int all_lo = first_key(a.shape, q.kv - q.n + token_of(a.shape, last_row));
-    const int all_hi = a.shape.causal ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
+    const int all_hi = a.shape.causal && !q.all ? min(q.kv, q.kv - q.n + token_of(a.shape, r0) + 1) : q.kv;
 
     float o[kDT][4];
 #pragma unroll
@@ -915,28 +899,18 @@ attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMa
 
     if (warp == 0) {
       const bool good = !bars.failed;  // as in attn_mma_kernel
-      const bool whole = kt0 == 0 && kt1 == it.tiles, final = whole && to_out(a);
+      const bool whole = kt0 == 0 && kt1 == it.tiles, final = whole && !kPrefix<A>;
       const float vscale = FP8 && p.v_scale ? __ldg(p.v_scale + it.h) : 1.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (qrow[i] < 0) continue;
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * 8 + 2 * t + i;
-        float2* const part_ml = part_ml_of(a, whole, qrow[i], piece);
-        float* const part = part_o_of<D>(a, whole, qrow[i], piece);
+        const Part to = part_of<D>(a, it, whole, qrow[i], piece);
+        float* const part = to.o;
+        if (g == 0 && kt0 == 0) say_found(a, it, qrow[i], good, kt1, 2 * t + i, share.chunk, piece);
         if (!good) {
-          if (g == 0 && !final) *part_ml = make_float2(0.0f, kNoPiece);
+          if (g == 0 && !final) *to.ml = make_float2(0.0f, kNoPiece);
           continue;
-        }
-        if constexpr (kPrefix<A>) if (final) {
-          float f_own, f_base;
-          if (!join_base(a, qrow[i], m[i], l[i], f_own, f_base)) continue;
-#pragma unroll
-          for (int d = 0; d < kDT; ++d) {  // in the order of the stores below
-            const float2 b = FP8 ? *reinterpret_cast<const float2*>(part + 16 * d + 2 * g)
-                                 : make_float2(part[16 * d + g], part[16 * d + g + 8]);
-            o[d][i] = o[d][i] * f_own + b.x * f_base;
-            o[d][2 + i] = o[d][2 + i] * f_own + b.y * f_base;
-          }
         }
         const float f = final ? (l[i] > 0.0f ? vscale / l[i] : (l[i] == 0.0f ? 0.0f : l[i])) : 1.0f;
         uint16_t* const dst = a.out + qrow[i] * D;
@@ -955,12 +929,12 @@ attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMa
           }
         }
         if (g == 0) {
-          if (!final) *part_ml = make_float2(m[i], l[i]);
+          if (!final) *to.ml = make_float2(m[i], l[i]);
           else if (a.lse) a.lse[qrow[i]] = l[i] == 0.0f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
         }
       }
     }
-    if (tid == 0 && kt0 == 0 && kt1 < it.tiles)
+    if (!kPrefix<A> && tid == 0 && kt0 == 0 && kt1 < it.tiles)
       say_cut(a, blockIdx.x, &it, kt1, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
     named_barrier(1, kComputeThreads);  // s_ml is free again
     first = false;
@@ -968,152 +942,12 @@ attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMa
   }
 }
 
-// Items that the cuts went through: blocks (j, *) finish the item that CTA j began and others went
-// on with, a share of its rows each.  The attention's CTAs leave behind what there is to join: found
-// again from the batch, as it once was, it took 11 of 34 us for one row of 30,000 keys per head.
-// Bound by round trips to L2, so everything a row needs is asked for at once where its pieces are few
-// (1,200 tokens over 4,000 keys, most items cut once: 80 us with the attention, 86 when the weights came
-// first and then pieces by eights).  Four blocks an SM: most blocks have nothing to join, and with
-// fewer at a time the others wait for them (16 tokens over 32,765 keys: 34.5 us, 35.4 with three).
-template <int D, class A>
-struct Join {
-  static constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart);  // a lane's elements of a row
-  const A& a;
-  long long slot0, c0;  // pieces: slot0, and slot 2 (c0 + i) for i = 1..n
-  int n, R, r0, h, row_base, lane;
-  float vscale;
-
-  __device__ __forceinline__ long long place(int i, int row) const { return (i ? 2 * (c0 + i) : slot0) * R + row; }
-  __device__ __forceinline__ void load(int i, int row, float (&v)[kParts][kPart]) const {
-    const float* src = a.piece_o + place(i, row) * D + lane * kPart;
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) {
-      if (kPart == 4) *reinterpret_cast<float4*>(v[q]) = *reinterpret_cast<const float4*>(src + q * 128);
-      else *reinterpret_cast<float2*>(v[q]) = *reinterpret_cast<const float2*>(src);
-    }
-  }
-  // The joined row (`all`: of all its pieces) leaves.
-  __device__ __forceinline__ void store(int row, bool all, float m, float l, float (&acc)[kParts][kPart]) const {
-    const int G = a.shape.G, r = r0 + row, tok = token_of(a.shape, r);
-    const long long orow = (long long)(row_base + tok) * a.Hq + h * G + (r - tok * G);
-    if constexpr (kPrefix<A>) {
-      float* const base = a.base_o + orow * D + lane * kPart;
-      if (a.shared) {
-        if (lane == 0) a.base_ml[orow] = make_float2(m, all ? l : kNoPiece);
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-#pragma unroll
-          for (int d = 0; d < kPart; d += 2) *reinterpret_cast<float2*>(base + q * 128 + d) = make_float2(acc[q][d], acc[q][d + 1]);
-        return;
-      }
-      float f_own, f_base;
-      all &= join_base(a, orow, m, l, f_own, f_base);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q)
-#pragma unroll
-        for (int d = 0; d < kPart; d += 2) {
-          const float2 b = *reinterpret_cast<const float2*>(base + q * 128 + d);
-          acc[q][d] = acc[q][d] * f_own + b.x * f_base;
-          acc[q][d + 1] = acc[q][d + 1] * f_own + b.y * f_base;
-        }
-    }
-    if (!all) return;
-    const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) {
-      uint16_t* dst = a.out + orow * D + q * 128 + lane * kPart;
-      const uint32_t lo = pack2<false>(acc[q][0] * s, acc[q][1] * s);
-      if (kPart == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2<false>(acc[q][kPart - 2] * s, acc[q][kPart - 1] * s));
-      else *reinterpret_cast<uint32_t*>(dst) = lo;
-    }
-    if (lane == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
-  }
-  // ROWS rows of up to PIECES pieces, by one warp.
-  template <int ROWS, int PIECES>
-  __device__ __forceinline__ void few(int row, int end) const {
-    float2 ml[ROWS][PIECES];
-    float v[ROWS][PIECES][kParts][kPart];
-#pragma unroll
-    for (int e = 0; e < ROWS; ++e)
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {  // past the last: it again, with weight 0
-        ml[e][k] = a.piece_ml[place(min(k, n), min(row + e, end - 1))];
-        load(min(k, n), min(row + e, end - 1), v[e][k]);
-      }
-#pragma unroll
-    for (int e = 0; e < ROWS; ++e) {
-      float m = ml[e][0].x, l = 0.0f, acc[kParts][kPart] = {};
-      bool all = ml[e][0].y != kNoPiece;
-#pragma unroll
-      for (int k = 1; k < PIECES; ++k) m = fmaxf(m, ml[e][k].x), all &= ml[e][k].y != kNoPiece;
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        if (k > n) break;
-        const float f = m == -INFINITY ? 0.0f : ex2(ml[e][k].x - m);
-        l += f * ml[e][k].y;
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-#pragma unroll
-          for (int d = 0; d < kPart; ++d) acc[q][d] += f * v[e][k][q][d];
-      }
-      if (row + e < end) store(row + e, all, m, l, acc);
-    }
-  }
-  // One row of any number of pieces: the lanes hold the pieces' (maximum, sum), 32 at a time.
-  __device__ __forceinline__ void many(int row) const {
-    float m = -INFINITY;
-    for (int i = lane; i <= n; i += 32) m = fmaxf(m, a.piece_ml[place(i, row)].x);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    float l = 0.0f, acc[kParts][kPart] = {};
-    bool all = true;
-    for (int i0 = 0; i0 <= n; i0 += 32) {
-      float f = 0.0f;
-      if (i0 + lane <= n) {
-        const float2 ml = a.piece_ml[place(i0 + lane, row)];
-        all &= ml.y != kNoPiece;
-        f = m == -INFINITY ? 0.0f : ex2(ml.x - m);
-        l += f * ml.y;
-      }
-      const int k1 = min(32, n + 1 - i0);
-      constexpr int kBatch = 8 / kParts;  // pieces asked for together
-      for (int k = 0; k < k1; k += kBatch) {
-        float v[kBatch][kParts][kPart];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) load(min(i0 + k + e, n), row, v[e]);
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const float fk = __shfl_sync(~0u, f, k + e);
-#pragma unroll
-          for (int q = 0; q < kParts; ++q)
-#pragma unroll
-            for (int d = 0; d < kPart; ++d)
-              if (k + e < k1) acc[q][d] += fk * v[e][q][d];
-        }
-      }
-    }
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    store(row, __all_sync(~0u, all), m, l, acc);
-  }
-};
-template <int D, class A>
-__global__ void __launch_bounds__(kJoinThreads, 4) attn_combine_kernel(const __grid_constant__ A a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 lo = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[0];
-  const int n = lo.x;
-  if (n == 0) return;
-  const int4 hi = reinterpret_cast<const int4*>(a.cuts + blockIdx.x)[1];
-  const int rows = lo.z, warp = threadIdx.x >> 5;
-  const int ra = rows * blockIdx.y / gridDim.y, rb = rows * (blockIdx.y + 1) / gridDim.y;
-  const Join<D, A> j = {a, lo.y, (long long)blockIdx.x, n, 1 << a.shape.r_shift, lo.w, hi.y, hi.x, (int)(threadIdx.x & 31),
-                     a.p.v_scale ? __ldg(a.p.v_scale + hi.y) : 1.0f};
-  constexpr int kWide = D == 256 ? 4 : 8;
-  if (n < 2) {
-    for (int row = ra + 2 * warp; row < rb; row += kJoinThreads / 16) j.template few<2, 2>(row, rb);
-  } else if (n < kWide) {
-    for (int row = ra + warp; row < rb; row += kJoinThreads / 32) j.template few<1, kWide>(row, rb);
-  } else {
-    for (int row = ra + warp; row < rb; row += kJoinThreads / 32) j.many(row);
-  }
+template <int D, bool FP8, class A>
+__global__ void __launch_bounds__(kThreads, Cfg8<D, FP8>::kCtas)
+attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  attn_row8_items<D, FP8>(a, kmap, vmap);
+  end_launch(a);
 }
 
 // `kernel` with 1 << r_shift rows per item on a resident grid, and the combine step behind it.
@@ -1145,7 +979,8 @@ cudaError_t launch_ring(void (*kernel)(const A, const CUtensorMap, const CUtenso
   cudaLaunchAttribute attr;
   attention_config(&cfg, &attr, ctas, kThreads, C::kSmem, s);
   e = cudaLaunchKernelEx(&cfg, kernel, a, kmap, vmap);
-  return e != cudaSuccess ? e : launch_combine(a, D, s);
+  if constexpr (kPrefix<A>) return e;
+  else return e != cudaSuccess ? e : launch_combine(a, D, s);
 }
 template <int D, int MT, bool FP8, class A>
 cudaError_t launch_mma(const A& a, cudaStream_t s) {
@@ -1156,34 +991,6 @@ template <int D, bool FP8, class A>
 cudaError_t launch_row8(const A& a, cudaStream_t s) {
   static std::atomic<int> ready[kMaxDevices];
   return launch_ring<Cfg8<D, FP8>>(attn_row8_kernel<D, FP8, A>, ready, a, D, FP8, 3, s);
-}
-
-template <int D, bool FP8, class A>
-cudaError_t launch_rows(const A& a, cudaStream_t s) {
-  // Rows that share a request's keys, on average: the host knows the totals only.
-  const long long rows = ((long long)a.p.T * a.shape.G + a.p.B - 1) / a.p.B;
-  if (rows <= 8) return launch_row8<D, FP8>(a, s);
-  if (rows <= 16) return launch_mma<D, 1, FP8>(a, s);
-  if (rows <= 32) return launch_mma<D, 2, FP8>(a, s);
-  return launch_mma<D, 4, FP8>(a, s);
-}
-
-template <class A>
-cudaError_t launch_join(const A& a, int D, cudaStream_t s) {
-  if (a.ctas < 2) return cudaSuccess;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr;
-  attention_config(&cfg, &attr, a.ctas - 1, kJoinThreads, 0, s);
-  cfg.gridDim.y = a.shape.r_shift > 4 ? 1u << (a.shape.r_shift - 4) : 1;  // 16 rows of an item each
-  if (D == 64) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, A>, a);
-  if (D == 128) return cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, A>, a);
-  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<256, A>, a);
-}
-template <class A>
-cudaError_t launch_by_dim(const A& a, int D, bool fp8, cudaStream_t s) {
-  if (D == 64) return fp8 ? launch_rows<64, true>(a, s) : launch_rows<64, false>(a, s);
-  if (D == 128) return fp8 ? launch_rows<128, true>(a, s) : launch_rows<128, false>(a, s);
-  return fp8 ? launch_rows<256, true>(a, s) : launch_rows<256, false>(a, s);
 }
 
 }  // namespace

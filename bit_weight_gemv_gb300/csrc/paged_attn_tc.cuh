@@ -211,12 +211,11 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
     tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_launch(a);
   Walk it;
   Share share;
   const bool busy = start_walk<C::kThreads>(a, blockIdx.x, it, share);
-  if (tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
+  if (!kPrefix<A> && tid == 0) say_cut(a, blockIdx.x, nullptr, 0, 1, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -537,7 +536,7 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
         const int r = r_tile + row, tok = token_of(a.shape, r);
         const bool in = r < rows;
         const int pos = it.q.kv - it.q.n + tok;
-        const int jhi = in ? (a.shape.causal ? min(it.q.kv, pos + 1) : it.q.kv) : 0;
+        const int jhi = in ? (a.shape.causal && !it.q.all ? min(it.q.kv, pos + 1) : it.q.kv) : 0;
         const int jlo = first_key(a.shape, pos);
         const bool work = __any_sync(~0u, in);  // a warp without rows only keeps the pace
 
@@ -676,8 +675,8 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
         }
 
         // ---- the item's rows leave
-        const bool whole = kt0 == 0 && n == it.tiles, final = whole && to_out(a);
-        if (tid == 0 && kt0 == 0 && !whole)
+        const bool whole = kt0 == 0 && n == it.tiles, final = whole && !kPrefix<A>;
+        if (!kPrefix<A> && tid == 0 && kt0 == 0 && !whole)
           say_cut(a, blockIdx.x, &it, n, share.chunk, 2 * blockIdx.x + (first ? 0 : 1));
         const long long piece = (2LL * blockIdx.x + (first ? 0 : 1)) * kRows + (PAIR ? slot * 128 : 0) + row;
         if (PAIR) {
@@ -710,14 +709,7 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
           }
           const bool two = !PAIR && n > 1;
           const long long orow = (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G);
-          float* const part = part_o_of<D>(a, whole, orow, piece);
-          bool stored = in;
-          float f_base = 0.0f;
-          if constexpr (kPrefix<A>) if (in && final) {
-            float f_own;
-            stored = join_base(a, orow, m, l, f_own, f_base);
-            f0 *= f_own, f1 *= f_own;
-          }
+          const Part to = part_of<D>(a, it, whole, orow, piece);
           const float inv = final ? (l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l)) : 1.0f;
           constexpr int kCols = PAIR ? D : D / 2;
           const int c0 = PAIR ? 0 : slot * kCols;
@@ -734,31 +726,20 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
               if (!PAIR) v[i] = two ? f0 * v[i] + f1 * __uint_as_float(y[i]) : f0 * v[i];
               if (!kPrefix<A>) v[i] *= inv;
             }
-            if constexpr (kPrefix<A>) {
-              if (stored && final) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                  const float4 b = *reinterpret_cast<const float4*>(part + c0 + c + i);
-                  if (PAIR) v[i] *= f0, v[i + 1] *= f0, v[i + 2] *= f0, v[i + 3] *= f0;
-                  v[i] += f_base * b.x, v[i + 1] += f_base * b.y, v[i + 2] += f_base * b.z, v[i + 3] += f_base * b.w;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= inv;
-            }
-            if (stored && final) {
+            if (in && final) {
               uint32_t w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
               st_global_32(a.out + orow * D + c0 + c, w, a.wide);
-            } else if (stored) {
+            } else if (in) {
               const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-              st_global_32(part + c0 + c, w, a.wide);
-              st_global_32(part + c0 + c + 8, w + 8, a.wide);
+              st_global_32(to.o + c0 + c, w, a.wide);
+              st_global_32(to.o + c0 + c + 8, w + 8, a.wide);
             }
           }
-          if (stored && (PAIR || slot == 0)) {
-            if (!final) *part_ml_of(a, whole, orow, piece) = make_float2(m, l);
+          if (in && (PAIR || slot == 0)) {
+            if (kt0 == 0) say_found(a, it, orow, true, n, (PAIR ? slot * 128 : 0) + row, share.chunk, piece);
+            if (!final) *to.ml = make_float2(m, l);
             else if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
           }
         }
@@ -774,10 +755,10 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
       if (!ok) {  // neither piece of this row is to be joined
         for (int i = 0; i < 2; ++i)
           a.piece_ml[(2LL * blockIdx.x + i) * kRows + (PAIR ? slot * 128 : 0) + row] = make_float2(0.0f, kNoPiece);
-        if constexpr (kPrefix<A>) if (a.shared)  // nor a base of what is left of the share
+        if constexpr (kPrefix<A>)  // nor what is left of the share
           do {
             const int r = it.qt * kRows + (PAIR ? slot * 128 : 0) + row, tok = token_of(a.shape, r);
-            if (r < it.q.n * G) a.base_ml[(long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G)] = make_float2(0.0f, kNoPiece);
+            if (r < it.q.n * G) say_found(a, it, (long long)(it.q.row0 + tok) * a.Hq + it.h * G + (r - tok * G), false, 0, 0, 1, 0);
           } while (left > 0 && walk_next(a, it) && walk_take(it, left));
       }
     }
@@ -786,6 +767,7 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  end_launch(a);
 }
 
 template <int D, bool PAIR, bool FP8, class A>
@@ -818,7 +800,8 @@ cudaError_t launch_tc(A a, cudaStream_t s) {
   cudaLaunchAttribute attr = {};
   attention_config(&cfg, &attr, ctas, C::kThreads, C::kSmem, s);
   e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, PAIR, FP8, A>, a, kmap, vmap);
-  return e != cudaSuccess ? e : launch_combine(a, D, s);
+  if constexpr (kPrefix<A>) return e;
+  else return e != cudaSuccess ? e : launch_combine(a, D, s);
 }
 
 template <int D, bool PAIR, class A>

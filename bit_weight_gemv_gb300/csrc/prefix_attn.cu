@@ -2,16 +2,164 @@
 //
 // With the keys of a row cut into the shared ones and its own, (m, l, o) of each part (paged_attn_mma.cuh) join
 // as any two sets of keys do.  So the shared part is computed with all rows of a group as one request without
-// a mask, which reads its keys and values once for the group, and the rows wait in the workspace, 4 (D + 2) bytes
-// each; then the own part, whose way out joins them.  The same kernels and schedule as lowbit_paged_attention
-// do both, each chosen by the rows that share a "request's" keys in its part.
+// a mask, which reads its keys and values once for the group, the own part as ever, and a last step joins a row's
+// pieces out of both.  The kernels and their schedule are lowbit_paged_attention's.
+//
+// Where one kernel suits both parts (few rows in the shared part; or many in the own one) one launch takes them,
+// laid end to end in its schedule; else two, of which the second starts as the CTAs of the first leave.
 #include "paged_attn_mma.cuh"
 
 namespace lowbit {
+namespace {
 
-cudaError_t launch_attention_mma(const PrefixArgs& a, int D, bool fp8, cudaStream_t s) { return launch_by_dim(a, D, fp8, s); }
-cudaError_t launch_combine(const PrefixArgs& a, int D, cudaStream_t s) { return launch_join(a, D, s); }
+constexpr int kPrefixJoinWarps = 8;
 
+// Request b with its group as the header asks for them: inside the group's bounds and rows, and with what it
+// shares computed.  False, and recorded, if not.
+__device__ __forceinline__ bool request_of_group(const PrefixArgs& a, int b, Request* own) {
+  const int g = group_of(a, b), from = a.cu_groups[g], to = a.cu_groups[g + 1];
+  const Request group = load_group(a, g);
+  *own = load_own(a, b);
+  if (own->n == 0) return false;
+  const bool bounds = from >= 0 && to <= a.requests && b >= from && b < to;
+  if (!bounds || own->row0 < a.p.cu_q[from] || own->row0 + own->n > a.p.cu_q[to] || (own->skip && group.n == 0)) {
+    record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
+    return false;
+  }
+  return true;
+}
+
+// A warp joins a row's pieces: of the shared part, then of its own.  Bound by round trips (where they are, their
+// statistics, the pieces), of which the row's request and checks are done before the kernels ahead have
+// ended.
+template <int D>
+__global__ void __launch_bounds__(kPrefixJoinWarps * 32)
+prefix_join_kernel(const __grid_constant__ PrefixArgs a, const float* own_o, const float2* own_ml) {
+  constexpr int kPart = D >= 128 ? 4 : 2, kParts = D / (32 * kPart), kBatch = 8 / kParts;
+  const int lane = threadIdx.x & 31, h = blockIdx.y * kPrefixJoinWarps + (threadIdx.x >> 5), t = blockIdx.x;
+  if (h >= a.Hq) return;
+  // the last request that begins at row t or before it
+  int b = 0;
+#pragma unroll 1
+  for (int end = a.requests; end - b > 1;) {
+    const int mid = (b + end) / 2;
+    if (a.p.cu_q[mid] <= t) b = mid;
+    else end = mid;
+  }
+  Request own;
+  const bool fits = a.p.cu_q[b] <= t && t < a.p.cu_q[b + 1] && request_of_group(a, b, &own);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!fits) return;
+  const long long row = (long long)t * a.Hq + h;
+  int4 f0 = make_int4(kInBase, 0, 0, 0);
+  if (own.skip) f0 = a.found[row];
+  const int4 f1 = a.found[a.rows + row];
+  if (f0.x == kLost || f1.x == kLost) return;
+  const int n0 = own.skip ? max(f0.x, 0) + 1 : 0, n = n0 + max(f1.x, 0) + 1;
+  // where piece i is
+  auto locate = [&](int i, const float2*& ml, const float*& o) {
+    const bool second = i >= n0;
+    const int4 f = second ? f1 : f0;
+    const int k = second ? i - n0 : i;
+    if (f.x == kInBase) {
+      const long long place = row + (second ? a.rows : 0);
+      ml = a.base_ml + place, o = a.base_o + place * D;
+    } else {
+      long long place = k ? (long long)f.z + (long long)(k - 1) * f.w : f.y;
+      place = min(max(place, 0LL), (long long)kMaxPieceRows - 1);
+      ml = (second ? own_ml : a.piece_ml) + place, o = (second ? own_o : a.piece_o) + place * D;
+    }
+  };
+  float m = -INFINITY, l = 0.0f, acc[kParts][kPart] = {};
+  bool all = true;
+  for (int i0 = 0; i0 < n; i0 += 32) {  // the lanes hold the pieces' statistics, 32 at a time
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    const float2* at_ml;
+    const float* at_o = nullptr;
+    if (i0 + lane < n) {
+      locate(i0 + lane, at_ml, at_o);
+      ml = *at_ml;
+      all &= ml.y != kNoPiece;
+    }
+    float top = ml.x;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    top = fmaxf(top, m);
+    const float before = top == -INFINITY ? 0.0f : ex2(m - top), f = top == -INFINITY ? 0.0f : ex2(ml.x - top);
+    m = top;
+    float sum = f * ml.y;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    l = l * before + sum;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int d = 0; d < kPart; ++d) acc[q][d] *= before;
+    const int k1 = min(32, n - i0);
+    for (int k = 0; k < k1; k += kBatch) {  // asked for together
+      float v[kBatch][kParts][kPart];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float* src = reinterpret_cast<const float*>(
+                               __shfl_sync(~0u, (unsigned long long)reinterpret_cast<uintptr_t>(at_o), min(k + e, k1 - 1))) + lane * kPart;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          if (kPart == 4) *reinterpret_cast<float4*>(v[e][q]) = *reinterpret_cast<const float4*>(src + q * 128);
+          else *reinterpret_cast<float2*>(v[e][q]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const float fk = __shfl_sync(~0u, f, min(k + e, 31));
+        if (k + e >= k1) continue;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int d = 0; d < kPart; ++d) acc[q][d] += fk * v[e][q][d];
+      }
+    }
+  }
+  if (!__all_sync(~0u, all)) return;
+  const float vscale = a.p.v_scale ? __ldg(a.p.v_scale + h / a.shape.G) : 1.0f;
+  const float s = l > 0.0f ? vscale / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+  for (int q = 0; q < kParts; ++q) {
+    uint16_t* dst = a.out + row * D + q * 128 + lane * kPart;
+    const uint32_t lo = pack2<false>(acc[q][0] * s, acc[q][1] * s);
+    if (kPart == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, pack2<false>(acc[q][kPart - 2] * s, acc[q][kPart - 1] * s));
+    else *reinterpret_cast<uint32_t*>(dst) = lo;
+  }
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+}
+
+// Records what the join step would have recorded.
+__global__ void __launch_bounds__(256) prefix_check_kernel(const __grid_constant__ PrefixArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  Request own;
+  if (i < a.groups) load_group(a, i);
+  if (i < a.requests) request_of_group(a, i, &own);
+}
+
+// The kernels by rows an item.
+enum Kind { kRow8, kMma16, kMma32, kMma64, kTc128, kTc256 };
+Kind kind_of(const AttnArgs& a, int D, long long rows, long long pair) {
+  if (rows > (D == 64 ? 48 : 32) && attention_tc_fits(a, D)) return rows > pair ? kTc256 : kTc128;
+  return rows <= 8 ? kRow8 : (rows <= 16 ? kMma16 : (rows <= 32 ? kMma32 : kMma64));
+}
+template <int D, bool FP8>
+cudaError_t launch_ring_kind(const PrefixArgs& a, Kind kind, cudaStream_t s) {
+  if (kind == kRow8) return launch_row8<D, FP8>(a, s);
+  if (kind == kMma16) return launch_mma<D, 1, FP8>(a, s);
+  if (kind == kMma32) return launch_mma<D, 2, FP8>(a, s);
+  return launch_mma<D, 4, FP8>(a, s);
+}
+cudaError_t launch_kind(const PrefixArgs& a, int D, bool fp8, Kind kind, cudaStream_t s) {
+  if (kind >= kTc128) return launch_attention_tc(a, D, fp8, kind == kTc256, s);
+  if (D == 64) return fp8 ? launch_ring_kind<64, true>(a, kind, s) : launch_ring_kind<64, false>(a, kind, s);
+  if (D == 128) return fp8 ? launch_ring_kind<128, true>(a, kind, s) : launch_ring_kind<128, false>(a, kind, s);
+  return fp8 ? launch_ring_kind<256, true>(a, kind, s) : launch_ring_kind<256, false>(a, kind, s);
+}
+
+}  // namespace
 }  // namespace lowbit
 
 using namespace lowbit;
@@ -20,7 +168,7 @@ extern "C" {
 
 size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D) {
   if (lowbit_paged_attention_workspace_bytes(T, B, Hq, Hk, D) == 0) return 0;
-  return 2 * pieces_bytes(D) + (size_t)T * (size_t)Hq * (size_t)(D + 2) * sizeof(float);
+  return 2 * pieces_bytes(D) + (size_t)T * (size_t)Hq * 2 * ((size_t)(D + 2) * sizeof(float) + sizeof(int4));
 }
 
 lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int Hq, const lowbit_paged_batch* batch,
@@ -34,31 +182,70 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   if (groups < 1 || groups > kMaxBatch) return LOWBIT_ERR_SHAPE;
   if (((uintptr_t)cu_groups | (uintptr_t)prefix_lens) & 3) return LOWBIT_ERR_ALIGN;
   if (a.p.T == 0) return LOWBIT_OK;
-  const int D = cache->head_dim;
-  if (!workspace || ws_bytes < lowbit_prefix_attention_workspace_bytes(a.p.T, a.p.B, Hq, cache->heads, D))
+  const int D = cache->head_dim, B = a.p.B;
+  if (!workspace || ws_bytes < lowbit_prefix_attention_workspace_bytes(a.p.T, B, Hq, cache->heads, D))
     return LOWBIT_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 15) return LOWBIT_ERR_ALIGN;
   a.p.err = device_error_word();
   if (!a.p.err) return LOWBIT_ERR_CUDA;
   a.wide = (((uintptr_t)out | (uintptr_t)workspace) & 31) == 0;
   a.groups = groups;
-  a.requests = a.p.B;
+  a.requests = B;
   a.cu_groups = cu_groups;
   a.prefix_lens = prefix_lens;
+  a.rows = (long long)a.p.T * Hq;
   a.base_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 2 * pieces_bytes(D));
-  a.base_ml = reinterpret_cast<float2*>(a.base_o + (size_t)a.p.T * (size_t)Hq * (size_t)D);
+  a.found = reinterpret_cast<int4*>(a.base_o + 2 * (size_t)a.rows * (size_t)D);
+  a.base_ml = reinterpret_cast<float2*>(a.found + 2 * a.rows);
   const bool fp8 = cache->dtype == LOWBIT_CACHE_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  use_pieces(&a, workspace, D);
 
-  PrefixArgs shared = a;
-  shared.shared = true;
-  shared.p.B = groups;
-  shared.shape.causal = 0;
-  use_pieces(&shared, workspace, D);
-  cudaError_t e = launch_attention(shared, D, fp8, s);
+  // By the rows that share keys, on average, in either part (the host knows the totals only, not the lengths).
+  // From about 100 rows a request on, its own tiles are full and its keys come out of L2 for the requests that
+  // follow: the plain call is as fast, and has no second part to join.  us here / plain, heads of 128, bf16:
+  // 6 requests behind 12,345 keys, 128 rows each 65 / 52, 256 rows 97 / 89, 1,024 rows 305 / 303; 24 behind
+  // 3,000, 256 rows 151 / 97; with 64 rows, 48 behind 16,000 215 / 377, 24 behind 3,000 53 / 53, 8 behind 8,000
+  // 46 / 44; with four, 64 behind 16,384 69 / 279, 16 behind 4,000 20 / 25, 8 16 / 16, 64 behind 500 46 / 34.
+  // On the warp-level MMA, whose items have 64 rows at most, from 50 on (heads of 256, 16 requests behind 6,000
+  // keys, 64 rows each 89 / 82, 32 rows 54 / 55).
+  const long long all = (long long)a.p.T * a.shape.G, shared_rows = (all + groups - 1) / groups, own_rows = (all + B - 1) / B;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  cudaError_t e;
+  if (own_rows > (attention_tc_fits(a, D) ? 96 : 48)) {
+    attention_config(&cfg, &attr, (std::max(B, groups) + 255) / 256, 256, 0, s);
+    e = cudaLaunchKernelEx(&cfg, prefix_check_kernel, a);
+    if (e == cudaSuccess) e = launch_attention(a, D, fp8, s);
+    return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+  }
+  // 256 rows an item in the shared part where there are many in all: 768 rows a group of 3,072 behind 16,000 keys
+  // 215 us, 279 with 128; but 1,536 rows behind 3,000 keys 61 and 53, 512 behind 4,000 63 and 58.
+  const Kind shared_kind = kind_of(a, D, shared_rows, all > 2000 ? 500 : 1 << 30), own_kind = kind_of(a, D, own_rows, 1024);
+  // One launch where the shared part's kernel suits the own part: its rows fill an item half or more, or items are
+  // few.  us in one / in two launches: 32 requests of 32 rows behind 10,000 keys 74 / 88 (e4m3 85 / 93), 16 of 4 behind
+  // 4,000 20 / 22, 16 of 16 rows behind 8,000 30 / 33; 64 of 4 behind 500 52 / 46 (e4m3 56 / 36), behind 16,384 61 / 69
+  // (77 / 61), 128 of 4 behind 4,000 61 / 58 (70 / 48).
+  const bool together = shared_kind == own_kind || shared_kind <= kMma64 ||
+                        (shared_kind == kTc128 && (own_rows > 16 || (long long)B * cache->heads <= 152));
+  PrefixArgs part = a;
+  part.p.B = together ? groups + B : groups;
+  e = launch_kind(part, D, fp8, shared_kind, s);
+  if (e == cudaSuccess && !together) {
+    part.p.B = B;
+    part.first = groups;
+    part.behind = 1;
+    use_pieces(&part, static_cast<uint8_t*>(workspace) + pieces_bytes(D), D);
+    e = launch_kind(part, D, fp8, own_kind, s);
+  }
   if (e != cudaSuccess) return LOWBIT_ERR_CUDA;
-  use_pieces(&a, static_cast<uint8_t*>(workspace) + pieces_bytes(D), D);
-  e = launch_attention(a, D, fp8, s);
+  attention_config(&cfg, &attr, a.p.T, kPrefixJoinWarps * 32, 0, s);
+  cfg.gridDim.y = (unsigned)((Hq + kPrefixJoinWarps - 1) / kPrefixJoinWarps);
+  const float* own_o = part.piece_o;
+  const float2* own_ml = part.piece_ml;
+  e = D == 64 ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<64>, a, own_o, own_ml)
+    : D == 128 ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<128>, a, own_o, own_ml)
+               : cudaLaunchKernelEx(&cfg, prefix_join_kernel<256>, a, own_o, own_ml);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 

@@ -437,7 +437,7 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
                                      size_t ws_bytes, void* stream);
 
 /* Bytes of lowbit_prefix_attention's workspace for up to T rows and B requests of Hq query and Hk
- * key/value heads of D (0 for invalid shapes): twice lowbit_paged_attention's, and 4 (D + 2) for each row
+ * key/value heads of D (0 for invalid shapes): twice lowbit_paged_attention's, and 8 D + 48 for each row
  * and query head. */
 size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D);
 
@@ -454,8 +454,8 @@ size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int
  *                 kv_lens[b] - new tokens >= the length of the whole pages.
  * kv_lens and block_table describe the whole requests, as for lowbit_kv_append and lowbit_paged_attention,
  * whose result over the same arguments is this one's but for rounding.  A group or request that the
- * arrays describe inconsistently counts as one without tokens and is recorded in the device error
- * word; its rows are not written.  Pages are compared by nobody: rows of different pages under the same
+ * arrays describe inconsistently is recorded in the device error word; rows of its are not written, or (where a
+ * group's arrays are at fault) attend to the request's own block table alone.  Pages are compared by nobody: rows of different pages under the same
  * prefix give each request the first one's.
  *   workspace : lowbit_prefix_attention_workspace_bytes() bytes, 16-byte aligned, any contents; calls that
  *   may run at the same time need one each.
