@@ -108,18 +108,24 @@ __device__ __forceinline__ void turn8(float (&x)[8], float (&y)[8], const float 
   }
 }
 // A thread's 16 elements of head h into the slot at byte `slot` of the keys or values.
-template <bool FP8>
+// ONCE: to be read once at most before the next 100 MB of them (a hint to L2).
+template <bool ONCE, class V>
+__device__ __forceinline__ void store(uint8_t* at, V v) {
+  if (ONCE) __stcs(reinterpret_cast<V*>(at), v);
+  else *reinterpret_cast<V*>(at) = v;
+}
+template <bool FP8, bool ONCE = false>
 __device__ __forceinline__ void store_cache(const PagedArgs& p, bool key, long long slot, int h, int ia, int ib,
                                             const float (&x)[8], const float (&y)[8]) {
   uint8_t* dst = (key ? p.k : p.v) + slot + (long long)h * p.head_stride;
   if (FP8) {
     const float* sc = key ? p.k_scale : p.v_scale;
     const float scale = sc ? __ldg(sc + h) : 1.0f;
-    *reinterpret_cast<uint2*>(dst + ia) = pack8_e4m3(x, scale);
-    *reinterpret_cast<uint2*>(dst + ib) = pack8_e4m3(y, scale);
+    store<ONCE>(dst + ia, pack8_e4m3(x, scale));
+    store<ONCE>(dst + ib, pack8_e4m3(y, scale));
   } else {
-    *reinterpret_cast<uint4*>(dst + 2 * ia) = pack8(x);
-    *reinterpret_cast<uint4*>(dst + 2 * ib) = pack8(y);
+    store<ONCE>(dst + 2 * ia, pack8(x));
+    store<ONCE>(dst + 2 * ib, pack8(y));
   }
 }
 
@@ -182,17 +188,25 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
 //   y = x * r * w,  r = 1 / sqrt(sum x^2 / D + eps),
 // everything in fp32 from the bf16 elements to the one rounding of what is stored.
 //
-// WARPS warps take a token, or one does (WARPS = 1): 32 lanes hold 512 elements, D / 16 lanes a head, so that
+// WARPS warps take a token: 32 lanes hold 512 elements, D / 16 lanes a head, so that
 // a head's sum of squares is a few exchanges between neighbouring lanes, the lane's part of the angles stays in
 // registers over the token's heads, and no warp waits for another.  The first heads are asked for before the
 // token's place is known.
+//
+// 16,396 tokens of 32 + 8 + 8 heads of 128, bf16: 75.6 us, 411 MB, 5.4 TB/s of 6.8 copied: HBM, reads and writes of
+// short runs in turn.  One step at a time 88 us, four 92 (more registers, fewer warps), blocks of 256 threads 77.9,
+// without the hints to L2 76.8, eight warps a token 128.  512 tokens into an e4m3 cache 4.5 us, one 4.0.
+template <int WARPS>
+constexpr int kNormThreads = WARPS < 8 ? 128 : 256;
 template <int D, bool FP8, bool INTER, int WARPS>
-__global__ void __launch_bounds__(256, 3) kv_append_norm_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kNormThreads<WARPS>, WARPS < 8 ? 6 : 3)
+kv_append_norm_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kPer = D / 16, kHeads = 32 / kPer;  // lanes per head, heads per step of a warp
-  constexpr int kBatch = WARPS == 1 ? 2 : 1;        // steps asked for together
+  constexpr bool kLong = WARPS == 1;
+  constexpr int kBatch = WARPS <= 2 ? 2 : 1;            // steps asked for together
   const PagedArgs& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (8 / WARPS) + warp / WARPS, part = warp % WARPS;
+  const int t = blockIdx.x * (kNormThreads<WARPS> / 32 / WARPS) + warp / WARPS, part = warp % WARPS;
   if (t >= p.T) return;
   const int j = lane % kPer, nq = a.q ? a.Hq : 0;
   const int q_steps = (nq + kHeads - 1) / kHeads, kv_steps = (p.Hk + kHeads - 1) / kHeads;
@@ -223,8 +237,8 @@ __global__ void __launch_bounds__(256, 3) kv_append_norm_kernel(const __grid_con
       const uint16_t* src = (w.kind == 0 ? a.q + (long long)t * a.q_stride
                            : w.kind == 1 ? a.k + (long long)t * a.k_stride
                                          : a.v + (long long)t * a.v_stride) + (long long)w.h * D;
-      va[e] = *reinterpret_cast<const uint4*>(src + ia);
-      vb[e] = *reinterpret_cast<const uint4*>(src + ib);
+      va[e] = kLong ? __ldcs(reinterpret_cast<const uint4*>(src + ia)) : *reinterpret_cast<const uint4*>(src + ia);
+      vb[e] = kLong ? __ldcs(reinterpret_cast<const uint4*>(src + ib)) : *reinterpret_cast<const uint4*>(src + ib);
     }
   };
   load(part);
@@ -268,11 +282,11 @@ __global__ void __launch_bounds__(256, 3) kv_append_norm_kernel(const __grid_con
       if (turned && w.kind != 2) turn8<INTER>(x, y, c, sn);
       if (!w.in) continue;
       if (w.kind == 0) {
-        uint16_t* dst = a.q_out + ((long long)t * a.Hq + w.h) * D;
-        *reinterpret_cast<uint4*>(dst + ia) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + ib) = pack8(y);
+        uint8_t* dst = reinterpret_cast<uint8_t*>(a.q_out + ((long long)t * a.Hq + w.h) * D);
+        store<kLong>(dst + 2 * ia, pack8(x));
+        store<kLong>(dst + 2 * ib, pack8(y));
       } else {
-        store_cache<FP8>(p, w.kind == 1, slot, w.h, ia, ib, x, y);
+        store_cache<FP8, kLong>(p, w.kind == 1, slot, w.h, ia, ib, x, y);
       }
     }
   }
@@ -310,8 +324,9 @@ cudaError_t launch_tokens(const AppendArgs& a, bool fp8, bool inter, cudaStream_
 template <int D, int WARPS>
 cudaError_t launch_norm(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.p.T + 8 / WARPS - 1) / (8 / WARPS)));
-  cfg.blockDim = dim3(256);
+  constexpr int kTokens = kNormThreads<WARPS> / 32 / WARPS;
+  cfg.gridDim = dim3((unsigned)((a.p.T + kTokens - 1) / kTokens));
+  cfg.blockDim = dim3(kNormThreads<WARPS>);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -326,7 +341,14 @@ cudaError_t launch_norm(const AppendArgs& a, bool fp8, bool inter, cudaStream_t 
 }
 template <int D>
 cudaError_t launch_norm_warps(const AppendArgs& a, bool fp8, bool inter, cudaStream_t s) {
-  return a.p.T > 2000 ? launch_norm<D, 1>(a, fp8, inter, s) : launch_norm<D, 8>(a, fp8, inter, s);
+  // As many warps a token as fit on the GPU at a time, 24 an SM.  us with 8 / 4 / 2 / 1 warps, 32 + 8 + 8 heads of
+  // 128, bf16: 304 tokens 4.0 / 4.2 / 5.4 / 8.1, 608 6.9 / 5.1 / 6.1 / 8.2, 1,216 9.7 / 8.3 / 7.4 / 9.5, 1,824 12.8 / 9.6 /
+  // 9.4 / 11.2, 3,648 27 / 20 / 19 / 17, 7,296 60 / 45 / 40 / 36.
+  const int T = a.p.T;
+  return T <= 3 * 152 ? launch_norm<D, 8>(a, fp8, inter, s)
+       : T <= 6 * 152 ? launch_norm<D, 4>(a, fp8, inter, s)
+       : T <= 12 * 152 ? launch_norm<D, 2>(a, fp8, inter, s)
+                       : launch_norm<D, 1>(a, fp8, inter, s);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

@@ -123,7 +123,9 @@ class Case:
     ([5, 6], [5, 70], 6, 3, 256, 1, 256, "token"),
     ([9], [33], 5, 1, 256, 8, 16, "head"),
     ([7], [7], 3, 3, 64, 1024, 0, "token"),
-    ([2001, 1], [2001, 9], 3, 1, 64, 64, 32, "token"),       # one warp a token
+    ([456, 1], [501, 9], 5, 1, 64, 64, 32, "token"),         # four warps a token, two, one
+    ([911, 3], [1000, 3], 5, 3, 128, 64, 96, "head"),
+    ([2001, 1], [2001, 9], 3, 1, 64, 64, 32, "token"),
     ([3, 2500], [77, 2600], 5, 2, 128, 16, 128, "head"),
     ([1030, 1031], [1030, 1100], 2, 1, 256, 32, 64, "head")])
 def test_parity(lb, new, kv, Hq, Hk, D, page, rot, order, inter, fp8):
