@@ -558,6 +558,17 @@ __device__ __forceinline__ void sample_row(const A& a) {
       for (int j = 1; j < 4; ++j) max_bf16x2(top2[0], top2[j]);
       top = fmaxf(top, fmaxf(__uint_as_float(top2[0] << 16), __uint_as_float(top2[0] & 0xFFFF0000u)));
     }
+    if (!BF16 && a.aligned) {  // eight loads of a lane under way
+      const int whole = min(seg_to, z_of.end);
+#pragma unroll 1
+      for (; from + 1024 <= whole; from += 1024) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __ldg(reinterpret_cast<const float4*>(z_of.at + 4 * (from + 128 * j + 4 * lane)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, v[j].x), v[j].y), fmaxf(v[j].z, v[j].w));
+      }
+    }
     z_of.template each4<false>(from, seg_to, [&](int, float (&z)[4]) {
       top = fmaxf(fmaxf(fmaxf(top, z[0]), z[1]), fmaxf(z[2], z[3]));  // not NaN, which loses against any number
       return false;
@@ -848,25 +859,36 @@ __device__ __forceinline__ void sample_row(const A& a) {
     return n;
   };
 
-  // Four tokens' masses, those with logits >= low, into the histogram; the additions to the low words
-  // are all under way before the first one's carry is looked at (128 rows with top-p 0.9 that keep 90,000
-  // tokens each: 226 us, 236 one after another).
-  auto add_masses = [&](const float (&z)[4], float low) {
-    if (!(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low)) return;
-    int bin[4];
-    uint32_t lo[4], up[4], old[4];
+  // The masses of the tokens with logits >= low into the histogram.  These are a fifth of the row where top-p
+  // keeps many, and each costs some forty instructions, so a warp lines them up first, 32 at a time (512 rows
+  // with top-p 0.95 at T = 1: 443 us, 520 with every token in its own lane's turn).
+  auto mass_histogram = [&](float low) {
+    float* const line = reinterpret_cast<float*>(s.all_mass) + warp * 64;  // a ring; not in use otherwise
+    uint32_t tail = 0, head = 0;
+    auto add = [&](float z) {
+      z = clean(z);
+      const int bin = step_of(z, origin, steps);
+      if (bin < kBins - 1) add_mass(s, bin, mass_of(weight_of(z, top, rate)));
+    };
+    z_of.template each4<false>(seg_from, seg_to, [&](int, float (&z)[4]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      bin[e] = step_of(z[e], origin, steps);
-      const u64 mass = z[e] >= low && bin[e] < kBins - 1 ? mass_of(weight_of(z[e], top, rate)) : 0;
-      lo[e] = (uint32_t)mass, up[e] = (uint32_t)(mass >> 32), old[e] = 0;
-      if (lo[e]) old[e] = atomicAdd(&s.lo[bin[e]], lo[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (lo[e] && old[e] > 0xFFFFFFFFu - lo[e]) ++up[e];
-      if (up[e]) atomicAdd(&s.hi[bin[e]], up[e]);
-    }
+      for (int e = 0; e < 4; ++e) {
+        const bool in = z[e] >= low;
+        const uint32_t all = __ballot_sync(~0u, in);
+        if (in) line[(tail + __popc(all & ((1u << lane) - 1))) & 63] = z[e];
+        tail += __popc(all);
+        if (tail - head >= 32) {
+          __syncwarp();
+          const float x = line[(head + lane) & 63];
+          head += 32;
+          __syncwarp();
+          add(x);
+        }
+      }
+      return false;
+    });
+    __syncwarp();
+    if (lane < tail - head) add(line[(head + lane) & 63]);
   };
 
   // In the first CTA: of its n candidates only those down to the step in which their mass reaches
@@ -949,11 +971,13 @@ __device__ __forceinline__ void sample_row(const A& a) {
     // hold all that top-k or top-p leaves, they finish the row, and no histogram of it is taken (one
     // row of 248,320 with top-k 20: 14.9 us, 17.5 by the histogram; with top-p 0.8: 19.8 and 25.7).  For
     // top-p the bound is that of 512 lanes (16 rows with top-p 0.8: 29 us, 46 with 256 and 30 with 1,024;
-    // 192 rows of mixed settings 145, 147 and 152).
+    // 192 rows of mixed settings 145, 147 and 152).  A larger k, up to three quarters of the lanes, has a bound of
+    // them too, below which its histogram need not look.
     const uint32_t reach = min(C * kThreads / 2, kCap / 2);
     u64 limit = 0;
     bool have_whole = false, beyond = false;
-    if (!by_count || k <= reach) {
+    float low = -INFINITY;  // logits below it are not looked at
+    if (!by_count || k <= C * kThreads * 3 / 4) {
       const int own = step_of(lane_max, origin, steps);
       if (own < kBins - 1) atomicAdd(&s.count[own], 1u);
       merge_histograms(s, C, rank, false);
@@ -962,7 +986,10 @@ __device__ __forceinline__ void sample_row(const A& a) {
       uint32_t n = kCap + 1;
       bool all = true;
       if (by_count) {
-        if (s.bin < kBins) n = gather(std::false_type(), 0, bin, -INFINITY);
+        if (s.bin < kBins) {
+          low = origin - (float)(bin + 2) / steps;
+          if (k <= reach) n = gather(std::false_type(), 0, bin, -INFINITY);
+        }
       } else {
         n = gather(std::true_type(), 0, bin, -INFINITY);
         have_whole = true;
@@ -977,7 +1004,6 @@ __device__ __forceinline__ void sample_row(const A& a) {
       clear_histogram(s);
       __syncthreads();
     }
-    float low = -INFINITY;  // logits below it are not looked at
     if (have_whole) {
       // Tokens of weights up to (1 - p) S / V sum to (1 - p) S at most.  Less a thousandth for expf and
       // logf, half a unit of 2^-40 for each mass's rounding, and a few ulps of the logits.
@@ -996,18 +1022,20 @@ __device__ __forceinline__ void sample_row(const A& a) {
     }
 
     // ---- the step in which the prefix ends
-    z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
-      if (by_count) {
+    if (by_count) {
+      z_of.template each4<false>(seg_from, seg_to, [&](int, float (&z)[4]) {
+        if (!(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low)) return false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int bin = step_of(z[e], origin, steps);
+          if (!(z[e] >= low)) continue;
+          const int bin = step_of(clean(z[e]), origin, steps);
           if (bin < kBins - 1) atomicAdd(&s.count[bin], 1u);  // no mass past the last step: a cut there cuts nothing
         }
-      } else {
-        add_masses(z, low);
-      }
-      return false;
-    });
+        return false;
+      });
+    } else {
+      mass_histogram(low);
+    }
     merge_histograms(s, C, rank, !by_count);
     find_bin(s, !by_count, k, limit);
     int bin = s.bin;
@@ -1030,10 +1058,7 @@ __device__ __forceinline__ void sample_row(const A& a) {
           limit = top_p_limit(p, total);
           clear_histogram(s);
           __syncthreads();
-          z_of.each4(seg_from, seg_to, [&](int, float (&z)[4]) {
-            add_masses(z, -INFINITY);
-            return false;
-          });
+          mass_histogram(low);
           merge_histograms(s, C, rank, true);
           find_bin(s, true, 0, limit);
           bin = s.bin, count_before = s.count_before, mass_before = s.mass_before;

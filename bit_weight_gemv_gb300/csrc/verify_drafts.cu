@@ -103,10 +103,33 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
   const int index0 = rank * kDrawWarps * a.per_warp;
   cluster_arrive();  // this CTA runs: the others may write its shared memory
   if (tid == 0) s.first = INT32_MAX;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = a.cu_drafts[b], c1 = a.cu_drafts[b + 1];
+  const bool fits = request_fits(b, c0, c1, a.N, a.M);
+  const int n = fits ? c1 - c0 : 0;
+  const uint8_t* const rows = static_cast<const uint8_t*>(a.logits);
+  const uint8_t* const draft_rows = static_cast<const uint8_t*>(a.draft_logits);
+  // What a draft is judged by, beside the rows' states: every CTA finds out for itself, and before the kernels
+  // that the states come from have ended (they have waited for all that came before them).
+  struct Judged {
+    int d, col;
+    float z, y, u;
+  };
+  auto look = [&](int i) {
+    const int r = c0 + i;
+    Judged g = {a.drafts[r], -1, -INFINITY, -INFINITY, a.u[r]};
+    if (g.d < 0 || g.d >= a.V) return g;
+    g.z = logit_at(rows + (long long)(r + b) * a.row_stride * kSize, BF16, g.d);
+    if (!draft_rows) return g;
+    g.col = a.draft_index ? a.draft_index[g.d] : g.d;
+    if (g.col >= a.Vd) g.col = -1;
+    if (g.col >= 0) g.y = logit_at(draft_rows + (long long)r * a.draft_stride * kDraftSize, DRAFT_BF16, g.col);
+    return g;
+  };
+  Judged mine = {};
+  if (tid < n) mine = look(tid);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
-  if (!request_fits(b, c0, c1, a.N, a.M)) {
+  if (!fits) {
     if (rank == 0 && tid == 0) {
       record_error(a.err, LOWBIT_ERR_INVALID_ARG);
       a.n_accept[b] = 0;
@@ -114,31 +137,19 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     cluster_wait();
     return;
   }
-  const int n = c1 - c0;
-  const uint8_t* const rows = static_cast<const uint8_t*>(a.logits);
-  const uint8_t* const draft_rows = static_cast<const uint8_t*>(a.draft_logits);
 
-  // ---- which drafts are accepted: every CTA finds out for itself
+  // ---- which drafts are accepted
   for (int i = tid; i < n; i += kDrawThreads) {
-    const int r = c0 + i, d = a.drafts[r];
-    const bool inside = d >= 0 && d < a.V;
-    double share = 0.0, given = 1.0;
-    if (inside) {
-      const RowState p = a.target[r + b];
-      const float z = logit_at(rows + (long long)(r + b) * a.row_stride * kSize, BF16, d);
-      share = p.total ? (double)mass_of(Kept(p).weight(z, d)) / (double)p.total : 0.0;
+    const Judged g = i == tid ? mine : look(i);
+    const int r = c0 + i;
+    const RowState p = a.target[r + b];
+    double share = 0.0, given = draft_rows ? 0.0 : 1.0;
+    if (g.d >= 0 && g.d < a.V && p.total) share = (double)mass_of(Kept(p).weight(g.z, g.d)) / (double)p.total;
+    if (g.col >= 0) {
+      const RowState q = a.draft[r];
+      if (q.total) given = (double)mass_of(Kept(q).weight(g.y, g.col)) / (double)q.total;
     }
-    if (draft_rows) {
-      given = 0.0;
-      const int col = inside ? (a.draft_index ? a.draft_index[d] : d) : -1;
-      if (col >= 0 && col < a.Vd) {
-        const RowState q = a.draft[r];
-        const float z = logit_at(draft_rows + (long long)r * a.draft_stride * kDraftSize, DRAFT_BF16, col);
-        if (q.total) given = (double)mass_of(Kept(q).weight(z, col)) / (double)q.total;
-      }
-    }
-    float u = a.u[r];
-    u = u >= 0.0f ? fminf(u, 1.0f) : 0.0f;
+    const float u = g.u >= 0.0f ? fminf(g.u, 1.0f) : 0.0f;
     if (!((double)u * given < share)) atomicMin(&s.first, i);
     if (rank == 0 && a.accept) a.accept[r] = given > 0.0 ? (float)fmin(share / given, 1.0) : (share > 0.0 ? 1.0f : 0.0f);
   }
