@@ -65,7 +65,6 @@ struct PrefixArgs : AttnArgs {
   float2* base_ml;  // [2][row]
   int4* found;      // [2][row]: {kInBase or kLost}, or {more, first, next, apart}: places of the first piece and of
                     // the `more` that follow it, the second at `next` and the others `apart` behind one another
-  int behind;       // launched behind another part, which it does not wait for before its end
 };
 constexpr int kInBase = -1, kLost = -2;
 template <class A>
@@ -212,8 +211,8 @@ __device__ __forceinline__ int start_walk_short(const A& a, int cta, Walk& w, Sh
   w.q.row0 = __shfl_sync(~0u, q.row0, src);
   w.q.n = __shfl_sync(~0u, q.n, src);
   w.q.kv = __shfl_sync(~0u, q.kv, src);
-  w.q.skip = __shfl_sync(~0u, q.skip, src);
-  w.q.all = __shfl_sync(~0u, q.all, src);
+  w.q.skip = kPrefix<A> ? __shfl_sync(~0u, q.skip, src) : 0;  // the constant leaves no trace in the plain kernels
+  w.q.all = kPrefix<A> ? __shfl_sync(~0u, q.all, src) : 0;
   w.span.lo = __shfl_sync(~0u, none ? 0 : lo, src);
   w.span.hi = __shfl_sync(~0u, none ? 0 : q.kv, src);
   w.h = (int)(off / each);
@@ -347,22 +346,6 @@ __device__ __forceinline__ bool walk_next(const A& a, Walk& w) {
   }
   walk_item(a, w, 0);
   return true;
-}
-
-// The first and the last step of an attention kernel.  A part of lowbit_prefix_attention that is launched behind another
-// one starts as soon as all of the other's CTAs run, which have waited for everything before; it waits for them at
-// its own end, so that the step behind it, which waits for it alone, finds both done.
-__device__ __forceinline__ void begin_launch(const AttnArgs&) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void end_launch(const AttnArgs&) {}
-__device__ __forceinline__ void begin_launch(const PrefixArgs& a) {
-  if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void end_launch(const PrefixArgs& a) {
-  if (a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Where a row's (reference, sum) and output go that do not go to out: to its piece, or to its base.

@@ -220,7 +220,9 @@ __device__ __forceinline__ void copy_tiles(const A& a, const CUtensorMap& kmap, 
 }
 
 template <int D, int MT, bool FP8, class A>
-__device__ __forceinline__ void attn_mma_items(const A& a, const CUtensorMap& kmap, const CUtensorMap& vmap) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
+attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, MT, FP8>;
   constexpr int RB = C::kRowBytes, S = C::kStages;
   constexpr int kNT = 2 * MT;       // 8-key tiles per warp
@@ -236,7 +238,8 @@ __device__ __forceinline__ void attn_mma_items(const A& a, const CUtensorMap& km
   if (tid == 0) {
     init_bars(bars, S);
   }
-  begin_launch(a);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();  // the barriers are initialised
   Walk it;
   Share share;
@@ -611,14 +614,6 @@ __device__ __forceinline__ void attn_mma_items(const A& a, const CUtensorMap& km
   }
 }
 
-template <int D, int MT, bool FP8, class A>
-__global__ void __launch_bounds__(kThreads, Cfg<D, MT, FP8>::kCtas)
-attn_mma_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap) {
-  attn_mma_items<D, MT, FP8>(a, kmap, vmap);
-  end_launch(a);
-}
-
 // Eight rows and fewer (a decode step: one token, up to eight heads a group).  The products change
 // sides, so that the keys, not the rows, fill the MMA's 16: S^T = K Q^T and O^T = V^T P^T, half the MMAs and half
 // the exponentials of the 16-row kernel.  A lane holds two keys' scores of rows 2t and 2t + 1; P^T
@@ -646,7 +641,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 template <int D, bool FP8, class A>
-__device__ __forceinline__ void attn_row8_items(const A& a, const CUtensorMap& kmap, const CUtensorMap& vmap) {
+__global__ void __launch_bounds__(kThreads, Cfg8<D, FP8>::kCtas)
+attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg8<D, FP8>;
   constexpr int RB = C::kRowBytes, S = C::kStages, kDT = D / 16;
   extern __shared__ uint8_t raw[];
@@ -660,7 +657,8 @@ __device__ __forceinline__ void attn_row8_items(const A& a, const CUtensorMap& k
   if (tid == 0) {
     init_bars(bars, S);
   }
-  begin_launch(a);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();  // the barriers are initialised
   Walk it;
   Share share;
@@ -940,14 +938,6 @@ __device__ __forceinline__ void attn_row8_items(const A& a, const CUtensorMap& k
     first = false;
     if (left <= 0 || !walk_next(a, it)) return;
   }
-}
-
-template <int D, bool FP8, class A>
-__global__ void __launch_bounds__(kThreads, Cfg8<D, FP8>::kCtas)
-attn_row8_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap kmap,
-                 const __grid_constant__ CUtensorMap vmap) {
-  attn_row8_items<D, FP8>(a, kmap, vmap);
-  end_launch(a);
 }
 
 // `kernel` with 1 << r_shift rows per item on a resident grid, and the combine step behind it.

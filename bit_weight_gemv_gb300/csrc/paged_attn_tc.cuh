@@ -211,7 +211,8 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
     tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_relinquish();
   }
-  begin_launch(a);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Walk it;
   Share share;
   const bool busy = start_walk<C::kThreads>(a, blockIdx.x, it, share);
@@ -767,7 +768,6 @@ attn_tc_kernel(const __grid_constant__ A a, const __grid_constant__ CUtensorMap 
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-  end_launch(a);
 }
 
 template <int D, bool PAIR, bool FP8, class A>

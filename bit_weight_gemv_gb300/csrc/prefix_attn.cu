@@ -6,7 +6,7 @@
 // pieces out of both.  The kernels and their schedule are lowbit_paged_attention's.
 //
 // Where one kernel suits both parts (few rows in the shared part; or many in the own one) one launch takes them,
-// laid end to end in its schedule; else two, of which the second starts as the CTAs of the first leave.
+// laid end to end in its schedule; else two, one after the other.
 #include "paged_attn_mma.cuh"
 
 namespace lowbit {
@@ -30,8 +30,8 @@ __device__ __forceinline__ bool request_of_group(const PrefixArgs& a, int b, Req
 }
 
 // A warp joins a row's pieces: of the shared part, then of its own.  Bound by round trips (where they are, their
-// statistics, the pieces), of which the row's request and checks are done before the kernels ahead have
-// ended.
+// statistics, the pieces).  The row's request and its checks come before the wait for the kernels ahead: what they
+// read was there before the first of these began, and each lets the next one start only after its own wait.
 template <int D>
 __global__ void __launch_bounds__(kPrefixJoinWarps * 32)
 prefix_join_kernel(const __grid_constant__ PrefixArgs a, const float* own_o, const float2* own_ml) {
@@ -222,19 +222,19 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   // 256 rows an item in the shared part where there are many in all: 768 rows a group of 3,072 behind 16,000 keys
   // 215 us, 279 with 128; but 1,536 rows behind 3,000 keys 61 and 53, 512 behind 4,000 63 and 58.
   const Kind shared_kind = kind_of(a, D, shared_rows, all > 2000 ? 500 : 1 << 30), own_kind = kind_of(a, D, own_rows, 1024);
-  // One launch where the shared part's kernel suits the own part: its rows fill an item half or more, or items are
-  // few.  us in one / in two launches: 32 requests of 32 rows behind 10,000 keys 74 / 88 (e4m3 85 / 93), 16 of 4 behind
-  // 4,000 20 / 22, 16 of 16 rows behind 8,000 30 / 33; 64 of 4 behind 500 52 / 46 (e4m3 56 / 36), behind 16,384 61 / 69
-  // (77 / 61), 128 of 4 behind 4,000 61 / 58 (70 / 48).
-  const bool together = shared_kind == own_kind || shared_kind <= kMma64 ||
-                        (shared_kind == kTc128 && (own_rows > 16 || (long long)B * cache->heads <= 152));
+  // One launch where the shared part's kernel suits the own part, which then costs no start of its own: where rows
+  // fill an item half or more, items are few, or (128 rows an item) tiles need no conversion.  us in one / in
+  // two launches: 32 requests of 32 rows behind 10,000 keys 74 / 88 (e4m3 85 / 93), 16 of 4 behind 4,000 20 / 22, 48 of
+  // 64 behind 16,000 215 / 228; 64 of 4 behind 16,384 61 / 79 (e4m3 77 / 67), behind 500 52 / 54 (56 / 37), 128 of 4
+  // behind 4,000 61 / 66 (70 / 51).
+  const bool together = shared_kind == own_kind || shared_kind <= kMma64 || own_kind >= kTc128 ||
+                        (shared_kind == kTc128 && (!fp8 || own_rows > 16 || (long long)B * cache->heads <= 152));
   PrefixArgs part = a;
   part.p.B = together ? groups + B : groups;
   e = launch_kind(part, D, fp8, shared_kind, s);
   if (e == cudaSuccess && !together) {
     part.p.B = B;
     part.first = groups;
-    part.behind = 1;
     use_pieces(&part, static_cast<uint8_t*>(workspace) + pieces_bytes(D), D);
     e = launch_kind(part, D, fp8, own_kind, s);
   }

@@ -80,7 +80,6 @@ constexpr int kList = 256;  // entries (key << 32 | index) of a row's list
 struct StateArgs : SampleArgs {
   RowState* state;
   u64* lists;           // [row][kList], or NULL
-  int behind;           // launched behind another call of this kernel that does not concern it (see there)
   const int32_t* cu_drafts;
   int B, N, rows, extra;  // requests, drafts and target rows of the arrays
 };
@@ -487,7 +486,7 @@ __device__ __forceinline__ void finish_candidates(const A& a, Shared& s, ulonglo
 }
 
 template <bool BF16, bool HELD, class A>
-__device__ __forceinline__ void sample_row(const A& a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ A a) {
   constexpr bool kState = std::is_same<A, StateArgs>::value;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
@@ -498,6 +497,8 @@ __device__ __forceinline__ void sample_row(const A& a) {
   const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;  // this warp's places in the slice
   const int index0 = rank * kWarps * a.per_warp;               // of the slice's first element
   cluster_arrive();  // this CTA runs: the others may write its shared memory
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (kState) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   int of = m;  // where its settings are
   if constexpr (kState) {
@@ -1295,23 +1296,6 @@ __device__ __forceinline__ void sample_row(const A& a) {
     ties_before += __shfl_sync(~0u, ties_incl, 31);
     return false;
   });
-}
-
-template <bool BF16, bool HELD, class A>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ A a) {
-  if constexpr (std::is_same<A, StateArgs>::value) {
-    // Two of these in a row (the drafter's rows, then the target's) do not depend on each other, so the second one
-    // does not wait for the first to end, which it follows as soon as all of the first's CTAs run: these
-    // have waited for everything before.  It waits at its own end, so that what comes behind it, which waits for
-    // it alone, finds both done.
-    if (!a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    sample_row<BF16, HELD>(a);
-    if (a.behind) asm volatile("griddepcontrol.wait;" ::: "memory");
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    sample_row<BF16, HELD>(a);
-  }
 }
 
 template <bool BF16, bool HELD, class A>

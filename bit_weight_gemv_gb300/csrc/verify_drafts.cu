@@ -108,8 +108,9 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
   const int n = fits ? c1 - c0 : 0;
   const uint8_t* const rows = static_cast<const uint8_t*>(a.logits);
   const uint8_t* const draft_rows = static_cast<const uint8_t*>(a.draft_logits);
-  // What a draft is judged by, beside the rows' states: every CTA finds out for itself, and before the kernels
-  // that the states come from have ended (they have waited for all that came before them).
+  // What a draft is judged by, beside the rows' states: every CTA finds out for itself, before it waits for the
+  // kernels that the states come from (what it reads was there before the first of these began, and each lets the
+  // next one start only after its own wait).
   struct Judged {
     int d, col;
     float z, y, u;
@@ -445,7 +446,6 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
     st.min_p = r->min_p;
     st.state = r == target ? states : states + target->rows;
     st.lists = r == target ? lists : nullptr;
-    st.behind = r == target && drafter;
     st.cu_drafts = cu_drafts;
     st.B = B;
     st.N = N;

@@ -168,8 +168,10 @@ def test_same_bits_again_and_on_another_stream(lb):  # noqa: F811
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
-def test_a_captured_step_serves_other_lengths_and_groups(lb):  # noqa: F811
-    pr = Shared(8, [0, 2, 5], [200, 64], [2, 2, 2, 2, 2], [9, 70, 1, 30, 5], 8, 2, 128, 16)
+# one launch for both parts; a launch each (tcgen05 and the warp-level MMA, of 128 rows and of 256); the plain kernels
+@pytest.mark.parametrize("fp8,B,new", [(False, 5, 2), (True, 40, 1), (False, 520, 1), (True, 40, 16), (False, 5, 40)])
+def test_a_captured_step_serves_other_lengths_and_groups(lb, fp8, B, new):  # noqa: F811
+    pr = Shared(8, [0, 2, B], [200, 64], [new] * B, [(7 * b) % 71 for b in range(B)], 8, 2, 128, 16, fp8)
     args = pr.args(lb)
     lb.lowbit_prefix_attention(**args)
     graph = torch.cuda.CUDAGraph()
