@@ -77,11 +77,6 @@ struct Kept {
     }
   }
 };
-// 2^40 / total: what a weight is multiplied by to become a probability.
-__device__ __forceinline__ float inverse(const RowState& s) {
-  return s.total ? (float)(0x1p40 / (double)s.total) : 0.0f;
-}
-
 // A thousand threads a CTA, so that few requests, which have 16 CTAs each at most, keep their SMs busy.
 constexpr int kDrawThreads = 1024, kDrawWarps = kDrawThreads / 32;
 
@@ -89,6 +84,7 @@ struct VerifyShared {
   u64 warp_mass[kDrawWarps], rank_mass[2][kMaxCluster];
   u64 token[kList], mass[kList];  // a listed row's
   u64 aim;
+  RowState p, q;  // of the rows that the next token comes from
   float ip, iq;
   int first;
 };
@@ -139,7 +135,10 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     return;
   }
 
-  // ---- which drafts are accepted
+  // ---- which drafts are accepted; a thread keeps the states that it has seen, and the last one those of the row
+  // behind all drafts
+  RowState p_seen = {}, q_seen = {};
+  if (tid == kDrawThreads - 1) p_seen = a.target[c1 + b];
   for (int i = tid; i < n; i += kDrawThreads) {
     const Judged g = i == tid ? mine : look(i);
     const int r = c0 + i;
@@ -150,14 +149,31 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
       const RowState q = a.draft[r];
       if (q.total) given = (double)mass_of(Kept(q).weight(g.y, g.col)) / (double)q.total;
     }
+    if (n < kDrawThreads) p_seen = p, q_seen = draft_rows ? a.draft[r] : RowState{};
     const float u = g.u >= 0.0f ? fminf(g.u, 1.0f) : 0.0f;
     if (!((double)u * given < share)) atomicMin(&s.first, i);
     if (rank == 0 && a.accept) a.accept[r] = given > 0.0 ? (float)fmin(share / given, 1.0) : (share > 0.0 ? 1.0f : 0.0f);
   }
   __syncthreads();
   const int j = min(s.first, n), t = c0 + b + j;  // the row that the next token comes from
-  const RowState p = a.target[t];
   const bool rejected = j < n;
+  // Its states, from the thread that has them, and 2^40 / S of both, what a weight is multiplied by to become
+  // a probability: in the lanes of one warp, since 64-bit floating point is slow here (two a clock and SM).
+  const int who = n >= kDrawThreads ? 0 : (rejected ? j : kDrawThreads - 1);
+  if (n >= kDrawThreads && tid == 0) {
+    p_seen = a.target[t];
+    q_seen = rejected && draft_rows ? a.draft[c0 + j] : RowState{};
+  }
+  if (warp == who >> 5) {
+    const u64 sp = __shfl_sync(~0u, p_seen.total, who & 31), sq = __shfl_sync(~0u, q_seen.total, who & 31);
+    const u64 total = lane == 0 ? sp : sq;
+    const float x = total ? (float)(0x1p40 / (double)total) : 0.0f;
+    if (lane == 0) s.ip = x;
+    if (lane == 1) s.iq = x;
+    if (lane == (who & 31)) s.p = p_seen, s.q = q_seen;
+  }
+  __syncthreads();
+  const RowState p = s.p, q = s.q;
   if (rank == 0) {
     for (int i = tid; i <= n; i += kDrawThreads)
       if (i != j) a.ids[c0 + b + i] = i < j ? a.drafts[c0 + i] : -1;
@@ -174,16 +190,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     cluster_wait();
     return;
   }
-  RowState q = {};
-  if (rejected && draft_rows) q = a.draft[c0 + j];
   const int out = rejected && !draft_rows ? a.drafts[c0 + j] : -1;  // proposed with certainty
-  // 64-bit floating point is slow here (two a clock and SM): one warp's worth of it
-  if (warp == 0) {
-    const float x = inverse(lane == 0 ? p : q);
-    if (lane == 0) s.ip = x;
-    if (lane == 1) s.iq = x;
-  }
-  __syncthreads();
   const float ip = s.ip, iq = s.iq;
   const uint8_t* const draft_row = draft_rows + (long long)(c0 + j) * a.draft_stride * kDraftSize;
   const Kept by_p(p), by_q(q);

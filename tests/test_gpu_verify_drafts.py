@@ -230,6 +230,18 @@ def test_sizes(lb, n, V, Vd, bf16, draft_bf16):
     Case(len(n) + V, n, V, Vd, bf16, draft_bf16, settings=SETTINGS, pad=0 if V % 8 == 0 else 3).check(lb)
 
 
+@pytest.mark.parametrize("certain", [True, False])
+def test_long_blocks(lb, certain):
+    """More drafts than a CTA has threads, accepted to the last or rejected far in."""
+    for n in (1022, 1023, 1024, 1500):
+        c = Case(n, [n, 2], 40, certain=certain, near=0.1)
+        c.u[:] = 0.0
+        got, _, _ = c.check(lb)
+        assert got == [n, 2]
+        c.z[n - 3, int(c.drafts[n - 3])] = -torch.inf      # p = 0: never accepted
+        assert c.check(lb)[0][0] == n - 3
+
+
 @pytest.mark.parametrize("V", [1000, 70001])
 def test_drafters_that_truncate(lb, V):
     c = Case(5, [4] * 16, V, settings=[PLAIN, (0.8, 40, 0.9, 0.0)], draft_settings=SETTINGS, near=1.5)
