@@ -1337,14 +1337,16 @@ cudaError_t launch(A a, int C, cudaStream_t s) {
 template <bool BF16, class A>
 cudaError_t launch_rows(const A& a, cudaStream_t s) {
   // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16
-  // find room at once, and rows that wait for room are done soonest by fours.  V = 248,320, fp32,
+  // find room at once, and rows that wait for room are done soonest in slices of up to 65,536.  V = 248,320, fp32,
   // top-k 20 and top-p / no truncation, us: six rows on 16 CTAs 15.7 / 10.9, on eight 16.6 / 13.3; eight
-  // rows 19.4 / 15.2 and 16.8 / 13.1; 32 rows on eight 22.8 / 22.6, on four 23.0 / 23.1; 48 rows 35.7 / 33.4
-  // and 27.4 / 33.2, on two 31.3 / 36.4; 192 rows 101 / 105, 73 / 89 and 89 / 91.
+  // rows 19.4 / 15.2 and 16.8 / 13.1; 32 rows on eight 22.8 / 22.6, on four 23.0 / 23.1; 192 rows on eight 101 / 105, on
+  // four 73 / 89, on two 89 / 91; 512 rows on four 195, on two 235 (mixed settings).  V = 32,768, 512 rows on two 57 / 42,
+  // on one 32 / 35; V = 65,536, 256 rows on four 47 / 44, on one 20 / 29; V = 131,072, 128 rows on eight 31 / 36, on
+  // four 20 / 29.
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
   if (C == 16 && a.M * 16 > 96) C = 8;
-  if (C == 8 && a.M * 8 > 256) C = 4;
+  while (C > 1 && C < 16 && (long long)a.M * C > 256 && (long long)C * 32768 >= a.V) C /= 2;
   // A slice is held in shared memory where two CTAs still share an SM (fp32, one row on 16: 14.7 / 9.4 us,
   // 15.0 / 10.4 read from L2), and a larger one where every CTA has an SM of its own (12 rows on eight:
   // 17.0 / 13.9 and 17.9 / 15.4; 16 rows: 27.0 / 23.9 and 19.9 / 20.6).
