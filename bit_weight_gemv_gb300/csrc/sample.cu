@@ -16,6 +16,6 @@ extern "C" lowbit_status lowbit_sample(const void* logits, int dtype, int64_t ro
   if ((uintptr_t)logits & (dtype == LOWBIT_LOGITS_BF16 ? 1 : 3) || words & 3) return LOWBIT_ERR_ALIGN;
   const SampleArgs a = {logits, row_stride, M, V, 1, 0, 0, temperature, top_k, top_p, min_p, u, id_map, ids, logprob, kept};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == LOWBIT_LOGITS_BF16 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
+  const cudaError_t e = dtype == LOWBIT_LOGITS_BF16 ? launch_rows<true>(a, M, V, s) : launch_rows<false>(a, M, V, s);
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }

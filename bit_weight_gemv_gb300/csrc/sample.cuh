@@ -83,6 +83,17 @@ struct StateArgs : SampleArgs {
   const int32_t* cu_drafts;
   int B, N, rows, extra;  // requests, drafts and target rows of the arrays
 };
+// Two sets of rows in one launch: the CTAs up to `split` take the first.
+struct StatePair {
+  StateArgs part[2];
+  int split;
+};
+__device__ __forceinline__ const SampleArgs& part_of(const SampleArgs& a, int&) { return a; }
+__device__ __forceinline__ const StateArgs& part_of(const StatePair& a, int& block) {
+  const bool second = block >= a.split;
+  if (second) block -= a.split;
+  return a.part[second];
+}
 // Whether request b, with the drafts c0 .. c1 - 1, lies inside the arrays.
 __device__ __forceinline__ bool request_fits(int b, int c0, int c1, int N, int rows) {
   return c0 >= 0 && c1 >= c0 && c1 <= N && (long long)c1 + b < rows;
@@ -485,14 +496,16 @@ __device__ __forceinline__ void finish_candidates(const A& a, Shared& s, ulonglo
   }
 }
 
-template <bool BF16, bool HELD, class A>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ A a) {
-  constexpr bool kState = std::is_same<A, StateArgs>::value;
+template <bool BF16, bool HELD, class P>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ P all) {
+  constexpr bool kState = std::is_same<P, StatePair>::value;
+  int block = blockIdx.x;
+  const auto& a = part_of(all, block);
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   uint8_t* const store = smem + (sizeof(Shared) + 15) / 16 * 16;
   constexpr int kSize = BF16 ? 2 : 4;
-  const int C = a.cluster, rank = blockIdx.x % C, m = blockIdx.x / C;
+  const int C = a.cluster, rank = block % C, m = block / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg_from = warp * a.per_warp, seg_to = seg_from + a.per_warp;  // this warp's places in the slice
   const int index0 = rank * kWarps * a.per_warp;               // of the slice's first element
@@ -1298,28 +1311,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   });
 }
 
-template <bool BF16, bool HELD, class A>
-cudaError_t launch(A a, int C, cudaStream_t s) {
-  a.cluster = C;
+// What a row's CTAs take of it; the bytes of shared memory of one.
+template <bool BF16, bool HELD>
+size_t divide_rows(SampleArgs* a, int C) {
+  a->cluster = C;
   const int step = HELD ? (BF16 ? 256 : 128) : 512;
-  a.per_warp = ((a.V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step;
-  a.aligned = ((uintptr_t)a.logits & 15) == 0 && (a.row_stride * (BF16 ? 2 : 4)) % 16 == 0;
-  const size_t slice = HELD ? (size_t)kWarps * a.per_warp * (BF16 ? 2 : 4) : 0;
-  const size_t bytes = (sizeof(Shared) + 15) / 16 * 16 + std::max(slice, (size_t)kCap * 16);
+  a->per_warp = ((a->V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step;
+  a->aligned = ((uintptr_t)a->logits & 15) == 0 && (a->row_stride * (BF16 ? 2 : 4)) % 16 == 0;
+  const size_t slice = HELD ? (size_t)kWarps * a->per_warp * (BF16 ? 2 : 4) : 0;
+  return (sizeof(Shared) + 15) / 16 * 16 + std::max(slice, (size_t)kCap * 16);
+}
+template <bool BF16, bool HELD, class P>
+cudaError_t launch(const P& all, int C, unsigned rows, size_t bytes, cudaStream_t s) {
   static std::atomic<int> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(sample_kernel<BF16, HELD, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    e = cudaFuncSetAttribute(sample_kernel<BF16, HELD, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(sample_kernel<BF16, HELD, A>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(sample_kernel<BF16, HELD, P>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ready[dev].store(1, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.M * a.cluster));
+  cfg.gridDim = dim3(rows * (unsigned)C);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
@@ -1327,15 +1344,28 @@ cudaError_t launch(A a, int C, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.x = (unsigned)C;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, HELD, A>, a);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, HELD, P>, all);
+}
+template <bool BF16, bool HELD>
+cudaError_t launch_divided(SampleArgs a, int C, cudaStream_t s) {
+  const size_t bytes = divide_rows<BF16, HELD>(&a, C);
+  return launch<BF16, HELD>(a, C, (unsigned)a.M, bytes, s);
+}
+template <bool BF16, bool HELD>
+cudaError_t launch_divided(StatePair a, int C, cudaStream_t s) {
+  size_t bytes = 0;
+  for (StateArgs& p : a.part)
+    if (p.M) bytes = std::max(bytes, divide_rows<BF16, HELD>(&p, C));
+  a.split = a.part[0].M * C;
+  return launch<BF16, HELD>(a, C, (unsigned)(a.part[0].M + a.part[1].M), bytes, s);
 }
 
-template <bool BF16, class A>
-cudaError_t launch_rows(const A& a, cudaStream_t s) {
+// CTAs for each of M rows of V.
+inline int ctas_per_row(int M, int V) {
   // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16
   // find room at once, and rows that wait for room are done soonest in slices of up to 65,536.  V = 248,320, fp32,
   // top-k 20 and top-p / no truncation, us: six rows on 16 CTAs 15.7 / 10.9, on eight 16.6 / 13.3; eight
@@ -1344,15 +1374,20 @@ cudaError_t launch_rows(const A& a, cudaStream_t s) {
   // on one 32 / 35; V = 65,536, 256 rows on four 47 / 44, on one 20 / 29; V = 131,072, 128 rows on eight 31 / 36, on
   // four 20 / 29.
   int C = 1;
-  while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
-  if (C == 16 && a.M * 16 > 96) C = 8;
-  while (C > 1 && C < 16 && (long long)a.M * C > 256 && (long long)C * 32768 >= a.V) C /= 2;
+  while (C < kMaxCluster && (long long)C * 16384 < V) C *= 2;
+  if (C == 16 && M * 16 > 96) C = 8;
+  while (C > 1 && C < 16 && (long long)M * C > 256 && (long long)C * 32768 >= V) C /= 2;
+  return C;
+}
+template <bool BF16, class P>
+cudaError_t launch_rows(const P& all, int M, int V, cudaStream_t s) {
+  const int C = ctas_per_row(M, V);
   // A slice is held in shared memory where two CTAs still share an SM (fp32, one row on 16: 14.7 / 9.4 us,
   // 15.0 / 10.4 read from L2), and a larger one where every CTA has an SM of its own (12 rows on eight:
   // 17.0 / 13.9 and 17.9 / 15.4; 16 rows: 27.0 / 23.9 and 19.9 / 20.6).
   const int step = BF16 ? 256 : 128;
-  const long long slice = (long long)((a.V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step * kWarps * (BF16 ? 2 : 4);
-  return slice <= (a.M * C <= 96 ? 163840 : 65536) ? launch<BF16, true>(a, C, s) : launch<BF16, false>(a, C, s);
+  const long long slice = (long long)((V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step * kWarps * (BF16 ? 2 : 4);
+  return slice <= ((long long)M * C <= 96 ? 163840 : 65536) ? launch_divided<BF16, true>(all, C, s) : launch_divided<BF16, false>(all, C, s);
 }
 
 }  // namespace

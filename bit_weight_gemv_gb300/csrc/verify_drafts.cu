@@ -395,8 +395,9 @@ cudaError_t launch_draw(VerifyArgs a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, verify_draw_kernel<BF16, DRAFT_BF16>, a);
 }
 
-cudaError_t launch_state(const StateArgs& a, bool bf16, cudaStream_t s) {
-  return bf16 ? launch_rows<true>(a, s) : launch_rows<false>(a, s);
+cudaError_t launch_state(const StatePair& a, int V, bool bf16, cudaStream_t s) {
+  const int M = a.part[0].M + a.part[1].M;
+  return bf16 ? launch_rows<true>(a, M, V, s) : launch_rows<false>(a, M, V, s);
 }
 bool known(int dtype) { return dtype == LOWBIT_LOGITS_FP32 || dtype == LOWBIT_LOGITS_BF16; }
 
@@ -440,8 +441,7 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   u64* const lists = reinterpret_cast<u64*>(states + target->rows + N);
   const bool drafter = draft && N > 0;
 
-  for (const lowbit_row_settings* r : {draft, target}) {
-    if (!r || (r == draft && !drafter)) continue;
+  auto rows_of = [&](const lowbit_row_settings* r) {
     StateArgs st = {};
     st.logits = r->logits;
     st.row_stride = r->row_stride;
@@ -458,8 +458,23 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
     st.N = N;
     st.rows = target->rows;
     st.extra = r == target;
-    if (launch_state(st, r->dtype == LOWBIT_LOGITS_BF16, s) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    return st;
+  };
+  const bool bf16 = target->dtype == LOWBIT_LOGITS_BF16, draft_bf16 = draft && draft->dtype == LOWBIT_LOGITS_BF16;
+  StatePair pair = {};
+  pair.part[0] = rows_of(target);
+  if (drafter) {
+    // Both in one launch, so that the short rows fill the gaps of the long ones (28 drafts of four requests 34 us, 40
+    // one after the other; 67 of nine with a trimmed vocabulary 59 and 67; 480 of 32 206 and 218).
+    if (bf16 == draft_bf16) {
+      pair.part[1] = rows_of(draft);
+    } else {
+      StatePair alone = {};
+      alone.part[0] = rows_of(draft);
+      if (launch_state(alone, draft->V, draft_bf16, s) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    }
   }
+  if (launch_state(pair, pair.part[1].M ? std::max(target->V, draft->V) : target->V, bf16, s) != cudaSuccess) return LOWBIT_ERR_CUDA;
   VerifyArgs a = {};
   a.logits = target->logits;
   a.row_stride = target->row_stride;
@@ -484,7 +499,6 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   a.ids = ids;
   a.accept = accept;
   a.err = err;
-  const bool bf16 = target->dtype == LOWBIT_LOGITS_BF16, draft_bf16 = draft && draft->dtype == LOWBIT_LOGITS_BF16;
   const cudaError_t e = bf16 ? (draft_bf16 ? launch_draw<true, true>(a, s) : launch_draw<true, false>(a, s))
                              : (draft_bf16 ? launch_draw<false, true>(a, s) : launch_draw<false, false>(a, s));
   return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
