@@ -5,8 +5,8 @@ caller), checks dtypes/shapes, passes raw pointers and the current CUDA stream t
 (include/lowbit.h) under the same name, and raises LowbitError on a non-zero status.  All
 arithmetic runs in the library's CUDA kernels; there is no CPU fallback.  The in-tree
 liblowbit.so is loaded on first use of any of these names and its absence raises ImportError.
-The cache, attention and sampling calls unpack their tensors in a compiled module beside it, made
-for one torch and one Python; without that module those three raise ImportError.  Build both with
+The cache, attention, sampling and draft-verification calls unpack their tensors in a compiled module beside
+it, made for one torch and one Python; without that module those raise ImportError.  Build both with
 ``python -m bit_weight_gemv_gb300.build``.
 """
 

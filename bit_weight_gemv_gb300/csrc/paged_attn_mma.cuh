@@ -9,8 +9,8 @@
 // ring that a fifth warp fills by TMA, one box per page and 128-byte part of a row; with MT < 4 row
 // groups the four compute warps take different keys of the tile and join at the item's end.  The
 // copying warp walks the items on its own, so the next item's tiles arrive while one is finished.
-// The grid is resident and the work is cut evenly over it (see paged.cuh); attn_combine_kernel
-// joins items that were cut.
+// The grid is resident and the work is cut evenly over it (see paged.cuh); a second kernel joins
+// items that were cut (attn_combine_kernel; for shared prefixes prefix_join_kernel).
 //
 // The weights exp(s_j - m) enter their product as bf16, or over an e4m3 cache as fp16: the MMA takes 16-bit
 // operands, and of the two each goes with a type that holds the values exactly.  l sums the weights
@@ -628,7 +628,7 @@ struct Cfg8 {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kSteps = D / 16;
   static constexpr int kCtas = kStage <= 8192 ? 4 : (kStage <= 16384 ? 3 : (kStage <= 32768 ? 2 : 1));
-  static constexpr int kFit = (227 * 1024 / kCtas - 3072) / kStage;
+  static constexpr int kFit = (227 * 1024 / kCtas - 3 * 1024) / kStage;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = 1024 + kStages * kStage;
   static_assert(64 * D <= kStage, "two warps' outputs pass through one stage");

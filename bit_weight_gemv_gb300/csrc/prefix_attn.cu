@@ -219,8 +219,8 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
     if (e == cudaSuccess) e = launch_attention(a, D, fp8, s);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
   }
-  // 256 rows an item in the shared part where there are many in all: 768 rows a group of 3,072 behind 16,000 keys
-  // 215 us, 279 with 128; but 1,536 rows behind 3,000 keys 61 and 53, 512 behind 4,000 63 and 58.
+  // 256 rows an item in the shared part where there are many in all: four groups of 768 rows behind 16,000
+  // keys 215 us, 279 with 128; but 1,536 rows behind 3,000 keys 61 and 53, 512 behind 4,000 63 and 58.
   const Kind shared_kind = kind_of(a, D, shared_rows, all > 2000 ? 500 : 1 << 30), own_kind = kind_of(a, D, own_rows, 1024);
   // One launch where the shared part's kernel suits the own part, which then costs no start of its own: where rows
   // fill an item half or more, items are few, or (128 rows an item) tiles need no conversion.  us in one / in

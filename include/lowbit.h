@@ -454,9 +454,12 @@ size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int
  *                 kv_lens[b] - new tokens >= the length of the whole pages.
  * kv_lens and block_table describe the whole requests, as for lowbit_kv_append and lowbit_paged_attention,
  * whose result over the same arguments is this one's but for rounding.  A group or request that the
- * arrays describe inconsistently is recorded in the device error word; rows of its are not written, or (where a
- * group's arrays are at fault) attend to the request's own block table alone.  Pages are compared by nobody: rows of different pages under the same
- * prefix give each request the first one's.
+ * arrays describe inconsistently is recorded in the device error word; its rows are not written, or (where only
+ * what it shares is at fault) attend to the request's own block table.  Pages are compared by nobody: where the
+ * table rows of a group differ in the shared pages, it is not defined which of them a request sees.
+ * Worth it where many requests with few rows each share much (16 requests of one token and more behind
+ * thousands of keys).  From about 100 rows a request on (tokens times query heads per key/value head)
+ * lowbit_paged_attention's kernels do the work, which are as fast there.
  *   workspace : lowbit_prefix_attention_workspace_bytes() bytes, 16-byte aligned, any contents; calls that
  *   may run at the same time need one each.
  * All else (rounding, non-finite values, alignment) is as in lowbit_paged_attention; a non-finite v in
@@ -616,7 +619,7 @@ lowbit_status lowbit_draft_argmax_path(const uint16_t* H, const void* packed_hea
  * wait then ends after about a millisecond instead of about a second.  Such a call writes no
  * output (Y, argmax, n_accept, bonus, ids keep their previous contents), leaves the LM-head
  * workspace zeroed, and records LOWBIT_ERR_TIMEOUT in the device error word.  A CTA still
- * waits for its own copies in flight before it exits.  lowbit_paged_attention's kernels then get no data
+ * waits for its own copies in flight before it exits.  The attention calls' kernels then get no data
  * (no key tiles, or on tcgen05 no queries): every role's wait runs out, after about a second, and
  * neither out nor lse is written.  The other tcgen05 kernels and the CUDA-core kernels are not
  * affected.  The setting is process-wide; pass 0 to restore normal operation. */
