@@ -399,6 +399,16 @@ cudaError_t launch_state(const StatePair& a, int V, bool bf16, cudaStream_t s) {
   const int M = a.part[0].M + a.part[1].M;
   return bf16 ? launch_rows<true>(a, M, V, s) : launch_rows<false>(a, M, V, s);
 }
+// What a call reads or writes: the cluster's CTAs find out about a request each for itself, so what one of them
+// writes must not be what another one reads.
+struct Span {
+  const void* at;
+  __int128 bytes;
+};
+bool meet(const Span& x, const Span& y) {
+  const __int128 a = (__int128)(uintptr_t)x.at, b = (__int128)(uintptr_t)y.at;
+  return x.at && y.at && a < b + y.bytes && b < a + x.bytes;
+}
 bool known(int dtype) { return dtype == LOWBIT_LOGITS_FP32 || dtype == LOWBIT_LOGITS_BF16; }
 
 }  // namespace
@@ -434,6 +444,24 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   if (words & 3) return LOWBIT_ERR_ALIGN;
   if (!workspace || ws_bytes < lowbit_verify_drafts_workspace_bytes(target->rows, N)) return LOWBIT_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 15) return LOWBIT_ERR_ALIGN;
+  const Span written[] = {{n_accept, (__int128)B * 4}, {ids, (__int128)target->rows * 4}, {accept, (__int128)N * 4},
+                          {workspace, (__int128)lowbit_verify_drafts_workspace_bytes(target->rows, N)}};
+  Span read[16] = {{cu_drafts, (__int128)(B + 1) * 4}, {drafts, (__int128)N * 4}, {draft_index, (__int128)target->V * 4},
+                   {u, (__int128)N * 4}, {v, (__int128)B * 4}};
+  int reads = 5;
+  for (const lowbit_row_settings* r : {target, draft}) {
+    if (!r) continue;
+    const __int128 size = r->dtype == LOWBIT_LOGITS_BF16 ? 2 : 4;
+    read[reads++] = {r->logits, r->rows < 1 ? 0 : ((__int128)(r->rows - 1) * r->row_stride + r->V) * size};
+    for (const void* x : {(const void*)r->temperature, (const void*)r->top_k, (const void*)r->top_p, (const void*)r->min_p})
+      read[reads++] = {x, (__int128)B * 4};
+  }
+  for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < reads; ++k)
+      if (meet(written[i], read[k])) return LOWBIT_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (meet(written[i], written[k])) return LOWBIT_ERR_INVALID_ARG;
+  }
   int* const err = device_error_word();
   if (!err) return LOWBIT_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -398,7 +398,8 @@ lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  *       is NULL where q is).  Values are never normalised.
  *   eps : finite, >= 0; with 0, a head of zeros becomes NaN.
  *   The squares are summed in fp32, so a head whose sum of squares passes 3.4e38 (elements past 2^60) becomes
- *   zeros, or NaN where it holds an infinity.  All else is as in lowbit_kv_append. */
+ *   zeros, or NaN where it holds an infinity; with eps 0, one whose squares all round to zero (elements under
+ *   2^-75) becomes infinities.  All else is as in lowbit_kv_append. */
 lowbit_status lowbit_kv_append_norm(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                                     int64_t k_stride, const uint16_t* v, int64_t v_stride, int Hq,
                                     const float* q_weight, const float* k_weight, float eps,
@@ -544,7 +545,9 @@ size_t lowbit_verify_drafts_workspace_bytes(int M, int N);
  * A request that cu_drafts describes inconsistently (decreasing, or outside the arrays) gets n = 0, no ids and
  * is recorded in the device error word.  Rows of no request are neither read nor written.
  *   workspace : lowbit_verify_drafts_workspace_bytes() bytes, 16-byte aligned, any contents; calls that may
- *   run at the same time need one each.  The result does not depend on timing. */
+ *   run at the same time need one each.  The result does not depend on timing.
+ * n_accept, ids, accept and workspace may lie over nothing else that the call is given
+ * (LOWBIT_ERR_INVALID_ARG). */
 lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowbit_row_settings* draft,
                                    int B, int N, const int32_t* cu_drafts, const int32_t* drafts,
                                    const int32_t* draft_index, const float* u, const float* v,

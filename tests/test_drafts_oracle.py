@@ -107,6 +107,36 @@ def test_refusals(native, kw, status):  # noqa: F811
     assert call(native, **kw) == status
 
 
+# Arrays of two requests and six drafts, a megabyte apart, and what of them lies over another one's bytes.
+APART = {x: P + (i << 20) for i, x in enumerate(("cu", "drafts", "index", "u", "v", "count", "ids", "accept", "ws"))}
+Z, Y = P + (20 << 20), P + (30 << 20)
+
+
+@pytest.mark.parametrize("written", ["count", "ids", "accept", "ws"])
+def test_outputs_over_anything_else_are_refused(native, written):  # noqa: F811
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("calls that are not refused would run on these addresses")
+    bytes_of = dict(cu=12, drafts=24, index=400, u=24, v=8, count=8, ids=32, accept=24, ws=8 * 2080 + 6 * 32)
+    temp = P + (40 << 20)
+
+    def status(**kw):
+        target, draft = rows(logits=Z, temperature=temp), rows(logits=Y, rows=6, min_p=temp + 4096)
+        return call(native, target, draft, **(APART | kw))
+
+    near = 16 if written == "ws" else 4
+    for other, at in APART.items():
+        if other == written:
+            continue
+        end = (bytes_of[other] + near - 1) // near * near
+        assert status(**{written: at}) == status(**{written: at + end - near}) == INVALID, other
+        assert status(**{written: at + end}) != INVALID, other      # a device is all that is missing
+    for at in (Z, Z + 4 * 796, Y + 4 * 592, temp, temp + 4096):
+        assert status(**{written: at}) == INVALID
+    assert status(**{written: Y + 4 * 600}) != INVALID
+    assert status(index=None) != INVALID
+
+
 def test_no_rows_at_all(native):  # noqa: F811
     f = native.lib.lowbit_verify_drafts
     assert f(None, None, 1, 0, P, None, None, None, P, P, P, None, P, 100, None) == INVALID
