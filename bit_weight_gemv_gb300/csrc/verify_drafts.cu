@@ -55,9 +55,11 @@ struct Kept {
     last = s.total ? (uint32_t)s.cut : 0u;
     least = s.total ? fmaxf(s.floor_w, __uint_as_float(__float_as_uint(kLeast) + 1)) : INFINITY;
   }
-  // The logit as it was given: clipped to 0..1, the weight of an infinity is that of the largest number.
+  // The logit as it was given: clipped to 0..1, the weight of an infinity is that of the largest number, which it is
+  // also ordered as (a NaN comes to no weight before its place in the order counts).
   __device__ __forceinline__ float weight(float z, int i) const {
     const float w = __saturatef(weight_of(z, top, rate));
+    z = fminf(z, 3.402823466e38f);
     return (z > cut || (z == cut && (uint32_t)i <= last)) && w >= least ? w : 0.0f;
   }
   // Of four neighbours, from token i on; a row that nothing is cut off takes the short way.
@@ -72,8 +74,10 @@ struct Kept {
       for (int e = 0; e < 4; ++e) w[e] = w[e] >= least ? w[e] : 0.0f;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = (z[e] > cut || (z[e] == cut && (uint32_t)(i + e) <= last)) && w[e] >= least ? w[e] : 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        const float c = fminf(z[e], 3.402823466e38f);
+        w[e] = (c > cut || (c == cut && (uint32_t)(i + e) <= last)) && w[e] >= least ? w[e] : 0.0f;
+      }
     }
   }
 };

@@ -309,6 +309,23 @@ def test_rows_without_finite_logits_and_odd_values(lb):
     assert got[0] == 0 and ids[0] == -1 and got[1] == 2 and ids[5] == -1 and got[2] == 0 and ids[6] >= 0
 
 
+@pytest.mark.parametrize("many", [3, 700])
+@pytest.mark.parametrize("settings", [(1.0, 2, 1.0, 0.0), (0.7, 400, 1.0, 0.0), (1.0, 0, 0.6, 0.0), (0.0, 0, 1.0, 0.0)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_several_infinities_count_as_equal(lb, many, settings, bf16):
+    """A cut through logits of +inf leaves the lower ones in, in the target's rows and the drafter's."""
+    c = Case(23, [4, 4], 6000, settings=[settings, PLAIN], draft_settings=[PLAIN, settings], bf16=bf16)
+    c.z, c.y = c.z.clone(), c.y.clone()
+    at = torch.arange(many, device="cuda") * 8 + 5
+    c.z[:5, at] = torch.inf
+    c.y[4:, at] = torch.inf
+    c.y[2, at] = torch.inf
+    first, last = int(at[0]), int(at[-1])
+    c.drafts = i32([first, first, first, last, last, first, last, first])
+    c.u[:] = [0.0, 0.0, 1e-6, 0.5, 0.5, 0.5, 0.999, 1.0]
+    c.check(lb)
+
+
 def test_drafts_outside_the_vocabulary(lb):
     for certain in (True, False):
         c = Case(14, [2, 2, 2], 400, Vd=100, certain=certain)
