@@ -96,10 +96,10 @@ __device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
   }
   return g;
 }
-// Request b without the keys that its group shares.  One that has new tokens among these counts as inconsistent;
+// Request b, of group g, without the keys that the group shares.  One that has new tokens among these counts as inconsistent;
 // what else can be wrong with it the join step looks for, which keeps its loads out of the way here.
-__device__ __forceinline__ Request load_own(const PrefixArgs& a, int b) {
-  const int g = group_of(a, b), skip = a.prefix_lens[g] & ~a.p.page_mask;
+__device__ __forceinline__ Request load_own(const PrefixArgs& a, int b, int g) {
+  const int skip = a.prefix_lens[g] & ~a.p.page_mask;
   Request r = check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
   if (r.n == 0) return r;
   if (skip < 0 || r.kv - r.n < skip) {
@@ -112,7 +112,7 @@ __device__ __forceinline__ Request load_own(const PrefixArgs& a, int b) {
 }
 __device__ __forceinline__ Request load_request(const PrefixArgs& a, int b) {
   b += a.first;
-  return b < a.groups ? load_group(a, b) : load_own(a, b - a.groups);
+  return b < a.groups ? load_group(a, b) : load_own(a, b - a.groups, group_of(a, b - a.groups));
 }
 // The block table from the page of the request's first counted key on.
 __device__ __forceinline__ const int32_t* table_of(const AttnArgs& a, int b, const Request&) {

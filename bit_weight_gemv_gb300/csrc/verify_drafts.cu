@@ -103,14 +103,13 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
   const int index0 = rank * kDrawWarps * a.per_warp;
   cluster_arrive();  // this CTA runs: the others may write its shared memory
   if (tid == 0) s.first = INT32_MAX;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = a.cu_drafts[b], c1 = a.cu_drafts[b + 1];
   const bool fits = request_fits(b, c0, c1, a.N, a.M);
   const int n = fits ? c1 - c0 : 0;
   const uint8_t* const rows = static_cast<const uint8_t*>(a.logits);
   const uint8_t* const draft_rows = static_cast<const uint8_t*>(a.draft_logits);
-  // What a draft is judged by, beside the rows' states: every CTA finds out for itself, before it waits for the
-  // kernels that the states come from (what it reads was there before the first of these began, and each lets the
-  // next one start only after its own wait).
+  // What a draft is judged by, beside the rows' states: every CTA finds out for itself.
   struct Judged {
     int d, col;
     float z, y, u;
@@ -128,7 +127,6 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
   };
   Judged mine = {};
   if (tid < n) mine = look(tid);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   if (!fits) {
     if (rank == 0 && tid == 0) {
