@@ -228,9 +228,19 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
     if (e == cudaSuccess) e = launch_attention(a, D, fp8, s);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
   }
-  // 256 rows an item in the shared part where there are many in all: four groups of 768 rows behind 16,000
-  // keys 215 us, 279 with 128; but 1,536 rows behind 3,000 keys 61 and 53, 512 behind 4,000 63 and 58.
-  const Kind shared_kind = kind_of(a, D, shared_rows, all > 2000 ? 500 : 1 << 30), own_kind = kind_of(a, D, own_rows, 1024);
+  // 256 rows an item in the shared part read its keys half as often, but leave more of an item empty in the own part if
+  // one launch takes both, and of the last one.  So they pay behind long prefixes, whose length the host knows a bound of,
+  // the block table's.  us with 256 / 128, bf16, 16,000 keys shared: 12 requests of 64 rows 67 / 72, 24 112 / 131, 48 in four
+  // groups 209 / 276, 5 48 / 41; 8,000 keys: 48 in four groups 145 / 157, 16 61 / 59; 4,000: 48 104 / 94, in four groups with
+  // 1,500 keys of their own 153 / 139.  With a launch for each part, 256 requests of 16 rows 312 / 370 behind 16,000, 225 / 223
+  // behind 4,000, 64 of 32 rows 168 / 167 and 122 / 98 (behind 6,000); over e4m3, 128 of 16 rows 194 / 213 behind 10,000, 136 /
+  // 140 behind 6,000, 64 of 32 rows 187 / 198 behind 16,000, 125 / 121 behind 6,000.
+  const Kind own_kind = kind_of(a, D, own_rows, 1024);
+  const long long reach = (long long)a.p.width << a.p.page_shift;
+  const bool tall = shared_rows > 600 && (own_kind >= kTc128 ? reach > 8192
+                                          : fp8             ? own_rows <= 16 || reach > 8192
+                                                            : all * reach > 1 << 25);
+  const Kind shared_kind = kind_of(a, D, shared_rows, tall ? 1 : 1 << 30);
   // One launch where the shared part's kernel suits the own part, which then costs no start of its own: where rows
   // fill an item half or more, items are few, or (128 rows an item) tiles need no conversion.  us in one / in
   // two launches: 32 requests of 32 rows behind 10,000 keys 74 / 88 (e4m3 85 / 93), 16 of 4 behind 4,000 20 / 22, 48 of

@@ -187,6 +187,48 @@ def test_a_captured_step_serves_other_lengths_and_groups(lb, fp8, B, new):  # no
     assert lb.lowbit_device_error() == 0
 
 
+# a table with room for long requests takes taller items: in one launch with the own part, and in one of their own
+TALL = [(False, 40, 16, 600), (True, 40, 16, 600), (True, 160, 1, 40), (False, 256, 1, 2100), (True, 80, 8, 600)]
+
+
+def tall(seed, fp8, B, new, width, prefix):
+    pr = Shared(seed, [0, B], [prefix], [new] * (B - 1) + [0], [(7 * b) % 71 for b in range(B)], 8, 2, 128, 16, fp8)
+    pr.table = np.concatenate([pr.table, np.full((B, width), -7, dtype=np.int64)], 1)
+    return pr
+
+
+@pytest.mark.parametrize("fp8,B,new,width", TALL)
+def test_tables_with_room_for_long_requests(lb, fp8, B, new, width):  # noqa: F811
+    pr = tall(13, fp8, B, new, width, 1000)
+    pr.check(*pr.shared(lb))
+    args = pr.args(lb)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lb.lowbit_prefix_attention(**args)
+    for prefix, kv in (([1000], pr.kv), ([90], [x - 3 for x in pr.kv])):
+        pr.prefix, pr.kv = prefix, kv
+        args["prefix_lens"].copy_(i32(prefix))
+        args["kv_lens"].copy_(i32(kv))
+        graph.replay()
+        torch.cuda.synchronize()
+        pr.check(pr.out[:pr.T], pr.ls[:pr.T])
+    assert lb.lowbit_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8,B,new,width", TALL)
+def test_stall_with_tall_items(lb, fp8, B, new, width):  # noqa: F811
+    pr = tall(14, fp8, B, new, width, 300)
+    want = [t.clone() for t in pr.shared(lb)]
+    lb.lowbit_debug_inject_stall(True)
+    try:
+        out, lse = pr.shared(lb)
+    finally:
+        lb.lowbit_debug_inject_stall(False)
+    assert lb.lowbit_device_error() == TIMEOUT
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all()), "a timed-out call wrote outputs"
+    assert all(torch.equal(x, y) for x, y in zip(pr.shared(lb), want)) and lb.lowbit_device_error() == 0
+
+
 def test_rows_of_nobody_are_left_alone(lb):  # noqa: F811
     pr = Shared(9, [0, 2], [100], [2, 3], [4, 5], 4, 2, 64, 16)
     wide = torch.cat([pr.q, pr.q])            # rows past cu_q[B], as captured graphs have them
