@@ -219,10 +219,16 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   // On the warp-level MMA, whose items have 64 rows at most, from 50 on (heads of 256, 16 requests behind 6,000
   // keys, 64 rows each 89 / 82, 32 rows 54 / 55).
   const long long all = (long long)a.p.T * a.shape.G, shared_rows = (all + groups - 1) / groups, own_rows = (all + B - 1) / B;
+  // Short requests are as quick on their own, too.  Their lengths the host knows a bound of, the block table's: us with one
+  // row tile shared / on their own, bf16, 100 keys each behind 256, 1,024 and 2,048: 8 of four rows 12 / 8, 14 / 10, 16 / 12, 32
+  // 22 / 12, 24 / 18, 24 / 26, 128 45 / 26, 49 / 49, 50 / 82; 16 of 64 rows 26 / 13, 29 / 24, 33 / 30, 128 115 / 64, 139 / 107,
+  // 173 / 164.
+  const long long reach = (long long)a.p.width << a.p.page_shift;
+  const bool brief = reach <= 1024 || (reach <= 2048 && (own_rows > 32 || B <= 16LL * groups));
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   cudaError_t e;
-  if (own_rows > (attention_tc_fits(a, D) ? 96 : 48)) {
+  if (brief || own_rows > (attention_tc_fits(a, D) ? 96 : 48)) {
     attention_config(&cfg, &attr, (std::max(B, groups) + 255) / 256, 256, 0, s);
     e = cudaLaunchKernelEx(&cfg, prefix_check_kernel, a);
     if (e == cudaSuccess) e = launch_attention(a, D, fp8, s);
@@ -236,7 +242,6 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   // behind 4,000, 64 of 32 rows 168 / 167 and 122 / 98 (behind 6,000); over e4m3, 128 of 16 rows 194 / 213 behind 10,000, 136 /
   // 140 behind 6,000, 64 of 32 rows 187 / 198 behind 16,000, 125 / 121 behind 6,000.
   const Kind own_kind = kind_of(a, D, own_rows, 1024);
-  const long long reach = (long long)a.p.width << a.p.page_shift;
   const bool tall = shared_rows > 600 && (own_kind >= kTc128 ? reach > 8192
                                           : fp8             ? own_rows <= 16 || reach > 8192
                                                             : all * reach > 1 << 25);

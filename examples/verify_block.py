@@ -48,7 +48,8 @@ class Answers:
         self.cache = lb.lowbit_paged_cache(k, v)
         i32 = dict(dtype=torch.int32, device="cuda")
         own = whole + torch.arange(batch * (per - whole), **i32).view(batch, per - whole)
-        self.block_table = torch.cat([torch.arange(whole, **i32).expand(batch, whole), own], 1).contiguous()
+        room = torch.zeros((batch, 4096 // PAGE), **i32)  # columns for longer answers, as a server's table has
+        self.block_table = torch.cat([torch.arange(whole, **i32).expand(batch, whole), own, room], 1).contiguous()
         self.prompt, self.batch, self.drafts, self.gen = whole * PAGE, batch, drafts, gen
         self.kv_lens = torch.full((batch,), self.prompt, **i32)
         self.last = torch.zeros(batch, **i32)

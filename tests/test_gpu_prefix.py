@@ -18,9 +18,10 @@ TIMEOUT = 5
 
 class Shared(Problem):
     """Requests in groups; bounds [groups + 1], prefix [groups]; own: keys of a request that are neither new nor
-    shared (None: an idle request whose table row is no page).  Slots that nobody uses hold NaN."""
+    shared (None: an idle request whose table row is no page).  The table has room for `room` keys a request: under short
+    ones the plain call's kernels do the work.  Slots that nobody uses hold NaN."""
 
-    def __init__(self, seed, bounds, prefix, new, own, Hq, Hk, D, page, fp8=False, order="token", qscale=1.0):
+    def __init__(self, seed, bounds, prefix, new, own, Hq, Hk, D, page, fp8=False, order="token", qscale=1.0, room=2304):
         g = np.random.default_rng(seed)
         B, T = len(new), int(sum(new))
         self.new, self.Hq, self.Hk, self.D, self.page, self.fp8, self.B, self.T = new, Hq, Hk, D, page, fp8, B, T
@@ -31,7 +32,7 @@ class Shared(Problem):
         need = [-(-x // page) for x in kv]
         pages = sum(whole) + sum(max(0, n - whole[c]) for n, c in zip(need, group)) + 2
         ids = g.permutation(pages)
-        width = max(need) + 1
+        width = max(max(need) + 1, room // page)
         table = np.full((B, width), -7, dtype=np.int64)
         live = np.zeros((pages, page), dtype=bool)
         at, common = 0, []
@@ -118,6 +119,18 @@ def test_parity(lb, i, fp8, causal, order):  # noqa: F811
         pytest.skip("pages below 128 bytes are refused")
     pr = Shared(50 + i, bounds, prefix, new, own, Hq, Hk, D, page, fp8, order)
     pr.check(*pr.shared(lb, causal=causal), causal=causal)
+    assert lb.lowbit_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("room", [0, 1024, 2048])
+def test_short_tables(lb, i, fp8, room):  # noqa: F811
+    bounds, prefix, new, own, Hq, Hk, D, page = SHAPES[i]
+    if fp8 and page * D < 128:
+        pytest.skip("pages below 128 bytes are refused")
+    pr = Shared(50 + i, bounds, prefix, new, own, Hq, Hk, D, page, fp8, room=room)
+    pr.check(*pr.shared(lb))
     assert lb.lowbit_device_error() == 0
 
 
