@@ -514,15 +514,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if constexpr (kState) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   int of = m;  // where its settings are
-  if constexpr (kState) {
-    if (tid == 0) s.found = a.B;
-    __syncthreads();
-    for (int b = tid; b < a.B; b += kThreads) {
+  if constexpr (kState) {  // the first request that the row is of
+    auto has = [&](int b) {
       const int c0 = a.cu_drafts[b], c1 = a.cu_drafts[b + 1];
-      if (request_fits(b, c0, c1, a.N, a.rows) && m >= c0 + a.extra * b && m < c1 + a.extra * (b + 1)) atomicMin(&s.found, b);
+      return request_fits(b, c0, c1, a.N, a.rows) && m >= c0 + a.extra * b && m < c1 + a.extra * (b + 1);
+    };
+    of = a.B;
+    if (a.B <= 128) {  // every warp for itself
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.B && of == a.B; b0 += 32) {
+        const uint32_t here = __ballot_sync(~0u, b0 + lane < a.B && has(b0 + lane));
+        if (here) of = b0 + __ffs(here) - 1;
+      }
+    } else {
+      if (tid == 0) s.found = a.B;
+      __syncthreads();
+      for (int b = tid; b < a.B; b += kThreads)
+        if (has(b)) atomicMin(&s.found, b);
+      __syncthreads();
+      of = s.found;
     }
-    __syncthreads();
-    of = s.found;
     if (of == a.B) {  // the whole cluster agrees
       cluster_wait();
       return;

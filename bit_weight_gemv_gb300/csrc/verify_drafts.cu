@@ -90,7 +90,7 @@ struct VerifyShared {
   u64 aim;
   RowState p, q;  // of the rows that the next token comes from
   float ip, iq;
-  int first;
+  int first, refused;  // the first draft that is not accepted, and its token
 };
 
 template <bool BF16, bool DRAFT_BF16>
@@ -125,6 +125,11 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     if (g.col >= 0) g.y = logit_at(draft_rows + (long long)r * a.draft_stride * kDraftSize, DRAFT_BF16, g.col);
     return g;
   };
+  // (asked for together; the last thread has the state of the row behind all drafts)
+  const float v = a.v[b];
+  RowState p_seen = {}, q_seen = {};
+  if (fits && (tid < n || tid == kDrawThreads - 1)) p_seen = a.target[c0 + b + min(tid, n)];
+  if (tid < n && draft_rows) q_seen = a.draft[c0 + tid];
   Judged mine = {};
   if (tid < n) mine = look(tid);
   __syncthreads();
@@ -137,21 +142,17 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     return;
   }
 
-  // ---- which drafts are accepted; a thread keeps the states that it has seen, and the last one those of the row
-  // behind all drafts
-  RowState p_seen = {}, q_seen = {};
-  if (tid == kDrawThreads - 1) p_seen = a.target[c1 + b];
+  // ---- which drafts are accepted
   for (int i = tid; i < n; i += kDrawThreads) {
     const Judged g = i == tid ? mine : look(i);
     const int r = c0 + i;
-    const RowState p = a.target[r + b];
+    const RowState p = i == tid ? p_seen : a.target[r + b];
     double share = 0.0, given = draft_rows ? 0.0 : 1.0;
     if (g.d >= 0 && g.d < a.V && p.total) share = (double)mass_of(Kept(p).weight(g.z, g.d)) / (double)p.total;
     if (g.col >= 0) {
-      const RowState q = a.draft[r];
+      const RowState q = i == tid ? q_seen : a.draft[r];
       if (q.total) given = (double)mass_of(Kept(q).weight(g.y, g.col)) / (double)q.total;
     }
-    if (n < kDrawThreads) p_seen = p, q_seen = draft_rows ? a.draft[r] : RowState{};
     const float u = g.u >= 0.0f ? fminf(g.u, 1.0f) : 0.0f;
     if (!((double)u * given < share)) atomicMin(&s.first, i);
     if (rank == 0 && a.accept) a.accept[r] = given > 0.0 ? (float)fmin(share / given, 1.0) : (share > 0.0 ? 1.0f : 0.0f);
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
   if (n >= kDrawThreads && tid == 0) {
     p_seen = a.target[t];
     q_seen = rejected && draft_rows ? a.draft[c0 + j] : RowState{};
+    mine.d = rejected ? a.drafts[c0 + j] : -1;
   }
   if (warp == who >> 5) {
     const u64 sp = __shfl_sync(~0u, p_seen.total, who & 31), sq = __shfl_sync(~0u, q_seen.total, who & 31);
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     const float x = total ? (float)(0x1p40 / (double)total) : 0.0f;
     if (lane == 0) s.ip = x;
     if (lane == 1) s.iq = x;
-    if (lane == (who & 31)) s.p = p_seen, s.q = q_seen;
+    if (lane == (who & 31)) s.p = p_seen, s.q = q_seen, s.refused = mine.d;
   }
   __syncthreads();
   const RowState p = s.p, q = s.q;
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     cluster_wait();
     return;
   }
-  const int out = rejected && !draft_rows ? a.drafts[c0 + j] : -1;  // proposed with certainty
+  const int out = rejected && !draft_rows ? s.refused : -1;  // proposed with certainty
   const float ip = s.ip, iq = s.iq;
   const uint8_t* const draft_row = draft_rows + (long long)(c0 + j) * a.draft_stride * kDraftSize;
   const Kept by_p(p), by_q(q);
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     __syncthreads();
     if (warp == 0) {
       const u64 all = warp_sum(s.warp_mass[lane]);
-      const u64 aim = aim_of(a.v[b], all);
+      const u64 aim = aim_of(v, all);
       if (lane == 0) s.aim = aim;
     }
     __syncthreads();
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
     differ = false;
   }
   if (warp == 0) {
-    const u64 at = aim_of(a.v[b], total);
+    const u64 at = aim_of(v, total);
     if (lane == 0) s.aim = at;
   }
   __syncthreads();
