@@ -22,9 +22,9 @@
 //      walks the segments that the warps own.  (A step with more than 2048 tokens, such as a row of
 //      equal logits, is narrowed down by its keys' digits.)
 //
-// Few rows wait on latency: one row of 248,320 takes 14.9 us with top-k 20 and top-p 0.95, of which the
+// Few rows wait on latency: one row of 248,320 takes 14.6 us with top-k 20 and top-p 0.95, of which the
 // merges and exchanges over 16 CTAs take 9, and 9.7 us without truncation.  Many rows are bound by
-// instructions, about 30 for each weight that is summed: 192 rows of mixed settings take 129 us, 28
+// instructions, about 30 for each weight that is summed: 192 rows of mixed settings take 124 us, 28
 // of them for reading the logits once at the copy rate.
 #pragma once
 
