@@ -1,6 +1,6 @@
 // Attention over a paged cache on the fifth-generation tensor cores, for many query rows per
 // key/value head (prompt chunks, verify blocks of grouped heads).  Same mathematics and schedule
-// as attn_mma_kernel (see paged_attn.cu and paged.cuh).
+// as attn_mma_kernel (see paged_attn_mma.cuh and paged.cuh).
 //
 // One CTA per SM, two "slots" of 128 query rows that keep the tensor pipe busy in turn:
 //   warps 0-3, 4-7 -- softmax of slot 0 and 1, one thread per row: read the row's 128 scores from
