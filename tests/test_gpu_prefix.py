@@ -242,6 +242,22 @@ def test_stall_with_tall_items(lb, fp8, B, new, width):  # noqa: F811
     assert all(torch.equal(x, y) for x, y in zip(pr.shared(lb), want)) and lb.lowbit_device_error() == 0
 
 
+def test_calls_at_the_same_time(lb):  # noqa: F811
+    """Two batches on two streams, a workspace each, over and over: the bits of either alone."""
+    batches = [tall(15, False, 40, 16, 600, 700), tall(16, True, 160, 1, 40, 500)]
+    want = [[t.clone() for t in pr.shared(lb)] for pr in batches]
+    args, streams = [pr.args(lb) for pr in batches], [torch.cuda.Stream() for _ in batches]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for a, s in zip(args, streams):
+            lb.lowbit_prefix_attention(**a, stream=s)
+    torch.cuda.synchronize()
+    for pr, w in zip(batches, want):
+        assert torch.equal(pr.out[:pr.T], w[0]) and torch.equal(pr.ls[:pr.T], w[1])
+    assert lb.lowbit_device_error() == 0
+
+
 def test_rows_of_nobody_are_left_alone(lb):  # noqa: F811
     pr = Shared(9, [0, 2], [100], [2, 3], [4, 5], 4, 2, 64, 16)
     wide = torch.cat([pr.q, pr.q])            # rows past cu_q[B], as captured graphs have them
