@@ -73,19 +73,8 @@ constexpr bool kPrefix = std::is_same<A, PrefixArgs>::value;
 __device__ __forceinline__ Request load_request(const AttnArgs& a, int b) {
   return check_request(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.kv_lens[b]);
 }
-// All rows of group g over the whole pages of its shared length; no rows where there are none.
-__device__ __forceinline__ Request load_group(const PrefixArgs& a, int g) {
-  const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
-  if (from < 0 || to < from || to > a.requests || len < 0) {
-    record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
-    return Request{0, 0, 0, 0, 1};
-  }
-  Request r = check_request(a.p, a.p.cu_q[from], a.p.cu_q[to], len & ~a.p.page_mask);
-  r.all = 1;
-  if (r.kv == 0) r.n = 0;
-  return r;
-}
-// The last group that begins at request b or before it.
+// The last group that begins at request b or before it, by bisection.  Every kernel of a call looks a request's group up
+// with it, so that all agree where cu_groups is not ascending.
 __device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
   int g = 0;
 #pragma unroll 1
@@ -95,6 +84,21 @@ __device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
     else end = mid;
   }
   return g;
+}
+// All rows of group g over the whole pages of its shared length; no rows where there are none.  A group that group_of does
+// not give for all of its requests counts as inconsistent: the requests that a bisection ends at one place for lie
+// side by side, so it is enough to ask for the first and the last, and no two groups have a request in common.
+__device__ __forceinline__ Request load_group(const PrefixArgs& a, int g) {
+  const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
+  if (from < 0 || to < from || to > a.requests || len < 0 ||
+      (to > from && (group_of(a, from) != g || group_of(a, to - 1) != g))) {
+    record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
+    return Request{0, 0, 0, 0, 1};
+  }
+  Request r = check_request(a.p, a.p.cu_q[from], a.p.cu_q[to], len & ~a.p.page_mask);
+  r.all = 1;
+  if (r.kv == 0) r.n = 0;
+  return r;
 }
 // Request b, of group g, without the keys that the group shares.  One that has new tokens among these counts as inconsistent;
 // what else can be wrong with it the join step looks for, which keeps its loads out of the way here.

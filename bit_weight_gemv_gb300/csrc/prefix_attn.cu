@@ -59,7 +59,7 @@ prefix_join_kernel(const __grid_constant__ PrefixArgs a, const float* own_o, con
   const int4 f1 = a.found[a.rows + row];
   // the last request that begins at row t or before it
   const int b = last_not_above(a.p.cu_q, a.requests, t, lane);
-  const int g = last_not_above(a.cu_groups, a.groups, b, lane);
+  const int g = group_of(a, b);
   Request own;
   if (a.p.cu_q[b] > t || t >= a.p.cu_q[b + 1] || !request_of_group(a, b, g, &own)) return;
   if (!own.skip) f0.x = kInBase;
