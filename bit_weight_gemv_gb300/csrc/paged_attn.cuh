@@ -32,6 +32,7 @@ struct CutItem {
   int row0, h, pad0, pad1;   // the request's first row, the key/value head
 };
 constexpr int kMaxCtas = kMaxPieceRows / 2 / 16;
+static_assert(kMaxCtas < 1 << 16);
 
 struct AttnArgs {
   PagedArgs p;
@@ -63,8 +64,9 @@ struct PrefixArgs : AttnArgs {
   long long rows;   // rows of out, T * Hq; of the arrays below first the shared part's, then the own part's
   float* base_o;    // [2][row][D]: rows that one CTA saw all keys of
   float2* base_ml;  // [2][row]
-  int4* found;      // [2][row]: {kInBase or kLost}, or {more, first, next, apart}: places of the first piece and of
-                    // the `more` that follow it, the second at `next` and the others `apart` behind one another
+  int4* found;      // [2][row]: {kInBase or kLost, 0, 0, entry}, or {more + (log2 rows << 16), first, next, entry}:
+                    // places of the first piece and of the `more` that follow it, the second at `next` and the others
+                    // two items' rows behind one another.  `entry`: the group, or the request, that the row was computed for
 };
 constexpr int kInBase = -1, kLost = -2;
 template <class A>
@@ -371,11 +373,12 @@ __device__ __forceinline__ Part part_of(const PrefixArgs& a, const Walk& w, bool
 __device__ __forceinline__ void say_found(const AttnArgs&, const Walk&, long long, bool, int, int, long long, long long) {}
 __device__ __forceinline__ void say_found(const PrefixArgs& a, const Walk& w, long long row, bool good, int done, int in_tile,
                                           long long chunk, long long piece) {
-  if (a.first + w.b >= a.groups) row += a.rows;
-  int4 f = make_int4(good ? kInBase : kLost, 0, 0, 0);
-  if (good && done < w.tiles)
-    f = make_int4((int)quotient(w.tiles - done + chunk - 1, chunk), (int)piece,
-                  (2 * ((int)blockIdx.x + 1) << a.shape.r_shift) + in_tile, 2 << a.shape.r_shift);
+  int entry = a.first + w.b;
+  if (entry >= a.groups) entry -= a.groups, row += a.rows;
+  int4 f = make_int4(good ? kInBase : kLost, 0, 0, entry);
+  if (good && done < w.tiles)  // a grid has kMaxCtas at most, so that 16 bits hold `more`
+    f = make_int4((int)quotient(w.tiles - done + chunk - 1, chunk) + (a.shape.r_shift << 16), (int)piece,
+                  (2 * ((int)blockIdx.x + 1) << a.shape.r_shift) + in_tile, entry);
   a.found[row] = f;
 }
 
