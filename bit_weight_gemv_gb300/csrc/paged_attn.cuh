@@ -32,7 +32,6 @@ struct CutItem {
   int row0, h, pad0, pad1;   // the request's first row, the key/value head
 };
 constexpr int kMaxCtas = kMaxPieceRows / 2 / 16;
-static_assert(kMaxCtas < 1 << 16);
 
 struct AttnArgs {
   PagedArgs p;
@@ -64,9 +63,8 @@ struct PrefixArgs : AttnArgs {
   long long rows;   // rows of out, T * Hq; of the arrays below first the shared part's, then the own part's
   float* base_o;    // [2][row][D]: rows that one CTA saw all keys of
   float2* base_ml;  // [2][row]
-  int4* found;      // [2][row]: {kInBase or kLost, 0, 0, entry}, or {more + (log2 rows << 16), first, next, entry}:
-                    // places of the first piece and of the `more` that follow it, the second at `next` and the others
-                    // two items' rows behind one another.  `entry`: the group, or the request, that the row was computed for
+  int4* found;      // [2][row]: {kInBase or kLost}, or {more, first, next, apart}: places of the first piece and of
+                    // the `more` that follow it, the second at `next` and the others `apart` behind one another
 };
 constexpr int kInBase = -1, kLost = -2;
 template <class A>
@@ -87,13 +85,10 @@ __device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
   }
   return g;
 }
-// All rows of group g over the whole pages of its shared length; no rows where there are none.  A group that group_of does
-// not give for all of its requests counts as inconsistent: the requests that a bisection ends at one place for lie
-// side by side, so it is enough to ask for the first and the last, and no two groups have a request in common.
+// All rows of group g over the whole pages of its shared length; no rows where there are none.
 __device__ __forceinline__ Request load_group(const PrefixArgs& a, int g) {
   const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
-  if (from < 0 || to < from || to > a.requests || len < 0 ||
-      (to > from && (group_of(a, from) != g || group_of(a, to - 1) != g))) {
+  if (from < 0 || to < from || to > a.requests || len < 0) {
     record_error(a.p.err, LOWBIT_ERR_INVALID_ARG);
     return Request{0, 0, 0, 0, 1};
   }
@@ -373,12 +368,11 @@ __device__ __forceinline__ Part part_of(const PrefixArgs& a, const Walk& w, bool
 __device__ __forceinline__ void say_found(const AttnArgs&, const Walk&, long long, bool, int, int, long long, long long) {}
 __device__ __forceinline__ void say_found(const PrefixArgs& a, const Walk& w, long long row, bool good, int done, int in_tile,
                                           long long chunk, long long piece) {
-  int entry = a.first + w.b;
-  if (entry >= a.groups) entry -= a.groups, row += a.rows;
-  int4 f = make_int4(good ? kInBase : kLost, 0, 0, entry);
-  if (good && done < w.tiles)  // a grid has kMaxCtas at most, so that 16 bits hold `more`
-    f = make_int4((int)quotient(w.tiles - done + chunk - 1, chunk) + (a.shape.r_shift << 16), (int)piece,
-                  (2 * ((int)blockIdx.x + 1) << a.shape.r_shift) + in_tile, entry);
+  if (a.first + w.b >= a.groups) row += a.rows;
+  int4 f = make_int4(good ? kInBase : kLost, 0, 0, 0);
+  if (good && done < w.tiles)
+    f = make_int4((int)quotient(w.tiles - done + chunk - 1, chunk), (int)piece,
+                  (2 * ((int)blockIdx.x + 1) << a.shape.r_shift) + in_tile, 2 << a.shape.r_shift);
   a.found[row] = f;
 }
 

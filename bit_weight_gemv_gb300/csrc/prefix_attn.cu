@@ -14,6 +14,20 @@ namespace {
 
 constexpr int kPrefixJoinWarps = 8;
 
+// The last of x[0..n), ascending, that is not above v, or 0: by a warp, so that it takes a round trip for
+// every factor of 32 in n.
+__device__ __forceinline__ int last_not_above(const int32_t* x, int n, int v, int lane) {
+  int at = 0;
+#pragma unroll 1
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const uint32_t in = __ballot_sync(~0u, lane * step < n && x[at + min(lane * step, n - 1)] <= v);
+    const int k = in ? 31 - __clz(in) : 0;
+    at += k * step;
+    n = min(step, n - k * step);
+  }
+  return at;
+}
 // Request b with its group g as the header asks for them: inside the group's bounds and rows, and with what it
 // shares computed.  False, and recorded, if not.
 __device__ __forceinline__ bool request_of_group(const PrefixArgs& a, int b, int g, Request* own) {
@@ -29,12 +43,30 @@ __device__ __forceinline__ bool request_of_group(const PrefixArgs& a, int b, int
   return true;
 }
 
-// A warp joins a row's pieces: of the shared part, then of its own.  Which request the row is of, the attention of its
-// own part has said beside where its pieces are (a search in cu_q would have to know that it is ascending).  For a row
-// that no request computed it says what the workspace held before, and a request that does not have the row, or is not
-// consistent, fails the checks; one that passes them was computed, and has said so.  Bound by round trips: where the
-// pieces are; the row's request and group; the pieces' statistics; the pieces.  Alone and cold 12 us for 256 rows, 26 for
-// 20,992 (36 MB).
+// The keys that row t shares where it is request b's, or -1 where it is not, or the request is not consistent.
+__device__ __forceinline__ int shared_keys(const PrefixArgs& a, int b, int t) {
+  Request own;
+  if (a.p.cu_q[b] > t || t >= a.p.cu_q[b + 1] || !request_of_group(a, b, group_of(a, b), &own)) return -1;
+  return own.skip;
+}
+// The same for whichever request has the row, -1 where none does: by a warp.  The search finds it where cu_q is
+// ascending.  Offsets out of order hide consistent requests from it, so a row without one is asked of all requests, but
+// for rows past cu_q[B], the padding of a captured graph, which are nobody's (asked as well they took 4,096 requests of a
+// token and as many such rows from 231 to 355 us).
+__device__ __forceinline__ int shared_keys_of_row(const PrefixArgs& a, int t, int lane) {
+  int skip = shared_keys(a, last_not_above(a.p.cu_q, a.requests, t, lane), t);
+  if (skip >= 0 || t >= a.p.cu_q[a.requests]) return skip;
+#pragma unroll 1
+  for (int b0 = 0; skip < 0 && b0 < a.requests; b0 += 32) {
+    const int b = b0 + lane, from = b < a.requests ? a.p.cu_q[b] : 0, to = b < a.requests ? a.p.cu_q[b + 1] : 0;
+    const uint32_t has = __ballot_sync(~0u, from >= 0 && from <= t && t < to && to <= a.p.T);
+    if (has) skip = shared_keys(a, b0 + __ffs(has) - 1, t);
+  }
+  return skip;
+}
+
+// A warp joins a row's pieces: of the shared part, then of its own.  Bound by round trips: where they are and, meanwhile,
+// the row's request and group; their statistics; the pieces.  Alone and cold 12 us for 256 rows, 26 for 20,992 (36 MB).
 // (Looking the request up before the wait would take 1 us off, but what earlier kernels wrote is promised to be seen
 // only behind it.)
 template <int D>
@@ -47,13 +79,11 @@ prefix_join_kernel(const __grid_constant__ PrefixArgs a, const float* own_o, con
   const long long row = (long long)t * a.Hq + h;
   int4 f0 = a.found[row];  // read only where the request shares anything
   const int4 f1 = a.found[a.rows + row];
-  const int b = f1.w;
-  Request own;
-  if (b < 0 || b >= a.requests || a.p.cu_q[b] > t || t >= a.p.cu_q[b + 1] || !request_of_group(a, b, group_of(a, b), &own)) return;
-  if (!own.skip) f0.x = kInBase;
+  const int skip = shared_keys_of_row(a, t, lane);
+  if (skip < 0) return;
+  if (!skip) f0.x = kInBase;
   if (f0.x == kLost || f1.x == kLost) return;
-  auto pieces = [](int4 f) { return f.x == kInBase ? 1 : (f.x & 0xFFFF) + 1; };
-  const int n0 = own.skip ? pieces(f0) : 0, n = n0 + pieces(f1);
+  const int n0 = skip ? max(f0.x, 0) + 1 : 0, n = n0 + max(f1.x, 0) + 1;
   // where piece i is
   auto locate = [&](int i, const float2*& ml, const float*& o) {
     const bool second = i >= n0;
@@ -63,7 +93,7 @@ prefix_join_kernel(const __grid_constant__ PrefixArgs a, const float* own_o, con
       const long long place = row + (second ? a.rows : 0);
       ml = a.base_ml + place, o = a.base_o + place * D;
     } else {
-      long long place = k ? (long long)f.z + ((long long)(k - 1) * 2 << (f.x >> 16 & 15)) : f.y;
+      long long place = k ? (long long)f.z + (long long)(k - 1) * f.w : f.y;
       place = min(max(place, 0LL), (long long)kMaxPieceRows - 1);
       ml = (second ? own_ml : a.piece_ml) + place, o = (second ? own_o : a.piece_o) + place * D;
     }
