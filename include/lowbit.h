@@ -458,7 +458,7 @@ size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int
  * arrays describe inconsistently is recorded in the device error word; its rows are not written, or (where only
  * what it shares is at fault) attend to the request's own block table.  Groups are looked up by bisection: where
  * cu_groups is not ascending, other groups may be left out with the one at fault.  What a row gets that several
- * requests claim (cu_q not ascending) is not defined.  Pages are compared by nobody: where the
+ * requests claim (cu_q not ascending), or a request that several groups claim, is not defined.  Pages are compared by nobody: where the
  * table rows of a group differ in the shared pages, it is not defined which of them a request sees.
  * Worth it where many requests with few rows each share much (16 requests of one token and more behind
  * thousands of keys).  From about 100 rows a request on (tokens times query heads per key/value head), and
