@@ -275,8 +275,9 @@ kv_append_norm_kernel(const __grid_constant__ AppendArgs a) {
         for (int i = 0; i < 8; i += 4) {
           const float4 wa = __ldg(reinterpret_cast<const float4*>(weight + ia + i));
           const float4 wb = __ldg(reinterpret_cast<const float4*>(weight + ib + i));
-          x[i] *= r * wa.x, x[i + 1] *= r * wa.y, x[i + 2] *= r * wa.z, x[i + 3] *= r * wa.w;
-          y[i] *= r * wb.x, y[i + 1] *= r * wb.y, y[i + 2] *= r * wb.z, y[i + 3] *= r * wb.w;
+          // (x r first, which is at most sqrt(D): r w may be out of range where x r w is not)
+          x[i] = x[i] * r * wa.x, x[i + 1] = x[i + 1] * r * wa.y, x[i + 2] = x[i + 2] * r * wa.z, x[i + 3] = x[i + 3] * r * wa.w;
+          y[i] = y[i] * r * wb.x, y[i + 1] = y[i + 1] * r * wb.y, y[i + 2] = y[i + 2] * r * wb.z, y[i + 3] = y[i + 3] * r * wb.w;
         }
       }
       if (turned && w.kind != 2) turn8<INTER>(x, y, c, sn);
