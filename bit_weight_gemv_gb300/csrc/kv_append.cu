@@ -265,12 +265,25 @@ kv_append_norm_kernel(const __grid_constant__ AppendArgs a) {
       unpack8(vb[e], y);
       const float* weight = w.kind == 0 ? a.q_weight : (w.kind == 1 ? a.k_weight : nullptr);
       if (weight) {
-        float sum = 0.0f;
+        auto mean_square = [&](float eps) {
+          float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
+          for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
 #pragma unroll
-        for (int o = kPer / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        const float r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
+          for (int o = kPer / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          return fmaf(sum, 1.0f / D, eps);
+        };
+        float mean = mean_square(a.eps);
+        // Near the end of fp32's range squares lose their bits, and the mean does: such a head (elements up to 2^-41, so
+        // that its squares stay finite) is multiplied by 2^100, which is exact, and eps by the square of that.
+        const bool small = mean < 0x1p-90f;
+        if (__any_sync(~0u, small)) {
+          const float up = small ? 0x1p100f : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= up, y[i] *= up;
+          mean = mean_square(a.eps * up * up);
+        }
+        const float r = rsqrtf(mean);
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           const float4 wa = __ldg(reinterpret_cast<const float4*>(weight + ia + i));

@@ -49,3 +49,26 @@ def test_weights_far_from_one(lb, x_scale, w_scale, T, D):  # noqa: F811
     """The reciprocal root and the weight are in range, and so is the result; their product is not."""
     x, w = heads(T, D)
     check(lb, x * 2.0 ** x_scale, w * 2.0 ** w_scale, 0.0)
+
+
+@pytest.mark.parametrize("T,D", SIZES)
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 1e-38, 2.0 ** -95, 2.0 ** -89])
+@pytest.mark.parametrize("scale", [-41, -46, -60, -64, -75, -100, -126])
+def test_heads_whose_squares_leave_fp32(lb, scale, eps, T, D):  # noqa: F811
+    """Elements are exact in bf16 down to 2^-133: those of a scale below 2^-120 are rounded to it before the oracle sees them."""
+    x, w = heads(T, D, 1)
+    x = x.float() * 2.0 ** scale
+    if T > 2:
+        x[1] *= 2.0 ** 30                     # an ordinary head beside a small one
+    x = x.to(torch.bfloat16)
+    check(lb, x, w, eps)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("e", [-60, -63, -70, -73, -75, -90, -120, -133])
+def test_a_head_with_one_small_element(lb, e, D):  # noqa: F811
+    x = torch.zeros((4, 1, D), device="cuda")
+    x[0, 0, 5] = x[2, 0, D - 1] = 2.0 ** e
+    x[1] = 1.0
+    x[3, 0, 7], x[3, 0, 8] = 2.0 ** e, 3.0
+    check(lb, x.to(torch.bfloat16), torch.ones(D, device="cuda"), 0.0)
