@@ -398,7 +398,8 @@ lowbit_status lowbit_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  *       is NULL where q is).  Values are never normalised.
  *   eps : finite, >= 0; with 0, a head of zeros becomes NaN.
  *   The squares are summed in fp32, so a head whose sum of squares passes 3.4e38 (elements past 2^60) becomes
- *   zeros, or NaN where it holds an infinity.  All else is as in lowbit_kv_append. */
+ *   zeros, or NaN where it holds an infinity.  Rows of nobody may be read here, whatever they hold, but reach nothing.
+ *   All else is as in lowbit_kv_append. */
 lowbit_status lowbit_kv_append_norm(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                                     int64_t k_stride, const uint16_t* v, int64_t v_stride, int Hq,
                                     const float* q_weight, const float* k_weight, float eps,
