@@ -167,6 +167,9 @@ __global__ void __launch_bounds__(256) prefix_check_kernel(const __grid_constant
   if (i < a.requests) request_of_group(a, i, group_of(a, i), &own);
 }
 
+// Rows a request, on average, up to which a request's own part is computed apart (measured below).
+constexpr long long kOwnRowsTc = 96, kOwnRowsMma = 48;
+
 // The kernels by rows an item.
 enum Kind { kRow8, kMma16, kMma32, kMma64, kTc128, kTc256 };
 Kind kind_of(const AttnArgs& a, int D, long long rows, long long pair) {
@@ -196,7 +199,10 @@ extern "C" {
 
 size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D) {
   if (lowbit_paged_attention_workspace_bytes(T, B, Hq, Hk, D) == 0) return 0;
-  return 2 * pieces_bytes(D) + (size_t)T * (size_t)Hq * 2 * ((size_t)(D + 2) * sizeof(float) + sizeof(int4));
+  // Calls of more rows a request leave none to the join; those of fewer rows or requests need no more than this.
+  const long long most = (D <= 128 ? kOwnRowsTc : kOwnRowsMma) * B * Hk;
+  const size_t rows = (size_t)std::min((long long)T * Hq, most);
+  return 2 * pieces_bytes(D) + rows * 2 * ((size_t)(D + 2) * sizeof(float) + sizeof(int4));
 }
 
 lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int Hq, const lowbit_paged_batch* batch,
@@ -247,7 +253,7 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   cudaError_t e;
-  if (brief || own_rows > (attention_tc_fits(a, D) ? 96 : 48)) {
+  if (brief || own_rows > (attention_tc_fits(a, D) ? kOwnRowsTc : kOwnRowsMma)) {
     attention_config(&cfg, &attr, (std::max(B, groups) + 255) / 256, 256, 0, s);
     e = cudaLaunchKernelEx(&cfg, prefix_check_kernel, a);
     if (e == cudaSuccess) e = launch_attention(a, D, fp8, s);

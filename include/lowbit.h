@@ -439,7 +439,7 @@ lowbit_status lowbit_paged_attention(const uint16_t* q, int64_t q_stride, int Hq
 
 /* Bytes of lowbit_prefix_attention's workspace for up to T rows and B requests of Hq query and Hk
  * key/value heads of D (0 for invalid shapes): twice lowbit_paged_attention's, and 8 D + 48 for each row
- * and query head. */
+ * and query head, up to 96 (heads of 256: 48) for each request and key/value head. */
 size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int D);
 
 /* lowbit_paged_attention (without a window) for requests whose first pages are the same ones: a long system
