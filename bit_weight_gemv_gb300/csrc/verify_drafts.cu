@@ -419,7 +419,7 @@ struct Span {
 };
 bool meet(const Span& x, const Span& y) {
   const __int128 a = (__int128)(uintptr_t)x.at, b = (__int128)(uintptr_t)y.at;
-  return x.at && y.at && a < b + y.bytes && b < a + x.bytes;
+  return x.at && y.at && x.bytes && y.bytes && a < b + y.bytes && b < a + x.bytes;
 }
 bool known(int dtype) { return dtype == LOWBIT_LOGITS_FP32 || dtype == LOWBIT_LOGITS_BF16; }
 
