@@ -53,7 +53,7 @@ struct SampleArgs {
   const void* logits;
   long long row_stride;
   int M, V, cluster;
-  int per_warp;   // elements of a warp's segment, a multiple of 128 (bf16: 256), or of 512 read from L2
+  int per_warp;   // elements of a warp's segment, a multiple of 128, or of 512 read from L2
   int aligned;    // every row starts on a 16-byte boundary
   const float* temperature;
   const int32_t* top_k;
@@ -177,7 +177,7 @@ struct Shared {
   u64 cand[kCap];                               // key << 32 | index: this CTA's, then in the first one all
   u64 warp_mass[kWarps], warp_tie[kWarps];
   uint32_t warp_count[kWarps], warp_ties[kWarps];
-  float warp_max[kWarps], rank_max[kMaxCluster];
+  float warp_max[kWarps], rank_max[kMaxCluster], rank_floor[kMaxCluster];
   u64 rank_mass[kMaxCluster], rank_tie[kMaxCluster], rank_total[kMaxCluster];
   uint32_t rank_count[kMaxCluster], rank_ties[kMaxCluster], rank_cand[kMaxCluster];
   // the bin that a search found, and what precedes it
@@ -185,6 +185,8 @@ struct Shared {
   uint32_t count_before, cut, stay;
   u64 mass_before, one;
 };
+extern __shared__ __align__(16) uint8_t smem[];  // Shared, then what the kernel keeps of the row
+__device__ __forceinline__ Shared& shared() { return *reinterpret_cast<Shared*>(smem); }
 
 __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -403,6 +405,141 @@ __device__ __noinline__ void sort_candidates(Shared& s, uint32_t n) {
   }
 }
 
+// The way of a row with a small top-k.  Every CTA lists its own k largest tokens and little more, by a bound from its own
+// lanes' maxima, in the first CTA's memory, and says what k of its tokens are not below.  s.warp_max holds the warps' maxima;
+// the CTA's is returned.
+template <bool BF16, bool HELD>
+__device__ __forceinline__ float list_largest(const Slice<BF16, HELD> z_of, float lane_max, float steps, uint32_t k, int seg_from,
+                                           int seg_to, int index0, int rank, int C) {
+  Shared& s = shared();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t room = kCap / C;  // of the first CTA's list, for each CTA
+  u64* const own_list = reinterpret_cast<u64*>(s.count);  // the histogram's place, which this does without
+  constexpr uint32_t kOwnList = 3 * kBins * sizeof(uint32_t) / sizeof(u64);
+  for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
+  __syncthreads();
+  float top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  auto count_step = [&](float z) {
+    const int own = step_of(z, top, steps);
+    if (own < kBins - 1) atomicAdd(&s.all_count[own], 1u);
+  };
+  if (lane_max > -INFINITY) count_step(lane_max);
+  __syncthreads();
+  find_bin(s, false, k, 0);
+  // steps past the last hold no mass, whatever the other CTAs' largest
+  int bin = min(s.bin, kBins - 2);
+  const uint32_t lanes = s.count_before + (uint32_t)s.found;  // whose maxima are in these steps
+  __syncthreads();
+  if (tid == 0) s.found = 0;
+  __syncthreads();
+  const float low = top - (float)(bin + 2) / steps;
+  // In a row whose large tokens lie side by side (a vocabulary by frequency) a CTA's tokens may crowd into these steps.
+  // Most likely it has none of the k largest, and its list is not made.
+  uint32_t mine = kCap + 1;
+  if (lanes <= k + 8 + k / 8) {
+    auto list = [&](int i, float z) {
+      z = clean(z);
+      if (!(z >= low) || step_of(z, top, steps) > bin) return;
+      const uint32_t at = atomicAdd(&s.found, 1);
+      if (at < kOwnList) own_list[at] = ((u64)down_key(z) << 32) | (uint32_t)(index0 + i);
+    };
+    // Such tokens lie with lanes whose own maximum is one: where they are few and the row is read again, the warp looks
+    // through a lane's units together, one load for 32 of them, and the segment as a whole is not read.
+    uint32_t hits = __ballot_sync(~0u, top > -INFINITY && lane_max >= low);
+    if (HELD ? hits != 0 : __popc(hits) > 8) {
+      z_of.template each4<false>(seg_from, seg_to, [&](int i, float (&z)[4]) {
+        if (fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) list(i + e, z[e]);
+        }
+        return false;
+      });
+    } else if (!HELD) {
+      const int unit = BF16 && z_of.aligned ? 8 : 4;  // as the lanes took them for their maxima
+#pragma unroll 1
+      for (; hits; hits &= hits - 1) {
+        const int of_lane = seg_from + (__ffs(hits) - 1) * unit;
+#pragma unroll 1
+        for (int i = of_lane + lane * 32 * unit; i < seg_to; i += 1024 * unit) {
+          for (int g = 0; g < unit; g += 4) {
+            float z[4];
+            z_of.load4(i + g, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) list(i + g + e, z[e]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const uint32_t listed = (uint32_t)s.found;
+    mine = listed;
+    // A long list (the largest tokens are those that lie side by side) is cut down by a count of the tokens themselves.
+    const bool cut_down = listed > room && listed <= kOwnList && bin > 0;
+    if (cut_down) {
+      for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
+      __syncthreads();
+      for (uint32_t i = tid; i < listed; i += kThreads) count_step(key_logit((uint32_t)(own_list[i] >> 32)));
+      __syncthreads();
+      find_bin(s, false, k, 0);
+      bin = min(bin, s.bin);
+      mine = s.count_before + (uint32_t)s.found;
+      __syncthreads();
+      if (tid == 0) s.found = 0;
+      __syncthreads();
+    }
+    cluster_wait();
+    if (mine <= room) {
+      const uint32_t to = map_to_rank(smem_addr(s.cand + rank * room), 0);
+      for (uint32_t i = tid; i < listed; i += kThreads) {
+        const u64 c = own_list[i];
+        if (!cut_down) st_dsmem_u64(to + 8 * i, c);
+        else if (step_of(key_logit((uint32_t)(c >> 32)), top, steps) <= bin) st_dsmem_u64(to + 8 * atomicAdd(&s.found, 1), c);
+      }
+    }
+  } else {
+    cluster_wait();
+  }
+  if (warp == 0 && lane < C) {
+    st_dsmem_u32(map_to_rank(smem_addr(&s.rank_cand[rank]), lane), mine);
+    st_dsmem_f32(map_to_rank(smem_addr(&s.rank_floor[rank]), lane), mine >= k ? top - (float)(bin + 2) / steps : -INFINITY);
+  }
+  return top;
+}
+
+// The lists of list_largest in the first CTA: of them the k largest and what shares their last step, unsorted; their number.
+__device__ __forceinline__ uint32_t pick_largest(float top, float steps, uint32_t k, int C) {
+  Shared& s = shared();
+  constexpr int kOwn = kCap / kThreads;
+  const int tid = threadIdx.x;
+  const uint32_t room = kCap / C;
+  for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
+  __syncthreads();
+  u64 c[kOwn];
+  int step[kOwn];
+#pragma unroll
+  for (int e = 0; e < kOwn; ++e) {
+    const uint32_t i = tid + e * kThreads, r = i / room;
+    step[e] = kBins;
+    if (s.rank_cand[r] <= room && i - r * room < s.rank_cand[r]) {
+      c[e] = s.cand[i];
+      step[e] = step_of(key_logit((uint32_t)(c[e] >> 32)), top, steps);
+      if (step[e] < kBins - 1) atomicAdd(&s.all_count[step[e]], 1u);
+    }
+  }
+  __syncthreads();
+  find_bin(s, false, k, 0);
+  const int last = min(s.bin, kBins - 2);
+  __syncthreads();
+  if (tid == 0) s.found = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kOwn; ++e)
+    if (step[e] <= last) s.cand[atomicAdd(&s.found, 1)] = c[e];
+  __syncthreads();
+  return (uint32_t)s.found;
+}
+
 // The first CTA's end of a row: n sorted candidates, of which top-k, top-p and min-p keep a part;
 // then the draw in index order.
 template <class A>
@@ -506,8 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   constexpr bool kState = std::is_same<P, StatePair>::value;
   int block = blockIdx.x;
   const auto& a = part_of(all, block);
-  extern __shared__ __align__(16) uint8_t smem[];
-  Shared& s = *reinterpret_cast<Shared*>(smem);
+  Shared& s = shared();
   uint8_t* const store = smem + (sizeof(Shared) + 15) / 16 * 16;
   constexpr int kSize = BF16 ? 2 : 4;
   const int C = a.cluster, rank = block % C, m = block / C;
@@ -661,76 +797,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float lane_max = top;
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) s.warp_max[warp] = top;
-  clear_histogram(s);
-  for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
-  __syncthreads();
-  top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
 
-  // ---- top-k with a small k: every CTA's own k largest and little more, by a bound from its own lanes' maxima,
-  // go to the first CTA with its largest logit: one exchange in all
+  // ---- top-k with a small k: one exchange in all.  Where the slice is held in shared memory the next walk over it costs
+  // little, and k up to 16 pays from two CTAs a row on; else up to 32.  us with / without, k = 1, 5, 20, 50: one row of
+  // 248,320, fp32 12.1 / 13.5, 13.1 / 14.5, 14.0 / 14.8, 15.5 / 14.4, bf16 11.7 / 13.1, 13.2 / 14.3, 14.1 / 14.6, 14.7 / 14.1; of
+  // 65,536, fp32 11.8 / 12.0, 13.2 / 13.2, 13.5 / 13.3, 13.5 / 12.9; 192 rows of 248,320, fp32 52.6 / 66.3, 56.0 / 68.5, 59.6 / 68.9,
+  // 63.0 / 67.3, bf16 38.4 / 52.6, 42.4 / 55.2, 48.4 / 55.5, 54.4 / 53.6; one CTA a row: 192 rows of 65,536, read again, 15.8 / 18.2,
+  // 17.6 / 19.7, 18.6 / 20.0, 19.9 / 19.8, of 8,000, held, 13.6 / 13.2, 14.9 / 14.5, 15.2 / 14.9, 15.1 / 14.8.
   const bool by_count = k < (uint32_t)a.V;
-  const bool alone = by_count && k <= kThreads / 2 && k * C <= kCap * 5 / 8;  // about k + k^2 / 1024 tokens a CTA
-  const uint32_t room = kCap / C;                                             // of the list, for each CTA
+  const bool alone = by_count && (HELD ? C > 1 && k <= 16 : k <= 32);
   if (alone) {
-    if (lane_max > -INFINITY) {
-      const int own = step_of(lane_max, top, steps);
-      if (own < kBins - 1) atomicAdd(&s.all_count[own], 1u);
-    }
-    __syncthreads();
-    find_bin(s, false, k, 0);
-    // steps past the last hold no mass, whatever the other CTAs' largest
-    const int bin = min(s.bin, kBins - 2);
-    if (tid == 0) s.found = 0;  // which the search has used
-    __syncthreads();
-    const float low = top - (float)(bin + 2) / steps;
-    auto list = [&](int i, float z) {
-      z = clean(z);
-      if (!(z >= low) || step_of(z, top, steps) > bin) return;
-      const uint32_t at = atomicAdd(&s.found, 1);
-      if (at < room) s.cand[at] = ((u64)down_key(z) << 32) | (uint32_t)(index0 + i);
-    };
-    // Such tokens lie with lanes whose own maximum is one: where they are few, the warp looks through a
-    // lane's units together, one load for 32 of them, and the segment as a whole is not read again.
-    uint32_t hits = __ballot_sync(~0u, top > -INFINITY && lane_max >= low);
-    if (__popc(hits) > 8) {
-      z_of.template each4<false>(seg_from, seg_to, [&](int i, float (&z)[4]) {
-        if (fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= low) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) list(i + e, z[e]);
-        }
-        return false;
-      });
-    } else {
-      const int unit = !a.aligned && HELD ? 1 : (BF16 && a.aligned ? 8 : 4);  // as the lanes took them above
-#pragma unroll 1
-      for (; hits; hits &= hits - 1) {
-        const int of_lane = seg_from + (__ffs(hits) - 1) * unit;
-#pragma unroll 1
-        for (int i = of_lane + lane * 32 * unit; i < seg_to; i += 1024 * unit) {
-          if (unit == 1) {
-            list(i, HELD ? (BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(z_of.at)[i])
-                                 : reinterpret_cast<const float*>(z_of.at)[i]) : -INFINITY);
-          } else {
-            for (int g = 0; g < unit; g += 4) {
-              float z[4];
-              z_of.load4(i + g, z);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) list(i + g + e, z[e]);
-            }
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const uint32_t mine = (uint32_t)s.found;
-    cluster_wait();
-    if (rank) {
-      const uint32_t to = map_to_rank(smem_addr(s.cand + rank * room), 0);
-      for (uint32_t i = tid; i < min(mine, room); i += kThreads) st_dsmem_u64(to + 8 * i, s.cand[i]);
-    }
-    if (warp == 0 && lane < C) st_dsmem_u32(map_to_rank(smem_addr(&s.rank_cand[rank]), lane), mine);
+    top = list_largest(z_of, lane_max, steps, k, seg_from, seg_to, index0, rank, C);
   } else {
+    clear_histogram(s);
+    __syncthreads();
+    if (warp == 0) {
+      top = lane < kWarps ? s.warp_max[lane] : -INFINITY;
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    }
     cluster_wait();
   }
   if (warp == 0 && lane < C) st_dsmem_f32(map_to_rank(smem_addr(&s.rank_max[rank]), lane), top);
@@ -964,47 +1048,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return (uint32_t)s.found;
   };
 
-  // The lists of `alone` in the first CTA: of them the k largest and what shares their last step, unsorted.
-  auto pick = [&]() {
-    constexpr int kOwn = kCap / kThreads;
-    for (int i = tid; i < kBins; i += kThreads) s.all_count[i] = 0;
-    __syncthreads();
-    u64 c[kOwn];
-    int step[kOwn];
-#pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-      const uint32_t i = tid + e * kThreads, r = i / room;
-      step[e] = kBins;
-      if (i - r * room < s.rank_cand[r]) {
-        c[e] = s.cand[i];
-        step[e] = step_of(key_logit((uint32_t)(c[e] >> 32)), top, steps);
-        if (step[e] < kBins - 1) atomicAdd(&s.all_count[step[e]], 1u);
-      }
-    }
-    __syncthreads();
-    find_bin(s, false, k, 0);
-    const int last = min(s.bin, kBins - 2);
-    if (tid == 0) s.found = 0;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kOwn; ++e)
-      if (step[e] <= last) s.cand[atomicAdd(&s.found, 1)] = c[e];
-    __syncthreads();
-    return (uint32_t)s.found;
-  };
-
   uint32_t cut = 0xFFFFFFFFu, r_keep = 0xFFFFFFFFu;  // a key that no token has
   constexpr uint32_t kNone = 0xFFFFFFFFu;
   uint32_t ready = kNone;  // candidates in the first CTA that hold all that stays
   if (by_count || !(p >= 1.0f)) do {
     if (alone) {
-      bool fits = true;
-      for (int r = 0; r < C; ++r) fits &= s.rank_cand[r] <= room;
-      if (fits) {  // no CTA touches another's memory from here on
-        ready = rank == 0 ? pick() : 0;
+      // a list may be left out whose CTA has no token among the k largest
+      float floor_z = lane < C ? s.rank_floor[lane] : -INFINITY;
+      for (int o = 16; o; o >>= 1) floor_z = fmaxf(floor_z, __shfl_xor_sync(~0u, floor_z, o));
+      const bool fits = lane >= C || s.rank_cand[lane] <= kCap / C || s.rank_max[lane] < floor_z;
+      if (__all_sync(~0u, fits)) {  // no CTA touches another's memory from here on
+        ready = rank == 0 ? pick_largest(top, steps, k, C) : 0;
         break;
       }
-      __syncthreads();  // rank_cand has been read
+      __syncthreads();  // the list has been read, and rank_cand
+      clear_histogram(s);
+      __syncthreads();
     }
     // ---- the lanes' own maxima first: at least k tokens lie in the steps down to the k-th largest
     // of them, and with k up to half the lanes not many more.  Where they number kCap at most and
@@ -1341,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 template <bool BF16, bool HELD>
 size_t divide_rows(SampleArgs* a, int C) {
   a->cluster = C;
-  const int step = HELD ? (BF16 ? 256 : 128) : 512;
+  const int step = HELD ? 128 : 512;
   a->per_warp = ((a->V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step;
   a->aligned = ((uintptr_t)a->logits & 15) == 0 && (a->row_stride * (BF16 ? 2 : 4)) % 16 == 0;
   const size_t slice = HELD ? (size_t)kWarps * a->per_warp * (BF16 ? 2 : 4) : 0;
@@ -1411,8 +1470,7 @@ cudaError_t launch_rows(const P& all, int M, int V, cudaStream_t s) {
   // A slice is held in shared memory where two CTAs still share an SM (fp32, one row on 16: 14.7 / 9.4 us,
   // 15.0 / 10.4 read from L2), and a larger one where every CTA has an SM of its own (12 rows on eight:
   // 17.0 / 13.9 and 17.9 / 15.4; 16 rows: 27.0 / 23.9 and 19.9 / 20.6).
-  const int step = BF16 ? 256 : 128;
-  const long long slice = (long long)((V + C * kWarps - 1) / (C * kWarps) + step - 1) / step * step * kWarps * (BF16 ? 2 : 4);
+  const long long slice = (long long)((V + C * kWarps - 1) / (C * kWarps) + 127) / 128 * 128 * kWarps * (BF16 ? 2 : 4);
   return slice <= ((long long)M * C <= 96 ? 163840 : 65536) ? launch_divided<BF16, true>(all, C, s) : launch_divided<BF16, false>(all, C, s);
 }
 
