@@ -1452,16 +1452,17 @@ cudaError_t launch_divided(StatePair a, int C, cudaStream_t s) {
 // CTAs for each of M rows of V.
 inline int ctas_per_row(int M, int V) {
   // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16
-  // find room at once, and rows that wait for room are done soonest in slices of up to 65,536.  V = 248,320, fp32,
-  // top-k 20 and top-p / no truncation, us: six rows on 16 CTAs 15.7 / 10.9, on eight 16.6 / 13.3; eight
-  // rows 19.4 / 15.2 and 16.8 / 13.1; 32 rows on eight 22.8 / 22.6, on four 23.0 / 23.1; 192 rows on eight 101 / 105, on
-  // four 73 / 89, on two 89 / 91; 512 rows on four 195, on two 235 (mixed settings).  V = 32,768, 512 rows on two 57 / 42,
-  // on one 32 / 35; V = 65,536, 256 rows on four 47 / 44, on one 20 / 29; V = 131,072, 128 rows on eight 31 / 36, on
-  // four 20 / 29.
+  // find room at once, and rows that wait for room are done soonest in slices of up to 65,536, or by four CTAs.  fp32,
+  // top-k 20 / no truncation, us: V = 248,320, six rows on 16 CTAs 15.2 / 10.6, on eight 15.6 / 12.6; eight rows 18.5 / 13.9
+  // and 15.9 / 12.6; 32 rows on eight 18.2 / 19.4, on four 16.5 / 19.3; 192 rows on eight 78 / 102, on four 59 / 85, on two
+  // 63 / 89; 512 rows 181 / 249, 127 / 186 and 140 / 191.  V = 500,000, 64 rows on eight 43 / 65, on four 37 / 62.  V = 131,072, 128
+  // rows on eight 58 / 50, on four 33 / 35, on two 20 / 29.  V = 65,536, 256 rows on four 57 / 48, on two 34 / 35, on one 19 / 29.
+  // V = 32,768, 512 rows on two 65 / 46, on one 33 / 35.  (Where top-p keeps thousands more CTAs would do: V = 65,536, 96 rows with 0.95
+  // at T = 1 on four 47, on two 52, on one 67; the settings are on the device.)
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < V) C *= 2;
   if (C == 16 && M * 16 > 96) C = 8;
-  while (C > 1 && C < 16 && (long long)M * C > 256 && (long long)C * 32768 >= V) C /= 2;
+  while (C > 1 && C < 16 && (long long)M * C > 256 && (C == 8 || (long long)C * 32768 >= V)) C /= 2;
   return C;
 }
 template <bool BF16, class P>
