@@ -529,7 +529,8 @@ size_t lowbit_verify_drafts_workspace_bytes(int M, int N);
  *   drafts    : int32 [N], tokens of the target's vocabulary.
  *   draft_index : int32 [target V]: the column of the drafter's rows that stands for a token, -1 for none (a
  *               trimmed vocabulary), or NULL: the token itself.  Needs draft.
- *   u : fp32 [N], v : fp32 [B], in [0, 1) (others are clamped, NaN counts as 0).
+ *   u : fp32 [N], v : fp32 [B], in [0, 1).  Smaller ones and NaN count as 0, larger ones as 1: a draft is then accepted
+ *   where q(d) < p(d), and the next token is the last one that may be drawn.
  * With p and q the shares m / S of lowbit_sample's masses, under the request's settings, in the target's
  * and the drafter's row (q = 1 for the draft and 0 else where draft is NULL; a token without column has
  * q = 0, a row without a finite logit p = 0 or q = 0 throughout):
