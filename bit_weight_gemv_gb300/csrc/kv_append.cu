@@ -193,9 +193,11 @@ __global__ void __launch_bounds__(256, 5) kv_append_kernel(const __grid_constant
 // registers over the token's heads, and no warp waits for another.  The first heads are asked for before the
 // token's place is known.
 //
-// 16,396 tokens of 32 + 8 + 8 heads of 128, bf16: 75.6 us, 411 MB, 5.4 TB/s of 6.8 copied: HBM, reads and writes of
+// 16,396 tokens of 32 + 8 + 8 heads of 128, bf16: 74.5 us, 411 MB, 5.5 TB/s of 6.8 copied: HBM, reads and writes of
 // short runs in turn.  One step at a time 88 us, four 92 (more registers, fewer warps), blocks of 256 threads 77.9,
-// without the hints to L2 76.8, eight warps a token 128.  512 tokens into an e4m3 cache 4.5 us, one 4.0.
+// without the hints to L2 76.8, eight warps a token 128 (of 75.6 then).  Into an e4m3 cache 92 us, 378 MB, 4.1 TB/s: as many
+// instructions a cycle (58% of the slots, with 24 warps an SM) but 23% more of them, for an exact quotient and a
+// conversion of each element of k and v.  512 tokens into an e4m3 cache 4.5 us, one 4.0.
 template <int WARPS>
 constexpr int kNormThreads = WARPS < 8 ? 128 : 256;
 template <int D, bool FP8, bool INTER, int WARPS>

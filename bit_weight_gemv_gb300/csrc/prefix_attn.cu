@@ -66,7 +66,7 @@ __device__ __forceinline__ int shared_keys_of_row(const PrefixArgs& a, int t, in
 }
 
 // A warp joins a row's pieces: of the shared part, then of its own.  Bound by round trips: where they are and, meanwhile,
-// the row's request and group; their statistics; the pieces.  Alone and cold 12 us for 256 rows, 26 for 20,992 (36 MB).
+// the row's request and group; their statistics; the pieces.  Alone and cold 11 us for 256 rows, 22 for 20,992 (36 MB).
 // (Looking the request up before the wait would take 1 us off, but what earlier kernels wrote is promised to be seen
 // only behind it.)
 template <int D>

@@ -7,8 +7,9 @@
 // A cluster of CTAs takes one row, each a contiguous slice, held in its shared memory where two such
 // CTAs share an SM (the row is then read once), else read again from L2, which holds the rows in
 // flight.  Truncation keeps a prefix of the order (larger logit, then lower index):
-//   1. the largest logit, over the cluster;
-//   2. a bound from the lanes' own maxima, of which k (or 512, for top-p alone) lie above it: a count of
+//   1. the largest logit, over the cluster; with it, for a small top-k (16 or 32, by where the slice is), the CTAs' own lists
+//      of their largest tokens, from which the first CTA finishes the row (list_largest, pick_largest);
+//   2. else a bound from the lanes' own maxima, of which k (or 512, for top-p alone) lie above it: a count of
 //      them in 1024 equal steps of (max - z) / T (28.5 covers every weight that does not round to
 //      zero).  The tokens down to that step, little more than k, go to the first CTA; for top-p the same
 //      pass takes the whole mass S.  Where they hold all that stays, the first CTA sorts them and
@@ -22,8 +23,11 @@
 //      walks the segments that the warps own.  (A step with more than 2048 tokens, such as a row of
 //      equal logits, is narrowed down by its keys' digits.)
 //
-// Few rows wait on latency: one row of 248,320 takes 14.6 us with top-k 20 and top-p 0.95, of which the
-// merges and exchanges over 16 CTAs take 9, and 9.7 us without truncation.  Many rows are bound by
+// For lowbit_verify_drafts (StatePair) the rows of the target and of the drafter go through the same steps in one launch, and
+// each leaves what it has settled, the largest logit, the cut and the mass of what stays, instead of a token.
+//
+// Few rows wait on latency: one row of 248,320 takes 14.9 us with top-k 20 and top-p 0.95, of which the
+// merges and exchanges over 16 CTAs take 9, 13.1 with top-k 5, and 10.2 us without truncation.  Many rows are bound by
 // instructions, about 30 for each weight that is summed: 192 rows of mixed settings take 124 us, 28
 // of them for reading the logits once at the copy rate.
 #pragma once
@@ -1067,10 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     // ---- the lanes' own maxima first: at least k tokens lie in the steps down to the k-th largest
     // of them, and with k up to half the lanes not many more.  Where they number kCap at most and
-    // hold all that top-k or top-p leaves, they finish the row, and no histogram of it is taken (one
+    // hold all that top-k or top-p leaves, they finish the row, and no histogram of it is taken (when it was brought in, one
     // row of 248,320 with top-k 20: 14.9 us, 17.5 by the histogram; with top-p 0.8: 19.8 and 25.7).  For
-    // top-p the bound is that of 512 lanes (16 rows with top-p 0.8: 29 us, 46 with 256 and 30 with 1,024;
-    // 192 rows of mixed settings 145, 147 and 152).  A larger k, up to three quarters of the lanes, has a bound of
+    // top-p the bound is that of 512 lanes (likewise, 16 rows with top-p 0.8: 29 us, 46 with 256 and 30 with 1,024;
+    // 192 rows of mixed settings, then 145, 147 and 152).  A larger k, up to three quarters of the lanes, has a bound of
     // them too, below which its histogram need not look.
     const uint32_t reach = min(C * kThreads / 2, kCap / 2);
     u64 limit = 0;

@@ -15,9 +15,9 @@
 // Differences are taken in fp32 of the two probabilities, each product and the difference rounded by
 // itself, and become whole numbers (2^-40 each) before they are summed, so the sums are exact, in any order.
 //
-// Bound: few rows by round trips (15 drafts of one request proposed with certainty, 16 rows of 248,320: 20.4 us, of which
+// Bound: few rows by round trips (15 drafts of one request proposed with certainty, 16 rows of 248,320: 20.6 us, of which
 // the states take some 13 and the draw from a list the rest; the rows at the copy rate 2.4), many by the instructions of
-// rows that sum masses (480 drafts of 32 requests under settings of all kinds, 574 MB: 204 to 242 us with the settings; 85 at
+// rows that sum masses (480 drafts of 32 requests under settings of all kinds, 574 MB: 204 to 248 us with the settings; 85 at
 // the copy rate).  Where nothing is cut off and the next token comes from a difference, the draw weighs two rows of the
 // vocabulary in 16 CTAs: 7 drafts of each of four requests against full drafter rows 34 us, 30 MB.  The states are a kernel
 // of their own because they are the same for every row, whoever needs them, and spread over all SMs; the draw, which
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kDrawThreads, 1) verify_draw_kernel(const __gr
 
 template <bool BF16, bool DRAFT_BF16>
 cudaError_t launch_draw(VerifyArgs a, cudaStream_t s) {
-  // Slices of 16,384 elements and more, and no more CTAs than fit at a time.
+  // Slices of up to 16,384 elements where the CTAs, one an SM, fit at a time, else longer ones, by two CTAs a request at least
+  // (one where 16,384 hold the row).
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < a.V) C *= 2;
   while (C > 2 && (long long)a.B * C > 152) C /= 2;
@@ -505,7 +506,7 @@ lowbit_status lowbit_verify_drafts(const lowbit_row_settings* target, const lowb
   pair.part[0] = rows_of(target);
   if (drafter) {
     // Both in one launch, so that the short rows fill the gaps of the long ones (28 drafts of four requests 34 us, 40
-    // one after the other; 67 of nine with a trimmed vocabulary 59 and 67; 480 of 32 206 and 218).
+    // one after the other; with the settings of one seed, 67 of nine with a trimmed vocabulary 59 and 67; 480 of 32 206 and 218).
     if (bf16 == draft_bf16) {
       pair.part[1] = rows_of(draft);
     } else {
