@@ -462,7 +462,7 @@ size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int
  * table rows of a group differ in the shared pages, it is not defined which of them a request sees.
  * Worth it where many requests with few rows each share much (16 requests of one token and more behind
  * thousands of keys).  From about 100 rows a request on (tokens times query heads per key/value head), and
- * under block tables of 1,024 slots (for few requests 2,048; not for very many over e4m3, or with heads of 256),
+ * under block tables of 1,024 slots (for small groups 2,048; not for very many requests over e4m3, or with heads of 256),
  * lowbit_paged_attention's kernels do the work, which are as fast there.  The kernels are chosen by averages (T / groups, T / B) and by the length that the block
  * table has room for: keep it about as wide as the requests need.
  *   workspace : lowbit_prefix_attention_workspace_bytes() bytes, 16-byte aligned, any contents; calls that

@@ -28,7 +28,7 @@ def test_nothing_behind_the_workspace_is_written(lb, D, new, fp8):  # noqa: F811
 # several groups of 16.
 @pytest.mark.parametrize("B,groups,Hq,Hk,D,fp8,room", [
     (512, 1, 16, 8, 64, True, 512), (511, 3, 16, 8, 64, True, 512), (128, 1, 32, 8, 256, False, 1024), (127, 1, 32, 8, 256, False, 1024),
-    (64, 4, 8, 2, 128, False, 2048), (16, 1, 8, 2, 128, False, 2048), (17, 1, 8, 2, 128, False, 2048)])
+    (64, 4, 32, 8, 128, False, 2048), (64, 4, 8, 2, 128, False, 2048), (16, 1, 8, 2, 128, False, 2048), (17, 1, 8, 2, 128, False, 2048)])
 def test_many_requests_under_short_tables(lb, B, groups, Hq, Hk, D, fp8, room):  # noqa: F811
     prefix = [64 + 32 * g for g in range(groups)]
     pr = Shared(41, [B * g // groups for g in range(groups + 1)], prefix, [int(b % 7 != 3) for b in range(B)],
