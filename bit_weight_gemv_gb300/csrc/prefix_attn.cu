@@ -244,16 +244,17 @@ lowbit_status lowbit_prefix_attention(const uint16_t* q, int64_t q_stride, int H
   // On the warp-level MMA, whose items have 64 rows at most, from 50 on (heads of 256, 16 requests behind 6,000
   // keys, 64 rows each 89 / 82, 32 rows 54 / 55).
   const long long all = (long long)a.p.T * a.shape.G, shared_rows = (all + groups - 1) / groups, own_rows = (all + B - 1) / B;
-  // Short requests are as quick on their own, too.  Their lengths the host knows a bound of, the block table's: us with one
-  // row tile shared / on their own, bf16, 100 keys each behind 256, 1,024 and 2,048: 8 of four rows 12 / 8, 14 / 10, 16 / 12, 32
-  // 22 / 12, 24 / 18, 24 / 26, 128 45 / 26, 49 / 49, 50 / 82; 16 of 64 rows 26 / 13, 29 / 24, 33 / 30, 128 115 / 64, 139 / 107,
-  // 173 / 164.  Groups of 16 and less under 2,048 slots so, too, unless there are many: 42 of 32 rows in ten groups, e4m3, 42 / 32,
-  // 36 in nine 30 / 27, 22 of five rows in two 16 / 11; 64 of four rows in four groups, behind 960 keys 52 / 54, 1,920 37 / 65.
-  // Under 1,024 slots it stays so with any number of requests (512 of four rows behind 448 keys 185 / 127, 512 216 / 192, 960
-  // 192 / 227; heads of 64, 8 rows each 56 / 31, 65 / 39, 55 / 44), but where reading a request's keys takes the plain
-  // kernels long: many few-row items over e4m3 (512 of four rows 81 / 95, 125 / 138, 93 / 158, heads of 64 64 / 73, 94 / 105,
-  // 67 / 122; 2,048 with two heads 99 / 110, 140 / 156, 107 / 174; 256 56 / 54, 82 / 75, 56 / 86; eight rows each 69 / 58, 96 / 80, 76 / 91),
-  // and heads of 256 in bf16 (128 of four rows 64 / 90, 102 / 139, 71 / 165; over e4m3 73 / 50, 119 / 70, 82 / 79).
+  // Short requests are as quick on their own, too.  Their lengths the host knows a bound of, the block table's: us with
+  // one row tile shared / on their own, bf16, 100 keys each behind 256, 1,024 and 2,048: 8 of four rows 12 / 8, 14 / 10,
+  // 16 / 12, 32 22 / 12, 24 / 18, 24 / 26, 128 45 / 26, 49 / 49, 50 / 82; 16 of 64 rows 26 / 13, 29 / 24, 33 / 30, 128
+  // 115 / 64, 139 / 107, 173 / 164.  Groups of 16 and less under 2,048 slots so, too, unless there are many: 42 of 32
+  // rows in ten groups, e4m3, 42 / 32, 36 in nine 30 / 27, 22 of five rows in two 16 / 11; 64 of four rows in four
+  // groups, behind 960 keys 52 / 54, 1,920 37 / 65. Under 1,024 slots it stays so with any number of requests (512 of
+  // four rows behind 448 keys 185 / 127, 512 216 / 192, 960 192 / 227; heads of 64, 8 rows each 56 / 31, 65 / 39, 55 /
+  // 44), but where reading a request's keys takes the plain kernels long: many few-row items over e4m3 (512 of four rows
+  // 81 / 95, 125 / 138, 93 / 158, heads of 64 64 / 73, 94 / 105, 67 / 122; 2,048 with two heads 99 / 110, 140 / 156, 107
+  // / 174; 256 56 / 54, 82 / 75, 56 / 86; eight rows each 69 / 58, 96 / 80, 76 / 91), and heads of 256 in bf16 (128 of
+  // four rows 64 / 90, 102 / 139, 71 / 165; over e4m3 73 / 50, 119 / 70, 82 / 79).
   const long long reach = (long long)a.p.width << a.p.page_shift, items = (long long)B * cache->heads;
   const bool slow_alone = own_rows <= 4 && (D == 256 ? !fp8 && items >= 1024 : fp8 && items >= 4096);
   const bool brief = (reach <= 1024 && !slow_alone) ||

@@ -804,10 +804,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // ---- top-k with a small k: one exchange in all.  Where the slice is held in shared memory the next walk over it costs
   // little, and k up to 16 pays from two CTAs a row on; else up to 32.  us with / without, k = 1, 5, 20, 50: one row of
-  // 248,320, fp32 12.1 / 13.5, 13.1 / 14.5, 14.0 / 14.8, 15.5 / 14.4, bf16 11.7 / 13.1, 13.2 / 14.3, 14.1 / 14.6, 14.7 / 14.1; of
-  // 65,536, fp32 11.8 / 12.0, 13.2 / 13.2, 13.5 / 13.3, 13.5 / 12.9; 192 rows of 248,320, fp32 52.6 / 66.3, 56.0 / 68.5, 59.6 / 68.9,
-  // 63.0 / 67.3, bf16 38.4 / 52.6, 42.4 / 55.2, 48.4 / 55.5, 54.4 / 53.6; one CTA a row: 192 rows of 65,536, read again, 15.8 / 18.2,
-  // 17.6 / 19.7, 18.6 / 20.0, 19.9 / 19.8, of 8,000, held, 13.6 / 13.2, 14.9 / 14.5, 15.2 / 14.9, 15.1 / 14.8.
+  // 248,320, fp32 12.1 / 13.5, 13.1 / 14.5, 14.0 / 14.8, 15.5 / 14.4, bf16 11.7 / 13.1, 13.2 / 14.3, 14.1 / 14.6, 14.7 /
+  // 14.1; of 65,536, fp32 11.8 / 12.0, 13.2 / 13.2, 13.5 / 13.3, 13.5 / 12.9; 192 rows of 248,320, fp32 52.6 / 66.3, 56.0
+  // / 68.5, 59.6 / 68.9, 63.0 / 67.3, bf16 38.4 / 52.6, 42.4 / 55.2, 48.4 / 55.5, 54.4 / 53.6; one CTA a row: 192 rows of
+  // 65,536, read again, 15.8 / 18.2, 17.6 / 19.7, 18.6 / 20.0, 19.9 / 19.8, of 8,000, held, 13.6 / 13.2, 14.9 / 14.5,
+  // 15.2 / 14.9, 15.1 / 14.8.
   const bool by_count = k < (uint32_t)a.V;
   const bool alone = by_count && (HELD ? C > 1 && k <= 16 : k <= 32);
   if (alone) {
@@ -1455,14 +1456,14 @@ cudaError_t launch_divided(StatePair a, int C, cudaStream_t s) {
 
 // CTAs for each of M rows of V.
 inline int ctas_per_row(int M, int V) {
-  // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16
-  // find room at once, and rows that wait for room are done soonest in slices of up to 65,536, or by four CTAs.  fp32,
-  // top-k 20 / no truncation, us: V = 248,320, six rows on 16 CTAs 15.2 / 10.6, on eight 15.6 / 12.6; eight rows 18.5 / 13.9
-  // and 15.9 / 12.6; 32 rows on eight 18.2 / 19.4, on four 16.5 / 19.3; 192 rows on eight 78 / 102, on four 59 / 85, on two
-  // 63 / 89; 512 rows 181 / 249, 127 / 186 and 140 / 191.  V = 500,000, 64 rows on eight 43 / 65, on four 37 / 62.  V = 131,072, 128
-  // rows on eight 58 / 50, on four 33 / 35, on two 20 / 29.  V = 65,536, 256 rows on four 57 / 48, on two 34 / 35, on one 19 / 29.
-  // V = 32,768, 512 rows on two 65 / 46, on one 33 / 35.  (Where top-p keeps thousands more CTAs would do: V = 65,536, 96 rows with 0.95
-  // at T = 1 on four 47, on two 52, on one 67; the settings are on the device.)
+  // The more CTAs the sooner a row is done, down to slices of 16,384 elements; but few clusters of 16 find room at once,
+  // and rows that wait for room are done soonest in slices of up to 65,536, or by four CTAs.  fp32, top-k 20 / no
+  // truncation, us: V = 248,320, six rows on 16 CTAs 15.2 / 10.6, on eight 15.6 / 12.6; eight rows 18.5 / 13.9 and 15.9 /
+  // 12.6; 32 rows on eight 18.2 / 19.4, on four 16.5 / 19.3; 192 rows on eight 78 / 102, on four 59 / 85, on two 63 / 89;
+  // 512 rows 181 / 249, 127 / 186 and 140 / 191.  V = 500,000, 64 rows on eight 43 / 65, on four 37 / 62.  V = 131,072,
+  // 128 rows on eight 58 / 50, on four 33 / 35, on two 20 / 29.  V = 65,536, 256 rows on four 57 / 48, on two 34 / 35, on
+  // one 19 / 29. V = 32,768, 512 rows on two 65 / 46, on one 33 / 35.  (Where top-p keeps thousands more CTAs would do: V
+  // = 65,536, 96 rows with 0.95 at T = 1 on four 47, on two 52, on one 67; the settings are on the device.)
   int C = 1;
   while (C < kMaxCluster && (long long)C * 16384 < V) C *= 2;
   if (C == 16 && M * 16 > 96) C = 8;

@@ -454,17 +454,19 @@ size_t lowbit_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hk, int
  *                 own.  0: nothing is shared.  New tokens come after the shared positions:
  *                 kv_lens[b] - new tokens >= the length of the whole pages.
  * kv_lens and block_table describe the whole requests, as for lowbit_kv_append and lowbit_paged_attention,
- * whose result over the same arguments is this one's but for rounding.  A group or request that the
- * arrays describe inconsistently is recorded in the device error word; its rows are not written, or (where only
- * what it shares is at fault) attend to the request's own block table.  Groups are looked up by bisection: where
- * cu_groups is not ascending, other groups may be left out with the one at fault.  What a row gets that several
- * requests claim (cu_q not ascending), or a request that several groups claim, is not defined.  Pages are compared by nobody: where the
- * table rows of a group differ in the shared pages, it is not defined which of them a request sees.
+ * whose result over the same arguments is this one's but for rounding.  A group or request that the arrays
+ * describe inconsistently is recorded in the device error word; its rows are not written, or (where only what
+ * it shares is at fault) attend to the request's own block table.  Groups are looked up by bisection: where
+ * cu_groups is not ascending, other groups may be left out with the one at fault.  What a row gets that
+ * several requests claim (cu_q not ascending), or a request that several groups claim, is not defined.  Pages
+ * are compared by nobody: where the table rows of a group differ in the shared pages, it is not defined which
+ * of them a request sees.
  * Worth it where many requests with few rows each share much (16 requests of one token and more behind
  * thousands of keys).  From about 100 rows a request on (tokens times query heads per key/value head), and
- * under block tables of 1,024 slots (for small groups 2,048; not for very many requests over e4m3, or with heads of 256),
- * lowbit_paged_attention's kernels do the work, which are as fast there.  The kernels are chosen by averages (T / groups, T / B) and by the length that the block
- * table has room for: keep it about as wide as the requests need.
+ * under block tables of 1,024 slots (for small groups 2,048; not for very many requests over e4m3, or with
+ * heads of 256), lowbit_paged_attention's kernels do the work, which are as fast there.  The kernels are
+ * chosen by averages (T / groups, T / B) and by the length that the block table has room for: keep it about
+ * as wide as the requests need.
  *   workspace : lowbit_prefix_attention_workspace_bytes() bytes, 16-byte aligned, any contents; calls that
  *   may run at the same time need one each.
  * All else (rounding, non-finite values, alignment) is as in lowbit_paged_attention; a non-finite v in
