@@ -7,7 +7,7 @@
 // A cluster of CTAs takes one row, each a contiguous slice, held in its shared memory where two such
 // CTAs share an SM (the row is then read once), else read again from L2, which holds the rows in
 // flight.  Truncation keeps a prefix of the order (larger logit, then lower index):
-//   1. the largest logit, over the cluster; with it, for a small top-k (16 or 32, by where the slice is), the CTAs' own lists
+//   1. the largest logit, over the cluster; with it, for a small top-k (20 or 32, by where the slice is), the CTAs' own lists
 //      of their largest tokens, from which the first CTA finishes the row (list_largest, pick_largest);
 //   2. else a bound from the lanes' own maxima, of which k (or 512, for top-p alone) lie above it: a count of
 //      them in 1024 equal steps of (max - z) / T (28.5 covers every weight that does not round to
@@ -26,8 +26,8 @@
 // For lowbit_verify_drafts (StatePair) the rows of the target and of the drafter go through the same steps in one launch, and
 // each leaves what it has settled, the largest logit, the cut and the mass of what stays, instead of a token.
 //
-// Few rows wait on latency: one row of 248,320 takes 14.9 us with top-k 20 and top-p 0.95, of which the
-// merges and exchanges over 16 CTAs take 9, 13.1 with top-k 5, and 10.2 us without truncation.  Many rows are bound by
+// Few rows wait on latency: one row of 248,320 takes 14.5 us with top-k 20 and top-p 0.95, of which the
+// merges and exchanges over 16 CTAs take 9, 13.4 with top-k 5, and 10.2 us without truncation.  Many rows are bound by
 // instructions, about 30 for each weight that is summed: 192 rows of mixed settings take 124 us, 28
 // of them for reading the logits once at the copy rate.
 #pragma once
@@ -439,9 +439,10 @@ __device__ __forceinline__ float list_largest(const Slice<BF16, HELD> z_of, floa
   __syncthreads();
   const float low = top - (float)(bin + 2) / steps;
   // In a row whose large tokens lie side by side (a vocabulary by frequency) a CTA's tokens may crowd into these steps.
-  // Most likely it has none of the k largest, and its list is not made.
+  // Most likely it has none of the k largest, and its list is not made (one row of 500,000, sorted, top-k 24: 17.0 us, 21.6
+  // with a list of the tokens of one step, which 32 lanes hold the most of).
   uint32_t mine = kCap + 1;
-  if (lanes <= k + 8 + k / 8) {
+  if (lanes <= k + 8 + k / 8 && (bin > 0 || k < 8)) {
     auto list = [&](int i, float z) {
       z = clean(z);
       if (!(z >= low) || step_of(z, top, steps) > bin) return;
@@ -803,14 +804,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (lane == 0) s.warp_max[warp] = top;
 
   // ---- top-k with a small k: one exchange in all.  Where the slice is held in shared memory the next walk over it costs
-  // little, and k up to 16 pays from two CTAs a row on; else up to 32.  us with / without, k = 1, 5, 20, 50: one row of
-  // 248,320, fp32 12.1 / 13.5, 13.1 / 14.5, 14.0 / 14.8, 15.5 / 14.4, bf16 11.7 / 13.1, 13.2 / 14.3, 14.1 / 14.6, 14.7 /
-  // 14.1; of 65,536, fp32 11.8 / 12.0, 13.2 / 13.2, 13.5 / 13.3, 13.5 / 12.9; 192 rows of 248,320, fp32 52.6 / 66.3, 56.0
-  // / 68.5, 59.6 / 68.9, 63.0 / 67.3, bf16 38.4 / 52.6, 42.4 / 55.2, 48.4 / 55.5, 54.4 / 53.6; one CTA a row: 192 rows of
-  // 65,536, read again, 15.8 / 18.2, 17.6 / 19.7, 18.6 / 20.0, 19.9 / 19.8, of 8,000, held, 13.6 / 13.2, 14.9 / 14.5,
-  // 15.2 / 14.9, 15.1 / 14.8.
+  // little, and k up to 20 pays from two CTAs a row on; else up to 32.  us with / without, k = 5, 20, 32, 40: held, one row
+  // of 248,320, fp32 13.4 / 14.6, 14.5 / 14.8, 14.7 / 14.9, 15.2 / 15.0, bf16 13.1 / 14.2, 14.2 / 14.4, 15.0 / 14.5, 15.2 /
+  // 14.6; 64 rows of 65,536, fp32 16.1 / 16.6, 16.8 / 16.8, 17.1 / 16.9, 17.2 / 16.9; 192 rows of 8,000, one CTA each, with
+  // k = 5, 20 and 50 14.9 / 14.5, 15.2 / 14.9, 15.1 / 14.8.  Read again, 64 rows of 248,320, fp32 18.4 / 21.9, 20.1 / 21.9,
+  // 20.6 / 21.9, 21.0 / 22.0, bf16 17.8 / 21.2, 20.2 / 21.2, 21.2 / 21.2, 21.9 / 21.3; 192 rows of 65,536, one CTA each,
+  // k = 5, 20 and 50 17.6 / 19.7, 18.6 / 20.0, 19.9 / 19.8.
   const bool by_count = k < (uint32_t)a.V;
-  const bool alone = by_count && (HELD ? C > 1 && k <= 16 : k <= 32);
+  const bool alone = by_count && (HELD ? C > 1 && k <= 20 : k <= 32);
   if (alone) {
     top = list_largest(z_of, lane_max, steps, k, seg_from, seg_to, index0, rank, C);
   } else {
